@@ -483,6 +483,168 @@ msm_status msm_graph_create_spec(msm_model* target, msm_model* draft, const void
                                  const void* embed_table, void* hidden_buf, int32_t* state, void* const* k_cache,
                                  void* const* v_cache, float* logits_out, int32_t* accept_result, msm_graph** out);
 
+/*
+ * Paged KV cache: the K/V rows of many sequences in fixed-size pages of one pool per
+ * layer, with the calls a serving loop makes around msm_verify_step and
+ * msm_draft_step for prompts, batches and searches.  (The pages that describe the
+ * verify step keep one user's contiguous caches; they describe none of this.)
+ *
+ * Layouts
+ *   pool (layer)   16-bit floats [n_pages][n_kv_heads][page_rows][head_dim], K and V.
+ *                  A page has the layout of a verify-step cache of page_rows rows: with
+ *                  page_rows = max_ctx, page p of a layer's pools can be passed to
+ *                  msm_verify_step as that layer's caches.
+ *   table          int32 [n_seqs][max_pages]: the pages of each sequence in order;
+ *                  -1 behind its last page
+ *   lens           int32 [n_seqs]: rows of each sequence (0: an unused slot)
+ *   refs           int32 [n_pages]: how many sequences hold the page; 0: free
+ *   status         int32 [1]: 0, or the first error that a kernel met
+ *   scratch        int32 [msm_pages_scratch_ints(n_pages, n_seqs)], contents of no
+ *                  interest between calls
+ * Row r of sequence s is row r % page_rows of page table[s][r / page_rows].  All of
+ * these are device buffers of the caller.  An empty cache has lens, refs and status
+ * zero and table -1.
+ *
+ * resize, fork and compact change table, lens and refs on the device, in stream order
+ * and without a host round trip, so a stream capture records them.  Their results do
+ * not depend on timing: pages are always taken in the order of their index, the lowest
+ * free one first.  Each of them either does what it was asked or, when it finds an
+ * error (below), changes nothing and leaves the error in status.  Calls on one cache
+ * must be ordered (one stream, or events); msm_pages_write and msm_paged_attention of
+ * different layers may overlap each other.
+ *
+ * Errors met on the device are reported by msm_pages_sync: MSM_ERR_OOM (no free page
+ * left), MSM_ERR_INVALID_ARG (values out of range).  Kernels never follow a page index
+ * outside [0, n_pages).  Host errors of every call: MSM_ERR_INVALID_ARG (NULL or
+ * misaligned pointers, sizes below 1, strides that are no multiple of 8 elements),
+ * MSM_ERR_UNSUPPORTED (head_dim other than 64 or 128, n_q_heads / n_kv_heads other
+ * than 1, 2, 4 or 8, 2^31 or more table entries, 2^32 or more rows in a pool);
+ * nothing is enqueued then.  The calls leave the current device as it was.
+ */
+typedef enum { MSM_BF16 = 0, MSM_FP16 = 1 } msm_dtype;
+
+typedef struct {
+  int device;
+  int dtype;                   /* msm_dtype of the pools, and of the rows and queries used with them */
+  int n_layers, n_pages, page_rows, n_kv_heads, head_dim;
+  int n_seqs, max_pages;       /* rows and columns of the table */
+  void* const* k_pages;        /* host arrays [n_layers] of device pointers, 16-byte aligned */
+  void* const* v_pages;
+  int32_t *table, *lens, *refs, *status, *scratch;
+} msm_pages;
+
+/* int32 entries of msm_pages.scratch (0 for sizes below 1) */
+size_t msm_pages_scratch_ints(int n_pages, int n_seqs);
+
+/*
+ * New lengths for the sequences: new_lens device int32 [n_seqs], -1 = leave as it is.
+ * A sequence that grows gets the pages it lacks from those free before the call, in
+ * the order of the sequences; if it ends inside a page that other sequences hold too,
+ * it first gets its own copy of that page's rows in every layer.  A sequence that
+ * shrinks gives back the pages behind its new end (their table entries become -1);
+ * length 0 frees it.  Rows that become part of a sequence hold what their pages held.
+ * Device errors: MSM_ERR_OOM; MSM_ERR_INVALID_ARG for a length below -1 or above
+ * max_pages * page_rows, or for tables that hold a page outside the pool.
+ */
+msm_status msm_pages_resize(const msm_pages* pages, const int32_t* new_lens, void* stream);
+
+/*
+ * Sequences that begin as another one stands: parent device int32 [n_seqs], -1 = none.
+ * Sequence s with parent[s] = p gets p's length and shares all of its pages; both may
+ * then be resized and written as if each had its own.  Device error:
+ * MSM_ERR_INVALID_ARG if a parent is out of range, is s itself or has a parent in this
+ * call, or if s is not empty.
+ */
+msm_status msm_pages_fork(const msm_pages* pages, const int32_t* parent, void* stream);
+
+/*
+ * The pages in use moved to the front of the pool in every layer: with n of them in
+ * use, those at index n and above take the free indices below n, both in ascending
+ * order, and the tables follow.  refs of the moved pages move with them.
+ */
+msm_status msm_pages_compact(const msm_pages* pages, void* stream);
+
+/*
+ * K/V rows of new tokens into one layer's pages.  The tokens of sequence s are rows
+ * starts[s] .. starts[s + 1] - 1 of k and v; they become the last rows of the
+ * sequence, which msm_pages_resize must have made room for.
+ *   k, v    device [n_tokens][n_kv_heads][head_dim], strides in elements between
+ *           tokens and between heads (multiples of 8), 16-byte aligned
+ *   starts  device int32 [n_seqs + 1], ascending from 0; tokens at or behind
+ *           starts[n_seqs] are ignored
+ * Device error: MSM_ERR_INVALID_ARG for a token without a row, or whose page is free
+ * or shared; that token is left out.
+ */
+msm_status msm_pages_write(const msm_pages* pages, int layer, const void* k, const void* v, int64_t k_token_stride,
+                           int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                           const int32_t* starts, int n_tokens, void* stream);
+
+/*
+ * Attention of one new token per sequence over one layer's pages (plain decoding):
+ *   out[s][h] = sum_r softmax_r(scale q[s][h] . k_r) v_r   over the rows r of sequence s,
+ * query head h reading kv head h / (n_q_heads / n_kv_heads).  The new token is the
+ * sequence's last row (written before the call); with window > 0 it sees the last
+ * `window` rows only, as on the verify step's sliding-window layers.  A sequence
+ * without rows gives zeros.  Rows behind a sequence's end or before its window are not
+ * read, whatever they hold.  32-bit sums; the weights are rounded to the 16-bit type
+ * for their product with v.
+ *   q, out     device [n_seqs][n_q_heads][head_dim], strides in elements between
+ *              sequences and between heads (multiples of 8), 16-byte aligned
+ *   workspace  device buffer of msm_paged_attention_workspace bytes (0: an argument is
+ *              wrong, see msm_last_error), 16-byte aligned; its contents are of no
+ *              interest before or after.  Calls that share one must
+ *              not overlap on the GPU.
+ * Device error: MSM_ERR_INVALID_ARG for a row on a page outside the pool; such rows are
+ * left out.
+ */
+size_t msm_paged_attention_workspace(const msm_pages* pages, int n_q_heads);
+msm_status msm_paged_attention(const msm_pages* pages, int layer, const void* q, int64_t q_seq_stride,
+                               int64_t q_head_stride, int n_q_heads, float scale, int window, void* out,
+                               int64_t out_seq_stride, int64_t out_head_stride, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Wait for `stream`, then return (and clear) the device status of the cache. */
+msm_status msm_pages_sync(const msm_pages* pages, void* stream);
+
+/*
+ * Causal attention of whole prompts, packed one behind the other: the pass that fills
+ * the caches which the verify step, the draft step and msm_paged_attention read.
+ * Sequence s has the queries q_starts[s] .. q_starts[s + 1] - 1 and the keys k_starts[s]
+ * .. k_starts[s + 1] - 1, aligned at their ends: with nq queries and nk keys, query i
+ * sees the keys j with 0 <= i + (nk - nq) - j, and with window > 0 only those with
+ * i + (nk - nq) - j < window (the verify step's sliding window).  nk > nq resumes a
+ * prompt whose first rows are cached already; a query that sees no key gives zeros.
+ *   out[i][h] = sum_j softmax_j(scale q[i][h] . k[j]) v[j]
+ * with kv head h / (n_q_heads / n_kv_heads).  32-bit sums; the weights are rounded to
+ * the 16-bit type for their product with v.  Keys that a query does not see have no
+ * part in its result, whatever they hold.
+ *   q, out   device [n_q][n_q_heads][head_dim]; k, v device [n_k][n_kv_heads][head_dim]:
+ *            strides in elements between tokens and between heads (multiples of 8, at
+ *            least head_dim, below 2^31), 16-byte aligned.  A verify-step cache is read in
+ *            place with token stride head_dim and head stride max_ctx * head_dim.  out must not
+ *            overlap the inputs.
+ *   q_starts, k_starts  device int32 [n_seqs + 1], ascending from 0, at most n_q and n_k
+ *            (larger values are cut off there); rows of out at or behind
+ *            q_starts[n_seqs] are left as they are.  n_q = 0 does nothing; with n_k = 0
+ *            k and v may be NULL.
+ * Host errors: MSM_ERR_INVALID_ARG (NULL or misaligned pointers, sizes out of range,
+ * strides), MSM_ERR_UNSUPPORTED (head_dim other than 64 or 128, n_q_heads / n_kv_heads
+ * other than 1, 2, 4 or 8, n_q or n_k of 2^27 or more).
+ */
+typedef struct {
+  int device;
+  int dtype;  /* msm_dtype */
+  int n_seqs, n_q, n_k, n_q_heads, n_kv_heads, head_dim;
+  int window; /* 0: every key up to the query's own position */
+  float scale;
+  const void *q, *k, *v;
+  void* out;
+  int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride,
+      out_token_stride, out_head_stride;
+  const int32_t *q_starts, *k_starts;
+} msm_prompt;
+msm_status msm_prompt_attention(const msm_prompt* prompt, void* stream);
+
 /* Message of the last error on the calling thread ("" if none). */
 const char* msm_last_error(void);
 

@@ -21,8 +21,9 @@ _BUILD = os.path.join(_HERE, "_build")
 _ROOT = os.path.dirname(_HERE)
 _INCLUDE = os.path.join(_ROOT, "include")
 LIB_PATH = os.path.join(_BUILD, "libmsm.so")
-_SOURCES = ["msm_kernel.cu", "msm_pack.cu", "msm_api.cu", "msm_accept.cu"]
-_HEADERS = ["msm_device.cuh", "msm_internal.h"]
+_SOURCES = ["msm_kernel.cu", "msm_pack.cu", "msm_api.cu", "msm_accept.cu", "msm_pages.cu", "msm_paged_attn.cu",
+            "msm_prompt.cu", "msm_paged_api.cu"]
+_HEADERS = ["msm_device.cuh", "msm_internal.h", "msm_paged.h"]
 NVCC_ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 MSM_OK, MSM_ERR_INVALID_ARG, MSM_ERR_CUDA, MSM_ERR_OOM, MSM_ERR_DEVICE_TIMEOUT, MSM_ERR_UNSUPPORTED = range(6)
@@ -35,6 +36,8 @@ MSM_FLAG_PDL = 0x8
 MSM_FLAG_DRAFT = 0x20
 MSM_FLAG_TEST_DROP_HANDOFF = 0x10000
 MSM_TIMING_EVENTS = 192
+# msm_dtype: the 16-bit types of a paged cache and of the prompt attention
+MSM_BF16, MSM_FP16 = 0, 1
 # entries of msm_accept's result buffer (MSM_ACCEPT_RESULT_INTS)
 MSM_ACCEPT_RESULT_INTS = 34
 # entries of the device-resident step state (MSM_STEP_STATE_INTS): pos0, parent[16], tokens[16], spare
@@ -62,7 +65,9 @@ EXPORTED = ["msm_model_create", "msm_model_destroy", "msm_verify_step", "msm_ver
             "msm_get_routing", "msm_get_tree", "msm_get_timing", "msm_get_stats", "msm_get_exchange",
             "msm_draft_step", "msm_last_error", "msm_verify_step_noalloc", "msm_accept", "msm_graph_create",
             "msm_graph_launch", "msm_graph_destroy", "msm_verify_step_dev", "msm_accept_dev",
-            "msm_graph_create_dev", "msm_draft_step_dev", "msm_embed_dev", "msm_graph_create_spec"]
+            "msm_graph_create_dev", "msm_draft_step_dev", "msm_embed_dev", "msm_graph_create_spec",
+            "msm_pages_scratch_ints", "msm_pages_resize", "msm_pages_fork", "msm_pages_compact", "msm_pages_write",
+            "msm_pages_sync", "msm_paged_attention_workspace", "msm_paged_attention", "msm_prompt_attention"]
 # capacity of the static scratch array behind msm_verify_step_noalloc (MSM_NOALLOC_SCRATCH_BYTES)
 MSM_NOALLOC_SCRATCH_BYTES = 10 << 20
 
@@ -136,6 +141,24 @@ class MsmStats(ctypes.Structure):
         ("noalloc_scratch_bytes", ctypes.c_uint64)]
 
 
+class MsmPages(ctypes.Structure):
+    """msm_pages: the description of a paged KV cache (caller-owned device buffers)."""
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "device", "dtype", "n_layers", "n_pages", "page_rows", "n_kv_heads", "head_dim", "n_seqs", "max_pages")] + [
+        ("k_pages", _PP), ("v_pages", _PP)] + [
+        (n, ctypes.c_void_p) for n in ("table", "lens", "refs", "status", "scratch")]
+
+
+class MsmPrompt(ctypes.Structure):
+    """msm_prompt: the arguments of msm_prompt_attention."""
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "device", "dtype", "n_seqs", "n_q", "n_k", "n_q_heads", "n_kv_heads", "head_dim", "window")] + [
+        ("scale", ctypes.c_float)] + [(n, ctypes.c_void_p) for n in ("q", "k", "v", "out")] + [
+        (n, ctypes.c_int64) for n in (
+            "q_token_stride", "q_head_stride", "k_token_stride", "k_head_stride", "v_token_stride", "v_head_stride",
+            "out_token_stride", "out_head_stride")] + [(n, ctypes.c_void_p) for n in ("q_starts", "k_starts")]
+
+
 _LIB = None
 _LOCK = threading.Lock()
 
@@ -195,6 +218,26 @@ def lib():
             L.msm_graph_create_spec.argtypes = [vp, vp, vp, _PP, _PP, vp, vp, vp, vp, _PP, _PP, vp, vp,
                                                 ctypes.POINTER(vp)]
             L.msm_graph_create_spec.restype = st
+            pp, i64 = ctypes.POINTER(MsmPages), ctypes.c_int64
+            L.msm_pages_scratch_ints.argtypes = [ctypes.c_int, ctypes.c_int]
+            L.msm_pages_scratch_ints.restype = ctypes.c_size_t
+            L.msm_pages_resize.argtypes = [pp, vp, vp]
+            L.msm_pages_resize.restype = st
+            L.msm_pages_fork.argtypes = [pp, vp, vp]
+            L.msm_pages_fork.restype = st
+            L.msm_pages_compact.argtypes = [pp, vp]
+            L.msm_pages_compact.restype = st
+            L.msm_pages_write.argtypes = [pp, ctypes.c_int, vp, vp, i64, i64, i64, i64, vp, ctypes.c_int, vp]
+            L.msm_pages_write.restype = st
+            L.msm_pages_sync.argtypes = [pp, vp]
+            L.msm_pages_sync.restype = st
+            L.msm_paged_attention_workspace.argtypes = [pp, ctypes.c_int]
+            L.msm_paged_attention_workspace.restype = ctypes.c_size_t
+            L.msm_paged_attention.argtypes = [pp, ctypes.c_int, vp, i64, i64, ctypes.c_int, ctypes.c_float,
+                                              ctypes.c_int, vp, i64, i64, vp, ctypes.c_size_t, vp]
+            L.msm_paged_attention.restype = st
+            L.msm_prompt_attention.argtypes = [ctypes.POINTER(MsmPrompt), vp]
+            L.msm_prompt_attention.restype = st
             L.msm_last_error.argtypes = []
             L.msm_last_error.restype = ctypes.c_char_p
             _LIB = L
@@ -373,6 +416,48 @@ def msm_graph_create_spec(target, draft, draft_hidden_in, dk_ptrs, dv_ptrs, draf
                                        ctypes.c_void_p(hidden_buf), ctypes.c_void_p(state), kp, vpp,
                                        ctypes.c_void_p(logits_out), ctypes.c_void_p(accept_result), ctypes.byref(g)))
     return g
+
+
+def msm_pages_scratch_ints(n_pages, n_seqs) -> int:
+    return lib().msm_pages_scratch_ints(n_pages, n_seqs)
+
+
+def msm_pages_resize(pages: MsmPages, new_lens, stream=0) -> int:
+    return lib().msm_pages_resize(pages, new_lens, stream)
+
+
+def msm_pages_fork(pages: MsmPages, parent, stream=0) -> int:
+    return lib().msm_pages_fork(pages, parent, stream)
+
+
+def msm_pages_compact(pages: MsmPages, stream=0) -> int:
+    return lib().msm_pages_compact(pages, stream)
+
+
+def msm_pages_write(pages: MsmPages, layer, k, v, k_strides, v_strides, starts, n_tokens, stream=0) -> int:
+    """k_strides, v_strides: (token, head) strides in elements."""
+    return lib().msm_pages_write(pages, layer, k, v, k_strides[0], k_strides[1], v_strides[0], v_strides[1], starts,
+                                 n_tokens, stream)
+
+
+def msm_pages_sync(pages: MsmPages, stream=0) -> int:
+    return lib().msm_pages_sync(pages, stream)
+
+
+def msm_paged_attention_workspace(pages: MsmPages, n_q_heads) -> int:
+    """Bytes of the workspace; 0 if an argument is wrong (see msm_last_error)."""
+    return lib().msm_paged_attention_workspace(pages, n_q_heads)
+
+
+def msm_paged_attention(pages: MsmPages, layer, q, q_strides, n_q_heads, scale, window, out, out_strides, workspace,
+                        workspace_bytes, stream=0) -> int:
+    """q_strides, out_strides: (sequence, head) strides in elements."""
+    return lib().msm_paged_attention(pages, layer, q, q_strides[0], q_strides[1], n_q_heads, scale, window, out,
+                                     out_strides[0], out_strides[1], workspace, workspace_bytes, stream)
+
+
+def msm_prompt_attention(prompt: MsmPrompt, stream=0) -> int:
+    return lib().msm_prompt_attention(prompt, stream)
 
 
 # ---------------------------------------------------------------- torch-facing wrapper
@@ -596,3 +681,6 @@ class StepGraph:
             self.close()
         except Exception:
             pass
+
+
+from .paged import PagedCache, prompt_attention  # noqa: E402  (uses the definitions above)

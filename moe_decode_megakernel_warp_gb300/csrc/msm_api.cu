@@ -19,6 +19,7 @@
 
 #include "msm.h"
 #include "msm_internal.h"
+#include "msm_paged.h"
 
 namespace msm {
 cudaError_t launch_pack_dense(const void* W, void* out, int N, int K, int kind, int hd, int hq, int hkv,
@@ -57,6 +58,12 @@ struct LayerPack {
   uint16_t *g_attn = nullptr, *g_moe = nullptr;
 };
 }  // namespace
+
+// the error message for the other translation units (msm_paged.h)
+namespace msm {
+msm_status report(msm_status st, const char* msg) { return fail(st, msg); }
+msm_status report_cuda(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+}  // namespace msm
 
 struct msm_model {
   int device = 0;

@@ -1,0 +1,513 @@
+// msm_pages.cu — the page operations of a paged KV cache: reserving and freeing pages
+// (with a copy of a shared last page), sharing them between sequences, moving the pages
+// in use to the front of the pool, and storing new K/V rows.
+//
+// The bookkeeping of one call runs in one thread-block cluster: its phases (check,
+// count, assign) need the whole cache's totals between them, which the blocks exchange
+// through distributed shared memory and cluster barriers inside one launch.  Page
+// indices are given out by rank (the k-th missing page is the k-th lowest free one,
+// both counted by prefix sums), so the result does not depend on the order of threads.
+// The rows that a call moves are copied by a second launch over the whole GPU, chained
+// with programmatic dependent launch; it reads the list that the first one left.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "msm_device.cuh"
+#include "msm_paged.h"
+
+namespace cg = cooperative_groups;
+
+namespace msm {
+namespace {
+
+constexpr int kMetaThreads = 1024;
+constexpr int kMetaWarps = kMetaThreads / 32;
+constexpr int kMetaBlocks = 8;      // the portable cluster size
+constexpr int kPagesPerThread = 8;  // pages one thread looks at per step of a scan
+
+__device__ __forceinline__ void latch(int32_t* status, int code, int call) {
+  atomicCAS(status, 0, code | (call << 8));
+}
+
+struct BlockShare {        // what a block tells the others
+  int need, count, holes;  // missing pages, free (or live) pages, holes below the live count
+  int bad;
+};
+
+struct Share {
+  BlockShare mine;
+  BlockShare all[kMetaBlocks];
+  int warp_sum[kMetaWarps];
+};
+
+// exclusive prefix of x over the block's threads; total = the block's sum
+__device__ int block_scan(int x, Share& sh, int& total) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  int v = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  if (lane == 31) sh.warp_sum[wid] = v;
+  __syncthreads();
+  int w = lane < kMetaWarps ? sh.warp_sum[lane] : 0, t = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, t, o);
+    if (lane >= o) t += y;
+  }
+  total = __shfl_sync(0xffffffffu, t, 31);
+  const int before = __shfl_sync(0xffffffffu, t - w, wid);
+  __syncthreads();  // warp_sum may be written again
+  return before + v - x;
+}
+
+// every block's share, visible to all of them after this barrier
+__device__ void exchange(Share& sh, cg::cluster_group& cl) {
+  cl.sync();
+  if (threadIdx.x < kMetaBlocks) sh.all[threadIdx.x] = *cl.map_shared_rank(&sh.mine, threadIdx.x);
+  __syncthreads();
+}
+
+__device__ __forceinline__ void block_range(int n, int rank, int& lo, int& hi) {
+  const int per = (n + kMetaBlocks - 1) / kMetaBlocks;
+  lo = min(n, rank * per);
+  hi = min(n, lo + per);
+}
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b != 0); }
+
+// pages of [lo, hi) that are free (live = false) or in use
+__device__ int count_pages(const int32_t* refs, int lo, int hi, bool live, Share& sh) {
+  int n = 0;
+  for (int p = lo + (int)threadIdx.x; p < hi; p += kMetaThreads * kPagesPerThread) {
+    int r[kPagesPerThread];
+#pragma unroll
+    for (int q = 0; q < kPagesPerThread; ++q) {
+      const int i = p + q * kMetaThreads;
+      r[q] = i < hi ? __ldcg(refs + i) : (live ? 0 : 1);
+    }
+#pragma unroll
+    for (int q = 0; q < kPagesPerThread; ++q) n += (r[q] > 0) == live;
+  }
+  int total;
+  block_scan(n, sh, total);
+  return total;
+}
+
+__global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThreads)
+    resize_kernel(const PagesMeta p) {
+  __shared__ Share sh;
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = (int)cl.block_rank(), lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const PagesScratch sc(p.scratch, p.n_pages, p.n_seqs);
+  const int64_t cap = (int64_t)p.max_pages * p.page_rows;
+  int s0, s1, p0, p1;
+  block_range(p.n_seqs, rank, s0, s1);
+  block_range(p.n_pages, rank, p0, p1);
+  if (threadIdx.x == 0) sh.mine.bad = 0;
+  if (rank == 0 && threadIdx.x == 0) sc.head[0] = 0;
+  __syncthreads();
+
+  // 1. each sequence: are its lengths and the pages it gives up in range, how many pages
+  //    does it lack, does it have to leave a shared last page (offset = 2 pages + leave)
+  for (int s = s0 + wid; s < s1; s += kMetaWarps) {
+    const int old = p.lens[s], asked = p.arg[s], now = asked == -1 ? old : asked;
+    bool bad = old < 0 || old > cap || now < 0 || now > cap;
+    int need = 0, leave = 0;
+    if (!bad) {
+      const int32_t* row = p.table + (size_t)s * p.max_pages;
+      const int n_old = ceil_div(old, p.page_rows), n_new = ceil_div(now, p.page_rows);
+      for (int j = n_new + lane; j < n_old; j += 32) {
+        const int pg = row[j];
+        bad |= pg < 0 || pg >= p.n_pages || p.refs[pg] <= 0;
+      }
+      if (now > old && old % p.page_rows) {
+        const int pg = row[old / p.page_rows];
+        bad |= pg < 0 || pg >= p.n_pages;
+        if (!bad) leave = p.refs[pg] > 1;
+      }
+      need = max(0, n_new - n_old) + leave;
+    }
+    if (__any_sync(0xffffffffu, bad)) {
+      sh.mine.bad = 1;
+      need = leave = 0;
+    }
+    if (lane == 0) sc.offset[s] = 2 * need + leave;
+  }
+  __syncthreads();
+  // 2. prefix of the needs over the block's sequences, free pages of its share of the pool
+  int base = 0;
+  for (int c = s0; c < s1; c += kMetaThreads) {
+    const int s = c + (int)threadIdx.x;
+    const int e = s < s1 ? sc.offset[s] : 0;
+    int total;
+    const int before = block_scan(e >> 1, sh, total);
+    if (s < s1) sc.offset[s] = 2 * (base + before) + (e & 1);
+    base += total;
+  }
+  const int n_free = count_pages(p.refs, p0, p1, false, sh);
+  if (threadIdx.x == 0) {
+    sh.mine.need = base;
+    sh.mine.count = n_free;
+  }
+  exchange(sh, cl);
+  int need_before = 0, free_before = 0, bad = 0;
+  int64_t need_all = 0, free_all = 0;
+#pragma unroll
+  for (int b = 0; b < kMetaBlocks; ++b) {
+    if (b < rank) {
+      need_before += sh.all[b].need;
+      free_before += sh.all[b].count;
+    }
+    need_all += sh.all[b].need;
+    free_all += sh.all[b].count;
+    bad |= sh.all[b].bad;
+  }
+  if (bad || need_all > free_all) {
+    if (rank == 0 && threadIdx.x == 0) latch(p.status, bad ? MSM_ERR_INVALID_ARG : MSM_ERR_OOM, kCallResize);
+    cl.sync();  // a block's shared memory stays until the others have read it
+    return;
+  }
+  // 3. list[r] = the r-th lowest free page, for the r that are needed
+  int at = free_before;
+  for (int c = p0; c < p1 && at < need_all; c += kMetaThreads * kPagesPerThread) {
+    const int q0 = c + (int)threadIdx.x * kPagesPerThread;
+    uint32_t mask = 0;
+#pragma unroll
+    for (int q = 0; q < kPagesPerThread; ++q)
+      if (q0 + q < p1 && __ldcg(p.refs + q0 + q) <= 0) mask |= 1u << q;
+    int total;
+    int r = at + block_scan(__popc(mask), sh, total);
+#pragma unroll
+    for (int q = 0; q < kPagesPerThread; ++q)
+      if (mask >> q & 1) {
+        if (r < need_all) sc.list[r] = q0 + q;
+        ++r;
+      }
+    at += total;
+  }
+  cl.sync();
+  // 4. the tables
+  for (int s = s0 + wid; s < s1; s += kMetaWarps) {
+    const int old = p.lens[s], asked = p.arg[s], now = asked == -1 ? old : asked;
+    if (now == old) continue;
+    int32_t* row = p.table + (size_t)s * p.max_pages;
+    const int n_old = ceil_div(old, p.page_rows), n_new = ceil_div(now, p.page_rows);
+    const int e = sc.offset[s];
+    int off = need_before + (e >> 1);
+    if (e & 1) {
+      if (lane == 0) {
+        const int j = old / p.page_rows, from = row[j], to = __ldcg(sc.list + off);
+        const int i = atomicAdd(sc.head, 1);
+        sc.copies[3 * i] = from;
+        sc.copies[3 * i + 1] = to;
+        sc.copies[3 * i + 2] = old % p.page_rows;
+        row[j] = to;
+        p.refs[to] = 1;
+        atomicSub(p.refs + from, 1);
+      }
+      ++off;
+    }
+    for (int j = n_old + lane; j < n_new; j += 32) {
+      const int pg = __ldcg(sc.list + off + j - n_old);
+      row[j] = pg;
+      p.refs[pg] = 1;
+    }
+    for (int j = n_new + lane; j < n_old; j += 32) {
+      atomicSub(p.refs + row[j], 1);
+      row[j] = -1;
+    }
+    if (lane == 0) p.lens[s] = now;
+  }
+}
+
+__global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThreads)
+    fork_kernel(const PagesMeta p) {
+  __shared__ Share sh;
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = (int)cl.block_rank(), lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int64_t cap = (int64_t)p.max_pages * p.page_rows;
+  const int w0 = rank * kMetaWarps + wid, n_warps = kMetaBlocks * kMetaWarps;
+  if (threadIdx.x == 0) sh.mine.bad = 0;
+  __syncthreads();
+  for (int s = w0; s < p.n_seqs; s += n_warps) {
+    const int par = p.arg[s];
+    if (par == -1) continue;
+    bool bad = par < 0 || par >= p.n_seqs || par == s || p.lens[s] != 0;
+    if (!bad) {
+      const int len = p.lens[par];
+      bad = p.arg[par] != -1 || len < 0 || len > cap;
+      if (!bad)
+        for (int j = lane; j < ceil_div(len, p.page_rows); j += 32) {
+          const int pg = p.table[(size_t)par * p.max_pages + j];
+          bad |= pg < 0 || pg >= p.n_pages || p.refs[pg] <= 0;
+        }
+    }
+    if (__any_sync(0xffffffffu, bad)) sh.mine.bad = 1;
+  }
+  exchange(sh, cl);
+  int bad = 0;
+#pragma unroll
+  for (int b = 0; b < kMetaBlocks; ++b) bad |= sh.all[b].bad;
+  cl.sync();
+  if (bad) {
+    if (rank == 0 && threadIdx.x == 0) latch(p.status, MSM_ERR_INVALID_ARG, kCallFork);
+    return;
+  }
+  for (int s = w0; s < p.n_seqs; s += n_warps) {
+    const int par = p.arg[s];
+    if (par == -1) continue;
+    const int len = p.lens[par];
+    for (int j = lane; j < ceil_div(len, p.page_rows); j += 32) {
+      const int pg = p.table[(size_t)par * p.max_pages + j];
+      p.table[(size_t)s * p.max_pages + j] = pg;
+      atomicAdd(p.refs + pg, 1);
+    }
+    if (lane == 0) p.lens[s] = len;
+  }
+}
+
+// With L pages in use, the moves pair the free indices below L with the pages in use at
+// L and above, both ascending.  A page in use with `before` of them in front of it is the
+// (L - 1 - before)-th from the end, so the sources are listed from their end, which needs
+// no count of the pages in use below L; the destinations are listed from the front.
+__global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThreads)
+    compact_kernel(const PagesMeta p) {
+  __shared__ Share sh;
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = (int)cl.block_rank();
+  const PagesScratch sc(p.scratch, p.n_pages, p.n_seqs);
+  int32_t* const dst = sc.list + p.n_pages / 2;
+  int p0, p1;
+  block_range(p.n_pages, rank, p0, p1);
+  const int n_live = count_pages(p.refs, p0, p1, true, sh);
+  if (threadIdx.x == 0) {
+    sh.mine.count = n_live;
+    sh.mine.holes = 0;
+  }
+  exchange(sh, cl);
+  int at = 0, live = 0;
+#pragma unroll
+  for (int b = 0; b < kMetaBlocks; ++b) {
+    if (b < rank) at += sh.all[b].count;
+    live += sh.all[b].count;
+  }
+  int holes = 0;
+  for (int c = p0; c < p1; c += kMetaThreads * kPagesPerThread) {
+    const int q0 = c + (int)threadIdx.x * kPagesPerThread;
+    uint32_t mask = 0;
+#pragma unroll
+    for (int q = 0; q < kPagesPerThread; ++q)
+      if (q0 + q < p1 && __ldcg(p.refs + q0 + q) > 0) mask |= 1u << q;
+    int total;
+    int before = at + block_scan(__popc(mask), sh, total);
+#pragma unroll
+    for (int q = 0; q < kPagesPerThread; ++q) {
+      const int pg = q0 + q;
+      if (pg >= p1) break;
+      const bool used = mask >> q & 1;
+      if (pg >= live) {
+        sc.to[pg] = pg;
+        if (used) sc.list[live - 1 - before] = pg;
+      } else if (!used) {
+        dst[pg - before] = pg;
+        ++holes;
+      }
+      before += used;
+    }
+    at += total;
+  }
+  int block_holes;
+  block_scan(holes, sh, block_holes);
+  if (threadIdx.x == 0) sh.mine.holes = block_holes;
+  exchange(sh, cl);
+  int moves = 0;
+#pragma unroll
+  for (int b = 0; b < kMetaBlocks; ++b) moves += sh.all[b].holes;
+  for (int m = rank * kMetaThreads + (int)threadIdx.x; m < moves; m += kMetaBlocks * kMetaThreads) {
+    const int from = __ldcg(sc.list + moves - 1 - m), to = __ldcg(dst + m);
+    sc.to[from] = to;
+    p.refs[to] = p.refs[from];
+    p.refs[from] = 0;
+  }
+  if (rank == 0 && threadIdx.x == 0) {
+    sc.head[0] = moves;
+    sc.head[1] = live;
+  }
+  cl.sync();  // a block's shared memory stays until the others have read it
+}
+
+// ---------------------------------------------------------------- row copies
+// Bound by memory: each byte is read once and written once.  One warp moves up to 8 KB
+// at a time, 16 loads of 16 bytes in flight per lane.
+constexpr int kCopyThreads = 256;
+constexpr int kCopyVecs = 16;  // 16-byte vectors per lane
+
+template <bool kCompact>
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const PagesCopy p) {
+  pdl_wait();
+  const PagesScratch sc(p.m.scratch, p.m.n_pages, p.m.n_seqs);
+  const int32_t* const dst = sc.list + p.m.n_pages / 2;
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = ((int64_t)blockIdx.x * kCopyThreads + threadIdx.x) >> 5;
+  const int64_t warps = ((int64_t)gridDim.x * kCopyThreads) >> 5;
+  const int entries = sc.head[0];
+  // a page is n_kv_heads runs of page_rows rows; all of it is one run when it moves whole
+  const int64_t head_vecs = (int64_t)p.m.page_rows * p.row_vecs, page_vecs = head_vecs * p.n_kv_heads;
+  const int runs = kCompact ? 1 : p.n_kv_heads;
+  const int64_t run_vecs = kCompact ? page_vecs : head_vecs;
+  const int64_t pieces = (run_vecs + 32 * kCopyVecs - 1) / (32 * kCopyVecs);
+  const int64_t per_entry = pieces * runs * 2 * p.n_layers;
+  for (int64_t u = warp; u < entries * per_entry; u += warps) {
+    const int64_t e = u / per_entry;
+    int64_t r = u - e * per_entry;
+    const int layer = (int)(r / (pieces * runs * 2));
+    r -= (int64_t)layer * (pieces * runs * 2);
+    const int kv = (int)(r / (pieces * runs));
+    r -= (int64_t)kv * (pieces * runs);
+    const int run = (int)(r / pieces);
+    const int64_t first = (r - (int64_t)run * pieces) * (32 * kCopyVecs);
+    int from, to;
+    int64_t n;
+    if (kCompact) {
+      from = sc.list[entries - 1 - e];
+      to = dst[e];
+      n = run_vecs;
+    } else {
+      from = sc.copies[3 * e];
+      to = sc.copies[3 * e + 1];
+      n = (int64_t)sc.copies[3 * e + 2] * p.row_vecs;
+    }
+    if (first >= n) continue;
+    uint4* const pool = kv ? p.v[layer] : p.k[layer];
+    const uint4* const src = pool + from * page_vecs + run * run_vecs;
+    uint4* const out = pool + to * page_vecs + run * run_vecs;
+    uint4 x[kCopyVecs];
+#pragma unroll
+    for (int q = 0; q < kCopyVecs; ++q) {
+      const int64_t i = first + q * 32 + lane;
+      if (i < n) x[q] = __ldcs(src + i);
+    }
+#pragma unroll
+    for (int q = 0; q < kCopyVecs; ++q) {
+      const int64_t i = first + q * 32 + lane;
+      if (i < n) __stcs(out + i, x[q]);
+    }
+  }
+  if (kCompact && p.renumber) {
+    const int live = sc.head[1];
+    for (int64_t s = warp; s < p.m.n_seqs; s += warps) {
+      const int n = ceil_div(min(max(p.m.lens[s], 0), p.m.max_pages * p.m.page_rows), p.m.page_rows);
+      int32_t* const row = p.m.table + s * p.m.max_pages;
+      for (int j = lane; j < n; j += 32) {
+        const int pg = row[j];
+        if (pg >= live && pg < p.m.n_pages) row[j] = sc.to[pg];
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- new rows
+// Bound by memory (and by the launch for a step's few tokens): a block looks up the row
+// of each of its tokens once, then all of its threads move 16-byte vectors.
+constexpr int kWriteThreads = 256;
+constexpr int kWriteTokens = 8;
+
+__global__ void __launch_bounds__(kWriteThreads) write_kernel(const PagesWrite p) {
+  __shared__ int64_t s_row[kWriteTokens];  // pool vector of head 0 of the token's row, or -1
+  const int t0 = blockIdx.x * kWriteTokens;
+  if (threadIdx.x < kWriteTokens) {
+    const int t = t0 + (int)threadIdx.x;
+    int64_t at = -1;
+    if (t < p.n_tokens && t < p.starts[p.m.n_seqs]) {
+      // the last sequence that starts at or before the token
+      int lo = 0, hi = p.m.n_seqs;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.starts[mid] <= t) lo = mid;
+        else hi = mid;
+      }
+      const int64_t pos = (int64_t)p.m.lens[lo] - p.starts[lo + 1] + t;
+      bool ok = t >= p.starts[lo] && t < p.starts[lo + 1] && pos >= 0 &&
+                pos < (int64_t)p.m.max_pages * p.m.page_rows;
+      if (ok) {
+        const int pg = p.m.table[(size_t)lo * p.m.max_pages + pos / p.m.page_rows];
+        ok = pg >= 0 && pg < p.m.n_pages && p.m.refs[pg] == 1;
+        if (ok) at = ((int64_t)pg * p.n_kv_heads * p.m.page_rows + pos % p.m.page_rows) * p.row_vecs;
+      }
+      if (!ok) latch(p.m.status, MSM_ERR_INVALID_ARG, kCallWrite);
+    }
+    s_row[threadIdx.x] = at;
+  }
+  __syncthreads();
+  const int half = p.n_kv_heads * p.row_vecs, per = 2 * half, n = kWriteTokens * per;
+  const int64_t head = (int64_t)p.m.page_rows * p.row_vecs;
+  constexpr int kU = 8;
+  for (int i0 = threadIdx.x; i0 < n; i0 += kU * kWriteThreads) {
+    uint4 x[kU];
+    uint4* to[kU];
+#pragma unroll
+    for (int q = 0; q < kU; ++q) {
+      const int i = i0 + q * kWriteThreads, tok = i / per;
+      to[q] = nullptr;
+      if (i < n && s_row[tok] >= 0) {
+        int r = i - tok * per;
+        const bool v = r >= half;
+        r -= v ? half : 0;
+        const int h = r / p.row_vecs, c = r - h * p.row_vecs;
+        const int64_t t = t0 + tok;
+        x[q] = v ? __ldcs(p.v + t * p.v_token + h * p.v_head + c) : __ldcs(p.k + t * p.k_token + h * p.k_head + c);
+        to[q] = (v ? p.pool_v : p.pool_k) + s_row[tok] + h * head + c;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kU; ++q)
+      if (to[q]) *to[q] = x[q];
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_pages_resize(const PagesMeta& p, cudaStream_t s) {
+  resize_kernel<<<kMetaBlocks, kMetaThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_fork(const PagesMeta& p, cudaStream_t s) {
+  fork_kernel<<<kMetaBlocks, kMetaThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_compact(const PagesMeta& p, cudaStream_t s) {
+  compact_kernel<<<kMetaBlocks, kMetaThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_copy(const PagesCopy& p, bool compact, int sms, cudaStream_t s) {
+  // at most as many warps as there can be 8 KB pieces, at most four blocks per SM
+  const int64_t vecs = (int64_t)p.m.page_rows * p.row_vecs * (compact ? p.n_kv_heads : 1);
+  const int64_t pieces = (vecs + 32 * kCopyVecs - 1) / (32 * kCopyVecs) * (compact ? 1 : p.n_kv_heads);
+  const int64_t entries = compact ? p.m.n_pages / 2 : p.m.n_seqs;
+  const int64_t warps = entries * pieces * 2 * p.n_layers;
+  const int64_t blocks = (warps + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(blocks, 4 * (int64_t)sms)));
+  lc.blockDim = dim3(kCopyThreads);
+  lc.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return compact ? cudaLaunchKernelEx(&lc, copy_kernel<true>, p) : cudaLaunchKernelEx(&lc, copy_kernel<false>, p);
+}
+
+cudaError_t launch_pages_write(const PagesWrite& p, cudaStream_t s) {
+  write_kernel<<<(p.n_tokens + kWriteTokens - 1) / kWriteTokens, kWriteThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace msm

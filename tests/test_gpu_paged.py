@@ -1,0 +1,676 @@
+"""The paged KV cache, the attention over it and the prompt attention on the GPU, against the
+64-bit reference in paged_reference.py."""
+import numpy as np
+import pytest
+
+from paged_reference import Pages, attend
+
+pytestmark = pytest.mark.gpu
+
+
+def _mods():
+    import torch
+    import moe_decode_megakernel_warp_gb300 as msm
+    return torch, msm
+
+
+def _dtype(kind):
+    torch, _ = _mods()
+    return {"bf16": torch.bfloat16, "fp16": torch.float16}[kind]
+
+
+def randn(kind, *shape, seed=0, std=1.0):
+    torch, _ = _mods()
+    gen = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=gen) * std).to(_dtype(kind))
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def ints(values):
+    torch, _ = _mods()
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+def starts_of(lens):
+    return [int(x) for x in np.concatenate([[0], np.cumsum(lens)])]
+
+
+def bits(t):
+    torch, _ = _mods()
+    return t.contiguous().view(torch.int16).cpu().numpy()
+
+
+def assert_close(got, want, tol, what=""):
+    got = f64(got)
+    assert not np.isnan(got).any(), what
+    bad = np.abs(got - want) > tol
+    assert not bad.any(), "%s: %d of %d off, worst %.3g of its bound at %s" % (
+        what, bad.sum(), bad.size, (np.abs(got - want) / tol).max(),
+        np.unravel_index((np.abs(got - want) / tol).argmax(), got.shape))
+
+
+# ------------------------------------------------------------------ page operations
+class Both:
+    """A cache on the GPU and its reference, called alike and compared after every call."""
+
+    def __init__(self, rng, layers, n_pages, rows, heads, hd, n_seqs, max_pages, kind="bf16"):
+        torch, msm = _mods()
+        self.kind = kind
+        shape = (n_pages, heads, rows, hd)
+        k = [randn(kind, *shape, seed=int(rng.integers(1 << 30))) for _ in range(layers)]
+        v = [randn(kind, *shape, seed=int(rng.integers(1 << 30))) for _ in range(layers)]
+        self.gpu = msm.PagedCache([t.cuda() for t in k], [t.cuda() for t in v], ints([[-1] * max_pages] * n_seqs),
+                                  ints([0] * n_seqs), ints([0] * n_pages))
+        self.ref = Pages(n_pages, rows, n_seqs, max_pages, [bits(t).copy() for t in k + v])
+
+    def same(self):
+        g, r = self.gpu, self.ref
+        assert np.array_equal(g.table.cpu().numpy(), r.table)
+        assert np.array_equal(g.lens.cpu().numpy(), r.lens)
+        assert np.array_equal(g.refs.cpu().numpy(), r.refs)
+        for a, b in zip(g.k_pages + g.v_pages, r.pools):
+            assert np.array_equal(bits(a), b)
+
+    def call(self, name, arg=None):
+        torch, msm = _mods()
+        args = () if arg is None else (ints(arg),)
+        getattr(self.gpu, name)(*args)
+        err = getattr(self.ref, name)(*(() if arg is None else (arg,)))
+        if err is None:
+            self.gpu.sync()
+        else:
+            with pytest.raises(msm.MsmError, match=name) as e:
+                self.gpu.sync()
+            assert msm.STATUS_NAMES[e.value.code] == err
+            self.gpu.sync()  # cleared
+        self.same()
+        return err
+
+    def write(self, counts, seed):
+        torch, _ = _mods()
+        st = starts_of(counts)
+        heads, hd = self.gpu.k_pages[0].shape[1], self.gpu.k_pages[0].shape[3]
+        for layer in range(len(self.gpu.k_pages)):
+            # both out of one packed tensor, and a row behind the last sequence
+            kv = randn(self.kind, st[-1] + 1, 2 * heads, hd, seed=seed + layer).cuda()
+            self.gpu.write(layer, kv[:, :heads], kv[:, heads:], ints(st))
+            rows = bits(kv)
+            self.ref.write(self.ref.pools[layer], rows[:, :heads], st)
+            self.ref.write(self.ref.pools[len(self.gpu.k_pages) + layer], rows[:, heads:], st)
+        self.gpu.sync()
+        self.same()
+
+
+@pytest.mark.parametrize("rows,heads,hd,kind", [(16, 2, 64, "bf16"), (1, 1, 128, "fp16"), (7, 3, 64, "fp16"),
+                                                (64, 8, 128, "bf16"), (33, 1, 64, "bf16")])
+def test_random_calls_equal_the_reference(rows, heads, hd, kind):
+    rng = np.random.default_rng(rows)
+    n_seqs, max_pages = 9, 6
+    c = Both(rng, 2, 40, rows, heads, hd, n_seqs, max_pages, kind)
+    for step in range(14):
+        new = [-1 if rng.random() < 0.3 else int(rng.integers(0, max_pages * rows + 1)) for _ in range(n_seqs)]
+        old = c.ref.lens.copy()
+        if c.call("resize", new) is None:
+            c.write(np.maximum(c.ref.lens - old, 0), 100 * step)
+        if step % 2:
+            parent = [-1] * n_seqs
+            live = [s for s in range(n_seqs) if c.ref.lens[s] > 0]
+            for s in range(n_seqs):
+                if c.ref.lens[s] == 0 and live:
+                    parent[s] = int(rng.choice(live))
+            c.call("fork", parent)
+        if step % 3 == 2:
+            c.call("compact")
+    c.ref.check()
+
+
+def test_a_shared_last_page_is_copied_once_for_each_that_grows():
+    rng = np.random.default_rng(3)
+    c = Both(rng, 3, 12, 16, 2, 64, 4, 3)
+    c.call("resize", [20, 0, 0, 0])
+    c.write([20, 0, 0, 0], 1)
+    c.call("fork", [-1, 0, 0, -1])
+    assert list(c.ref.refs[:2]) == [3, 3]
+    c.call("resize", [-1, 21, -1, -1])    # one child leaves the shared page
+    c.write([0, 1, 0, 0], 2)
+    c.call("resize", [21, 21, 22, -1])    # the parent and the other child both do
+    c.write([1, 0, 2, 0], 3)
+    c.call("resize", [5, 0, 17, -1])      # back into the shared first page
+    c.call("resize", [6, -1, -1, -1])     # which the growth must leave
+    c.write([1, 0, 0, 0], 4)
+    c.ref.check()
+
+
+def test_a_pool_of_many_pages_and_sequences():
+    rng = np.random.default_rng(4)
+    n_seqs, rows = 1500, 2
+    c = Both(rng, 1, 60000, rows, 1, 64, n_seqs, 40)
+    for i in range(3):
+        c.call("resize", [int(x) for x in rng.integers(0, 40 * rows + 1, n_seqs)])
+    c.call("resize", [0 if s % 3 else -1 for s in range(n_seqs)])
+    c.call("fork", [s - s % 3 if s % 3 else -1 for s in range(n_seqs)])
+    c.call("compact")
+    c.call("resize", [int(n) + 1 if n < 80 else -1 for n in c.ref.lens])
+    c.ref.check()
+
+
+def test_more_layers_than_one_copy_launch_carries():
+    rng = np.random.default_rng(5)
+    c = Both(rng, 70, 9, 4, 1, 64, 3, 3)
+    c.call("resize", [6, 5, 0])
+    c.call("fork", [-1, -1, 0])
+    c.call("resize", [7, 0, 8])
+    c.call("compact")
+    c.ref.check()
+
+
+def test_refusals_on_the_device_change_nothing():
+    rng = np.random.default_rng(6)
+    c = Both(rng, 1, 6, 16, 1, 64, 4, 4)
+    c.call("resize", [30, 10, 0, 0])
+    assert c.call("resize", [-1, -1, 64, 1]) == "MSM_ERR_OOM"
+    assert c.call("resize", [0, 0, 65, 0]) == "MSM_ERR_INVALID_ARG"
+    assert c.call("resize", [-2, -1, -1, -1]) == "MSM_ERR_INVALID_ARG"
+    for parent in ([-1, -1, 2, -1], [-1, -1, 4, -1], [-1, -1, -2, -1], [-1, 0, -1, -1], [-1, -1, 3, 0]):
+        assert c.call("fork", parent) == "MSM_ERR_INVALID_ARG"
+    # the OOM is about the pages free before the call: a second call has those that the first gave up
+    assert c.call("resize", [0, -1, 64, -1]) == "MSM_ERR_OOM"
+    assert c.call("resize", [0, -1, -1, -1]) is None
+    assert c.call("resize", [-1, -1, 64, -1]) is None
+
+
+def test_write_leaves_out_tokens_without_a_row_of_their_own():
+    torch, msm = _mods()
+    rng = np.random.default_rng(7)
+    c = Both(rng, 1, 6, 16, 2, 64, 3, 2)
+    c.call("resize", [20, 3, 0])
+    c.call("fork", [-1, -1, 0])
+    k = randn("bf16", 9, 2, 64).cuda()
+    for st in ([0, 2, 2, 2],      # a shared page
+               [0, 0, 4, 4],      # one row more than the sequence has: its first token has none
+               [0, 0, 0, 1]):     # a shared page through the child
+        before = [bits(t) for t in c.gpu.k_pages + c.gpu.v_pages]
+        c.gpu.write(0, k, k, ints(st))
+        with pytest.raises(msm.MsmError, match="msm_pages_write"):
+            c.gpu.sync()
+        if st == [0, 0, 4, 4]:
+            c.ref.write(c.ref.pools[0], bits(k)[1:], [0, 0, 3, 3])
+            c.ref.write(c.ref.pools[1], bits(k)[1:], [0, 0, 3, 3])
+        else:
+            assert all(np.array_equal(a, bits(b)) for a, b in zip(before, c.gpu.k_pages + c.gpu.v_pages))
+        c.same()
+
+
+def test_tables_that_name_pages_outside_the_pool():
+    torch, msm = _mods()
+    for bad in (-1, -5, 6, 1 << 30):
+        c = Both(np.random.default_rng(8), 1, 6, 16, 1, 64, 2, 3)
+        c.call("resize", [40, 10])
+        c.gpu.table[0, 2] = bad
+        for call in (lambda: c.gpu.resize(ints([1, -1])), lambda: c.gpu.resize(ints([41, -1])),
+                     lambda: c.gpu.resize(ints([0, 0]))):
+            call()
+            with pytest.raises(msm.MsmError, match="msm_pages_resize"):
+                c.gpu.sync()
+        k = randn("bf16", 1, 1, 64).cuda()
+        c.gpu.write(0, k, k, ints([0, 1, 1]))
+        with pytest.raises(msm.MsmError, match="msm_pages_write"):
+            c.gpu.sync()
+        out = c.gpu.attention(0, randn("bf16", 2, 2, 64).cuda())
+        with pytest.raises(msm.MsmError, match="msm_paged_attention"):
+            c.gpu.sync()
+        assert not torch.isnan(out).any()  # the rows on the other pages are there
+        c.gpu.compact()
+        c.gpu.sync()
+        assert c.gpu.table[0, 2].item() == bad
+        c.gpu.table[0, 2] = int(c.ref.table[0, 2])
+        c.same()
+
+
+# ------------------------------------------------------------------ paged attention
+def filled(rng, kind, lens, rows, hkv, hd, extra=5, max_pages=None):
+    """A cache of the given lengths on random pages; every row that no sequence holds is NaN."""
+    torch, msm = _mods()
+    per = [-(-n // rows) for n in lens]
+    n_pages = sum(per) + extra
+    order = rng.permutation(n_pages)
+    width = max_pages or max(1, max(per))
+    table, refs, at = np.full((len(lens), width), -7, np.int64), np.zeros(n_pages, np.int64), 0
+    k = torch.full((n_pages, hkv, rows, hd), float("nan"), dtype=_dtype(kind))
+    v = torch.full_like(k, float("nan"))
+    rows_k, rows_v = [], []
+    for s, n in enumerate(lens):
+        kk = randn(kind, n, hkv, hd, seed=int(rng.integers(1 << 30)))
+        vv = randn(kind, n, hkv, hd, seed=int(rng.integers(1 << 30)))
+        for j in range(per[s]):
+            p = int(order[at])
+            at += 1
+            table[s, j], refs[p] = p, 1
+            part = slice(j * rows, min(n, (j + 1) * rows))
+            cnt = part.stop - part.start
+            k[p, :, :cnt] = kk[part].transpose(0, 1)
+            v[p, :, :cnt] = vv[part].transpose(0, 1)
+        rows_k.append(kk)
+        rows_v.append(vv)
+    c = msm.PagedCache([k.cuda()], [v.cuda()], ints(table.tolist()), ints(lens), ints(refs.tolist()))
+    return c, rows_k, rows_v
+
+
+def decode_want(q, rows_k, rows_v, window, scale, kind):
+    outs, tols = [], []
+    for s in range(len(rows_k)):
+        n = rows_k[s].shape[0]
+        o, t = attend(f64(q[s:s + 1]), f64(rows_k[s]), f64(rows_v[s]), n - 1, window, scale, kind)
+        outs.append(o)
+        tols.append(t)
+    return np.concatenate(outs), np.concatenate(tols)
+
+
+LENS = [0, 1, 2, 15, 16, 17, 31, 33, 127, 128, 129, 255, 300, 1000]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("hkv,group", [(1, 1), (2, 8), (8, 4), (3, 2)])
+@pytest.mark.parametrize("rows", [16, 64, 1, 13])
+def test_paged_attention_equals_the_formula(kind, hd, hkv, group, rows):
+    rng = np.random.default_rng(hd + rows + group)
+    c, rk, rv = filled(rng, kind, LENS, rows, hkv, hd)
+    q = randn(kind, len(LENS), hkv * group, hd, seed=9).cuda()
+    for window in (0, 1, 20, 128):
+        got = c.attention(0, q, window=window)
+        c.sync()
+        want, tol = decode_want(q, rk, rv, window, hd ** -0.5, kind)
+        assert_close(got, want, tol, "window %d" % window)
+
+
+@pytest.mark.parametrize("kind,lens,rows,window", [
+    ("bf16", [40000], 64, 0), ("fp16", [33001, 7], 48, 0), ("bf16", [20000] * 3, 16, 5000),
+    ("bf16", [1] * 700, 16, 0), ("fp16", [100 + 3 * i for i in range(300)], 32, 0), ("bf16", [39999, 0, 0, 1], 100, 0)])
+def test_long_and_many_sequences(kind, lens, rows, window):
+    rng = np.random.default_rng(len(lens))
+    c, rk, rv = filled(rng, kind, lens, rows, 2, 128)
+    q = randn(kind, len(lens), 4, 128, seed=2).cuda()
+    got = c.attention(0, q, window=window)
+    c.sync()
+    want, tol = decode_want(q, rk, rv, window, 128 ** -0.5, kind)
+    assert_close(got, want, tol)
+    for _ in range(3):  # the split does not change a bit
+        assert np.array_equal(bits(c.attention(0, q, window=window)), bits(got))
+
+
+def test_scales_and_large_scores():
+    rng = np.random.default_rng(11)
+    lens = [50, 700, 16]
+    for scale, std in ((1.0, 1.0), (-0.2, 1.0), (0.0, 1.0), (0.125, 8.0)):
+        c, rk, rv = filled(rng, "bf16", lens, 16, 2, 64)
+        q = randn("bf16", 3, 4, 64, seed=3, std=std).cuda()
+        want, tol = decode_want(q, rk, rv, 0, scale, "bf16")
+        assert_close(c.attention(0, q, scale=scale), want, tol, "scale %g" % scale)
+
+
+def test_infinities_and_nan_reach_only_the_rows_that_see_them():
+    torch, _ = _mods()
+    rng = np.random.default_rng(12)
+    c, rk, rv = filled(rng, "bf16", [100, 100, 100, 100], 16, 1, 64)
+    at = lambda s, r: (int(c.table[s, r // 16]), 0, r % 16)
+    c.k_pages[0][at(0, 10)] = float("nan")
+    c.v_pages[0][at(1, 10)][3] = float("inf")
+    c.k_pages[0][at(2, 99)] = float("inf")
+    q = randn("bf16", 4, 2, 64, seed=1).cuda()
+    seen = c.attention(0, q).cpu()
+    assert torch.isnan(seen[0]).all()
+    assert (seen[1, :, 3] == float("inf")).all() and torch.isfinite(seen[1, :, :3]).all()
+    assert torch.isnan(seen[2]).any()
+    want, tol = decode_want(q, rk, rv, 0, 0.125, "bf16")
+    assert_close(seen[3:], want[3:], tol[3:])
+    # behind a window the first two are clean
+    want, tol = decode_want(q, rk, rv, 89, 0.125, "bf16")
+    assert_close(c.attention(0, q, window=89)[:2], want[:2], tol[:2])
+    # scores that are all -inf: 0 / 0, as the formula has it
+    c.k_pages[0].fill_(float("-inf"))
+    assert torch.isnan(c.attention(0, q.abs())).all()
+
+
+def test_strided_queries_and_results():
+    torch, _ = _mods()
+    rng = np.random.default_rng(13)
+    c, rk, rv = filled(rng, "fp16", [37, 200, 0], 16, 2, 64)
+    qkv = randn("fp16", 3, 8 + 4, 64, seed=4).cuda()
+    big = torch.full((3, 16, 3, 64), 7.0, dtype=torch.float16, device="cuda")
+    out = big[:, ::2, 1]
+    got = c.attention(0, qkv[:, :8], out=out)
+    assert got is out
+    want, tol = decode_want(qkv[:, :8], rk, rv, 0, 0.125, "fp16")
+    assert_close(out, want, tol)
+    big[:, ::2, 1] = 7.0
+    assert (big == 7.0).all()
+
+
+def test_lengths_beyond_the_table_are_cut_off():
+    torch, _ = _mods()
+    rng = np.random.default_rng(14)
+    c, rk, rv = filled(rng, "bf16", [32, 20], 16, 1, 64)
+    q = randn("bf16", 2, 1, 64).cuda()
+    want = bits(c.attention(0, q))
+    c.lens.copy_(ints([1 << 30, 20]))
+    assert np.array_equal(bits(c.attention(0, q)), want)
+    c.lens.copy_(ints([-3, 20]))
+    got = c.attention(0, q)
+    assert (got[0] == 0).all() and np.array_equal(bits(got[1:]), want[1:])
+
+
+def test_the_wrappers_refuse_what_does_not_fit():
+    torch, msm = _mods()
+    rng = np.random.default_rng(15)
+    c, _, _ = filled(rng, "bf16", [32, 20], 16, 2, 64)
+    q = randn("bf16", 2, 4, 64).cuda()
+    for bad in (q[:1], q.half(), q.cpu(), q[:, :, :32], q.transpose(1, 2).contiguous().transpose(1, 2), q[0]):
+        with pytest.raises(ValueError):
+            c.attention(0, bad)
+    with pytest.raises(ValueError):
+        c.attention(0, q, out=q[:1])
+    with pytest.raises(msm.MsmError):
+        c.attention(1, q)
+    with pytest.raises(msm.MsmError, match="1, 2, 4 or 8"):
+        c.attention(0, randn("bf16", 2, 6, 64).cuda())
+    with pytest.raises(ValueError):
+        c.resize(ints([1]))
+    with pytest.raises(ValueError):
+        c.fork(torch.zeros(2, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError):
+        c.write(0, q, q, ints([0, 1, 2]))
+    with pytest.raises(ValueError):
+        msm.prompt_attention(q, q[:1], q, ints([0, 2]))
+    with pytest.raises(ValueError):
+        msm.prompt_attention(q.float(), q.float(), q.float(), ints([0, 2]))
+    with pytest.raises(msm.MsmError, match="strides"):
+        msm.prompt_attention(q, q[:1].expand(2, 4, 64), q, ints([0, 2]))
+    c.sync()
+
+
+# ------------------------------------------------------------------ prompt attention
+def prompt_want(q, k, v, qs, ks, window, scale, kind):
+    out, tol = np.zeros(q.shape), np.full(q.shape, 1e-30)
+    for s in range(len(qs) - 1):
+        a, b = slice(qs[s], qs[s + 1]), slice(ks[s], ks[s + 1])
+        o, t = attend(f64(q[a]), f64(k[b]), f64(v[b]), (b.stop - b.start) - (a.stop - a.start), window, scale, kind)
+        out[a], tol[a] = o, t
+    return out, tol
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("hkv,group", [(1, 1), (1, 8), (2, 4), (3, 2)])
+def test_prompt_attention_equals_the_formula(kind, hd, hkv, group):
+    _, msm = _mods()
+    lens = [1, 0, 17, 64, 5, 130, 257, 31]
+    st = starts_of(lens)
+    qkv = randn(kind, st[-1], (group + 2) * hkv, hd, seed=hd + group).cuda()
+    q, k, v = qkv[:, :hkv * group], qkv[:, hkv * group:hkv * (group + 1)], qkv[:, hkv * (group + 1):]
+    for window in (0, 1, 40, 128):
+        got = msm.prompt_attention(q, k, v, ints(st), window=window)
+        want, tol = prompt_want(q, k, v, st, st, window, hd ** -0.5, kind)
+        assert_close(got, want, tol, "window %d" % window)
+
+
+@pytest.mark.parametrize("hd,group", [(64, 2), (128, 8)])
+@pytest.mark.parametrize("qlens,klens", [([3, 40, 1], [300, 40, 129]), ([1, 1, 1], [1, 128, 513]),
+                                         ([70, 20], [30, 0]), ([200], [500]), ([5, 5], [0, 5])])
+def test_resumed_prompts_and_rows_without_keys(hd, group, qlens, klens):
+    torch, msm = _mods()
+    qs, ks = starts_of(qlens), starts_of(klens)
+    q = randn("bf16", qs[-1], 2 * group, hd, seed=1).cuda()
+    # the keys in a verify-step cache's order, NaN behind the last one
+    kc = torch.full((2, ks[-1] + 9, hd), float("nan"), dtype=torch.bfloat16, device="cuda")
+    vc = torch.full_like(kc, float("nan"))
+    kc[:, :ks[-1]] = randn("bf16", 2, ks[-1], hd, seed=2).cuda()
+    vc[:, :ks[-1]] = randn("bf16", 2, ks[-1], hd, seed=3).cuda()
+    k, v = kc.transpose(0, 1), vc.transpose(0, 1)
+    for window in (0, 33):
+        got = msm.prompt_attention(q, k, v, ints(qs), ints(ks), window=window)
+        want, tol = prompt_want(q, k[:ks[-1]], v[:ks[-1]], qs, ks, window, hd ** -0.5, "bf16")
+        assert_close(got, want, tol, "window %d" % window)
+
+
+@pytest.mark.parametrize("kind,n,hq,hkv,hd,window", [("bf16", 1500, 2, 1, 128, 0), ("fp16", 1100, 1, 1, 64, 0),
+                                                     ("bf16", 1300, 4, 1, 64, 300), ("fp16", 900, 8, 1, 128, 257)])
+def test_longer_prompts(kind, n, hq, hkv, hd, window):
+    _, msm = _mods()
+    q, k, v = (randn(kind, n, h, hd, seed=h + i).cuda() for i, h in enumerate((hq, hkv, hkv)))
+    got = msm.prompt_attention(q, k, v, ints([0, n]), window=window)
+    want, tol = prompt_want(q, k, v, [0, n], [0, n], window, hd ** -0.5, kind)
+    assert_close(got, want, tol)
+    for _ in range(3):
+        assert np.array_equal(bits(msm.prompt_attention(q, k, v, ints([0, n]), window=window)), bits(got))
+
+
+def test_prompt_scales_and_large_scores():
+    _, msm = _mods()
+    st = [0, 200, 333]
+    for scale, std in ((1.0, 1.0), (-0.2, 1.0), (0.0, 1.0), (0.125, 8.0)):
+        q, k, v = (randn("bf16", 333, 2, 64, seed=i, std=std if i == 0 else 1.0).cuda() for i in range(3))
+        want, tol = prompt_want(q, k, v, st, st, 0, scale, "bf16")
+        assert_close(msm.prompt_attention(q, k, v, ints(st), scale=scale), want, tol, "scale %g" % scale)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("bad", ["nan", "inf", "-inf"])
+def test_keys_that_a_query_does_not_see_have_no_part(hd, bad):
+    """One row of K or V is not finite: the queries that see it follow the formula, every
+    other one is as if the row were not there."""
+    torch, msm = _mods()
+    n, window = 400, 150
+    st = [0, n, n + 30]
+    for which in (1, 2):
+        for row in (0, 131, 255, 399):
+            x = [randn("bf16", n + 30, 2, hd, seed=i).cuda() for i in range(3)]
+            clean = [t.clone() for t in x]
+            x[which][row, 0, 5:9] = float(bad)
+            for w in (0, window):
+                got = msm.prompt_attention(*x, ints(st), window=w).cpu().double()
+                want, tol = prompt_want(*clean, st, st, w, hd ** -0.5, "bf16")
+                seen = torch.zeros(n + 30, 2, dtype=torch.bool)
+                seen[row:(min(n, row + w) if w else n), 0] = True
+                free = ~seen
+                assert torch.isfinite(got[free]).all()
+                assert (np.abs(got.numpy() - want)[free.numpy()] <= tol[free.numpy()]).all()
+                if which == 2:  # V: those columns take the value, the others are untouched
+                    hit = got[seen][:, 5:9]
+                    assert torch.isnan(hit).all() if bad == "nan" else (hit == float(bad)).all()
+                    rest = [c for c in range(hd) if c < 5 or c >= 9]
+                    s = seen.numpy()
+                    assert (np.abs(got.numpy()[s][:, rest] - want[s][:, rest]) <= tol[s][:, rest]).all()
+                elif bad == "nan":
+                    assert torch.isnan(got[seen]).all()
+
+
+def test_prompt_leaves_what_is_not_its_own():
+    torch, msm = _mods()
+    x = [randn("bf16", 100, 4, 64, seed=i).cuda() for i in range(3)]
+    big = torch.full((120, 2, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    out = big[10:110, 1]
+    st = [0, 20, 81]
+    assert msm.prompt_attention(*x, ints(st), out=out) is out
+    want, tol = prompt_want(*x, st, st, 0, 0.125, "bf16")
+    assert_close(out[:81], want[:81], tol[:81])
+    out[:81] = 3.0
+    assert (big == 3.0).all()
+
+
+def test_starts_out_of_range_are_cut_off():
+    torch, msm = _mods()
+    x = [randn("bf16", 50, 2, 64, seed=i).cuda() for i in range(3)]
+    for st in ([0, 50, 1 << 30], [-5, 50, 50], [0, 50, 20]):
+        got = msm.prompt_attention(*x, ints(st))
+        want, tol = prompt_want(*x, [0, 50], [0, 50], 0, 0.125, "bf16")
+        assert_close(got, want, tol, str(st))
+
+
+def test_empty_prompts():
+    torch, msm = _mods()
+    e = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    assert msm.prompt_attention(e, e, e, ints([0, 0])).shape == (0, 2, 64)
+    q = randn("bf16", 3, 2, 64).cuda()
+    assert (msm.prompt_attention(q, e, e, ints([0, 3]), ints([0, 0])) == 0).all()
+
+
+# ------------------------------------------------------------------ together
+def test_a_prompt_a_search_and_single_tokens():
+    """Two prompts through the prompt attention into pages, one of them forked, every branch
+    continued token by token, the others freed, the pool compacted: at each step the paged
+    attention equals the formula over the rows that the sequence was given."""
+    torch, msm = _mods()
+    rng = np.random.default_rng(20)
+    hq, hkv, hd, slots = 8, 2, 64, 5
+    cache = msm.PagedCache.allocate(2, 40, 16, hkv, hd, slots, 12, dtype=torch.bfloat16)
+    hist = [[torch.empty((0, hkv, hd), dtype=torch.bfloat16)] * 2 for _ in range(slots)]  # per sequence: K, V
+    prompts = [70, 33, 0, 0, 0]
+    st = starts_of(prompts)
+    x = randn("bf16", st[-1], hq + 2 * hkv, hd, seed=1).cuda()
+    q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+    cache.resize(ints(prompts))
+    cache.write(1, k, v, ints(st))
+    got = msm.prompt_attention(q, k, v, ints(st))
+    want, tol = prompt_want(q, k, v, st, st, 0, hd ** -0.5, "bf16")
+    assert_close(got, want, tol)
+    for s in range(slots):
+        hist[s] = [k[st[s]:st[s + 1]].cpu(), v[st[s]:st[s + 1]].cpu()]
+    cache.fork(ints([-1, -1, 0, 0, 1]))
+    for s, p in ((2, 0), (3, 0), (4, 1)):
+        hist[s] = list(hist[p])
+    active = list(range(slots))
+    for step in range(8):
+        n = [hist[s][0].shape[0] + 1 if s in active else 0 for s in range(slots)]
+        cache.resize(ints(n))
+        cnt = starts_of([int(s in active) for s in range(slots)])
+        y = randn("bf16", cnt[-1], 2 * hkv, hd, seed=50 + step).cuda()
+        cache.write(1, y[:, :hkv], y[:, hkv:], ints(cnt))
+        for i, s in enumerate(active):
+            hist[s] = [torch.cat([hist[s][0], y[i:i + 1, :hkv].cpu()]), torch.cat([hist[s][1], y[i:i + 1, hkv:].cpu()])]
+        qq = randn("bf16", slots, hq, hd, seed=70 + step).cuda()
+        got = cache.attention(1, qq)
+        cache.sync()
+        for s in range(slots):
+            if s in active:
+                nk = hist[s][0].shape[0]
+                want, tol = attend(f64(qq[s:s + 1]), f64(hist[s][0]), f64(hist[s][1]), nk - 1, 0, hd ** -0.5, "bf16")
+                assert_close(got[s:s + 1], want, tol, "step %d sequence %d" % (step, s))
+            else:
+                assert (got[s] == 0).all()
+        if step == 3:
+            active = [0, 3, 4]
+        if step == 5:
+            cache.resize(ints([-1 if s in active else 0 for s in range(slots)]))
+            cache.compact()
+            used = int((cache.refs > 0).sum())
+            assert (cache.refs[:used] > 0).all()
+
+
+def test_pages_are_caches_of_the_verify_step():
+    """With page_rows = max_ctx a page is what msm_verify_step takes: histories that
+    msm_pages_write stored give the step's results bit for bit, and its new rows are in the
+    sequence's page."""
+    torch, msm = _mods()
+    import synth
+    from gpu_cases import make_case
+    case = make_case("cfg1_stack")
+    cfg, dev = case.cfg, torch.device("cuda", 0)
+    model = msm.Model(cfg, [synth.to_torch(w, dev) for w in case.layers], synth.to_torch(case.final, dev), device=0)
+    try:
+        hid = torch.from_numpy(case.hidden.view(np.int16)).to(dev)
+
+        def step(kc, vc):
+            logits = torch.empty((16, cfg.vocab), dtype=torch.float32, device=dev)
+            model.verify_step(hid, case.parent, case.pos0, kc, vc, logits_out=logits)
+            assert model.sync() == msm.MSM_OK
+            return logits
+        as_bf16 = lambda a: torch.from_numpy(a.view(np.int16)).to(dev).view(torch.bfloat16)
+        kc, vc = [as_bf16(k) for k, _ in case.kv], [as_bf16(v) for _, v in case.kv]
+        cache = msm.PagedCache.allocate(cfg.n_layers, 3, cfg.max_ctx, cfg.hkv, cfg.hd, 2, 1)
+        cache.resize(ints([5, case.pos0]))
+        for l in range(cfg.n_layers):
+            cache.write(l, kc[l][:, :case.pos0].transpose(0, 1), vc[l][:, :case.pos0].transpose(0, 1),
+                        ints([0, 0, case.pos0]))
+        cache.resize(ints([-1, case.pos0 + 16]))
+        cache.sync()
+        page = int(cache.table[1, 0])
+        got = step([t[page] for t in cache.k_pages], [t[page] for t in cache.v_pages])
+        want = step(kc, vc)
+        assert torch.equal(got, want)
+        for l in range(cfg.n_layers):
+            rows = slice(0, case.pos0 + 16)
+            assert np.array_equal(bits(cache.k_pages[l][page][:, rows]), bits(kc[l][:, rows]))
+            assert np.array_equal(bits(cache.v_pages[l][page][:, rows]), bits(vc[l][:, rows]))
+    finally:
+        model.close()
+
+
+def test_captured_and_replayed_with_other_lengths():
+    torch, msm = _mods()
+    rng = np.random.default_rng(21)
+    c, rk, rv = filled(rng, "bf16", [60, 200, 33], 16, 2, 64, extra=20, max_pages=16)
+    q = randn("bf16", 3, 4, 64, seed=5).cuda()
+    new = ints([61, 201, 34])
+    st = ints([0, 1, 2, 3])
+    kv = randn("bf16", 3, 4, 64, seed=6).cuda()
+    c.attention(0, q)
+    c.table[c.table < 0] = -1
+    saved = [t.clone() for t in (c.table, c.lens, c.refs)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        c.resize(new)
+        c.write(0, kv[:, :2], kv[:, 2:], st)
+        out = c.attention(0, q)
+        p_out = msm.prompt_attention(kv, kv[:, :2], kv[:, 2:], st)
+    other = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(other, stream=side):
+        out2 = c.attention(0, q, window=20)
+    for lens in ([61, 201, 34], [100, 0, 250], [0, 17, 16]):
+        for t, x in zip((c.table, c.lens, c.refs), saved):
+            t.copy_(x)
+        # rows that a sequence gains beyond those it had are whatever its pages held: zeros
+        c.k_pages[0].nan_to_num_(0.0)
+        c.v_pages[0].nan_to_num_(0.0)
+        new.copy_(ints(lens))
+        st.copy_(ints(starts_of([int(n > 0) for n in lens])))
+        g.replay()
+        other.replay()
+        c.sync()
+        ref_k, ref_v = [], []
+        table, kp, vp = c.table.cpu().numpy(), c.k_pages[0].cpu(), c.v_pages[0].cpu()
+        for s, n in enumerate(lens):
+            ids = [int(table[s, r // 16]) for r in range(n)]
+            ref_k.append(torch.stack([kp[p, :, r % 16] for r, p in enumerate(ids)]) if n else kp[0, :, :0].transpose(0, 1))
+            ref_v.append(torch.stack([vp[p, :, r % 16] for r, p in enumerate(ids)]) if n else vp[0, :, :0].transpose(0, 1))
+        want, tol = decode_want(q, ref_k, ref_v, 0, 0.125, "bf16")
+        assert_close(out, want, tol, str(lens))
+        want, tol = decode_want(q, ref_k, ref_v, 20, 0.125, "bf16")
+        assert_close(out2, want, tol, str(lens))
+        n = sum(int(x > 0) for x in lens)
+        assert np.array_equal(f64(p_out[:n]), f64(kv[:n, [2, 2, 3, 3]]))  # one key each: its v
+
+
+def test_two_streams_at_once():
+    """Attention calls of one cache on two streams, each with its own workspace."""
+    torch, msm = _mods()
+    rng = np.random.default_rng(22)
+    c, rk, rv = filled(rng, "bf16", [9000, 500, 3000], 64, 2, 128)
+    qs = [randn("bf16", 3, 8, 128, seed=i).cuda() for i in range(2)]
+    want = [bits(c.attention(0, q)) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[], []]
+    for _ in range(30):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(c.attention(0, qs[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in outs[i]:
+            assert np.array_equal(bits(o), want[i])
