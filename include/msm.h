@@ -591,9 +591,10 @@ msm_status msm_pages_write(const msm_pages* pages, int layer, const void* k, con
  *   q, out     device [n_seqs][n_q_heads][head_dim], strides in elements between
  *              sequences and between heads (multiples of 8), 16-byte aligned
  *   workspace  device buffer of msm_paged_attention_workspace bytes (0: an argument is
- *              wrong, see msm_last_error), 16-byte aligned; its contents are of no
- *              interest before or after.  Calls that share one must
- *              not overlap on the GPU.
+ *              wrong, see msm_last_error), 16-byte aligned.  It must be zero before its
+ *              first call; a call leaves its counters zero for the next one.  Calls that
+ *              share a workspace must not overlap on the GPU (neither must graphs that
+ *              recorded them), and must have the same n_q_heads, n_kv_heads and head_dim.
  * Device error: MSM_ERR_INVALID_ARG for a row on a page outside the pool; such rows are
  * left out.
  */

@@ -236,7 +236,7 @@ def lib():
             L.msm_paged_attention.argtypes = [pp, ctypes.c_int, vp, i64, i64, ctypes.c_int, ctypes.c_float,
                                               ctypes.c_int, vp, i64, i64, vp, ctypes.c_size_t, vp]
             L.msm_paged_attention.restype = st
-            L.msm_prompt_attention.argtypes = [ctypes.POINTER(MsmPrompt), vp]
+            L.msm_prompt_attention.argtypes = [vp, vp]
             L.msm_prompt_attention.restype = st
             L.msm_last_error.argtypes = []
             L.msm_last_error.restype = ctypes.c_char_p
@@ -457,7 +457,7 @@ def msm_paged_attention(pages: MsmPages, layer, q, q_strides, n_q_heads, scale, 
 
 
 def msm_prompt_attention(prompt: MsmPrompt, stream=0) -> int:
-    return lib().msm_prompt_attention(prompt, stream)
+    return lib().msm_prompt_attention(ctypes.byref(prompt), stream)
 
 
 # ---------------------------------------------------------------- torch-facing wrapper

@@ -64,9 +64,9 @@ struct PagedAttn {
   uint16_t* out;
   int64_t q_seq, q_head, out_seq, out_head;  // strides in elements
   float scale_log2;                          // softmax scale x log2(e)
-  float* part;                               // workspace: partial results, two per block
+  uint32_t* counters;                        // workspace: three per block, zero between calls,
+  float* part;                               // and partial results, two per block
 };
-constexpr int kPagedAttnPerSm = 2;  // blocks per SM
 size_t paged_attn_workspace(int blocks, int group, int head_dim);
 cudaError_t launch_paged_attn(const PagedAttn& p, int dtype, int head_dim, int blocks, cudaStream_t s);
 

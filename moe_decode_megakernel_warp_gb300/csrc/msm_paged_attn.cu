@@ -4,22 +4,25 @@
 // query head h reading kv head h / group.
 //
 // Bound by memory: every K and V row is read once, 4 flops per element.  The work is cut
-// into tiles of 128 rows of one (sequence, kv head); every block takes an equal, contiguous
-// run of the tiles of the whole batch, so ragged lengths and a single long sequence load
-// all SMs alike.  A (sequence, head) whose tiles all fall to one block is finished there;
-// the others leave partial results (maximum, sum, unnormalised output in 32 bits), at most
-// two per block, which a second launch joins.
+// into tiles of 128 rows of one (sequence, kv head); every block (one per SM) takes an equal,
+// contiguous run of the tiles of the whole batch, so ragged lengths and a single long
+// sequence load all SMs alike.  A (sequence, head) whose tiles all fall to one block is
+// finished there; the others leave partial results (maximum, sum, unnormalised output in 32
+// bits), at most two per block, which the last block of them to arrive joins in the order of
+// the tiles, so the result does not depend on which one that is.
 //
-// Inside a block the eight warps take 16 rows each and work without shared memory: with
-// S^T = K Q^T the K rows are the A operand of m16n8k16 products (16 rows x up to 8 query
-// heads of the group), loaded straight into its registers 16 bytes at a time -- the order
-// of the contraction index is free, so lane t of a quad takes 8 consecutive elements for
-// two products.  O^T = V^T P^T takes V rows the same way, interleaving pairs of rows with
-// byte permutes, and P^T comes out of S^T by an 8 x 8 transpose in registers.
+// Inside a block the eight warps take 16 or 32 rows at a time each, every warp with a ring of its
+// own in shared memory that cp.async keeps filled across the ends of items (rows outside the
+// sequence or its window are filled with zeros, never read).  With S^T = K Q^T the K rows
+// are the A operand of m16n8k16 products (16 rows x up to 8 query heads of the group), read
+// 16 bytes at a time -- the order of the contraction index is free, so lane t of a quad takes
+// 8 consecutive elements for two products.  O^T = V^T P^T takes V rows the same way,
+// interleaving pairs of rows with byte permutes, and P^T comes out of S^T by an 8 x 8
+// transpose in registers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include <algorithm>
+#include <atomic>
 
 #include "msm_device.cuh"
 #include "msm_paged.h"
@@ -29,8 +32,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreadsA = kWarps * 32;
-constexpr int kChunk = 16;               // rows of one warp step
-constexpr int kTile = kWarps * kChunk;   // rows of one work unit
+constexpr int kTile = 128;               // rows of one work unit
 constexpr int kHeads = 8;                // columns of the products: query heads of a kv head
 
 struct Bf16 {
@@ -64,14 +66,23 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ uint4 ld_row(const uint16_t* p, bool ok) {
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if (ok) v = __ldcs(reinterpret_cast<const uint4*>(p));
+// 16 bytes to shared memory, zeros where `bytes` is 0
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
 
-// a partial result in the workspace: item, maxima and sums, outputs
-__host__ __device__ constexpr int part_floats(int group, int hd) { return 4 + 2 * kHeads + group * hd; }
+// a partial result in the workspace: maxima, sums, outputs
+__host__ __device__ constexpr int part_floats(int group, int hd) { return 2 * kHeads + group * hd; }
 
 struct Rows {  // the rows of one sequence that a call reads
   int lo, hi, base, tiles;  // [lo, hi); base = lo rounded down to a chunk
@@ -81,37 +92,199 @@ __device__ __forceinline__ Rows seq_rows(const PagedAttn& p, int s) {
   const int64_t cap = (int64_t)p.max_pages * p.page_rows;
   r.hi = (int)min((int64_t)max(p.lens[s], 0), cap);
   r.lo = p.window > 0 ? max(0, r.hi - p.window) : 0;
-  r.base = r.lo & ~(kChunk - 1);
+  r.base = r.lo & ~31;
   r.tiles = (r.hi - r.base + kTile - 1) / kTile;
   return r;
 }
 
-// kPaged16: page_rows is a multiple of 16, so a warp's 16 rows lie in one page (one table
-// look-up per step instead of one per row)
-template <class El, int HD, bool kPaged16>
-__global__ void __launch_bounds__(kThreadsA, 2) paged_attn_kernel(const PagedAttn p) {
+// The work of one block on one (sequence, head): rows [base + 128 ta, end), base + 128 ta
+// being the first row of its tile ta.
+struct Segment {
+  int s, h;
+  int lo, end, first;  // rows below lo are not seen
+  int ta, tb, tiles;   // its tiles of the item's
+  int64_t item0;       // the batch's tiles before the item
+};
+
+// Walks the segments of a block's run of tiles [u, u1).
+struct Walk {
+  int64_t u, u1, before;  // before: tiles of the sequences in front of s
+  int s;
+  __device__ bool next(const PagedAttn& p, Segment& g) {
+    if (u >= u1) return false;
+    Rows rw = seq_rows(p, s);
+    while (u >= before + (int64_t)rw.tiles * p.n_kv_heads) {
+      before += (int64_t)rw.tiles * p.n_kv_heads;
+      rw = seq_rows(p, ++s);
+    }
+    g.s = s;
+    g.h = (int)((u - before) / rw.tiles);
+    g.item0 = before + (int64_t)g.h * rw.tiles;
+    g.ta = (int)(u - g.item0);
+    g.tb = (int)min((int64_t)rw.tiles, u1 - g.item0);
+    g.tiles = rw.tiles;
+    g.lo = rw.lo;
+    g.first = rw.base + g.ta * kTile;
+    g.end = min(rw.hi, rw.base + g.tb * kTile);
+    u = g.item0 + g.tb;
+    return true;
+  }
+};
+
+template <int HD>
+struct Cfg {
+  static constexpr int kRowBytes = HD * 2;
+  static constexpr int kChunk = HD == 128 ? 16 : 32;          // rows of one warp step: 8 KB of K and V
+  static constexpr int kStep = kWarps * kChunk;               // rows of one step of the block
+  static constexpr int kStageBytes = 2 * kChunk * kRowBytes;
+  // One step on the way while another one is worked on: 64 KB per SM cover the latency, and
+  // more of them cost DRAM locality (head_dim 128, 64 sequences of 16,384 rows: two stages
+  // 6,736 GB/s, three 6,457).
+  static constexpr int kStages = 2;
+  static constexpr int kOutStride = HD + 4;
+  static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+  static constexpr int kSmem = kRingBytes + kWarps * kHeads * kOutStride * 4;
+};
+
+// 16-byte piece c of row r of a chunk: the permutation keeps the eight lanes of a phase on
+// different banks for the K reads (two rows x four pieces) and the V reads (four rows of one
+// parity x two pieces) alike
+__device__ __forceinline__ int swizzle(int r, int c) { return c ^ (((r >> 1) & 3) << 1) ^ ((r & 1) << 2); }
+
+// Parts of an item, in the order of its tiles: part i stands in slot 1 of block b0 (i = 0) or
+// in slot 0 of block b0 + i.  Joins parts i0, i0 + step, ... (n of them) and writes the
+// output, or a joined part in the place of the first one.
+constexpr int kJoinGroup = 16;
+template <class El, int HD>
+__device__ void join_parts(const PagedAttn& p, int b0, int i0, int step, int n, int s, int h, bool final,
+                           float (*s_ml)[2], float4* s_x) {
+  const int part_len = part_floats(p.group, HD);
+  const int cols = p.group * HD / 4, rows = kThreadsA / cols;  // float4 columns; parts taken at a time
+  const int c = threadIdx.x % cols, r = threadIdx.x / cols, hd = 4 * c / HD;
+  auto part = [&](int k) -> float* {
+    const int i = i0 + k * step;
+    return p.part + (size_t)(2 * (b0 + i) + (i == 0 ? 1 : 0)) * part_len;
+  };
+  float m = -INFINITY, l = 0.f;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = r; k0 < n; k0 += 4 * rows) {
+    float mq[4], lq[4];
+    float4 v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int k = k0 + q * rows;
+      mq[q] = -INFINITY;
+      lq[q] = 0.f;
+      v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k < n) {
+        const float* const a = part(k);
+        mq[q] = __ldcg(a + hd);
+        lq[q] = __ldcg(a + kHeads + hd);
+        v[q] = __ldcg(reinterpret_cast<const float4*>(a + 2 * kHeads) + c);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float mn = fmaxf(m, mq[q]), ref = mn == -INFINITY ? 0.f : mn;
+      const float fa = exp2_fast(m - ref), fb = exp2_fast(mq[q] - ref);
+      l = l * fa + lq[q] * fb;
+      x.x = x.x * fa + v[q].x * fb;
+      x.y = x.y * fa + v[q].y * fb;
+      x.z = x.z * fa + v[q].z * fb;
+      x.w = x.w * fa + v[q].w * fb;
+      m = mn;
+    }
+  }
+  __syncthreads();
+  s_ml[threadIdx.x][0] = m;
+  s_ml[threadIdx.x][1] = l;
+  s_x[threadIdx.x] = x;
+  __syncthreads();
+  if (r == 0) {
+    for (int k = 1; k < rows; ++k) {
+      const int o = k * cols + c;
+      const float mq = s_ml[o][0], mn = fmaxf(m, mq), ref = mn == -INFINITY ? 0.f : mn;
+      const float fa = exp2_fast(m - ref), fb = exp2_fast(mq - ref);
+      const float4 v = s_x[o];
+      l = l * fa + s_ml[o][1] * fb;
+      x.x = x.x * fa + v.x * fb;
+      x.y = x.y * fa + v.y * fb;
+      x.z = x.z * fa + v.z * fb;
+      x.w = x.w * fa + v.w * fb;
+      m = mn;
+    }
+    if (final) {
+      const float inv = 1.f / l;
+      uint2 o;
+      o.x = El::pack(x.x * inv, x.y * inv);
+      o.y = El::pack(x.z * inv, x.w * inv);
+      *reinterpret_cast<uint2*>(p.out + s * p.out_seq + (h * p.group + hd) * p.out_head + 4 * c % HD) = o;
+    } else {
+      float* const a = part(0);
+      reinterpret_cast<float4*>(a + 2 * kHeads)[c] = x;
+      if (4 * c % HD == 0) {
+        a[hd] = m;
+        a[kHeads + hd] = l;
+      }
+    }
+  }
+}
+
+// true for the block that arrives last of n at a counter (which it leaves at zero); what the
+// others wrote before they arrived is then visible to it
+__device__ bool arrive_last(uint32_t* counter, int n, int* s_flag) {
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const bool last = atomicAdd(counter, 1u) == (uint32_t)n - 1u;
+    if (last) *counter = 0u;
+    *s_flag = last;
+  }
+  __syncthreads();
+  const bool last = *s_flag != 0;
+  if (last) __threadfence();
+  return last;
+}
+
+template <class El, int HD>
+__global__ void __launch_bounds__(kThreadsA, 1) paged_attn_kernel(const PagedAttn p) {
+  using C = Cfg<HD>;
   constexpr int KB = HD / 32;  // 32-element blocks of a K row
   constexpr int VB = HD / 64;  // 64-element blocks of a V row
-  constexpr int kOutStride = HD + 4;
+  constexpr int kAhead = C::kStages - 1;
+  constexpr int kSub = C::kChunk / 16;
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int64_t s_sum[kWarps];
   __shared__ int64_t s_find[2];  // first sequence of the block's run, tiles before it
   __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
-  __shared__ float s_o[kWarps][kHeads][kOutStride];
+  __shared__ int s_flag;
+  float (*const s_o)[kHeads][C::kOutStride] =
+      reinterpret_cast<float (*)[kHeads][C::kOutStride]>(smem + C::kRingBytes);
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int G = gridDim.x, b = blockIdx.x;
   const int part_len = part_floats(p.group, HD);
+  const uint32_t ring = smem_u32(smem) + wid * C::kStages * C::kStageBytes;
 
-  // the batch's tiles and where this block's run begins
-  int64_t total = 0;
+  // the batch's tiles and where this block's run begins; one scan when one round of the
+  // block's threads covers the sequences
+  int64_t total = 0, mine = 0, upto = 0;  // this thread's sequence's tiles, and with those in front (last round)
   for (int c = 0; c < p.n_seqs; c += kThreadsA) {
-    int64_t x = c + tid < p.n_seqs ? (int64_t)seq_rows(p, c + tid).tiles * p.n_kv_heads : 0;
+    mine = c + tid < p.n_seqs ? (int64_t)seq_rows(p, c + tid).tiles * p.n_kv_heads : 0;
+    int64_t v = mine;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if (lane == 0) s_sum[wid] = x;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    if (lane == 31) s_sum[wid] = v;
     __syncthreads();
+    upto = total + v;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += s_sum[w];
+    for (int q = 0; q < kWarps; ++q) {
+      if (q < wid) upto += s_sum[q];
+      total += s_sum[q];
+    }
     __syncthreads();
   }
   // (no more blocks than tiles, so that the parts of an item lie in consecutive blocks)
@@ -122,147 +295,160 @@ __global__ void __launch_bounds__(kThreadsA, 2) paged_attn_kernel(const PagedAtt
     if (seq_rows(p, s).tiles == 0)
       for (int i = tid; i < p.n_kv_heads * p.group * HD; i += kThreadsA)
         p.out[s * p.out_seq + (i / HD) * p.out_head + i % HD] = 0;
-  if (tid < 2) p.part[(size_t)(2 * b + tid) * part_len] = __int_as_float(-1);  // no partial result yet
   if (u0 >= u1) return;
-  int64_t run = 0;
-  for (int c = 0; c < p.n_seqs; c += kThreadsA) {
-    const int64_t x = c + tid < p.n_seqs ? (int64_t)seq_rows(p, c + tid).tiles * p.n_kv_heads : 0;
-    int64_t v = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += y;
+  if (p.n_seqs <= kThreadsA) {
+    if (upto - mine <= u0 && u0 < upto) {
+      s_find[0] = tid;
+      s_find[1] = upto - mine;
     }
-    if (lane == 31) s_sum[wid] = v;
-    __syncthreads();
-    for (int w = 0; w < wid; ++w) v += s_sum[w];
-    int64_t all = 0;
+  } else {
+    int64_t run = 0;
+    for (int c = 0; run <= u0; c += kThreadsA) {
+      const int64_t x = c + tid < p.n_seqs ? (int64_t)seq_rows(p, c + tid).tiles * p.n_kv_heads : 0;
+      int64_t v = x;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) all += s_sum[w];
-    if (run + v - x <= u0 && u0 < run + v) {
-      s_find[0] = c + tid;
-      s_find[1] = run + v - x;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      if (lane == 31) s_sum[wid] = v;
+      __syncthreads();
+      v += run;
+#pragma unroll
+      for (int q = 0; q < kWarps; ++q) {
+        if (q < wid) v += s_sum[q];
+        run += s_sum[q];
+      }
+      if (v - x <= u0 && u0 < v) {
+        s_find[0] = c + tid;
+        s_find[1] = v - x;
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    run += all;
-    if (run > u0) break;
   }
-  int s = (int)s_find[0];
-  int64_t before = s_find[1];  // tiles of the sequences before s
+  __syncthreads();
 
-  for (int64_t u = u0; u < u1;) {
-    Rows rw = seq_rows(p, s);
-    while (u >= before + (int64_t)rw.tiles * p.n_kv_heads) {
-      before += (int64_t)rw.tiles * p.n_kv_heads;
-      rw = seq_rows(p, ++s);
+  // ---- loads: every warp keeps kAhead chunks of its own on the way, across the ends of items
+  Walk ahead{u0, u1, s_find[1], (int)s_find[0]};
+  Segment fs{};
+  int fc = 0;  // the next chunk to fetch: row of its first row; -1: none left
+  int page = 0;
+  // the page of row lane % kChunk of the next chunk
+  auto look = [&]() {
+    const int r = fc + lane % C::kChunk;
+    page = fc >= 0 && r < fs.end ? p.table[(size_t)fs.s * p.max_pages + r / p.page_rows] : -1;
+  };
+  // the next chunk of this warp, in this or a later segment
+  auto find_chunk = [&]() {
+    while (fc < 0 || fc >= fs.end) {
+      if (!ahead.next(p, fs)) {
+        fc = -1;
+        return;
+      }
+      fc = fs.first + wid * C::kChunk;
     }
-    const int h = (int)((u - before) / rw.tiles);
-    const int64_t item0 = before + (int64_t)h * rw.tiles;  // first tile of (s, h)
-    const int ta = (int)(u - item0), tb = (int)min((int64_t)rw.tiles, u1 - item0);
-    const int k_end = min(rw.hi, rw.base + tb * kTile);
+  };
+  int f_stage = 0;
+  bool lost = false;  // a table entry outside the pool
+  // fetches a chunk and returns which of its rows take part (0 when none is left)
+  auto fetch = [&]() -> uint32_t {
+    uint32_t rows = 0;
+    if (fc >= 0) {
+      const int r = fc + lane % C::kChunk;
+      bool ok = r >= fs.lo && r < fs.end;
+      if (ok && (page < 0 || page >= p.n_pages)) {
+        lost = true;
+        ok = false;
+      }
+      rows = __ballot_sync(0xffffffffu, ok);
+      // pool row of row lane % kChunk
+      const uint32_t at = ((uint32_t)page * p.n_kv_heads + fs.h) * p.page_rows + r % p.page_rows;
+      const uint32_t dst = ring + f_stage * C::kStageBytes;
+      constexpr int kPieces = HD / 8, kRowsAtOnce = 32 / kPieces;  // 16-byte pieces of a row
+      const int c = lane % kPieces, sub = lane / kPieces;
+#pragma unroll
+      for (int i = 0; i < C::kChunk / kRowsAtOnce; ++i) {
+        const int row = i * kRowsAtOnce + sub;
+        const uint32_t pr = __shfl_sync(0xffffffffu, at, row);
+        const bool in = rows >> row & 1;
+        const size_t off = in ? (size_t)pr * HD + c * 8 : 0;
+        const uint32_t d = dst + row * C::kRowBytes + swizzle(row, c) * 16;
+        cp_async16(d, p.k + off, in ? 16 : 0);
+        cp_async16(d + C::kChunk * C::kRowBytes, p.v + off, in ? 16 : 0);
+      }
+      f_stage = f_stage + 1 == C::kStages ? 0 : f_stage + 1;
+      fc += C::kStep;
+      find_chunk();
+      look();
+    }
+    cp_async_commit();
+    return rows;
+  };
+  fc = -1;
+  find_chunk();
+  look();
+  uint32_t queue[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) queue[i] = fetch();
 
-    // q of the group as the B operand: column g = query head, the contraction index in the
-    // order of the K loads
-    uint32_t qf[KB][4];
+  Walk walk{u0, u1, s_find[1], (int)s_find[0]};
+  Segment sg;
+  int stage = 0;
+  // q of the group as the B operand: column g = query head, the contraction index in the
+  // order of the K reads
+  uint4 qf[KB];
+  auto load_q = [&]() {
 #pragma unroll
     for (int j = 0; j < KB; ++j) {
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      qf[j] = make_uint4(0u, 0u, 0u, 0u);
       if (g < p.group)
-        x = *reinterpret_cast<const uint4*>(p.q + s * p.q_seq + (h * p.group + g) * p.q_head + j * 32 + t * 8);
-      qf[j][0] = x.x;
-      qf[j][1] = x.y;
-      qf[j][2] = x.z;
-      qf[j][3] = x.w;
+        qf[j] = *reinterpret_cast<const uint4*>(p.q + sg.s * p.q_seq + (sg.h * p.group + g) * p.q_head + j * 32 + t * 8);
     }
+  };
+  bool more = walk.next(p, sg);
+  load_q();
+  while (more) {
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2t, 2t + 1
     float o[HD / 16][4];
 #pragma unroll
     for (int i = 0; i < HD / 16; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) o[i][q] = 0.f;
-
-    const int32_t* const row_tab = p.table + (size_t)s * p.max_pages;
-    bool lost = false;  // a table entry outside the pool
-    // page of the chunk's first row (kPaged16), or of row c0 + lane % 16
-    auto look = [&](int c0) -> int {
-      const int r = kPaged16 ? c0 : c0 + (lane & 15);
-      return r < k_end ? row_tab[r / p.page_rows] : 0;
-    };
-    // pool row of the chunk's row 0 (kPaged16) or of row lane % 16; -1: not in the pool
-    auto pool_row = [&](int c0, int page) -> int64_t {
-      const int r = kPaged16 ? c0 : c0 + (lane & 15);
-      if (page < 0 || page >= p.n_pages) {
-        lost |= r < k_end && (kPaged16 || r >= rw.lo);
-        return -1;
+    for (int c0 = sg.first + wid * C::kChunk; c0 < sg.end; c0 += C::kStep) {
+      cp_async_wait<kAhead - 1>();
+      __syncwarp();
+      const uint32_t rows = queue[0];
+      const uint32_t kb = ring + stage * C::kStageBytes, vb = kb + C::kChunk * C::kRowBytes;
+      stage = stage + 1 == C::kStages ? 0 : stage + 1;
+#pragma unroll
+      for (int i = 0; i + 1 < kAhead; ++i) queue[i] = queue[i + 1];
+      queue[kAhead - 1] = fetch();  // into the stage that the previous step read
+      // 16 rows at a time: rows g (sc[0], sc[1]) and g + 8 (sc[2], sc[3]); heads 2t and 2t + 1
+      float sc[kSub][4];
+      float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < kSub; ++u) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sc[u][q] = 0.f;
+        const uint32_t k0 = kb + (u * 16 + g) * C::kRowBytes, k1 = k0 + 8 * C::kRowBytes;
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          const uint4 a = lds128(k0 + swizzle(g, j * 4 + t) * 16), c = lds128(k1 + swizzle(g, j * 4 + t) * 16);
+          El::mma(sc[u], a.x, c.x, a.y, c.y, qf[j].x, qf[j].y);
+          El::mma(sc[u], a.z, c.z, a.w, c.w, qf[j].z, qf[j].w);
+        }
+        const bool ok0 = rows >> (u * 16 + g) & 1, ok1 = rows >> (u * 16 + g + 8) & 1;
+        sc[u][0] = ok0 ? sc[u][0] * p.scale_log2 : -INFINITY;
+        sc[u][1] = ok0 ? sc[u][1] * p.scale_log2 : -INFINITY;
+        sc[u][2] = ok1 ? sc[u][2] * p.scale_log2 : -INFINITY;
+        sc[u][3] = ok1 ? sc[u][3] * p.scale_log2 : -INFINITY;
+        x0 = fmaxf(x0, fmaxf(sc[u][0], sc[u][2]));
+        x1 = fmaxf(x1, fmaxf(sc[u][1], sc[u][3]));
       }
-      return ((int64_t)page * p.n_kv_heads + h) * p.page_rows + r % p.page_rows;
-    };
-    auto row_of = [&](int64_t pr, int i) -> int64_t {  // pool row of the chunk's row i, or -1
-      if (kPaged16) return pr < 0 ? pr : pr + i;
-      return __shfl_sync(0xffffffffu, pr, i);
-    };
-    auto seen = [&](int c0, int i, int64_t row) -> bool {
-      const int r = c0 + i;
-      return r >= rw.lo && r < k_end && row >= 0;
-    };
-    auto load_k = [&](int c0, int64_t pr, uint4 (&kf)[2][KB], bool (&ok)[2]) {
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int i = g + 8 * hf;
-        const int64_t row = row_of(pr, i);
-        const uint16_t* const src = p.k + row * HD + t * 8;
-        ok[hf] = seen(c0, i, row);
-#pragma unroll
-        for (int j = 0; j < KB; ++j) kf[hf][j] = ld_row(src + j * 32, ok[hf]);
-      }
-    };
-
-    int c0 = rw.base + ta * kTile + wid * kChunk;
-    int64_t pr = -1;
-    int page_next = 0;
-    uint4 kf[2][KB];
-    bool ok[2] = {false, false};
-    if (c0 < k_end) {
-      pr = pool_row(c0, look(c0));
-      load_k(c0, pr, kf, ok);
-      if (c0 + kTile < k_end) page_next = look(c0 + kTile);
-    }
-    while (c0 < k_end) {
-      // V rows 2t, 2t + 1, 2t + 8, 2t + 9 of the chunk, elements 8g .. 8g + 7 of each block
-      uint4 vf[4][VB];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int i = 2 * t + (q & 1) + 8 * (q >> 1);
-        const int64_t row = row_of(pr, i);
-        const uint16_t* const src = p.v + row * HD + g * 8;
-        const bool see = seen(c0, i, row);
-#pragma unroll
-        for (int j = 0; j < VB; ++j) vf[q][j] = ld_row(src + j * 64, see);
-      }
-      float sc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < KB; ++j) {
-        El::mma(sc, kf[0][j].x, kf[1][j].x, kf[0][j].y, kf[1][j].y, qf[j][0], qf[j][1]);
-        El::mma(sc, kf[0][j].z, kf[1][j].z, kf[0][j].w, kf[1][j].w, qf[j][2], qf[j][3]);
-      }
-      // rows g (sc[0], sc[1]) and g + 8 (sc[2], sc[3]); heads 2t and 2t + 1
-      sc[0] = ok[0] ? sc[0] * p.scale_log2 : -INFINITY;
-      sc[1] = ok[0] ? sc[1] * p.scale_log2 : -INFINITY;
-      sc[2] = ok[1] ? sc[2] * p.scale_log2 : -INFINITY;
-      sc[3] = ok[1] ? sc[3] * p.scale_log2 : -INFINITY;
-      // the next chunk's K rows travel while this one's softmax and second product run
-      const int cn = c0 + kTile;
-      int64_t prn = -1;
-      if (cn < k_end) {
-        prn = pool_row(cn, page_next);
-        load_k(cn, prn, kf, ok);
-        if (cn + kTile < k_end) page_next = look(cn + kTile);
-      }
-      float x0 = fmaxf(sc[0], sc[2]), x1 = fmaxf(sc[1], sc[3]);
-#pragma unroll
-      for (int w = 4; w <= 16; w <<= 1) {
-        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, w));
-        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, w));
+      for (int q = 4; q <= 16; q <<= 1) {
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, q));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, q));
       }
       const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
       if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
@@ -281,32 +467,40 @@ __global__ void __launch_bounds__(kThreadsA, 2) paged_attn_kernel(const PagedAtt
         m1 = n1;
       }
       const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
-      const float e0 = exp2_fast(sc[0] - r0), e1 = exp2_fast(sc[1] - r1), e2 = exp2_fast(sc[2] - r0),
-                  e3 = exp2_fast(sc[3] - r1);
-      l0 += e0 + e2;
-      l1 += e1 + e3;
-      // P rounded to the 16-bit type for the product (a relative error of half a step per
-      // weight, as V itself carries); its sum keeps 32 bits
-      const uint32_t b0 = transpose8x8(El::pack(e0, e1)), b1 = transpose8x8(El::pack(e2, e3));
 #pragma unroll
-      for (int j = 0; j < VB; ++j)
+      for (int u = 0; u < kSub; ++u) {
+        const float e0 = exp2_fast(sc[u][0] - r0), e1 = exp2_fast(sc[u][1] - r1), e2 = exp2_fast(sc[u][2] - r0),
+                    e3 = exp2_fast(sc[u][3] - r1);
+        l0 += e0 + e2;
+        l1 += e1 + e3;
+        // P rounded to the 16-bit type for the product (a relative error of half a step per
+        // weight, as V itself carries); its sum keeps 32 bits
+        const uint32_t b0 = transpose8x8(El::pack(e0, e1)), b1 = transpose8x8(El::pack(e2, e3));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t v0 = (&vf[0][j].x)[i], v1 = (&vf[1][j].x)[i], v2 = (&vf[2][j].x)[i], v3 = (&vf[3][j].x)[i];
-          // element 64 j + 8 g + 2 i in row g of the product, the next one in row g + 8
-          El::mma(o[j * 4 + i], __byte_perm(v0, v1, 0x5410), __byte_perm(v0, v1, 0x7632),
-                  __byte_perm(v2, v3, 0x5410), __byte_perm(v2, v3, 0x7632), b0, b1);
+        for (int j = 0; j < VB; ++j) {
+          // V rows 2t, 2t + 1, 2t + 8, 2t + 9, elements 8g .. 8g + 7 of the block
+          uint4 v[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int i = 2 * t + (q & 1) + 8 * (q >> 1);
+            v[q] = lds128(vb + (u * 16 + i) * C::kRowBytes + swizzle(i, j * 8 + g) * 16);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t v0 = (&v[0].x)[i], v1 = (&v[1].x)[i], v2 = (&v[2].x)[i], v3 = (&v[3].x)[i];
+            // element 64 j + 8 g + 2 i in row g of the product, the next one in row g + 8
+            El::mma(o[j * 4 + i], __byte_perm(v0, v1, 0x5410), __byte_perm(v0, v1, 0x7632),
+                    __byte_perm(v2, v3, 0x5410), __byte_perm(v2, v3, 0x7632), b0, b1);
+          }
         }
-      c0 = cn;
-      pr = prn;
+      }
     }
-    if (lost) atomicCAS(p.status, 0, MSM_ERR_INVALID_ARG | (kCallAttention << 8));
 
-    // the warps' results joined
+    // the warps' results joined; the next segment's q travels meanwhile
 #pragma unroll
-    for (int w = 4; w <= 16; w <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, w);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, w);
+    for (int q = 4; q <= 16; q <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, q);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, q);
     }
     if (g == 0) {
       s_m[wid][2 * t] = m0;
@@ -322,149 +516,83 @@ __global__ void __launch_bounds__(kThreadsA, 2) paged_attn_kernel(const PagedAtt
         *reinterpret_cast<float2*>(&s_o[wid][2 * t][d]) = make_float2(o[j * 4 + i][0], o[j * 4 + i][2]);
         *reinterpret_cast<float2*>(&s_o[wid][2 * t + 1][d]) = make_float2(o[j * 4 + i][1], o[j * 4 + i][3]);
       }
+    const Segment done = sg;
+    more = walk.next(p, sg);
+    if (more) load_q();
     __syncthreads();
-    const bool whole = ta == 0 && tb == rw.tiles;
+    const bool whole = done.ta == 0 && done.tb == done.tiles;
     // a run's first item that began before it goes to the block's slot 0, the last one that
     // goes on behind it to slot 1
-    float* const part = p.part + (size_t)(2 * b + (ta > 0 ? 0 : 1)) * part_len;
+    float* const part = p.part + (size_t)(2 * b + (done.ta > 0 ? 0 : 1)) * part_len;
     for (int i = tid; i < p.group * HD / 2; i += kThreadsA) {
       const int hd = i / (HD / 2), d = (i - hd * (HD / 2)) * 2;
       float m = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w][hd]);
+      for (int q = 0; q < kWarps; ++q) m = fmaxf(m, s_m[q][hd]);
       const float ref = m == -INFINITY ? 0.f : m;
       float l = 0.f, x = 0.f, y = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+      for (int q = 0; q < kWarps; ++q) {
         // (a NaN sum passes on; a warp without rows has m = -inf and zeros)
-        const float f = exp2_fast(s_m[w][hd] - ref);
-        const float2 v = *reinterpret_cast<const float2*>(&s_o[w][hd][d]);
-        l += f * s_l[w][hd];
+        const float f = exp2_fast(s_m[q][hd] - ref);
+        const float2 v = *reinterpret_cast<const float2*>(&s_o[q][hd][d]);
+        l += f * s_l[q][hd];
         x += f * v.x;
         y += f * v.y;
       }
       if (whole) {
         const float inv = 1.f / l;
-        *reinterpret_cast<uint32_t*>(p.out + s * p.out_seq + (h * p.group + hd) * p.out_head + d) =
+        *reinterpret_cast<uint32_t*>(p.out + done.s * p.out_seq + (done.h * p.group + hd) * p.out_head + d) =
             El::pack(x * inv, y * inv);
       } else {
-        *reinterpret_cast<float2*>(part + 4 + 2 * kHeads + hd * HD + d) = make_float2(x, y);
+        *reinterpret_cast<float2*>(part + 2 * kHeads + hd * HD + d) = make_float2(x, y);
         if (d == 0) {
-          part[4 + hd] = m;
-          part[4 + kHeads + hd] = l;
+          part[hd] = m;
+          part[kHeads + hd] = l;
         }
       }
     }
-    if (!whole && tid == 0) {
-      part[0] = __int_as_float(s);
-      part[1] = __int_as_float(h);
-      part[2] = __int_as_float(tb == rw.tiles);  // the item ends here
+    if (!whole) {
+      // the blocks that hold the item's first and last tile; the last one to arrive joins the
+      // parts, groups of kJoinGroup first when there are more
+      const int b0 = (int)(((done.item0 + 1) * busy - 1) / total);
+      const int n = (int)(((done.item0 + done.tiles) * busy - 1) / total) - b0 + 1;
+      const int k = (b - b0) / kJoinGroup, groups = (n + kJoinGroup - 1) / kJoinGroup;
+      float4* const s_x = reinterpret_cast<float4*>(s_o);  // (the warps' results are used up)
+      float (*const s_ml)[2] = reinterpret_cast<float (*)[2]>(s_x + kThreadsA);
+      // (counters: one of the item that a block begins, one for the groups of that item, one of the
+      // group whose first part is the block's slot 0)
+      if (arrive_last(p.counters + (k == 0 ? b0 : 2 * G + b0 + k * kJoinGroup), min(kJoinGroup, n - k * kJoinGroup), &s_flag)) {
+        join_parts<El, HD>(p, b0, k * kJoinGroup, 1, min(kJoinGroup, n - k * kJoinGroup), done.s, done.h, groups == 1,
+                           s_ml, s_x);
+        if (groups > 1 && arrive_last(p.counters + G + b0, groups, &s_flag))
+          join_parts<El, HD>(p, b0, 0, kJoinGroup, groups, done.s, done.h, true, s_ml, s_x);
+      }
     }
     __syncthreads();
-    u = item0 + tb;
   }
-}
-
-// Joins the partial results: block (b, y) finishes the item that begins in block b's slot 1
-// (blocks b + 1, b + 2, ... hold its further parts in slot 0 until one says that it ends
-// there), columns [64 y, 64 y + 64) of its group * HD outputs; 16 threads across the
-// columns, 16 parts at a time.
-constexpr int kJoinCols = 64;
-template <class El, int HD>
-__global__ void __launch_bounds__(256) paged_join_kernel(const PagedAttn p, int G) {
-  __shared__ float s_m[16], s_l[16];
-  __shared__ float4 s_x[16][kJoinCols / 4];
-  __shared__ int s_n;
-  pdl_wait();
-  const int part_len = part_floats(p.group, HD);
-  const int b = blockIdx.x, c = threadIdx.x & 15, r = threadIdx.x >> 4;
-  const float* const first = p.part + (size_t)(2 * b + 1) * part_len;
-  const int s = __float_as_int(first[0]);
-  if (s < 0) return;
-  const int h = __float_as_int(first[1]);
-  const int col = blockIdx.y * kJoinCols + 4 * c, hd = (int)blockIdx.y * kJoinCols / HD;
-  // parts of the item: up to and with the first one that ends it
-  if (threadIdx.x == 0) s_n = G;
-  __syncthreads();
-  for (int i0 = 1; b + i0 < G; i0 += 256) {
-    const int i = i0 + (int)threadIdx.x;
-    if (b + i < G) {
-      const float* const q = p.part + (size_t)(2 * (b + i)) * part_len;
-      if (__float_as_int(q[0]) != s || __float_as_int(q[1]) != h) atomicMin(&s_n, i);
-      else if (__float_as_int(q[2])) atomicMin(&s_n, i + 1);
-    }
-    __syncthreads();
-    if (s_n <= i0 + 256) break;
-  }
-  const int n = min(s_n, G - b);
-  float m = -INFINITY, l = 0.f;
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = r; i < n; i += 16) {
-    const float* const q = i == 0 ? first : p.part + (size_t)(2 * (b + i)) * part_len;
-    const float mq = q[4 + hd], lq = q[4 + kHeads + hd];
-    const float4 v = *reinterpret_cast<const float4*>(q + 4 + 2 * kHeads + col);
-    const float mn = fmaxf(m, mq);
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    const float fa = exp2_fast(m - ref), fb = exp2_fast(mq - ref);
-    l = l * fa + lq * fb;
-    x.x = x.x * fa + v.x * fb;
-    x.y = x.y * fa + v.y * fb;
-    x.z = x.z * fa + v.z * fb;
-    x.w = x.w * fa + v.w * fb;
-    m = mn;
-  }
-  if (c == 0) {
-    s_m[r] = m;
-    s_l[r] = l;
-  }
-  s_x[r][c] = x;
-  __syncthreads();
-  if (r != 0) return;
-  float mm = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) mm = fmaxf(mm, s_m[i]);
-  const float ref = mm == -INFINITY ? 0.f : mm;
-  float ll = 0.f;
-  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float f = exp2_fast(s_m[i] - ref);
-    const float4 v = s_x[i][c];
-    ll += f * s_l[i];
-    y.x += f * v.x;
-    y.y += f * v.y;
-    y.z += f * v.z;
-    y.w += f * v.w;
-  }
-  const float inv = 1.f / ll;
-  uint2 w;
-  w.x = El::pack(y.x * inv, y.y * inv);
-  w.y = El::pack(y.z * inv, y.w * inv);
-  *reinterpret_cast<uint2*>(p.out + s * p.out_seq + (h * p.group + hd) * p.out_head + col % HD) = w;
+  if (lost) atomicCAS(p.status, 0, MSM_ERR_INVALID_ARG | (kCallAttention << 8));
 }
 
 template <class El, int HD>
 cudaError_t launch(const PagedAttn& p, int blocks, cudaStream_t s) {
-  if (p.page_rows % kChunk == 0) paged_attn_kernel<El, HD, true><<<blocks, kThreadsA, 0, s>>>(p);
-  else paged_attn_kernel<El, HD, false><<<blocks, kThreadsA, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit for this kernel is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3(blocks, p.group * HD / kJoinCols);
-  lc.blockDim = dim3(256);
-  lc.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, paged_join_kernel<El, HD>, p, blocks);
+  if (!(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(paged_attn_kernel<El, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cfg<HD>::kSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
+  paged_attn_kernel<El, HD><<<blocks, kThreadsA, Cfg<HD>::kSmem, s>>>(p);
+  return cudaGetLastError();
 }
-
 }  // namespace
 
 size_t paged_attn_workspace(int blocks, int group, int head_dim) {
-  return (size_t)2 * blocks * part_floats(group, head_dim) * sizeof(float);
+  return (size_t)2 * blocks * part_floats(group, head_dim) * sizeof(float) + 3 * blocks * sizeof(uint32_t);
 }
 
 cudaError_t launch_paged_attn(const PagedAttn& p, int dtype, int head_dim, int blocks, cudaStream_t s) {

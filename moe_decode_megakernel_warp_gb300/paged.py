@@ -9,18 +9,17 @@ by the library and raises ``MsmError``.
 from __future__ import annotations
 
 import ctypes
-import math
+import struct
 
 from . import MSM_BF16, MSM_FP16, MsmPages, MsmPrompt, _check, _ptr_array, lib
 
-_DTYPES = None
+# msm_prompt in the C layout (a bytes object takes a third of the time of a ctypes structure)
+_PROMPT = struct.Struct("9if4P8q2P")
+assert _PROMPT.size == ctypes.sizeof(MsmPrompt)
 
 
 def _torch():
-    global _DTYPES
     import torch
-    if _DTYPES is None:
-        _DTYPES = {torch.bfloat16: MSM_BF16, torch.float16: MSM_FP16}
     return torch
 
 
@@ -30,31 +29,33 @@ def _need(ok, msg):
 
 
 def _dtype(t):
-    _torch()
-    _need(t.dtype in _DTYPES, "expected bfloat16 or float16, got %s" % t.dtype)
-    return _DTYPES[t.dtype]
-
-
-def _rows(t, name, heads, head_dim, like):
-    """(first, second) strides of a [n][heads][head_dim] tensor; a dimension of one element
-    has no stride of its own."""
-    _need(t.dim() == 3 and (heads is None or t.shape[1] == heads) and t.shape[2] == head_dim,
-          "%s must be [n, %s, %d], got %s" % (name, "heads" if heads is None else heads, head_dim, tuple(t.shape)))
-    _need(t.dtype == like.dtype and t.device == like.device, "%s must have the type and device of the others" % name)
-    _need(t.stride(2) == 1, "%s: the elements of a row must be consecutive" % name)
-    n0, n1, _ = t.shape
-    return (t.stride(0) if n0 > 1 else n1 * head_dim), (t.stride(1) if n1 > 1 else head_dim)
-
-
-def _int32(t, name, n, device):
     torch = _torch()
-    _need(t.dtype == torch.int32 and t.is_contiguous() and t.device == device and (n is None or t.numel() == n),
-          "%s must be a contiguous int32 tensor%s on %s" % (name, "" if n is None else " of %d entries" % n, device))
+    if t.dtype is torch.bfloat16:
+        return MSM_BF16
+    _need(t.dtype is torch.float16, "expected bfloat16 or float16, got %s" % t.dtype)
+    return MSM_FP16
+
+
+def _rows(t, name, shape, dtype, index):
+    """(first, second) strides of a tensor [n][heads][head_dim] of the given shape, type and
+    CUDA device; a dimension of one element has no stride of its own."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        raise ValueError("%s must be %s, %s, on cuda:%d; got %s, %s, on %s"
+                         % (name, list(shape), dtype, index, list(t.shape), t.dtype, t.device))
+    s0, s1, s2 = t.stride()
+    _need(s2 == 1, "%s: the elements of a row must be consecutive" % name)
+    n0, n1, hd = shape
+    return (s0 if n0 > 1 else n1 * hd), (s1 if n1 > 1 else hd)
+
+
+def _int32(t, name, n, index):
+    if t.dtype is not _torch().int32 or t.get_device() != index or t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor of %d entries on cuda:%d" % (name, n, index))
     return t.data_ptr()
 
 
-def _stream(device):
-    return _torch().cuda.current_stream(device).cuda_stream
+def _stream(index):
+    return _torch()._C._cuda_getCurrentRawStream(index)
 
 
 class PagedCache:
@@ -88,10 +89,14 @@ class PagedCache:
         kp, self._k_ptrs = _ptr_array([t.data_ptr() for t in k_pages])
         vp, self._v_ptrs = _ptr_array([t.data_ptr() for t in v_pages])
         self._c = MsmPages(dev.index, _dtype(first), len(k_pages), n_pages, page_rows, n_kv_heads, head_dim, n_seqs,
-                           max_pages, kp, vp, _int32(table, "table", None, dev), _int32(lens, "lens", n_seqs, dev),
-                           _int32(refs, "refs", n_pages, dev), self.status.data_ptr(), self.scratch.data_ptr())
+                           max_pages, kp, vp, _int32(table, "table", n_seqs * max_pages, dev.index),
+                           _int32(lens, "lens", n_seqs, dev.index), _int32(refs, "refs", n_pages, dev.index),
+                           self.status.data_ptr(), self.scratch.data_ptr())
         self._ref = ctypes.byref(self._c)
-        self._workspace = {}  # bytes by number of query heads
+        self._index, self._n_seqs, self._kv_heads, self._head_dim = dev.index, n_seqs, n_kv_heads, head_dim
+        self._dtype = first.dtype
+        self._bytes = {}      # bytes of the attention's workspace by number of query heads
+        self._workspace = {}  # workspaces by (stream, number of query heads)
 
     @classmethod
     def allocate(cls, n_layers, n_pages, page_rows, n_kv_heads, head_dim, n_seqs, max_pages, dtype=None, device=None):
@@ -109,58 +114,63 @@ class PagedCache:
 
     def resize(self, new_lens):
         """msm_pages_resize: int32 [n_seqs] on the device, -1 = leave as it is."""
-        _check(lib().msm_pages_resize(self._ref, _int32(new_lens, "new_lens", self._c.n_seqs, self.device),
-                                      _stream(self.device)))
+        _check(lib().msm_pages_resize(self._ref, _int32(new_lens, "new_lens", self._n_seqs, self._index),
+                                      _stream(self._index)))
 
     def fork(self, parent):
         """msm_pages_fork: int32 [n_seqs] on the device, -1 = none."""
-        _check(lib().msm_pages_fork(self._ref, _int32(parent, "parent", self._c.n_seqs, self.device),
-                                    _stream(self.device)))
+        _check(lib().msm_pages_fork(self._ref, _int32(parent, "parent", self._n_seqs, self._index),
+                                    _stream(self._index)))
 
     def compact(self):
         """msm_pages_compact."""
-        _check(lib().msm_pages_compact(self._ref, _stream(self.device)))
+        _check(lib().msm_pages_compact(self._ref, _stream(self._index)))
 
     def write(self, layer, k, v, starts):
         """msm_pages_write: k, v [n_tokens, n_kv_heads, head_dim], starts int32 [n_seqs + 1]."""
-        c, like = self._c, self.k_pages[0]
-        kt, kh = _rows(k, "k", c.n_kv_heads, c.head_dim, like)
-        vt, vh = _rows(v, "v", c.n_kv_heads, c.head_dim, like)
-        _need(k.shape[0] == v.shape[0], "k and v must have as many tokens")
+        n, i = len(k), self._index
+        shape = (n, self._kv_heads, self._head_dim)
+        kt, kh = _rows(k, "k", shape, self._dtype, i)
+        vt, vh = _rows(v, "v", shape, self._dtype, i)
         _check(lib().msm_pages_write(self._ref, layer, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh,
-                                     _int32(starts, "starts", c.n_seqs + 1, self.device), k.shape[0],
-                                     _stream(self.device)))
+                                     _int32(starts, "starts", self._n_seqs + 1, i), n, _stream(i)))
 
     def attention(self, layer, q, window=0, scale=None, out=None):
         """msm_paged_attention: q [n_seqs, n_q_heads, head_dim]; scale defaults to
         1 / sqrt(head_dim).  Returns out."""
         torch = _torch()
-        c = self._c
-        qs, qh = _rows(q, "q", None, c.head_dim, self.k_pages[0])
-        _need(q.shape[0] == c.n_seqs, "q must have one row per sequence of the table (%d)" % c.n_seqs)
-        heads = q.shape[1]
+        _need(q.dim() == 3, "q must be [n_seqs, n_q_heads, head_dim]")
+        heads, i = q.shape[1], self._index
+        shape = (self._n_seqs, heads, self._head_dim)
+        qs, qh = _rows(q, "q", shape, self._dtype, i)
         if out is None:
-            out = torch.empty((c.n_seqs, heads, c.head_dim), dtype=q.dtype, device=self.device)
-        os_, oh = _rows(out, "out", heads, c.head_dim, q)
-        _need(out.shape[0] == c.n_seqs, "out must have the shape of q")
-        n = self._workspace.get(heads)
+            out = torch.empty(shape, dtype=self._dtype, device=self.device)
+        os_, oh = _rows(out, "out", shape, self._dtype, i)
+        stream = _stream(i)
+        n = self._bytes.get(heads)
         if n is None:
             n = lib().msm_paged_attention_workspace(self._ref, heads)
-            _check(0 if n else lib().msm_paged_attention(self._ref, layer, None, qs, qh, heads, 1.0, 0, None, os_, oh,
-                                                         None, 0, None))
-            self._workspace[heads] = n
-        # taken from torch's allocator for every call: memory of the stream (or of the graph
-        # that records the call), so calls on different streams do not share it
-        ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+            if n == 0:  # the call says what is wrong
+                _check(lib().msm_paged_attention(self._ref, layer, None, qs, qh, heads, 1.0, 0, None, os_, oh, None, 0,
+                                                 None))
+            self._bytes[heads] = n
+        # one workspace per stream, and one per call that a graph records (graphs recorded on
+        # one stream may be replayed on two)
+        if torch._C._cuda_isCurrentStreamCapturing():
+            ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
+        else:
+            ws = self._workspace.get((stream, heads))
+            if ws is None:
+                ws = self._workspace[stream, heads] = torch.zeros(n, dtype=torch.uint8, device=self.device)
         _check(lib().msm_paged_attention(self._ref, layer, q.data_ptr(), qs, qh, heads,
-                                         1.0 / math.sqrt(c.head_dim) if scale is None else scale, window,
-                                         out.data_ptr(), os_, oh, ws.data_ptr(), n, _stream(self.device)))
+                                         self._head_dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
+                                         os_, oh, ws.data_ptr(), n, stream))
         return out
 
     def sync(self):
         """msm_pages_sync: waits for the current stream; raises MsmError for an error that a
         call met on the device (and clears it)."""
-        _check(lib().msm_pages_sync(self._ref, _stream(self.device)))
+        _check(lib().msm_pages_sync(self._ref, _stream(self._index)))
 
 
 def prompt_attention(q, k, v, q_starts, k_starts=None, window=0, scale=None, out=None):
@@ -171,24 +181,22 @@ def prompt_attention(q, k, v, q_starts, k_starts=None, window=0, scale=None, out
     head_dim] is read in place), q_starts and k_starts int32 [n_seqs + 1] on the device
     (k_starts defaults to q_starts), scale defaults to 1 / sqrt(head_dim).  Returns out; a new
     one is uninitialised behind the last sequence."""
-    torch = _torch()
     _need(q.is_cuda, "q must be a CUDA tensor")
     _need(q.dim() == 3 and k.dim() == 3, "q and k must be [tokens, heads, head_dim]")
-    n_q, heads, hd = q.shape
+    n_q, heads, hd = shape = q.shape
     n_k, kv_heads, _ = k.shape
-    _need(v.shape == k.shape, "v must have the shape of k")
-    qt, qh = _rows(q, "q", heads, hd, q)
-    kt, kh = _rows(k, "k", kv_heads, hd, q)
-    vt, vh = _rows(v, "v", kv_heads, hd, q)
+    i, dtype, k_shape = q.get_device(), q.dtype, (n_k, kv_heads, hd)
+    qt, qh = _rows(q, "q", shape, dtype, i)
+    kt, kh = _rows(k, "k", k_shape, dtype, i)
+    vt, vh = _rows(v, "v", k_shape, dtype, i)
     if out is None:
-        out = torch.empty((n_q, heads, hd), dtype=q.dtype, device=q.device)
-    ot, oh = _rows(out, "out", heads, hd, q)
-    _need(out.shape[0] == n_q, "out must have the shape of q")
+        out = q.new_empty(shape)
+    ot, oh = _rows(out, "out", shape, dtype, i)
     n_seqs = q_starts.numel() - 1
-    qs = _int32(q_starts, "q_starts", None, q.device)
-    ks = qs if k_starts is None else _int32(k_starts, "k_starts", n_seqs + 1, q.device)
-    a = MsmPrompt(q.device.index, _dtype(q), n_seqs, n_q, n_k, heads, kv_heads, hd, window,
-                  1.0 / math.sqrt(hd) if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                  out.data_ptr(), qt, qh, kt, kh, vt, vh, ot, oh, qs, ks)
-    _check(lib().msm_prompt_attention(ctypes.byref(a), _stream(q.device)))
+    qs = _int32(q_starts, "q_starts", n_seqs + 1, i)
+    ks = qs if k_starts is None else _int32(k_starts, "k_starts", n_seqs + 1, i)
+    a = _PROMPT.pack(i, _dtype(q), n_seqs, n_q, n_k, heads, kv_heads, hd, window,
+                     hd ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                     out.data_ptr(), qt, qh, kt, kh, vt, vh, ot, oh, qs, ks)
+    _check(lib().msm_prompt_attention(a, _stream(i)))
     return out
