@@ -48,7 +48,7 @@ struct PagesCopy {
 
 struct PagesWrite {
   PagesMeta m;
-  int n_kv_heads, row_vecs, n_tokens;
+  int n_kv_heads, row_shift, n_tokens;  // 2^row_shift 16-byte vectors per row
   uint4 *pool_k, *pool_v;
   const uint4 *k, *v;
   int64_t k_token, k_head, v_token, v_head;  // strides in 16-byte vectors

@@ -203,7 +203,7 @@ msm_status msm_pages_write(const msm_pages* c, int layer, const void* k, const v
   PagesWrite p;
   p.m = meta(c, nullptr);
   p.n_kv_heads = c->n_kv_heads;
-  p.row_vecs = c->head_dim / 8;
+  p.row_shift = c->head_dim == 64 ? 3 : 4;
   p.n_tokens = n_tokens;
   p.pool_k = static_cast<uint4*>(c->k_pages[layer]);
   p.pool_v = static_cast<uint4*>(c->v_pages[layer]);

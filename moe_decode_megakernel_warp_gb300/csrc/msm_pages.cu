@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kMetaThreads = 1024;
 constexpr int kMetaWarps = kMetaThreads / 32;
-constexpr int kMetaBlocks = 8;      // the portable cluster size
+constexpr int kMetaBlocks = 8;      // the portable cluster size (one block for small caches: 0.6 us slower)
 constexpr int kPagesPerThread = 8;  // pages one thread looks at per step of a scan
 
 __device__ __forceinline__ void latch(int32_t* status, int code, int call) {
@@ -71,9 +71,10 @@ __device__ void exchange(Share& sh, cg::cluster_group& cl) {
   __syncthreads();
 }
 
+// the block's share of n things
 __device__ __forceinline__ void block_range(int n, int rank, int& lo, int& hi) {
-  const int per = (n + kMetaBlocks - 1) / kMetaBlocks;
-  lo = min(n, rank * per);
+  const int per = (n - 1) / kMetaBlocks + 1;
+  lo = (int)min((int64_t)n, (int64_t)rank * per);
   hi = min(n, lo + per);
 }
 
@@ -100,6 +101,7 @@ __device__ int count_pages(const int32_t* refs, int lo, int hi, bool live, Share
 __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThreads)
     resize_kernel(const PagesMeta p) {
   __shared__ Share sh;
+  pdl_launch_dependents();  // the copy launch waits for this one's end itself
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const PagesScratch sc(p.scratch, p.n_pages, p.n_seqs);
@@ -110,6 +112,15 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThrea
   if (threadIdx.x == 0) sh.mine.bad = 0;
   if (rank == 0 && threadIdx.x == 0) sc.head[0] = 0;
   __syncthreads();
+
+  // free pages among this thread's first kPagesPerThread of the block's share (their loads
+  // travel during step 1)
+  const int mine = p0 + (int)threadIdx.x * kPagesPerThread;
+  uint32_t mine_free = 0;
+#pragma unroll
+  for (int q = 0; q < kPagesPerThread; ++q)
+    if (mine + q < p1 && __ldcg(p.refs + mine + q) <= 0) mine_free |= 1u << q;
+  const int p_rest = p0 + kMetaThreads * kPagesPerThread;  // the share's pages behind those
 
   // 1. each sequence: are its lengths and the pages it gives up in range, how many pages
   //    does it lack, does it have to leave a shared last page (offset = 2 pages + leave)
@@ -148,7 +159,9 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThrea
     if (s < s1) sc.offset[s] = 2 * (base + before) + (e & 1);
     base += total;
   }
-  const int n_free = count_pages(p.refs, p0, p1, false, sh);
+  int n_free;
+  const int mine_rank = block_scan(__popc(mine_free), sh, n_free);
+  if (p_rest < p1) n_free += count_pages(p.refs, p_rest, p1, false, sh);
   if (threadIdx.x == 0) {
     sh.mine.need = base;
     sh.mine.count = n_free;
@@ -172,22 +185,33 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThrea
     return;
   }
   // 3. list[r] = the r-th lowest free page, for the r that are needed
-  int at = free_before;
-  for (int c = p0; c < p1 && at < need_all; c += kMetaThreads * kPagesPerThread) {
-    const int q0 = c + (int)threadIdx.x * kPagesPerThread;
-    uint32_t mask = 0;
-#pragma unroll
-    for (int q = 0; q < kPagesPerThread; ++q)
-      if (q0 + q < p1 && __ldcg(p.refs + q0 + q) <= 0) mask |= 1u << q;
-    int total;
-    int r = at + block_scan(__popc(mask), sh, total);
+  auto give = [&](int first, uint32_t mask, int64_t r) {
 #pragma unroll
     for (int q = 0; q < kPagesPerThread; ++q)
       if (mask >> q & 1) {
-        if (r < need_all) sc.list[r] = q0 + q;
+        if (r < need_all) sc.list[r] = first + q;
         ++r;
       }
-    at += total;
+  };
+  if (free_before < need_all) {
+    give(mine, mine_free, (int64_t)free_before + mine_rank);
+    int64_t at = free_before;
+    if (p_rest < p1) {
+      int first_step;
+      block_scan(__popc(mine_free), sh, first_step);
+      at += first_step;
+    }
+    for (int c = p_rest; c < p1 && at < need_all; c += kMetaThreads * kPagesPerThread) {
+      const int q0 = c + (int)threadIdx.x * kPagesPerThread;
+      uint32_t mask = 0;
+#pragma unroll
+      for (int q = 0; q < kPagesPerThread; ++q)
+        if (q0 + q < p1 && __ldcg(p.refs + q0 + q) <= 0) mask |= 1u << q;
+      int total;
+      const int before = block_scan(__popc(mask), sh, total);
+      give(q0, mask, at + before);
+      at += total;
+    }
   }
   cl.sync();
   // 4. the tables
@@ -277,6 +301,7 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThrea
 __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThreads)
     compact_kernel(const PagesMeta p) {
   __shared__ Share sh;
+  pdl_launch_dependents();  // the copy launch waits for this one's end itself
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank();
   const PagesScratch sc(p.scratch, p.n_pages, p.n_seqs);
@@ -341,10 +366,12 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThrea
 }
 
 // ---------------------------------------------------------------- row copies
-// Bound by memory: each byte is read once and written once.  One warp moves up to 8 KB
-// at a time, 16 loads of 16 bytes in flight per lane.
+// Bound by memory: each byte is read once and written once.  blockIdx.y = (layer, K or V); the
+// warps of a row of blocks share out the pieces of up to 8 KB, 16 loads of 16 bytes in flight
+// per lane (8: 20 % slower on short runs).
 constexpr int kCopyThreads = 256;
 constexpr int kCopyVecs = 16;  // 16-byte vectors per lane
+constexpr int kPieceVecs = 32 * kCopyVecs;
 
 template <bool kCompact>
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const PagesCopy p) {
@@ -352,52 +379,42 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const PagesCopy p) {
   const PagesScratch sc(p.m.scratch, p.m.n_pages, p.m.n_seqs);
   const int32_t* const dst = sc.list + p.m.n_pages / 2;
   const int lane = threadIdx.x & 31;
-  const int64_t warp = ((int64_t)blockIdx.x * kCopyThreads + threadIdx.x) >> 5;
-  const int64_t warps = ((int64_t)gridDim.x * kCopyThreads) >> 5;
-  const int entries = sc.head[0];
+  const uint32_t warp = (blockIdx.x * kCopyThreads + threadIdx.x) >> 5, warps = (gridDim.x * kCopyThreads) >> 5;
+  const uint32_t entries = sc.head[0];
   // a page is n_kv_heads runs of page_rows rows; all of it is one run when it moves whole
   const int64_t head_vecs = (int64_t)p.m.page_rows * p.row_vecs, page_vecs = head_vecs * p.n_kv_heads;
-  const int runs = kCompact ? 1 : p.n_kv_heads;
   const int64_t run_vecs = kCompact ? page_vecs : head_vecs;
-  const int64_t pieces = (run_vecs + 32 * kCopyVecs - 1) / (32 * kCopyVecs);
-  const int64_t per_entry = pieces * runs * 2 * p.n_layers;
-  for (int64_t u = warp; u < entries * per_entry; u += warps) {
-    const int64_t e = u / per_entry;
-    int64_t r = u - e * per_entry;
-    const int layer = (int)(r / (pieces * runs * 2));
-    r -= (int64_t)layer * (pieces * runs * 2);
-    const int kv = (int)(r / (pieces * runs));
-    r -= (int64_t)kv * (pieces * runs);
-    const int run = (int)(r / pieces);
-    const int64_t first = (r - (int64_t)run * pieces) * (32 * kCopyVecs);
+  const uint32_t pieces = (uint32_t)((run_vecs + kPieceVecs - 1) / kPieceVecs);
+  const uint32_t per_entry = kCompact ? pieces : pieces * p.n_kv_heads;
+  uint4* const pool = blockIdx.y & 1 ? p.v[blockIdx.y >> 1] : p.k[blockIdx.y >> 1];
+  for (uint64_t u = warp; u < (uint64_t)entries * per_entry; u += warps) {
+    // (a pool holds fewer than 2^32 rows, so fewer than 2^32 pieces)
+    const uint32_t e = (uint32_t)u / per_entry, r = (uint32_t)u - e * per_entry;
+    const uint32_t run = kCompact ? 0 : r / pieces;
+    const int64_t first = (int64_t)(r - run * pieces) * kPieceVecs;
     int from, to;
-    int64_t n;
+    int64_t n = run_vecs;
     if (kCompact) {
       from = sc.list[entries - 1 - e];
       to = dst[e];
-      n = run_vecs;
     } else {
-      from = sc.copies[3 * e];
-      to = sc.copies[3 * e + 1];
-      n = (int64_t)sc.copies[3 * e + 2] * p.row_vecs;
+      from = sc.copies[3 * (size_t)e];
+      to = sc.copies[3 * (size_t)e + 1];
+      n = (int64_t)sc.copies[3 * (size_t)e + 2] * p.row_vecs;
     }
     if (first >= n) continue;
-    uint4* const pool = kv ? p.v[layer] : p.k[layer];
-    const uint4* const src = pool + from * page_vecs + run * run_vecs;
-    uint4* const out = pool + to * page_vecs + run * run_vecs;
+    const uint4* const src = pool + from * page_vecs + run * run_vecs + first;
+    uint4* const out = pool + to * page_vecs + run * run_vecs + first;
+    const int left = (int)min(n - first, (int64_t)kPieceVecs);
     uint4 x[kCopyVecs];
 #pragma unroll
-    for (int q = 0; q < kCopyVecs; ++q) {
-      const int64_t i = first + q * 32 + lane;
-      if (i < n) x[q] = __ldcs(src + i);
-    }
+    for (int q = 0; q < kCopyVecs; ++q)
+      if (q * 32 + lane < left) x[q] = __ldcs(src + q * 32 + lane);
 #pragma unroll
-    for (int q = 0; q < kCopyVecs; ++q) {
-      const int64_t i = first + q * 32 + lane;
-      if (i < n) __stcs(out + i, x[q]);
-    }
+    for (int q = 0; q < kCopyVecs; ++q)
+      if (q * 32 + lane < left) __stcs(out + q * 32 + lane, x[q]);
   }
-  if (kCompact && p.renumber) {
+  if (kCompact && p.renumber && blockIdx.y == 0) {
     const int live = sc.head[1];
     for (int64_t s = warp; s < p.m.n_seqs; s += warps) {
       const int n = ceil_div(min(max(p.m.lens[s], 0), p.m.max_pages * p.m.page_rows), p.m.page_rows);
@@ -411,61 +428,61 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const PagesCopy p) {
 }
 
 // ---------------------------------------------------------------- new rows
-// Bound by memory (and by the launch for a step's few tokens): a block looks up the row
-// of each of its tokens once, then all of its threads move 16-byte vectors.
-constexpr int kWriteThreads = 256;
-constexpr int kWriteTokens = 8;
+// Bound by memory (and by latency for a step's few tokens): one warp per token.  Its loads
+// do not depend on where the rows go, so they are on their way while the warp looks that up.
+constexpr int kWriteThreads = 128;
+constexpr int kWriteVecs = 8;  // 16-byte vectors per lane at a time
 
 __global__ void __launch_bounds__(kWriteThreads) write_kernel(const PagesWrite p) {
-  __shared__ int64_t s_row[kWriteTokens];  // pool vector of head 0 of the token's row, or -1
-  const int t0 = blockIdx.x * kWriteTokens;
-  if (threadIdx.x < kWriteTokens) {
-    const int t = t0 + (int)threadIdx.x;
-    int64_t at = -1;
-    if (t < p.n_tokens && t < p.starts[p.m.n_seqs]) {
-      // the last sequence that starts at or before the token
-      int lo = 0, hi = p.m.n_seqs;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.starts[mid] <= t) lo = mid;
-        else hi = mid;
-      }
-      const int64_t pos = (int64_t)p.m.lens[lo] - p.starts[lo + 1] + t;
-      bool ok = t >= p.starts[lo] && t < p.starts[lo + 1] && pos >= 0 &&
-                pos < (int64_t)p.m.max_pages * p.m.page_rows;
-      if (ok) {
-        const int pg = p.m.table[(size_t)lo * p.m.max_pages + pos / p.m.page_rows];
-        ok = pg >= 0 && pg < p.m.n_pages && p.m.refs[pg] == 1;
-        if (ok) at = ((int64_t)pg * p.n_kv_heads * p.m.page_rows + pos % p.m.page_rows) * p.row_vecs;
-      }
-      if (!ok) latch(p.m.status, MSM_ERR_INVALID_ARG, kCallWrite);
-    }
-    s_row[threadIdx.x] = at;
+  const int lane = threadIdx.x & 31;
+  const int t = (int)((blockIdx.x * (int64_t)kWriteThreads + threadIdx.x) >> 5);
+  if (t >= p.n_tokens || t >= p.starts[p.m.n_seqs]) return;
+  const int half = p.n_kv_heads << p.row_shift, n = 2 * half;
+  auto load = [&](int i) -> uint4 {
+    const bool v = i >= half;
+    const int r = v ? i - half : i, h = r >> p.row_shift, c = r & ((1 << p.row_shift) - 1);
+    return v ? __ldcs(p.v + t * p.v_token + h * p.v_head + c) : __ldcs(p.k + t * p.k_token + h * p.k_head + c);
+  };
+  uint4 x[kWriteVecs];
+#pragma unroll
+  for (int q = 0; q < kWriteVecs; ++q)
+    if (lane + q * 32 < n) x[q] = load(lane + q * 32);
+  // the last sequence that starts at or before the token, 32 probes at a time
+  int lo = 0, hi = p.m.n_seqs;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, i < hi && p.starts[i] <= t);
+    lo += le ? (31 - __clz(le)) * step : 0;
+    hi = min(hi, lo + step);
   }
-  __syncthreads();
-  const int half = p.n_kv_heads * p.row_vecs, per = 2 * half, n = kWriteTokens * per;
-  const int64_t head = (int64_t)p.m.page_rows * p.row_vecs;
-  constexpr int kU = 8;
-  for (int i0 = threadIdx.x; i0 < n; i0 += kU * kWriteThreads) {
-    uint4 x[kU];
-    uint4* to[kU];
+  const int first = p.starts[lo], end = p.starts[lo + 1];
+  const int64_t pos = (int64_t)p.m.lens[lo] - end + t;
+  bool ok = t >= first && t < end && pos >= 0 && pos < (int64_t)p.m.max_pages * p.m.page_rows;
+  int64_t at = 0;  // pool vector of head 0 of the token's row
+  if (ok) {
+    const int pg = p.m.table[(size_t)lo * p.m.max_pages + (int)pos / p.m.page_rows];
+    ok = pg >= 0 && pg < p.m.n_pages && p.m.refs[pg] == 1;
+    at = ((int64_t)pg * p.n_kv_heads * p.m.page_rows + (int)pos % p.m.page_rows) << p.row_shift;
+  }
+  if (!ok) {
+    if (lane == 0) latch(p.m.status, MSM_ERR_INVALID_ARG, kCallWrite);
+    return;
+  }
+  const int64_t head = (int64_t)p.m.page_rows << p.row_shift;
+  for (int i0 = lane; i0 < n; i0 += 32 * kWriteVecs) {
+    if (i0 != lane) {
 #pragma unroll
-    for (int q = 0; q < kU; ++q) {
-      const int i = i0 + q * kWriteThreads, tok = i / per;
-      to[q] = nullptr;
-      if (i < n && s_row[tok] >= 0) {
-        int r = i - tok * per;
-        const bool v = r >= half;
-        r -= v ? half : 0;
-        const int h = r / p.row_vecs, c = r - h * p.row_vecs;
-        const int64_t t = t0 + tok;
-        x[q] = v ? __ldcs(p.v + t * p.v_token + h * p.v_head + c) : __ldcs(p.k + t * p.k_token + h * p.k_head + c);
-        to[q] = (v ? p.pool_v : p.pool_k) + s_row[tok] + h * head + c;
-      }
+      for (int q = 0; q < kWriteVecs; ++q)
+        if (i0 + q * 32 < n) x[q] = load(i0 + q * 32);
     }
 #pragma unroll
-    for (int q = 0; q < kU; ++q)
-      if (to[q]) *to[q] = x[q];
+    for (int q = 0; q < kWriteVecs; ++q) {
+      const int i = i0 + q * 32;
+      if (i >= n) break;
+      const bool v = i >= half;
+      const int r = v ? i - half : i, h = r >> p.row_shift, c = r & ((1 << p.row_shift) - 1);
+      (v ? p.pool_v : p.pool_k)[at + h * head + c] = x[q];
+    }
   }
 }
 
@@ -487,14 +504,14 @@ cudaError_t launch_pages_compact(const PagesMeta& p, cudaStream_t s) {
 }
 
 cudaError_t launch_pages_copy(const PagesCopy& p, bool compact, int sms, cudaStream_t s) {
-  // at most as many warps as there can be 8 KB pieces, at most four blocks per SM
+  // at most as many warps as there can be pieces, about sixteen blocks per SM in all
   const int64_t vecs = (int64_t)p.m.page_rows * p.row_vecs * (compact ? p.n_kv_heads : 1);
-  const int64_t pieces = (vecs + 32 * kCopyVecs - 1) / (32 * kCopyVecs) * (compact ? 1 : p.n_kv_heads);
+  const int64_t pieces = (vecs - 1) / kPieceVecs + 1;
   const int64_t entries = compact ? p.m.n_pages / 2 : p.m.n_seqs;
-  const int64_t warps = entries * pieces * 2 * p.n_layers;
-  const int64_t blocks = (warps + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
+  const int64_t warps = entries * pieces * (compact ? 1 : p.n_kv_heads);
+  const int64_t blocks = (warps - 1) / (kCopyThreads / 32) + 1, most = (16 * sms - 1) / (2 * p.n_layers) + 1;
   cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(blocks, 4 * (int64_t)sms)));
+  lc.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min(blocks, most)), 2 * p.n_layers);
   lc.blockDim = dim3(kCopyThreads);
   lc.stream = s;
   cudaLaunchAttribute attr[1];
@@ -506,7 +523,8 @@ cudaError_t launch_pages_copy(const PagesCopy& p, bool compact, int sms, cudaStr
 }
 
 cudaError_t launch_pages_write(const PagesWrite& p, cudaStream_t s) {
-  write_kernel<<<(p.n_tokens + kWriteTokens - 1) / kWriteTokens, kWriteThreads, 0, s>>>(p);
+  constexpr int kTokens = kWriteThreads / 32;
+  write_kernel<<<(p.n_tokens - 1) / kTokens + 1, kWriteThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
