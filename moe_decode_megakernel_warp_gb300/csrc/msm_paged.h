@@ -67,6 +67,7 @@ struct PagedAttn {
   uint32_t* counters;                        // workspace: three per block, zero between calls,
   float* part;                               // and partial results, two per block
 };
+constexpr int kPagedAttnPerSm = 2;  // blocks per SM
 size_t paged_attn_workspace(int blocks, int group, int head_dim);
 cudaError_t launch_paged_attn(const PagedAttn& p, int dtype, int head_dim, int blocks, cudaStream_t s);
 

@@ -222,7 +222,7 @@ size_t msm_paged_attention_workspace(const msm_pages* c, int n_q_heads) {
   if (check_pages(c) != MSM_OK || check_group(n_q_heads, c->n_kv_heads) != MSM_OK) return 0;
   int sms = 0;
   if (device_sms(c->device, &sms) != MSM_OK) return 0;
-  return paged_attn_workspace(sms, n_q_heads / c->n_kv_heads, c->head_dim);
+  return paged_attn_workspace(sms * kPagedAttnPerSm, n_q_heads / c->n_kv_heads, c->head_dim);
 }
 
 msm_status msm_paged_attention(const msm_pages* c, int layer, const void* q, int64_t q_seq_stride,
@@ -243,7 +243,7 @@ msm_status msm_paged_attention(const msm_pages* c, int layer, const void* q, int
   REQUIRE(workspace && !misaligned(workspace, 16), MSM_ERR_INVALID_ARG, "workspace is NULL or misaligned");
   int sms = 0;
   if ((st = device_sms(c->device, &sms)) != MSM_OK) return st;
-  const int blocks = sms, group = n_q_heads / c->n_kv_heads;  // one block per SM
+  const int blocks = sms * kPagedAttnPerSm, group = n_q_heads / c->n_kv_heads;
   REQUIRE(workspace_bytes >= paged_attn_workspace(blocks, group, c->head_dim), MSM_ERR_INVALID_ARG,
           "workspace is smaller than msm_paged_attention_workspace");
   DeviceGuard dev;

@@ -30,9 +30,9 @@
 namespace msm {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreadsA = kWarps * 32;
-constexpr int kTile = 128;               // rows of one work unit
+constexpr int kTile = kWarps * 16;       // rows of a tile
 constexpr int kHeads = 8;                // columns of the products: query heads of a kv head
 
 struct Bf16 {
@@ -84,8 +84,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 // a partial result in the workspace: maxima, sums, outputs
 __host__ __device__ constexpr int part_floats(int group, int hd) { return 2 * kHeads + group * hd; }
 
-struct Rows {  // the rows of one sequence that a call reads
-  int lo, hi, base, tiles;  // [lo, hi); base = lo rounded down to a chunk
+// The rows of one sequence that a call reads: [lo, hi), in tiles from base (lo rounded down to
+// a chunk).  An item costs its block one unit more than its tiles: finishing it takes about as long
+// as a tile (64 sequences of 1 to 8,192 rows: 80 us without that unit, 60 us with it).
+struct Rows {
+  int lo, hi, base, tiles, units;
 };
 __device__ __forceinline__ Rows seq_rows(const PagedAttn& p, int s) {
   Rows r;
@@ -94,6 +97,7 @@ __device__ __forceinline__ Rows seq_rows(const PagedAttn& p, int s) {
   r.lo = p.window > 0 ? max(0, r.hi - p.window) : 0;
   r.base = r.lo & ~31;
   r.tiles = (r.hi - r.base + kTile - 1) / kTile;
+  r.units = r.tiles > 0 ? r.tiles + 1 : 0;
   return r;
 }
 
@@ -103,31 +107,33 @@ struct Segment {
   int s, h;
   int lo, end, first;  // rows below lo are not seen
   int ta, tb, tiles;   // its tiles of the item's
-  int64_t item0;       // the batch's tiles before the item
+  int64_t unit0;       // the batch's unit that holds the item's first tile
 };
 
-// Walks the segments of a block's run of tiles [u, u1).
+// Walks the segments of a block's run of units [u, u1).  Unit 0 of an item has no tile.
 struct Walk {
-  int64_t u, u1, before;  // before: tiles of the sequences in front of s
+  int64_t u, u1, before;  // before: units of the sequences in front of s
   int s;
   __device__ bool next(const PagedAttn& p, Segment& g) {
-    if (u >= u1) return false;
-    Rows rw = seq_rows(p, s);
-    while (u >= before + (int64_t)rw.tiles * p.n_kv_heads) {
-      before += (int64_t)rw.tiles * p.n_kv_heads;
-      rw = seq_rows(p, ++s);
+    while (u < u1) {
+      Rows rw = seq_rows(p, s);
+      while (u >= before + (int64_t)rw.units * p.n_kv_heads) {
+        before += (int64_t)rw.units * p.n_kv_heads;
+        rw = seq_rows(p, ++s);
+      }
+      g.s = s;
+      g.h = (int)((u - before) / rw.units);
+      g.unit0 = before + (int64_t)g.h * rw.units + 1;
+      g.ta = max(0, (int)(u - g.unit0));
+      g.tb = (int)min((int64_t)rw.tiles, u1 - g.unit0);
+      g.tiles = rw.tiles;
+      g.lo = rw.lo;
+      g.first = rw.base + g.ta * kTile;
+      g.end = min(rw.hi, rw.base + g.tb * kTile);
+      u = g.unit0 + g.tb;
+      if (g.tb > g.ta) return true;
     }
-    g.s = s;
-    g.h = (int)((u - before) / rw.tiles);
-    g.item0 = before + (int64_t)g.h * rw.tiles;
-    g.ta = (int)(u - g.item0);
-    g.tb = (int)min((int64_t)rw.tiles, u1 - g.item0);
-    g.tiles = rw.tiles;
-    g.lo = rw.lo;
-    g.first = rw.base + g.ta * kTile;
-    g.end = min(rw.hi, rw.base + g.tb * kTile);
-    u = g.item0 + g.tb;
-    return true;
+    return false;
   }
 };
 
@@ -152,65 +158,56 @@ struct Cfg {
 __device__ __forceinline__ int swizzle(int r, int c) { return c ^ (((r >> 1) & 3) << 1) ^ ((r & 1) << 2); }
 
 // Parts of an item, in the order of its tiles: part i stands in slot 1 of block b0 (i = 0) or
-// in slot 0 of block b0 + i.  Joins parts i0, i0 + step, ... (n of them) and writes the
-// output, or a joined part in the place of the first one.
+// in slot 0 of block b0 + i.  Joins parts i0, i0 + step, ... (n of them, at most kJoinGroup
+// unless `step` is above 1) and writes the output, or a joined part in the place of the
+// first one.
 constexpr int kJoinGroup = 16;
 template <class El, int HD>
 __device__ void join_parts(const PagedAttn& p, int b0, int i0, int step, int n, int s, int h, bool final,
-                           float (*s_ml)[2], float4* s_x) {
+                           float* s_m, float* s_l) {
   const int part_len = part_floats(p.group, HD);
-  const int cols = p.group * HD / 4, rows = kThreadsA / cols;  // float4 columns; parts taken at a time
-  const int c = threadIdx.x % cols, r = threadIdx.x / cols, hd = 4 * c / HD;
   auto part = [&](int k) -> float* {
     const int i = i0 + k * step;
     return p.part + (size_t)(2 * (b0 + i) + (i == 0 ? 1 : 0)) * part_len;
   };
-  float m = -INFINITY, l = 0.f;
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = r; k0 < n; k0 += 4 * rows) {
-    float mq[4], lq[4];
-    float4 v[4];
+  for (int c = threadIdx.x; c < p.group * HD / 4; c += kThreadsA) {  // float4 columns
+    const int hd = 4 * c / HD;
+    float m = -INFINITY, l = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < n; k0 += 8) {
+      float mq[8], lq[8];
+      float4 v[8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int k = k0 + q * rows;
-      mq[q] = -INFINITY;
-      lq[q] = 0.f;
-      v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (k < n) {
-        const float* const a = part(k);
-        mq[q] = __ldcg(a + hd);
-        lq[q] = __ldcg(a + kHeads + hd);
-        v[q] = __ldcg(reinterpret_cast<const float4*>(a + 2 * kHeads) + c);
+      for (int q = 0; q < 8; ++q) {
+        mq[q] = -INFINITY;
+        lq[q] = 0.f;
+        v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k0 + q < n) {
+          const float* const a = part(k0 + q);
+          mq[q] = __ldcg(a + hd);
+          lq[q] = __ldcg(a + kHeads + hd);
+          v[q] = __ldcg(reinterpret_cast<const float4*>(a + 2 * kHeads) + c);
+        }
       }
-    }
+      float mn = m;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float mn = fmaxf(m, mq[q]), ref = mn == -INFINITY ? 0.f : mn;
-      const float fa = exp2_fast(m - ref), fb = exp2_fast(mq[q] - ref);
-      l = l * fa + lq[q] * fb;
-      x.x = x.x * fa + v[q].x * fb;
-      x.y = x.y * fa + v[q].y * fb;
-      x.z = x.z * fa + v[q].z * fb;
-      x.w = x.w * fa + v[q].w * fb;
-      m = mn;
-    }
-  }
-  __syncthreads();
-  s_ml[threadIdx.x][0] = m;
-  s_ml[threadIdx.x][1] = l;
-  s_x[threadIdx.x] = x;
-  __syncthreads();
-  if (r == 0) {
-    for (int k = 1; k < rows; ++k) {
-      const int o = k * cols + c;
-      const float mq = s_ml[o][0], mn = fmaxf(m, mq), ref = mn == -INFINITY ? 0.f : mn;
-      const float fa = exp2_fast(m - ref), fb = exp2_fast(mq - ref);
-      const float4 v = s_x[o];
-      l = l * fa + s_ml[o][1] * fb;
-      x.x = x.x * fa + v.x * fb;
-      x.y = x.y * fa + v.y * fb;
-      x.z = x.z * fa + v.z * fb;
-      x.w = x.w * fa + v.w * fb;
+      for (int q = 0; q < 8; ++q) mn = fmaxf(mn, mq[q]);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      const float fa = exp2_fast(m - ref);
+      l *= fa;
+      x.x *= fa;
+      x.y *= fa;
+      x.z *= fa;
+      x.w *= fa;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float f = exp2_fast(mq[q] - ref);
+        l += lq[q] * f;
+        x.x += v[q].x * f;
+        x.y += v[q].y * f;
+        x.z += v[q].z * f;
+        x.w += v[q].w * f;
+      }
       m = mn;
     }
     if (final) {
@@ -220,12 +217,18 @@ __device__ void join_parts(const PagedAttn& p, int b0, int i0, int step, int n, 
       o.y = El::pack(x.z * inv, x.w * inv);
       *reinterpret_cast<uint2*>(p.out + s * p.out_seq + (h * p.group + hd) * p.out_head + 4 * c % HD) = o;
     } else {
-      float* const a = part(0);
-      reinterpret_cast<float4*>(a + 2 * kHeads)[c] = x;
+      reinterpret_cast<float4*>(part(0) + 2 * kHeads)[c] = x;
       if (4 * c % HD == 0) {
-        a[hd] = m;
-        a[kHeads + hd] = l;
+        s_m[hd] = m;
+        s_l[hd] = l;
       }
+    }
+  }
+  if (!final) {
+    __syncthreads();  // every column has read the first part's maxima and sums
+    if ((int)threadIdx.x < p.group) {
+      part(0)[threadIdx.x] = s_m[threadIdx.x];
+      part(0)[kHeads + threadIdx.x] = s_l[threadIdx.x];
     }
   }
 }
@@ -247,7 +250,7 @@ __device__ bool arrive_last(uint32_t* counter, int n, int* s_flag) {
 }
 
 template <class El, int HD>
-__global__ void __launch_bounds__(kThreadsA, 1) paged_attn_kernel(const PagedAttn p) {
+__global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(const PagedAttn p) {
   using C = Cfg<HD>;
   constexpr int KB = HD / 32;  // 32-element blocks of a K row
   constexpr int VB = HD / 64;  // 64-element blocks of a V row
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attn_kernel(const PagedAtt
   constexpr int kSub = C::kChunk / 16;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int64_t s_sum[kWarps];
-  __shared__ int64_t s_find[2];  // first sequence of the block's run, tiles before it
+  __shared__ int64_t s_find[2];  // first sequence of the block's run, units before it
   __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
   __shared__ int s_flag;
   float (*const s_o)[kHeads][C::kOutStride] =
@@ -266,11 +269,11 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attn_kernel(const PagedAtt
   const int part_len = part_floats(p.group, HD);
   const uint32_t ring = smem_u32(smem) + wid * C::kStages * C::kStageBytes;
 
-  // the batch's tiles and where this block's run begins; one scan when one round of the
+  // the batch's units and where this block's run begins; one scan when one round of the
   // block's threads covers the sequences
-  int64_t total = 0, mine = 0, upto = 0;  // this thread's sequence's tiles, and with those in front (last round)
+  int64_t total = 0, mine = 0, upto = 0;  // this thread's sequence's units, and with those in front (last round)
   for (int c = 0; c < p.n_seqs; c += kThreadsA) {
-    mine = c + tid < p.n_seqs ? (int64_t)seq_rows(p, c + tid).tiles * p.n_kv_heads : 0;
+    mine = c + tid < p.n_seqs ? (int64_t)seq_rows(p, c + tid).units * p.n_kv_heads : 0;
     int64_t v = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -287,7 +290,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attn_kernel(const PagedAtt
     }
     __syncthreads();
   }
-  // (no more blocks than tiles, so that the parts of an item lie in consecutive blocks)
+  // (no more blocks than units, so that the parts of an item lie in consecutive blocks)
   const int64_t busy = min((int64_t)G, total);
   const int64_t u0 = b < busy ? total * b / busy : 0, u1 = b < busy ? total * (b + 1) / busy : 0;
   // sequences without rows: zeros, shared out over the blocks
@@ -304,7 +307,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attn_kernel(const PagedAtt
   } else {
     int64_t run = 0;
     for (int c = 0; run <= u0; c += kThreadsA) {
-      const int64_t x = c + tid < p.n_seqs ? (int64_t)seq_rows(p, c + tid).tiles * p.n_kv_heads : 0;
+      const int64_t x = c + tid < p.n_seqs ? (int64_t)seq_rows(p, c + tid).units * p.n_kv_heads : 0;
       int64_t v = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -555,18 +558,17 @@ __global__ void __launch_bounds__(kThreadsA, 1) paged_attn_kernel(const PagedAtt
     if (!whole) {
       // the blocks that hold the item's first and last tile; the last one to arrive joins the
       // parts, groups of kJoinGroup first when there are more
-      const int b0 = (int)(((done.item0 + 1) * busy - 1) / total);
-      const int n = (int)(((done.item0 + done.tiles) * busy - 1) / total) - b0 + 1;
+      const int b0 = (int)(((done.unit0 + 1) * busy - 1) / total);
+      const int n = (int)(((done.unit0 + done.tiles) * busy - 1) / total) - b0 + 1;
       const int k = (b - b0) / kJoinGroup, groups = (n + kJoinGroup - 1) / kJoinGroup;
-      float4* const s_x = reinterpret_cast<float4*>(s_o);  // (the warps' results are used up)
-      float (*const s_ml)[2] = reinterpret_cast<float (*)[2]>(s_x + kThreadsA);
+      const int in_group = min(kJoinGroup, n - k * kJoinGroup);
       // (counters: one of the item that a block begins, one for the groups of that item, one of the
       // group whose first part is the block's slot 0)
-      if (arrive_last(p.counters + (k == 0 ? b0 : 2 * G + b0 + k * kJoinGroup), min(kJoinGroup, n - k * kJoinGroup), &s_flag)) {
-        join_parts<El, HD>(p, b0, k * kJoinGroup, 1, min(kJoinGroup, n - k * kJoinGroup), done.s, done.h, groups == 1,
-                           s_ml, s_x);
+      if (arrive_last(p.counters + (k == 0 ? b0 : 2 * G + b0 + k * kJoinGroup), in_group, &s_flag)) {
+        join_parts<El, HD>(p, b0, k * kJoinGroup, 1, in_group, done.s, done.h, groups == 1,
+                           s_m[0], s_l[0]);
         if (groups > 1 && arrive_last(p.counters + G + b0, groups, &s_flag))
-          join_parts<El, HD>(p, b0, 0, kJoinGroup, groups, done.s, done.h, true, s_ml, s_x);
+          join_parts<El, HD>(p, b0, 0, kJoinGroup, groups, done.s, done.h, true, s_m[0], s_l[0]);
       }
     }
     __syncthreads();

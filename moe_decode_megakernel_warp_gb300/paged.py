@@ -181,6 +181,7 @@ def prompt_attention(q, k, v, q_starts, k_starts=None, window=0, scale=None, out
     head_dim] is read in place), q_starts and k_starts int32 [n_seqs + 1] on the device
     (k_starts defaults to q_starts), scale defaults to 1 / sqrt(head_dim).  Returns out; a new
     one is uninitialised behind the last sequence."""
+    torch = _torch()
     _need(q.is_cuda, "q must be a CUDA tensor")
     _need(q.dim() == 3 and k.dim() == 3, "q and k must be [tokens, heads, head_dim]")
     n_q, heads, hd = shape = q.shape
@@ -190,7 +191,7 @@ def prompt_attention(q, k, v, q_starts, k_starts=None, window=0, scale=None, out
     kt, kh = _rows(k, "k", k_shape, dtype, i)
     vt, vh = _rows(v, "v", k_shape, dtype, i)
     if out is None:
-        out = q.new_empty(shape)
+        out = torch.empty(shape, dtype=dtype, device=q.device)
     ot, oh = _rows(out, "out", shape, dtype, i)
     n_seqs = q_starts.numel() - 1
     qs = _int32(q_starts, "q_starts", n_seqs + 1, i)
