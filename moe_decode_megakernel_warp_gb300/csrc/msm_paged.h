@@ -78,9 +78,10 @@ struct PromptAttn {
   int64_t q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;  // strides in elements
   const int32_t *q_starts, *k_starts;
   int n_seqs, n_q, n_k, n_kv_heads, group, window;
+  int out_32;        // every row of out starts on a 32-byte boundary
   float scale_log2;  // softmax scale x log2(e)
 };
-cudaError_t launch_prompt_attn(const PromptAttn& p, int dtype, int head_dim, cudaStream_t s);
+cudaError_t launch_prompt_attn(const PromptAttn& p, int dtype, int head_dim, int sms, cudaStream_t s);
 
 cudaError_t launch_pages_resize(const PagesMeta& p, cudaStream_t s);
 cudaError_t launch_pages_fork(const PagesMeta& p, cudaStream_t s);

@@ -342,6 +342,7 @@ msm_status msm_prompt_attention(const msm_prompt* a, void* stream) {
   p.v_head = a->v_head_stride;
   p.out_token = a->out_token_stride;
   p.out_head = a->out_head_stride;
+  p.out_32 = !misaligned(a->out, 32) && a->out_token_stride % 16 == 0 && a->out_head_stride % 16 == 0;
   p.q_starts = a->q_starts;
   p.k_starts = a->k_starts;
   p.n_seqs = a->n_seqs;
@@ -351,7 +352,7 @@ msm_status msm_prompt_attention(const msm_prompt* a, void* stream) {
   p.group = a->n_q_heads / a->n_kv_heads;
   p.window = a->window;
   p.scale_log2 = a->scale * kLog2e;
-  CKP(launch_prompt_attn(p, a->dtype, a->head_dim, static_cast<cudaStream_t>(stream)));
+  CKP(launch_prompt_attn(p, a->dtype, a->head_dim, sms, static_cast<cudaStream_t>(stream)));
   return MSM_OK;
 }
 

@@ -9,21 +9,23 @@
 //   S, P and O in tensor memory.  While one tile's softmax runs, the tensor cores work on
 //   the other's: P0 V, Q0 K(next), P1 V, Q1 K(next), ...
 //   A softmax thread owns a row (128 scores in registers), so its maximum and sum need no
-//   exchange.  P takes the place of S (16-bit, half its columns).  O is only rescaled when a
-//   row's maximum has grown by more than 2^8 since the last time (P stays below 2^8, well
-//   inside fp16); S(j + 1) being there means that P(j) V is done, the products of a block being issued
+//   exchange.  P takes the place of S (16-bit, half its columns).  P is computed with the
+//   maximum that the row had before the tile; only when the tile's own is larger by more than
+//   a factor 2^8 (P stays below 2^8, well inside fp16) O is rescaled and P computed again.
+//   S(j + 1) being there means that P(j) V is done, the products of a block being issued
 //   and completed in order, so the thread may then change O itself.
-// Warps 0-7: softmax; 8: product issue; 9: TMA loads; 10, 11: finite check of V.
+// Warps 0-7: softmax; 8, 10: products of a tile each; 9: TMA loads; 11: finite check of V.
 //
 // A weight of zero does not stop an infinite or NaN element of V (0 x inf = NaN), and a
-// masked score has such a weight.  In key tiles that some row sees only in part, warps 10 and
-// 11 therefore take these elements out before the product; the rows that do see their keys
+// masked score has such a weight.  In key tiles that some row sees only in part, warp 11
+// therefore takes these elements out before the product; the rows that do see their keys
 // get them back at the end.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "msm_device.cuh"
@@ -79,6 +81,18 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// 32 bytes at once: the threads of a warp write different rows, so a store's cost is its number of
+// separate sectors (32 bytes each)
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 // two fp32 operations in one instruction
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
   uint64_t r;
@@ -99,9 +113,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Waits for a phase of a barrier, at most kWaitNs: false (and `dead` set, which ends the other
-// warps' waits) when it did not come.
-__device__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* dead) {
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* dead) {
   uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -116,6 +128,15 @@ __device__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* dead) {
     }
   }
 }
+
+// Waits for a phase of a barrier, at most kWaitNs: false (and `dead` set, which ends the other
+// warps' waits) when it did not come.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* dead) {
+  return mbar_try_wait(bar, parity) || wait_long(bar, parity, dead);
+}
+
+// bits 0 .. n
+__device__ __forceinline__ uint32_t bits_upto(int n) { return n < 0 ? 0u : n >= 31 ? 0xFFFFFFFFu : (2u << n) - 1u; }
 
 template <int kCount>
 __device__ __forceinline__ void set_max_regs_up() {
@@ -165,12 +186,11 @@ __device__ bool find_tile(const PromptAttn& p, int t, int& seq, int& tile) {
   return false;
 }
 
-// the block's work
+// 256 rows of one kv head
 struct Work {
-  int q0, nq, k0, shift, window;
+  int h, q0, nq, k0, shift, window;
   int row0, tok0, tok1;  // first row, its token, one past the last token
-  int hi;                // one past the last key that any row sees
-  int t_lo, n;           // first key tile, their number
+  int t_lo, n;           // first key tile, their number (0: no row sees a key)
   bool two;              // the second tile has rows
   __device__ int tile(int j) const { return t_lo + n - 1 - j; }
   // does some row see only a part of tile j?
@@ -179,50 +199,73 @@ struct Work {
     return a + kKeys - 1 > tok0 + shift || (window > 0 && a < tok1 + shift - window);
   }
 };
+__device__ bool find_work(const PromptAttn& p, int idx, Work& w) {
+  int seq, tile;
+  w.h = idx % p.n_kv_heads;
+  if (!find_tile(p, idx / p.n_kv_heads, seq, tile)) return false;
+  const Seq sq = prompt_seq(p, seq);
+  w.q0 = sq.q0;
+  w.nq = sq.nq;
+  w.k0 = sq.k0;
+  w.shift = sq.nk - sq.nq;
+  w.window = p.window;
+  w.row0 = tile * kBlockRows;
+  w.tok0 = w.row0 / p.group;
+  w.tok1 = min(sq.nq, w.tok0 + kBlockRows / p.group);
+  const int hi = max(0, w.tok1 + w.shift), lo = p.window > 0 ? max(0, w.tok0 + w.shift - p.window + 1) : 0;
+  w.t_lo = lo / kKeys;
+  w.n = hi > 0 ? (hi + kKeys - 1) / kKeys - w.t_lo : 0;
+  w.two = w.row0 + kRows < sq.nq * p.group;
+  return true;
+}
+
+// A block's pieces of work: one of every round of gridDim.x, the rounds alternately from the front
+// and from the back.  (The work is listed from the longest to the shortest of a sequence: the
+// block that got the longest piece of a round gets the shortest of the next.)
+struct Rounds {
+  int round = 0;
+  __device__ __forceinline__ bool next(const PromptAttn& p, int n_work, Work& w) {
+    const int64_t base = (int64_t)round * gridDim.x;
+    const int64_t idx = base + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    ++round;
+    return idx < n_work && find_work(p, (int)idx, w);
+  }
+};
+
+// The ring of K and V tiles, in the order K(0), V(0), K(1), V(1), ... of one piece of work
+// after the other, as one of its readers walks it.  Every reader waits for every tile and
+// signs it off, so that none can fall or run a turn of the ring behind or ahead (a barrier only tells
+// neighbouring phases apart).
+template <int kStages>
+struct Ring {
+  int st = 0;
+  uint32_t phase = 0;
+  // waits for the next tile and returns its stage, -1 when it did not come
+  __device__ __forceinline__ int next(uint64_t* full, volatile int* dead) {
+    const int now = st;
+    if (!wait_bar(&full[now], phase, dead)) return -1;
+    if (++st == kStages) {
+      st = 0;
+      phase ^= 1;
+    }
+    return now;
+  }
+};
 
 template <class El, int HD>
 __global__ void __launch_bounds__(kPromptThreads, 1)
-    prompt_kernel(const __grid_constant__ Maps maps, const PromptAttn p) {
+    prompt_kernel(const __grid_constant__ Maps maps, const PromptAttn p, const int n_work) {
   using C = Cfg<HD>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t b_q[2], b_full[C::kStages], b_empty[C::kStages], b_clean[C::kStages], b_s[2], b_p[2],
-      b_o[2], b_drain;
+      b_o[2], b_turn[2], b_drain[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_dead, s_taken;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  int seq, tile;
-  const int h = blockIdx.x % p.n_kv_heads;
-  if (!find_tile(p, blockIdx.x / p.n_kv_heads, seq, tile)) return;
-  Work w;
-  {
-    const Seq sq = prompt_seq(p, seq);
-    w.q0 = sq.q0;
-    w.nq = sq.nq;
-    w.k0 = sq.k0;
-    w.shift = sq.nk - sq.nq;
-    w.window = p.window;
-    w.row0 = tile * kBlockRows;
-    w.tok0 = w.row0 / p.group;
-    w.tok1 = min(sq.nq, w.tok0 + kBlockRows / p.group);
-    w.hi = max(0, w.tok1 + w.shift);
-    const int lo = p.window > 0 ? max(0, w.tok0 + w.shift - p.window + 1) : 0;
-    w.t_lo = lo / kKeys;
-    w.n = w.hi > 0 ? (w.hi + kKeys - 1) / kKeys - w.t_lo : 0;
-    w.two = w.row0 + kRows < sq.nq * p.group;
-  }
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const s_q = smem;
   uint8_t* const s_kv = smem + 2 * C::kTileBytes;
 
-  if (w.n == 0) {  // no row sees a key
-    for (int r = wid; r < kBlockRows; r += kPromptThreads / 32) {
-      const int tok = (w.row0 + r) / p.group;
-      if (tok >= w.nq) break;
-      uint16_t* const dst = p.out + (int64_t)(w.q0 + tok) * p.out_token + (h * p.group + r % p.group) * p.out_head;
-      if (lane < HD / 8) reinterpret_cast<uint4*>(dst)[lane] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    return;
-  }
   if (wid == 8) tmem_alloc(&s_tmem, 512);
   if (tid == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -230,164 +273,231 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&b_s[t], 1);
       mbar_init(&b_p[t], 4);
       mbar_init(&b_o[t], 1);
+      mbar_init(&b_turn[t], 1);
+      mbar_init(&b_drain[t], 1);
     }
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&b_full[i], 1);
-      mbar_init(&b_empty[i], 1);
-      mbar_init(&b_clean[i], 2);
+      mbar_init(&b_empty[i], 3);  // the readers: warps 8, 10 and 11
+      mbar_init(&b_clean[i], 1);
     }
-    mbar_init(&b_drain, 1);
     s_dead = s_taken = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_shared();
+  }
+  if (tid >= kPromptThreads - 3) {
+    const int m = kPromptThreads - 1 - tid;
+    prefetch_tensormap(m == 0 ? &maps.q : m == 1 ? &maps.k : &maps.v);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const uint32_t t_s[2] = {tmem, tmem + 128}, t_o[2] = {tmem + 256, tmem + 256 + HD};
+  // tensor memory: S (and P) of the two tiles, then O
+  auto t_s = [&](int t) { return tmem + t * 128; };
+  auto t_o = [&](int t) { return tmem + 256 + t * HD; };
   volatile int* const dead = &s_dead;
+  Work w;
 
   if (wid >= 8) {
     set_max_regs_down<kOtherRegs>();
     if (wid == 9) {
-      // ---- loads: Q0, K(0), Q1, then V(j), K(j + 1), ... through the ring
-      if (lane == 0) {
-        int issued = 0;
-        auto load_q = [&](int t) {
-          mbar_expect_tx(&b_q[t], C::kTileBytes);
-          for (int x = 0; x < C::kBoxes; ++x)
-            tma_load_4d(s_q + t * C::kTileBytes + x * kBoxBytes, &maps.q, x * 64, 0, h,
-                        w.q0 + w.tok0 + t * (kRows / p.group), &b_q[t]);
-        };
-        load_q(0);
-        for (int i = 0; i < 2 * w.n; ++i) {
-          const int st = i % C::kStages;
-          if (i >= C::kStages && !wait_bar(&b_empty[st], (i / C::kStages + 1) & 1, dead)) break;
-          mbar_expect_tx(&b_full[st], C::kTileBytes);
-          const CUtensorMap* const map = i & 1 ? &maps.v : &maps.k;
-          for (int x = 0; x < C::kBoxes; ++x)
-            tma_load_3d(s_kv + st * C::kTileBytes + x * kBoxBytes, map, x * 64, h, w.k0 + w.tile(i >> 1) * kKeys,
-                        &b_full[st]);
-          issued = i + 1;
-          if (i == 0 && w.two) load_q(1);
+      // ---- loads
+      int i = 0, q_loads[2] = {0, 0};
+      bool ok = true;
+      auto load_q = [&](int t) {  // once the work before is through with the place
+        if (q_loads[t] > 0 && !wait_bar(&b_o[t], (q_loads[t] - 1) & 1, dead)) return false;
+        ++q_loads[t];
+        mbar_expect_tx(&b_q[t], C::kTileBytes);
+        for (int x = 0; x < C::kBoxes; ++x)
+          tma_load_4d(s_q + t * C::kTileBytes + x * kBoxBytes, &maps.q, x * 64, 0, w.h,
+                      w.q0 + w.tok0 + t * (kRows / p.group), &b_q[t]);
+        return true;
+      };
+      for (Rounds todo; ok && todo.next(p, n_work, w);) {
+        if (lane == 0) {
+          for (int e = 0; ok && e < 2 * w.n; ++e) {
+            const int st = i % C::kStages;
+            // the tile that the stage held, i - kStages, is used up; if it was a V, with the K
+            // behind it.  (With an odd number of stages a stage holds a K every other time.)
+            const int before = i - C::kStages, sig = before + (before & 1);
+            constexpr int kTurn = C::kStages % 2 ? 2 * C::kStages : C::kStages;
+            if (before >= 0 && !(ok = wait_bar(&b_empty[sig % C::kStages], (sig / kTurn) & 1, dead))) break;
+            mbar_expect_tx(&b_full[st], C::kTileBytes);
+            const CUtensorMap* const map = e & 1 ? &maps.v : &maps.k;
+            for (int x = 0; x < C::kBoxes; ++x)
+              tma_load_3d(s_kv + st * C::kTileBytes + x * kBoxBytes, map, x * 64, w.h, w.k0 + w.tile(e >> 1) * kKeys,
+                          &b_full[st]);
+            ++i;
+            if (e == 0) ok = load_q(0) && (!w.two || load_q(1));
+          }
         }
-        if (*dead) {  // nothing of this block may be on its way when it ends
-          int never = 0;
-          wait_bar(&b_q[0], 0, &never);
-          if (w.two) wait_bar(&b_q[1], 0, &never);
-          for (int i = max(0, issued - C::kStages); i < issued; ++i)
-            wait_bar(&b_full[i % C::kStages], (i / C::kStages) & 1, &never);
-        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
       }
-    } else if (wid == 8) {
-      // ---- products
-      if (lane == 0) {
-        const uint32_t i_s = idesc_f16(El::kBf16, p.scale_log2 < 0.f, false, kKeys);
-        const uint32_t i_o = idesc_f16(El::kBf16, false, true, HD);
-        auto full = [&](int i) { return wait_bar(&b_full[i % C::kStages], (i / C::kStages) & 1, dead); };
-        auto scores = [&](int t, int i) {  // S = Q K^T
-          const uint32_t a = smem_u32(s_q + t * C::kTileBytes), b = smem_u32(s_kv + (i % C::kStages) * C::kTileBytes);
+      if (lane == 0 && *dead) {  // nothing of this block may be on its way when it ends
+        int never = 0;
+        for (int t = 0; t < 2; ++t)
+          if (q_loads[t] > 0) wait_bar(&b_q[t], (q_loads[t] - 1) & 1, &never);
+        for (int k = max(0, i - C::kStages); k < i; ++k)
+          wait_bar(&b_full[k % C::kStages], (k / C::kStages) & 1, &never);
+      }
+    } else if (wid == 8 || wid == 10) {
+      // ---- products of one tile.  A round of waits and commits takes its thread some 600 cycles
+      // beside the 1,024 of its products; with one thread for both tiles the tensor cores
+      // idled meanwhile (3,400 cycles a step, 2,048 of them products).  The two threads take
+      // turns: left to themselves both tiles fall into step, their products and then their
+      // softmaxes at the same time.
+      const int t = wid == 8 ? 0 : 1;
+      const uint32_t i_s = idesc_f16(El::kBf16, p.scale_log2 < 0.f, false, kKeys);
+      const uint32_t i_o = idesc_f16(El::kBf16, false, true, HD);
+      const uint64_t d_q = sdesc_k_sw128(smem_u32(s_q)), d_k = sdesc_k_sw128(smem_u32(s_kv)),
+                     d_v = sdesc_mn_sw128(smem_u32(s_kv), kBoxBytes);
+      constexpr uint32_t kTile16 = C::kTileBytes >> 4;  // (descriptors count 16 bytes)
+      constexpr int kTurnAt = HD / 16 - 1;
+      const uint32_t ts = t_s(t), to = t_o(t);
+      auto scores = [&](int st, bool turn) {  // S = Q K^T
+        const uint64_t a = d_q + (uint32_t)t * kTile16, b = d_k + (uint32_t)st * kTile16;
 #pragma unroll
-          for (int k = 0; k < HD / 16; ++k) {
-            const uint32_t off = (k / 4) * kBoxBytes + (k % 4) * 32;
-            mma_f16_ss(t_s[t], sdesc_k_sw128(a + off), sdesc_k_sw128(b + off), i_s, k > 0);
-          }
-          tc_commit(&b_s[t]);
-        };
-        auto values = [&](int t, int i, bool first) {  // O += P V
-          const uint32_t b = smem_u32(s_kv + (i % C::kStages) * C::kTileBytes);
-#pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            mma_f16_ts(t_o[t], t_s[t] + k * 8, sdesc_mn_sw128(b + k * 2048, kBoxBytes), i_o, !first || k > 0);
-        };
-        uint32_t clean_phase = 0;
-        bool ok = wait_bar(&b_q[0], 0, dead) && full(0);
-        if (ok) {
-          tc_fence_after();
-          scores(0, 0);
-          if (w.two) {
-            ok = wait_bar(&b_q[1], 0, dead);
-            if (ok) scores(1, 0);
-          }
-          tc_commit(&b_empty[0]);
+        for (int k = 0; k < HD / 16; ++k) {
+          const uint32_t off = ((k / 4) * kBoxBytes + (k % 4) * 32) >> 4;
+          // (the other thread needs some 150 cycles to notice; much earlier and its products delay
+          // these: 1,388 us for 16,384 tokens here, 1,427 behind the last one, 1,438 halfway)
+          if (k == kTurnAt && turn) mbar_arrive(&b_turn[1 - t], 1);
+          mma_f16_ss(ts, a + off, b + off, i_s, k > 0);
         }
-        for (int j = 0; ok && j < w.n; ++j) {
-          const int iv = 2 * j + 1, ik = 2 * j + 2, st = iv % C::kStages;
-          ok = full(iv);
-          if (ok && w.partial(j)) {
-            ok = wait_bar(&b_clean[st], clean_phase >> st & 1, dead);
-            clean_phase ^= 1u << st;
-          }
-          if (!ok) break;
-          for (int t = 0; t < (w.two ? 2 : 1); ++t) {
-            if (!(ok = wait_bar(&b_p[t], j & 1, dead))) break;
+        tc_commit(&b_s[t]);
+      };
+      auto values = [&](int st, bool first) {  // O += P V
+        const uint64_t b = d_v + (uint32_t)st * kTile16;
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k) mma_f16_ts(to, ts + k * 8, b + (k * 2048 >> 4), i_o, !first || k > 0);
+      };
+      Ring<C::kStages> ring;
+      uint32_t clean_phase = 0;
+      int steps = 0, loads = 0, turns = 0;  // of this tile's P and Q, and of the two threads, so far
+      bool ok = true;
+      for (Rounds todo; ok && todo.next(p, n_work, w);) {
+        if (lane == 0 && w.n > 0) {
+          const bool mine = t == 0 || w.two;  // without a second tile its thread only signs the ring
+          int k_st = ring.next(b_full, dead);
+          ok = k_st >= 0 && (!mine || wait_bar(&b_q[t], loads++ & 1, dead));
+          if (ok && mine) {
             tc_fence_after();
-            values(t, iv, j == 0);
-            if (j + 1 < w.n) {
-              if (t == 0 && !(ok = full(ik))) break;
-              scores(t, ik);
+            scores(k_st, false);
+            tc_commit(&b_empty[k_st]);
+          } else if (ok) {
+            mbar_arrive(&b_empty[k_st], 1);
+          }
+          for (int j = 0; ok && j < w.n; ++j) {
+            const bool more = j + 1 < w.n;
+            const int v_st = ring.next(b_full, dead);
+            ok = v_st >= 0;
+            if (!ok) break;
+            if (w.partial(j)) {
+              if (mine && !(ok = wait_bar(&b_clean[v_st], clean_phase >> v_st & 1, dead))) break;
+              clean_phase ^= 1u << v_st;
+            }
+            if (more && !(ok = (k_st = ring.next(b_full, dead)) >= 0)) break;
+            if (!mine) {
+              if (more) mbar_arrive(&b_empty[k_st], 1);
+              continue;
+            }
+            if (!(ok = wait_bar(&b_p[t], steps++ & 1, dead))) break;
+            if (w.two) {
+              if ((t == 1 || turns > 0) && !(ok = wait_bar(&b_turn[t], (t == 1 ? turns : turns - 1) & 1, dead))) break;
+              ++turns;
+            }
+            tc_fence_after();
+            values(v_st, j == 0);
+            if (more) {
+              scores(k_st, w.two);
+              // V(j) and K(j + 1) are used up together: one signal, on K's stage.  (The last V's comes
+              // with the next work's first K.)
+              tc_commit(&b_empty[k_st]);
             } else {
+              if (w.two) mbar_arrive(&b_turn[1 - t], 1);
               tc_commit(&b_o[t]);
             }
           }
-          tc_commit(&b_empty[st]);
-          if (j + 1 < w.n) tc_commit(&b_empty[ik % C::kStages]);
         }
-        if (*dead) {  // nor any product
-          int never = 0;
-          tc_commit(&b_drain);
-          wait_bar(&b_drain, 0, &never);
-        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
       }
-    } else {
+      if (lane == 0 && *dead) {  // no product may be under way when the block ends
+        int never = 0;
+        tc_commit(&b_drain[t]);
+        wait_bar(&b_drain[t], 0, &never);
+      }
+    } else if (wid == 11) {
       // ---- finite check of the V tiles that some row sees in part
       constexpr uint32_t kE = El::kExponent, kLow = kE & (~kE + 1u);  // exponent field, its lowest bit
-      for (int j = 0; j < w.n; ++j) {
-        if (!w.partial(j)) continue;
-        const int i = 2 * j + 1, st = i % C::kStages;
-        if (!__all_sync(0xffffffffu, wait_bar(&b_full[st], (i / C::kStages) & 1, dead))) break;
-        uint4* const v = reinterpret_cast<uint4*>(s_kv + st * C::kTileBytes);
-        bool any = false;
-#pragma unroll 4
-        for (int c = (wid - 10) * 32 + lane; c < C::kTileBytes / 16; c += 64) {
-          const uint4 x = v[c];
-          // an exponent of all ones carries into the sign's place
-          const uint32_t m = kE * 0x10001u, a = kLow * 0x10001u;
-          const uint32_t bad = (((x.x & m) + a) | ((x.y & m) + a) | ((x.z & m) + a) | ((x.w & m) + a)) & 0x80008000u;
-          if (bad) {
-            any = true;
-            uint16_t* const e = reinterpret_cast<uint16_t*>(v + c);
-            for (int q = 0; q < 8; ++q)
-              if ((e[q] & kE) == kE) e[q] = 0;
+      Ring<C::kStages> ring;
+      bool ok = true;
+      for (Rounds todo; ok && todo.next(p, n_work, w);) {
+        for (int e = 0; e < 2 * w.n; ++e) {
+          const int st = ring.next(b_full, dead);
+          if (!(ok = __all_sync(0xffffffffu, st >= 0))) break;
+          if (e % 2 == 0) {
+            if (lane == 0) mbar_arrive(&b_empty[st], 1);
+            continue;
           }
+          if (!w.partial(e >> 1)) continue;
+          uint4* const v = reinterpret_cast<uint4*>(s_kv + st * C::kTileBytes);
+          bool any = false;
+#pragma unroll 8
+          for (int c = lane; c < C::kTileBytes / 16; c += 32) {
+            const uint4 x = v[c];
+            // an exponent of all ones carries into the sign's place
+            const uint32_t m = kE * 0x10001u, a = kLow * 0x10001u;
+            const uint32_t bad = (((x.x & m) + a) | ((x.y & m) + a) | ((x.z & m) + a) | ((x.w & m) + a)) & 0x80008000u;
+            if (bad) {
+              any = true;
+              uint16_t* const el = reinterpret_cast<uint16_t*>(v + c);
+              for (int q = 0; q < 8; ++q)
+                if ((el[q] & kE) == kE) el[q] = 0;
+            }
+          }
+          if (any) {
+            s_taken = 1;  // (for all of the block's further work: its rows then look for themselves)
+            fence_proxy_async_shared();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b_clean[st], 1);
         }
-        if (any) {
-          s_taken = 1;
-          fence_proxy_async_shared();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&b_clean[st], 1);
       }
     }
   } else {
     // ---- softmax: thread = row
     set_max_regs_up<kSoftmaxRegs>();
     const int t = wid >> 2;
-    if (t == 0 || w.two) {
+    const uint32_t lanes = (uint32_t)((wid & 3) * 32) << 16;
+    const uint32_t ts = t_s(t) + lanes, to = t_o(t) + lanes;
+    // (a negative scale negates Q in the product; a scale of zero must still leave -inf x scale = -inf)
+    const float scale = fmaxf(fabsf(p.scale_log2), 1e-30f);
+    int steps = 0, works = 0;
+    Rounds todo;
+    Work ahead;
+    for (bool more = todo.next(p, n_work, ahead); more;) {
+      w = ahead;
+      if (w.n > 0 && t == 1 && !w.two) {
+        more = todo.next(p, n_work, ahead);
+        continue;
+      }
       const int row = w.row0 + t * kRows + (wid & 3) * 32 + lane;
-      const int tok = row / p.group, head = h * p.group + row % p.group;
+      const int tok = row / p.group, head = w.h * p.group + row % p.group;
       const int last = tok + w.shift;                                // the last key that the row sees
       const int first = w.window > 0 ? max(0, last - w.window + 1) : 0;  // and the first one
-      const uint32_t lanes = (uint32_t)((wid & 3) * 32) << 16;
-      const uint32_t ts = t_s[t] + lanes, to = t_o[t] + lanes;
-      // (a negative scale negates Q in the product; a scale of zero must still leave -inf x scale = -inf)
-      const float scale = fmaxf(fabsf(p.scale_log2), 1e-30f);
+      uint16_t* const dst = p.out + (int64_t)(w.q0 + tok) * p.out_token + head * p.out_head;
+      if (w.n == 0) {  // no row sees a key
+        if (tok < w.nq)
+          for (int c = 0; c < HD / 8; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0u, 0u, 0u, 0u);
+        more = todo.next(p, n_work, ahead);
+        continue;
+      }
       float m = -INFINITY;
       uint64_t l2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-      bool ok = true;
-      for (int j = 0; j < w.n; ++j) {
-        ok = __all_sync(0xffffffffu, wait_bar(&b_s[t], j & 1, dead));
+      bool ok = !*dead;
+      for (int j = 0; ok && j < w.n; ++j) {
+        ok = __all_sync(0xffffffffu, wait_bar(&b_s[t], steps++ & 1, dead));
         if (!ok) break;
         tc_fence_after();
         uint32_t s[4][32];
@@ -397,69 +507,80 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (w.partial(j)) {
           const int a = first - w.tile(j) * kKeys, b = last - w.tile(j) * kKeys;
 #pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t see = bits_upto(b - c * 32) & ~bits_upto(a - 1 - c * 32);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[c][i] = see >> i & 1 ? s[c][i] : 0xFF800000u;
+          }
+        }
+        // P from the scores with the maximum so far, and the tile's own maximum on the side
+        float mx;
+        uint64_t sum[2];
+        auto weights = [&]() {
+          const float neg = m == -INFINITY ? 0.f : -m * scale;
+          const uint64_t sc2 = pair(scale, scale), neg2 = pair(neg, neg);
+          float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          sum[0] = sum[1] = pair(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float s0 = __uint_as_float(s[c][2 * i]), s1 = __uint_as_float(s[c][2 * i + 1]);
+              float e0, e1;
+              unpair(fma2(pair(s0, s1), sc2, neg2), e0, e1);
+              x[i & 3] = max3(x[i & 3], s0, s1);
+              e0 = exp2_fast(e0);
+              e1 = exp2_fast(e1);
+              sum[i & 1] = add2(sum[i & 1], pair(e0, e1));
+              // rounded to the 16-bit type for the product with V; the sum keeps 32 bits
+              pk[i] = El::pack(e0, e1);
+            }
+            tmem_st16(ts + c * 16, pk);
+          }
+          mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        };
+        if (j == 0) {
+          m = -INFINITY;
+#pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c * 32 + i < a || c * 32 + i > b) s[c][i] = 0xFF800000u;
+            for (int i = 0; i < 32; i += 2) m = max3(m, __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
         }
-        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            x[c] = fmaxf(x[c], fmaxf(__uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1])));
-        const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-        if (j == 0) {
-          m = mx;
-        } else {
-          const bool grow = (mx - m) * scale > kGrow;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float f = grow ? exp2_fast((m - mx) * scale) : 1.f;
-            if (grow) m = mx;
-            const uint64_t ff = pair(f, f);
-            l2[0] = fma2(l2[0], ff, pair(0.f, 0.f));
-            l2[1] = fma2(l2[1], ff, pair(0.f, 0.f));
+        weights();
+        const bool grow = (mx - m) * scale > kGrow;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow ? exp2_fast((m - mx) * scale) : 1.f;
+          if (grow) m = mx;
+          const uint64_t ff = pair(f, f), zero = pair(0.f, 0.f);
+          l2[0] = fma2(l2[0], ff, zero);
+          l2[1] = fma2(l2[1], ff, zero);
 #pragma unroll 1
-            for (int c = 0; c < HD / 16; ++c) {
-              uint32_t o[16];
-              tmem_ld16(to + c * 16, o);
-              tmem_ld_wait();
+          for (int c = 0; c < HD / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(to + c * 16, o);
+            tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st16(to + c * 16, o);
-            }
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(to + c * 16, o);
           }
+          weights();
         }
-        const float neg = m == -INFINITY ? 0.f : -m * scale;
-        const uint64_t sc2 = pair(scale, scale), neg2 = pair(neg, neg);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float e0, e1;
-            unpair(fma2(pair(__uint_as_float(s[c][2 * i]), __uint_as_float(s[c][2 * i + 1])), sc2, neg2), e0, e1);
-            e0 = exp2_fast(e0);
-            e1 = exp2_fast(e1);
-            l2[i & 1] = add2(l2[i & 1], pair(e0, e1));
-            // rounded to the 16-bit type for the product with V; the sum keeps 32 bits
-            pk[i] = El::pack(e0, e1);
-          }
-          tmem_st16(ts + c * 16, pk);
-        }
+        l2[0] = add2(l2[0], sum[0]);
+        l2[1] = add2(l2[1], sum[1]);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b_p[t], 1);
       }
-      ok = ok && __all_sync(0xffffffffu, wait_bar(&b_o[t], 0, dead));
+      more = todo.next(p, n_work, ahead);  // (looked up while the last product runs)
+      ok = ok && __all_sync(0xffffffffu, wait_bar(&b_o[t], works++ & 1, dead));
       tc_fence_after();
       float l0, l1;
       unpair(add2(l2[0], l2[1]), l0, l1);
       // no key seen: zeros; a wait that ran out: NaN
       const float inv = !ok ? NAN : last < 0 ? 0.f : 1.f / (l0 + l1);
       const bool taken = *(volatile int*)&s_taken != 0;
-      uint16_t* const dst = p.out + (int64_t)(w.q0 + tok) * p.out_token + head * p.out_head;
 #pragma unroll 1
       for (int c = 0; c < HD / 32; ++c) {
         uint32_t o[32];
@@ -473,7 +594,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (!w.partial(j)) continue;
             const int a = max(first, w.tile(j) * kKeys), b = min(last, w.tile(j) * kKeys + kKeys - 1);
             for (int key = a; key <= b; ++key) {
-              const uint16_t* const v = p.v + (int64_t)(w.k0 + key) * p.v_token + h * p.v_head + c * 32;
+              const uint16_t* const v = p.v + (int64_t)(w.k0 + key) * p.v_token + w.h * p.v_head + c * 32;
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if ((v[i] & El::kExponent) == El::kExponent) f[i] += El::value(v[i]);
@@ -481,11 +602,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
         }
         if (tok < w.nq) {
+          uint32_t h[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(dst + c * 32 + i) =
-                make_uint4(El::pack(f[i], f[i + 1]), El::pack(f[i + 2], f[i + 3]), El::pack(f[i + 4], f[i + 5]),
-                           El::pack(f[i + 6], f[i + 7]));
+          for (int i = 0; i < 16; ++i) h[i] = El::pack(f[2 * i], f[2 * i + 1]);
+#pragma unroll
+          for (int i = 0; i < 16; i += 8) {
+            uint16_t* const d = dst + c * 32 + 2 * i;
+            if (p.out_32) {
+              st_global_32(d, &h[i]);
+            } else {
+              reinterpret_cast<uint4*>(d)[0] = make_uint4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+              reinterpret_cast<uint4*>(d)[1] = make_uint4(h[i + 4], h[i + 5], h[i + 6], h[i + 7]);
+            }
+          }
         }
       }
     }
@@ -519,10 +648,10 @@ cudaError_t encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
 
 // rows [tokens][heads][HD] as boxes of 64 elements; Q's heads are split into (group, kv head)
 template <class El, int HD>
-cudaError_t launch(const PromptAttn& p, cudaStream_t s) {
+cudaError_t launch(const PromptAttn& p, int sms, cudaStream_t s) {
   const int64_t tiles = ((int64_t)p.n_q * p.group + kBlockRows - 1) / kBlockRows + p.n_seqs;
-  const int64_t blocks = tiles * p.n_kv_heads;
-  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  const int64_t works = tiles * p.n_kv_heads;  // at most
+  if (works > 0x7FFF0000) return cudaErrorInvalidConfiguration;
   PFN_cuTensorMapEncodeTiled_v12000 encode;
   cudaError_t e = encoder(&encode);
   if (e != cudaSuccess) return e;
@@ -560,15 +689,15 @@ cudaError_t launch(const PromptAttn& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  prompt_kernel<El, HD><<<(unsigned)blocks, kPromptThreads, Cfg<HD>::kSmem, s>>>(maps, p);
+  prompt_kernel<El, HD><<<(unsigned)std::min<int64_t>(works, sms), kPromptThreads, Cfg<HD>::kSmem, s>>>(maps, p, (int)works);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_prompt_attn(const PromptAttn& p, int dtype, int head_dim, cudaStream_t s) {
-  if (dtype == MSM_BF16) return head_dim == 64 ? launch<Bf16, 64>(p, s) : launch<Bf16, 128>(p, s);
-  return head_dim == 64 ? launch<Fp16, 64>(p, s) : launch<Fp16, 128>(p, s);
+cudaError_t launch_prompt_attn(const PromptAttn& p, int dtype, int head_dim, int sms, cudaStream_t s) {
+  if (dtype == MSM_BF16) return head_dim == 64 ? launch<Bf16, 64>(p, sms, s) : launch<Bf16, 128>(p, sms, s);
+  return head_dim == 64 ? launch<Fp16, 64>(p, sms, s) : launch<Fp16, 128>(p, sms, s);
 }
 
 }  // namespace msm
