@@ -238,7 +238,7 @@ msm_status msm_paged_attention(const msm_pages* c, int layer, const void* q, int
           "strides must be multiples of 8, not negative and below 2^31");
   REQUIRE(!bad_stride(out_seq_stride, c->head_dim) && !bad_stride(out_head_stride, c->head_dim), MSM_ERR_INVALID_ARG,
           "strides of out must be multiples of 8, at least head_dim and below 2^31");
-  REQUIRE(std::isfinite(scale), MSM_ERR_INVALID_ARG, "scale must be finite");
+  REQUIRE(std::isfinite(scale * kLog2e), MSM_ERR_INVALID_ARG, "scale must be finite");
   REQUIRE(window >= 0, MSM_ERR_INVALID_ARG, "window is negative");
   REQUIRE(workspace && !misaligned(workspace, 16), MSM_ERR_INVALID_ARG, "workspace is NULL or misaligned");
   int sms = 0;
@@ -313,7 +313,7 @@ msm_status msm_prompt_attention(const msm_prompt* a, void* stream) {
   REQUIRE(a->n_q < (1 << 27) && a->n_k < (1 << 27) && a->n_kv_heads < 65536, MSM_ERR_UNSUPPORTED,
           "prompt: more than 2^27 tokens or 65535 kv heads");
   REQUIRE(a->window >= 0, MSM_ERR_INVALID_ARG, "window is negative");
-  REQUIRE(std::isfinite(a->scale), MSM_ERR_INVALID_ARG, "scale must be finite");
+  REQUIRE(std::isfinite(a->scale * kLog2e), MSM_ERR_INVALID_ARG, "scale must be finite");
   if (a->n_q == 0) return MSM_OK;
   REQUIRE(a->q && a->out && a->q_starts && a->k_starts && (a->n_k == 0 || (a->k && a->v)), MSM_ERR_INVALID_ARG,
           "prompt: NULL pointer");

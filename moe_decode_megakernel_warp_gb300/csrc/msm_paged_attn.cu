@@ -110,16 +110,35 @@ struct Segment {
   int64_t unit0;       // the batch's unit that holds the item's first tile
 };
 
-// Walks the segments of a block's run of units [u, u1).  Unit 0 of an item has no tile.
+// Walks the segments of a block's run of units [u, u1) (a whole warp together).  Unit 0 of an item
+// has no tile.
 struct Walk {
   int64_t u, u1, before;  // before: units of the sequences in front of s
   int s;
   __device__ bool next(const PagedAttn& p, Segment& g) {
     while (u < u1) {
       Rows rw = seq_rows(p, s);
-      while (u >= before + (int64_t)rw.units * p.n_kv_heads) {
-        before += (int64_t)rw.units * p.n_kv_heads;
-        rw = seq_rows(p, ++s);
+      if (u >= before + (int64_t)rw.units * p.n_kv_heads) {
+        // the sequence that holds u, 32 at a time (most slots of a batch may be empty)
+        const int lane = threadIdx.x & 31;
+        for (;; s += 32) {
+          const int64_t x = s + lane < p.n_seqs ? (int64_t)seq_rows(p, s + lane).units * p.n_kv_heads : 0;
+          int64_t v = x;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+          }
+          const uint32_t hit = __ballot_sync(0xffffffffu, u < before + v);
+          const int l = hit ? __ffs(hit) - 1 : 31;
+          before += __shfl_sync(0xffffffffu, hit ? v - x : v, l);
+          if (hit) {
+            s += l;
+            break;
+          }
+          if (s + 32 >= p.n_seqs) return false;  // (lengths that changed during the call)
+        }
+        rw = seq_rows(p, s);
       }
       g.s = s;
       g.h = (int)((u - before) / rw.units);
@@ -162,6 +181,7 @@ __device__ __forceinline__ int swizzle(int r, int c) { return c ^ (((r >> 1) & 3
 // unless `step` is above 1) and writes the output, or a joined part in the place of the
 // first one.
 constexpr int kJoinGroup = 16;
+constexpr int kJoinLoads = 16;
 template <class El, int HD>
 __device__ void join_parts(const PagedAttn& p, int b0, int i0, int step, int n, int s, int h, bool final,
                            float* s_m, float* s_l) {
@@ -174,11 +194,11 @@ __device__ void join_parts(const PagedAttn& p, int b0, int i0, int step, int n, 
     const int hd = 4 * c / HD;
     float m = -INFINITY, l = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < n; k0 += 8) {
-      float mq[8], lq[8];
-      float4 v[8];
+    for (int k0 = 0; k0 < n; k0 += kJoinLoads) {
+      float mq[kJoinLoads], lq[kJoinLoads];
+      float4 v[kJoinLoads];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
+      for (int q = 0; q < kJoinLoads; ++q) {
         mq[q] = -INFINITY;
         lq[q] = 0.f;
         v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -191,7 +211,7 @@ __device__ void join_parts(const PagedAttn& p, int b0, int i0, int step, int n, 
       }
       float mn = m;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) mn = fmaxf(mn, mq[q]);
+      for (int q = 0; q < kJoinLoads; ++q) mn = fmaxf(mn, mq[q]);
       const float ref = mn == -INFINITY ? 0.f : mn;
       const float fa = exp2_fast(m - ref);
       l *= fa;
@@ -200,7 +220,7 @@ __device__ void join_parts(const PagedAttn& p, int b0, int i0, int step, int n, 
       x.z *= fa;
       x.w *= fa;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
+      for (int q = 0; q < kJoinLoads; ++q) {
         const float f = exp2_fast(mq[q] - ref);
         l += lq[q] * f;
         x.x += v[q].x * f;
@@ -269,11 +289,11 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
   const int part_len = part_floats(p.group, HD);
   const uint32_t ring = smem_u32(smem) + wid * C::kStages * C::kStageBytes;
 
-  // the batch's units and where this block's run begins; one scan when one round of the
-  // block's threads covers the sequences
-  int64_t total = 0, mine = 0, upto = 0;  // this thread's sequence's units, and with those in front (last round)
-  for (int c = 0; c < p.n_seqs; c += kThreadsA) {
-    mine = c + tid < p.n_seqs ? (int64_t)seq_rows(p, c + tid).units * p.n_kv_heads : 0;
+  // the batch's units: a prefix over the sequences when every thread has one, else their sum
+  // first (the prefix is then taken up to the block's run only)
+  int64_t total = 0, mine = 0, upto = 0;  // this thread's sequence's units, and with those in front
+  for (int c = tid; c < p.n_seqs; c += kThreadsA) mine += (int64_t)seq_rows(p, c).units * p.n_kv_heads;
+  {
     int64_t v = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -282,7 +302,7 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
     }
     if (lane == 31) s_sum[wid] = v;
     __syncthreads();
-    upto = total + v;
+    upto = v;
 #pragma unroll
     for (int q = 0; q < kWarps; ++q) {
       if (q < wid) upto += s_sum[q];

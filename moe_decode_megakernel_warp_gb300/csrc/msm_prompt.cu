@@ -159,11 +159,18 @@ __device__ __forceinline__ Seq prompt_seq(const PromptAttn& p, int s) {
   return r;
 }
 
-// sequence and tile of tile t of the batch (each warp looks for itself); false: behind the last
-__device__ bool find_tile(const PromptAttn& p, int t, int& seq, int& tile) {
+// A warp's place in the batch, in shared memory (registers that last through the softmax cost 2 %)
+struct Place {
+  int round;
+  int c, before;  // first sequence of the 32 looked at last, tiles of the sequences in front of it
+};
+
+// Finds the sequence and the tile of the batch's tile t (each warp for itself); false: behind the
+// last tile.  t must not fall from call to call: the search goes on where the last one ended.
+__device__ bool find_tile(const PromptAttn& p, volatile Place* place, int t, int& seq, int& tile) {
   const int lane = threadIdx.x & 31;
-  int before = 0;
-  for (int c = 0; c < p.n_seqs; c += 32) {
+  int c = place->c, before = place->before;
+  for (; c < p.n_seqs; c += 32) {
     int n = 0;
     if (c + lane < p.n_seqs) n = (prompt_seq(p, c + lane).nq * p.group + kBlockRows - 1) / kBlockRows;
     int v = n;
@@ -179,6 +186,11 @@ __device__ bool find_tile(const PromptAttn& p, int t, int& seq, int& tile) {
       const int first = __shfl_sync(0xffffffffu, before + v - n, l);
       const int cnt = __shfl_sync(0xffffffffu, n, l);
       tile = cnt - 1 - (t - first);  // those with the most keys first
+      if (lane == 0) {
+        place->c = c;
+        place->before = before;
+      }
+      __syncwarp();
       return true;
     }
     before += __shfl_sync(0xffffffffu, v, 31);
@@ -199,10 +211,10 @@ struct Work {
     return a + kKeys - 1 > tok0 + shift || (window > 0 && a < tok1 + shift - window);
   }
 };
-__device__ bool find_work(const PromptAttn& p, int idx, Work& w) {
+__device__ bool find_work(const PromptAttn& p, volatile Place* place, int idx, Work& w) {
   int seq, tile;
   w.h = idx % p.n_kv_heads;
-  if (!find_tile(p, idx / p.n_kv_heads, seq, tile)) return false;
+  if (!find_tile(p, place, idx / p.n_kv_heads, seq, tile)) return false;
   const Seq sq = prompt_seq(p, seq);
   w.q0 = sq.q0;
   w.nq = sq.nq;
@@ -222,15 +234,13 @@ __device__ bool find_work(const PromptAttn& p, int idx, Work& w) {
 // A block's pieces of work: one of every round of gridDim.x, the rounds alternately from the front
 // and from the back.  (The work is listed from the longest to the shortest of a sequence: the
 // block that got the longest piece of a round gets the shortest of the next.)
-struct Rounds {
-  int round = 0;
-  __device__ __forceinline__ bool next(const PromptAttn& p, int n_work, Work& w) {
-    const int64_t base = (int64_t)round * gridDim.x;
-    const int64_t idx = base + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    ++round;
-    return idx < n_work && find_work(p, (int)idx, w);
-  }
-};
+__device__ __forceinline__ bool next_work(const PromptAttn& p, volatile Place* place, int n_work, Work& w) {
+  const int round = place->round;
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) place->round = round + 1;
+  const int64_t idx = (int64_t)round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  return idx < n_work && find_work(p, place, (int)idx, w);
+}
 
 // The ring of K and V tiles, in the order K(0), V(0), K(1), V(1), ... of one piece of work
 // after the other, as one of its readers walks it.  Every reader waits for every tile and
@@ -261,11 +271,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       b_o[2], b_turn[2], b_drain[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_dead, s_taken;
+  __shared__ Place s_place[kPromptThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const s_q = smem;
   uint8_t* const s_kv = smem + 2 * C::kTileBytes;
 
+  volatile Place* const place = &s_place[wid];
+  if (lane == 0) place->round = place->c = place->before = 0;
   if (wid == 8) tmem_alloc(&s_tmem, 512);
   if (tid == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -314,7 +327,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                       w.q0 + w.tok0 + t * (kRows / p.group), &b_q[t]);
         return true;
       };
-      for (Rounds todo; ok && todo.next(p, n_work, w);) {
+      while (ok && next_work(p, place, n_work, w)) {
         if (lane == 0) {
           for (int e = 0; ok && e < 2 * w.n; ++e) {
             const int st = i % C::kStages;
@@ -376,7 +389,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       uint32_t clean_phase = 0;
       int steps = 0, loads = 0, turns = 0;  // of this tile's P and Q, and of the two threads, so far
       bool ok = true;
-      for (Rounds todo; ok && todo.next(p, n_work, w);) {
+      while (ok && next_work(p, place, n_work, w)) {
         if (lane == 0 && w.n > 0) {
           const bool mine = t == 0 || w.two;  // without a second tile its thread only signs the ring
           int k_st = ring.next(b_full, dead);
@@ -432,7 +445,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       constexpr uint32_t kE = El::kExponent, kLow = kE & (~kE + 1u);  // exponent field, its lowest bit
       Ring<C::kStages> ring;
       bool ok = true;
-      for (Rounds todo; ok && todo.next(p, n_work, w);) {
+      while (ok && next_work(p, place, n_work, w)) {
         for (int e = 0; e < 2 * w.n; ++e) {
           const int st = ring.next(b_full, dead);
           if (!(ok = __all_sync(0xffffffffu, st >= 0))) break;
@@ -474,12 +487,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // (a negative scale negates Q in the product; a scale of zero must still leave -inf x scale = -inf)
     const float scale = fmaxf(fabsf(p.scale_log2), 1e-30f);
     int steps = 0, works = 0;
-    Rounds todo;
     Work ahead;
-    for (bool more = todo.next(p, n_work, ahead); more;) {
+    for (bool more = next_work(p, place, n_work, ahead); more;) {
       w = ahead;
       if (w.n > 0 && t == 1 && !w.two) {
-        more = todo.next(p, n_work, ahead);
+        more = next_work(p, place, n_work, ahead);
         continue;
       }
       const int row = w.row0 + t * kRows + (wid & 3) * 32 + lane;
@@ -490,7 +502,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       if (w.n == 0) {  // no row sees a key
         if (tok < w.nq)
           for (int c = 0; c < HD / 8; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0u, 0u, 0u, 0u);
-        more = todo.next(p, n_work, ahead);
+        more = next_work(p, place, n_work, ahead);
         continue;
       }
       float m = -INFINITY;
@@ -573,7 +585,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&b_p[t], 1);
       }
-      more = todo.next(p, n_work, ahead);  // (looked up while the last product runs)
+      more = next_work(p, place, n_work, ahead);  // (looked up while the last product runs)
       ok = ok && __all_sync(0xffffffffu, wait_bar(&b_o[t], works++ & 1, dead));
       tc_fence_after();
       float l0, l1;

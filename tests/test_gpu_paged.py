@@ -363,6 +363,16 @@ def test_lengths_beyond_the_table_are_cut_off():
     assert (got[0] == 0).all() and np.array_equal(bits(got[1:]), want[1:])
 
 
+@pytest.mark.parametrize("lens", [[0, 0, 0], [0] * 400, [0] * 150 + [77] + [0] * 300 + [200, 0, 1] + [0] * 90])
+def test_batches_of_mostly_empty_slots(lens):
+    rng = np.random.default_rng(16)
+    c, rk, rv = filled(rng, "bf16", lens, 16, 2, 64)
+    q = randn("bf16", len(lens), 8, 64, seed=6).cuda()
+    want, tol = decode_want(q, rk, rv, 0, 0.125, "bf16")
+    assert_close(c.attention(0, q), want, tol)
+    c.sync()
+
+
 def test_the_wrappers_refuse_what_does_not_fit():
     torch, msm = _mods()
     rng = np.random.default_rng(15)
@@ -486,6 +496,57 @@ def test_keys_that_a_query_does_not_see_have_no_part(hd, bad):
                     assert (np.abs(got.numpy()[s][:, rest] - want[s][:, rest]) <= tol[s][:, rest]).all()
                 elif bad == "nan":
                     assert torch.isnan(got[seen]).all()
+
+
+@pytest.mark.parametrize("window", [0, 300])
+def test_values_that_are_not_finite_in_longer_prompts(window):
+    """NaN rows of V and K throughout three packed prompts whose work the blocks share: only the
+    queries that see one are touched."""
+    torch, msm = _mods()
+    lens = [1400, 700, 33]
+    st = starts_of(lens)
+    x = [randn("bf16", st[-1], h, 64, seed=i).cuda() for i, h in enumerate((8, 2, 2))]
+    clean = [t.clone() for t in x]
+    rows = [(1, 900), (2, 5), (2, 1399), (1, 1400), (2, 1700), (2, st[-1] - 1)]
+    seen = np.zeros(st[-1], bool)
+    for which, r in rows:
+        x[which][r, :, 7] = float("nan")
+        end = next(e for e in st if e > r)
+        seen[r:min(end, r + window) if window else end] = True
+    got = f64(msm.prompt_attention(*x, ints(st), window=window))
+    base = f64(msm.prompt_attention(*clean, ints(st), window=window))
+    assert np.array_equal(got[~seen], base[~seen])
+    assert np.isnan(got[seen][:, :, 7]).all()
+
+
+@pytest.mark.parametrize("n_seqs,most", [(700, 3), (150, 40)])
+def test_many_short_prompts(n_seqs, most):
+    _, msm = _mods()
+    rng = np.random.default_rng(n_seqs)
+    st = starts_of(rng.integers(0, most + 1, n_seqs))
+    q, k, v = (randn("fp16", st[-1], h, 64, seed=h).cuda() for h in (4, 2, 2))
+    want, tol = prompt_want(q, k, v, st, st, 0, 0.125, "fp16")
+    assert_close(msm.prompt_attention(q, k, v, ints(st)), want, tol)
+
+
+def test_prompts_on_two_streams_at_once():
+    torch, msm = _mods()
+    n = 3000
+    x = [[randn("bf16", n, h, 128, seed=s + h).cuda() for h in (8, 2, 2)] for s in range(2)]
+    x = [[q, k, v] for q, k, v in x]
+    st = ints([0, n])
+    want = [bits(msm.prompt_attention(*y, st)) for y in x]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(msm.prompt_attention(*x[i], st))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in outs[i]:
+            assert np.array_equal(bits(o), want[i])
 
 
 def test_prompt_leaves_what_is_not_its_own():
