@@ -18,22 +18,20 @@ _PROMPT = struct.Struct("9if4P8q2P")
 assert _PROMPT.size == ctypes.sizeof(MsmPrompt)
 
 
-def _torch():
+_torch = None  # the module, imported at the first call
+_CODES = {}
+
+
+def _load():
+    global _torch
     import torch
-    return torch
+    _CODES.update({torch.bfloat16: MSM_BF16, torch.float16: MSM_FP16})
+    _torch = torch
 
 
 def _need(ok, msg):
     if not ok:
         raise ValueError(msg)
-
-
-def _dtype(t):
-    torch = _torch()
-    if t.dtype is torch.bfloat16:
-        return MSM_BF16
-    _need(t.dtype is torch.float16, "expected bfloat16 or float16, got %s" % t.dtype)
-    return MSM_FP16
 
 
 def _rows(t, name, shape, dtype, index):
@@ -43,19 +41,20 @@ def _rows(t, name, shape, dtype, index):
         raise ValueError("%s must be %s, %s, on cuda:%d; got %s, %s, on %s"
                          % (name, list(shape), dtype, index, list(t.shape), t.dtype, t.device))
     s0, s1, s2 = t.stride()
-    _need(s2 == 1, "%s: the elements of a row must be consecutive" % name)
+    if s2 != 1:
+        raise ValueError("%s: the elements of a row must be consecutive" % name)
     n0, n1, hd = shape
     return (s0 if n0 > 1 else n1 * hd), (s1 if n1 > 1 else hd)
 
 
 def _int32(t, name, n, index):
-    if t.dtype is not _torch().int32 or t.get_device() != index or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not _torch.int32 or t.get_device() != index or t.numel() != n or not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 tensor of %d entries on cuda:%d" % (name, n, index))
     return t.data_ptr()
 
 
 def _stream(index):
-    return _torch()._C._cuda_getCurrentRawStream(index)
+    return _torch._C._cuda_getCurrentRawStream(index)
 
 
 class PagedCache:
@@ -68,7 +67,9 @@ class PagedCache:
     stream order and without a host round trip; ``sync`` waits and raises what they met."""
 
     def __init__(self, k_pages, v_pages, table, lens, refs):
-        torch = _torch()
+        if _torch is None:
+            _load()
+        torch = _torch
         k_pages, v_pages = list(k_pages), list(v_pages)
         _need(len(k_pages) == len(v_pages) and k_pages, "one K and one V pool per layer")
         first = k_pages[0]
@@ -78,6 +79,7 @@ class PagedCache:
             _need(t.shape == first.shape and t.dtype == first.dtype and t.device == first.device and t.is_contiguous(),
                   "the pools must be contiguous and alike in shape, type and device")
         _need(table.dim() == 2, "table is [n_seqs, max_pages]")
+        _need(first.dtype in _CODES, "the pools must be bfloat16 or float16, got %s" % first.dtype)
         n_pages, n_kv_heads, page_rows, head_dim = first.shape
         n_seqs, max_pages = table.shape
         dev = first.device
@@ -88,11 +90,12 @@ class PagedCache:
                                    device=dev)
         kp, self._k_ptrs = _ptr_array([t.data_ptr() for t in k_pages])
         vp, self._v_ptrs = _ptr_array([t.data_ptr() for t in v_pages])
-        self._c = MsmPages(dev.index, _dtype(first), len(k_pages), n_pages, page_rows, n_kv_heads, head_dim, n_seqs,
+        self._c = MsmPages(dev.index, _CODES[first.dtype], len(k_pages), n_pages, page_rows, n_kv_heads, head_dim, n_seqs,
                            max_pages, kp, vp, _int32(table, "table", n_seqs * max_pages, dev.index),
                            _int32(lens, "lens", n_seqs, dev.index), _int32(refs, "refs", n_pages, dev.index),
                            self.status.data_ptr(), self.scratch.data_ptr())
         self._ref = ctypes.byref(self._c)
+        self._lib = lib()
         self._index, self._n_seqs, self._kv_heads, self._head_dim = dev.index, n_seqs, n_kv_heads, head_dim
         self._dtype = first.dtype
         self._bytes = {}      # bytes of the attention's workspace by number of query heads
@@ -101,7 +104,9 @@ class PagedCache:
     @classmethod
     def allocate(cls, n_layers, n_pages, page_rows, n_kv_heads, head_dim, n_seqs, max_pages, dtype=None, device=None):
         """An empty cache (bfloat16 by default)."""
-        torch = _torch()
+        if _torch is None:
+            _load()
+        torch = _torch
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
 
         def pools():
@@ -114,17 +119,17 @@ class PagedCache:
 
     def resize(self, new_lens):
         """msm_pages_resize: int32 [n_seqs] on the device, -1 = leave as it is."""
-        _check(lib().msm_pages_resize(self._ref, _int32(new_lens, "new_lens", self._n_seqs, self._index),
+        _check(self._lib.msm_pages_resize(self._ref, _int32(new_lens, "new_lens", self._n_seqs, self._index),
                                       _stream(self._index)))
 
     def fork(self, parent):
         """msm_pages_fork: int32 [n_seqs] on the device, -1 = none."""
-        _check(lib().msm_pages_fork(self._ref, _int32(parent, "parent", self._n_seqs, self._index),
+        _check(self._lib.msm_pages_fork(self._ref, _int32(parent, "parent", self._n_seqs, self._index),
                                     _stream(self._index)))
 
     def compact(self):
         """msm_pages_compact."""
-        _check(lib().msm_pages_compact(self._ref, _stream(self._index)))
+        _check(self._lib.msm_pages_compact(self._ref, _stream(self._index)))
 
     def write(self, layer, k, v, starts):
         """msm_pages_write: k, v [n_tokens, n_kv_heads, head_dim], starts int32 [n_seqs + 1]."""
@@ -132,26 +137,28 @@ class PagedCache:
         shape = (n, self._kv_heads, self._head_dim)
         kt, kh = _rows(k, "k", shape, self._dtype, i)
         vt, vh = _rows(v, "v", shape, self._dtype, i)
-        _check(lib().msm_pages_write(self._ref, layer, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh,
+        _check(self._lib.msm_pages_write(self._ref, layer, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh,
                                      _int32(starts, "starts", self._n_seqs + 1, i), n, _stream(i)))
 
     def attention(self, layer, q, window=0, scale=None, out=None):
         """msm_paged_attention: q [n_seqs, n_q_heads, head_dim]; scale defaults to
         1 / sqrt(head_dim).  Returns out."""
-        torch = _torch()
+        torch = _torch
         _need(q.dim() == 3, "q must be [n_seqs, n_q_heads, head_dim]")
-        heads, i = q.shape[1], self._index
-        shape = (self._n_seqs, heads, self._head_dim)
+        heads, i, hd = q.shape[1], self._index, self._head_dim
+        shape = (self._n_seqs, heads, hd)
         qs, qh = _rows(q, "q", shape, self._dtype, i)
         if out is None:
             out = torch.empty(shape, dtype=self._dtype, device=self.device)
-        os_, oh = _rows(out, "out", shape, self._dtype, i)
+            os_, oh = heads * hd, hd
+        else:
+            os_, oh = _rows(out, "out", shape, self._dtype, i)
         stream = _stream(i)
         n = self._bytes.get(heads)
         if n is None:
-            n = lib().msm_paged_attention_workspace(self._ref, heads)
+            n = self._lib.msm_paged_attention_workspace(self._ref, heads)
             if n == 0:  # the call says what is wrong
-                _check(lib().msm_paged_attention(self._ref, layer, None, qs, qh, heads, 1.0, 0, None, os_, oh, None, 0,
+                _check(self._lib.msm_paged_attention(self._ref, layer, None, qs, qh, heads, 1.0, 0, None, os_, oh, None, 0,
                                                  None))
             self._bytes[heads] = n
         # one workspace per stream, and one per call that a graph records (graphs recorded on
@@ -162,15 +169,15 @@ class PagedCache:
             ws = self._workspace.get((stream, heads))
             if ws is None:
                 ws = self._workspace[stream, heads] = torch.zeros(n, dtype=torch.uint8, device=self.device)
-        _check(lib().msm_paged_attention(self._ref, layer, q.data_ptr(), qs, qh, heads,
-                                         self._head_dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
+        _check(self._lib.msm_paged_attention(self._ref, layer, q.data_ptr(), qs, qh, heads,
+                                         hd ** -0.5 if scale is None else scale, window, out.data_ptr(),
                                          os_, oh, ws.data_ptr(), n, stream))
         return out
 
     def sync(self):
         """msm_pages_sync: waits for the current stream; raises MsmError for an error that a
         call met on the device (and clears it)."""
-        _check(lib().msm_pages_sync(self._ref, _stream(self._index)))
+        _check(self._lib.msm_pages_sync(self._ref, _stream(self._index)))
 
 
 def prompt_attention(q, k, v, q_starts, k_starts=None, window=0, scale=None, out=None):
@@ -181,22 +188,27 @@ def prompt_attention(q, k, v, q_starts, k_starts=None, window=0, scale=None, out
     head_dim] is read in place), q_starts and k_starts int32 [n_seqs + 1] on the device
     (k_starts defaults to q_starts), scale defaults to 1 / sqrt(head_dim).  Returns out; a new
     one is uninitialised behind the last sequence."""
-    torch = _torch()
-    _need(q.is_cuda, "q must be a CUDA tensor")
-    _need(q.dim() == 3 and k.dim() == 3, "q and k must be [tokens, heads, head_dim]")
-    n_q, heads, hd = shape = q.shape
-    n_k, kv_heads, _ = k.shape
-    i, dtype, k_shape = q.get_device(), q.dtype, (n_k, kv_heads, hd)
+    if _torch is None:
+        _load()
+    i, dtype, shape, k_shape = q.get_device(), q.dtype, q.shape, k.shape
+    _need(i >= 0, "q must be a CUDA tensor")
+    _need(dtype in _CODES, "expected bfloat16 or float16, got %s" % dtype)
+    _need(len(shape) == 3 and len(k_shape) == 3 and k_shape[2] == shape[2],
+          "q and k must be [tokens, heads, head_dim]")
+    n_q, heads, hd = shape
+    n_k, kv_heads, _ = k_shape
     qt, qh = _rows(q, "q", shape, dtype, i)
     kt, kh = _rows(k, "k", k_shape, dtype, i)
     vt, vh = _rows(v, "v", k_shape, dtype, i)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device)
-    ot, oh = _rows(out, "out", shape, dtype, i)
+        out = _torch.empty(shape, dtype=dtype, device=q.device)
+        ot, oh = heads * hd, hd
+    else:
+        ot, oh = _rows(out, "out", shape, dtype, i)
     n_seqs = q_starts.numel() - 1
     qs = _int32(q_starts, "q_starts", n_seqs + 1, i)
     ks = qs if k_starts is None else _int32(k_starts, "k_starts", n_seqs + 1, i)
-    a = _PROMPT.pack(i, _dtype(q), n_seqs, n_q, n_k, heads, kv_heads, hd, window,
+    a = _PROMPT.pack(i, _CODES[dtype], n_seqs, n_q, n_k, heads, kv_heads, hd, window,
                      hd ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                      out.data_ptr(), qt, qh, kt, kh, vt, vh, ot, oh, qs, ks)
     _check(lib().msm_prompt_attention(a, _stream(i)))
