@@ -23,7 +23,7 @@ _INCLUDE = os.path.join(_ROOT, "include")
 LIB_PATH = os.path.join(_BUILD, "libmsm.so")
 _SOURCES = ["msm_kernel.cu", "msm_pack.cu", "msm_api.cu", "msm_accept.cu", "msm_pages.cu", "msm_paged_attn.cu",
             "msm_prompt.cu", "msm_paged_api.cu"]
-_HEADERS = ["msm_device.cuh", "msm_internal.h", "msm_paged.h"]
+_HEADERS = ["msm_device.cuh", "msm_internal.h", "msm_paged.h", "msm_attn.cuh"]
 NVCC_ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 MSM_OK, MSM_ERR_INVALID_ARG, MSM_ERR_CUDA, MSM_ERR_OOM, MSM_ERR_DEVICE_TIMEOUT, MSM_ERR_UNSUPPORTED = range(6)

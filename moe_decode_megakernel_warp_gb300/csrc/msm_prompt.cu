@@ -20,15 +20,24 @@
 // masked score has such a weight.  In key tiles that some row sees only in part, warp 11
 // therefore takes these elements out before the product; the rows that do see their keys
 // get them back at the end.
+//
+// Bound by the chain of one tile's softmax (1,000 cycles) and its products (1,260 cycles; 1,024
+// at the tensor cores' rate -- Q K^T takes all of shared memory's bandwidth, which the TMA
+// writes share), two tiles of which overlap: about 2,900 cycles for 256 rows x 128 keys, 2,048 of
+// them products.  On one GB300 (1,926 TFLOP/s measured cuBLAS burst), 32 query heads on 8 kv
+// heads of 128, bf16: 16,384 tokens 1.40 ms (1,570 TFLOP/s), 2,048 tokens 37 us, 32,768
+// tokens on a window of 2,048 0.9 ms (1,160 TFLOP/s: two of 17 key tiles are masked, and a
+// piece of work ends every 17); head_dim 64 1.24 ms (890 TFLOP/s: as many exponentials for half
+// the products).  Tried and slower: P handed over in two or four parts (+5, +13 %), results
+// written by four more warps (+5 %; fewer registers for the softmax) or through shared memory
+// with four stages of the ring instead of five (+4 %), 192 or 208 registers (+7, +2 %).
 #include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <atomic>
 
-#include "msm_device.cuh"
+#include "msm_attn.cuh"
 #include "msm_paged.h"
 
 namespace msm {
@@ -45,25 +54,6 @@ constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
 constexpr float kGrow = 8.0f;  // log2 of the largest unnormalised weight
 constexpr uint64_t kWaitNs = 2000000000ull;
 
-struct Bf16 {
-  static constexpr bool kBf16 = true;
-  static constexpr uint32_t kExponent = 0x7F80u;
-  static __device__ __forceinline__ float value(uint16_t b) { return bf16_to_f32(b); }
-  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-  }
-};
-struct Fp16 {
-  static constexpr bool kBf16 = false;
-  static constexpr uint32_t kExponent = 0x7C00u;
-  static __device__ __forceinline__ float value(uint16_t b) { return __half2float(__ushort_as_half(b)); }
-  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-  }
-};
-
 template <int HD>
 struct Cfg {
   static constexpr int kBoxes = HD / 64;
@@ -76,11 +66,6 @@ struct Maps {
   CUtensorMap q, k, v;
 };
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
