@@ -144,14 +144,21 @@ def test_a_shared_last_page_is_copied_once_for_each_that_grows():
     c.ref.check()
 
 
-def test_a_pool_of_many_pages_and_sequences():
+@pytest.mark.parametrize("n_pages", [60000, 150001])
+def test_a_pool_of_many_pages_and_sequences(n_pages):
     rng = np.random.default_rng(4)
     n_seqs, rows = 1500, 2
-    c = Both(rng, 1, 60000, rows, 1, 64, n_seqs, 40)
+    c = Both(rng, 1, n_pages, rows, 1, 64, n_seqs, 40)
+    if n_pages > 100000:  # the free pages begin far behind the front
+        c.gpu.refs[:99990] = 1
+        c.ref.refs[:99990] = 1
     for i in range(3):
         c.call("resize", [int(x) for x in rng.integers(0, 40 * rows + 1, n_seqs)])
     c.call("resize", [0 if s % 3 else -1 for s in range(n_seqs)])
     c.call("fork", [s - s % 3 if s % 3 else -1 for s in range(n_seqs)])
+    if n_pages > 100000:
+        c.gpu.refs[:99990] = 0
+        c.ref.refs[:99990] = 0
     c.call("compact")
     c.call("resize", [int(n) + 1 if n < 80 else -1 for n in c.ref.lens])
     c.ref.check()
@@ -402,6 +409,38 @@ def test_the_wrappers_refuse_what_does_not_fit():
     c.sync()
 
 
+def test_pools_of_more_than_2_to_the_31_elements():
+    """The last pages of a 4.6 GB pool: written, read, copied and moved."""
+    torch, msm = _mods()
+    n_pages, rows, hkv, hd = 4400, 1024, 8, 64
+    c = msm.PagedCache.allocate(1, n_pages, rows, hkv, hd, 2, 3)
+    assert c.k_pages[0].numel() > 1 << 31
+    c.refs.fill_(1)
+    c.refs[n_pages - 4:] = 0
+    c.resize(ints([1100, 0]))
+    kv = randn("bf16", 1100, 2 * hkv, hd, seed=1).cuda()
+    c.write(0, kv[:, :hkv], kv[:, hkv:], ints([0, 1100, 1100]))
+    c.sync()
+    assert c.table[0].tolist() == [n_pages - 4, n_pages - 3, -1]
+    assert torch.equal(c.k_pages[0][n_pages - 3, :, :76], kv[1024:, :hkv].transpose(0, 1))
+    q = randn("bf16", 2, hkv, hd, seed=2).cuda()
+    rows_k, rows_v = [kv[:, :hkv]] * 2, [kv[:, hkv:]] * 2
+    c.fork(ints([-1, 0]))
+    c.resize(ints([-1, 1101]))
+    new = randn("bf16", 1, 2 * hkv, hd, seed=3).cuda()
+    c.write(0, new[:, :hkv], new[:, hkv:], ints([0, 0, 1]))
+    rows_k[1], rows_v[1] = torch.cat([rows_k[1], new[:, :hkv]]), torch.cat([rows_v[1], new[:, hkv:]])
+    c.sync()
+    assert c.table[1].tolist() == [n_pages - 4, n_pages - 2, -1]
+    want, tol = decode_want(q, rows_k, rows_v, 0, 0.125, "bf16")
+    assert_close(c.attention(0, q), want, tol)
+    c.refs[:n_pages - 4] = 0
+    c.compact()
+    c.sync()
+    assert c.table.tolist() == [[0, 1, -1], [0, 2, -1]]
+    assert_close(c.attention(0, q), want, tol)
+
+
 # ------------------------------------------------------------------ prompt attention
 def prompt_want(q, k, v, qs, ks, window, scale, kind):
     out, tol = np.zeros(q.shape), np.full(q.shape, 1e-30)
@@ -560,6 +599,18 @@ def test_prompt_leaves_what_is_not_its_own():
     assert_close(out[:81], want[:81], tol[:81])
     out[:81] = 3.0
     assert (big == 3.0).all()
+
+
+def test_rows_more_than_2_to_the_32_elements_apart():
+    torch, msm = _mods()
+    n, stride = 70, 1 << 26
+    big = torch.empty(n * stride, dtype=torch.bfloat16, device="cuda")  # 9.4 GB
+    views = [big.as_strided((n, 2, 64), (stride, 64, 1), i * 4096) for i in range(4)]
+    for i in range(3):
+        views[i].copy_(randn("bf16", n, 2, 64, seed=i))
+    got = msm.prompt_attention(*views[:3], ints([0, 30, n]), out=views[3])
+    want, tol = prompt_want(*views[:3], [0, 30, n], [0, 30, n], 0, 0.125, "bf16")
+    assert_close(got, want, tol)
 
 
 def test_starts_out_of_range_are_cut_off():
