@@ -11,7 +11,7 @@
 //   A softmax thread owns a row (128 scores in registers), so its maximum and sum need no
 //   exchange.  P takes the place of S (16-bit, half its columns).  P is computed with the
 //   maximum that the row had before the tile; only when the tile's own is larger by more than
-//   a factor 2^8 (P stays below 2^8, well inside fp16) O is rescaled and P computed again.
+//   a factor 2^12 (P stays below 2^12, well inside fp16) O is rescaled and P computed again.
 //   S(j + 1) being there means that P(j) V is done, the products of a block being issued
 //   and completed in order, so the thread may then change O itself.
 // Warps 0-7: softmax; 8, 10: products of a tile each; 9: TMA loads; 11: finite check of V.
@@ -25,8 +25,8 @@
 // at the tensor cores' rate -- Q K^T takes all of shared memory's bandwidth, which the TMA
 // writes share), two tiles of which overlap: about 2,900 cycles for 256 rows x 128 keys, 2,048 of
 // them products.  On one GB300 (1,926 TFLOP/s measured cuBLAS burst), 32 query heads on 8 kv
-// heads of 128, bf16: 16,384 tokens 1.40 ms (1,570 TFLOP/s), 2,048 tokens 37 us, 32,768
-// tokens on a window of 2,048 0.9 ms (1,160 TFLOP/s: two of 17 key tiles are masked, and a
+// heads of 128, bf16: 16,384 tokens 1.41 ms (1,560 TFLOP/s), 2,048 tokens 37 us, 32,768
+// tokens on a window of 2,048 0.85 ms (1,250 TFLOP/s: two of 17 key tiles are masked, and a
 // piece of work ends every 17); head_dim 64 1.24 ms (890 TFLOP/s: as many exponentials for half
 // the products).  Tried and slower: P handed over in two or four parts (+5, +13 %), results
 // written by four more warps (+5 %; fewer registers for the softmax) or through shared memory
@@ -51,7 +51,7 @@ constexpr int kBoxBytes = kRows * 128;       // 128 rows x 64 elements, one swiz
 // Registers: 384 threads start with 168; warps 8-11 give up 64 each, warps 0-7 take 32
 // (256 x 200 + 128 x 104 = 384 x 168).
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
-constexpr float kGrow = 8.0f;  // log2 of the largest unnormalised weight
+constexpr float kGrow = 12.0f;  // log2 of the largest unnormalised weight
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 template <int HD>
