@@ -18,14 +18,20 @@ _PROMPT = struct.Struct("9if4P8q2P")
 assert _PROMPT.size == ctypes.sizeof(MsmPrompt)
 
 
-_torch = None  # the module, imported at the first call
+# Set at the first call: the torch module and what every call takes from it, the library, and
+# msm_dtype by torch type.  (A small call is host time: 17 us for a short prompt's, of which the
+# launch is 2.4.)
+_torch = _empty = _raw_stream = _capturing = _INT32 = _LIBRARY = None
 _CODES = {}
 
 
 def _load():
-    global _torch
+    global _torch, _empty, _raw_stream, _capturing, _INT32, _LIBRARY
     import torch
+    _LIBRARY = lib()
     _CODES.update({torch.bfloat16: MSM_BF16, torch.float16: MSM_FP16})
+    _empty, _INT32 = torch.empty, torch.int32
+    _raw_stream, _capturing = torch._C._cuda_getCurrentRawStream, torch._C._cuda_isCurrentStreamCapturing
     _torch = torch
 
 
@@ -48,13 +54,9 @@ def _rows(t, name, shape, dtype, index):
 
 
 def _int32(t, name, n, index):
-    if t.dtype is not _torch.int32 or t.get_device() != index or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not _INT32 or t.get_device() != index or t.numel() != n or not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 tensor of %d entries on cuda:%d" % (name, n, index))
     return t.data_ptr()
-
-
-def _stream(index):
-    return _torch._C._cuda_getCurrentRawStream(index)
 
 
 class PagedCache:
@@ -86,7 +88,7 @@ class PagedCache:
         self.k_pages, self.v_pages, self.table, self.lens, self.refs = k_pages, v_pages, table, lens, refs
         self.device = dev
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.scratch = torch.empty(max(1, lib().msm_pages_scratch_ints(n_pages, n_seqs)), dtype=torch.int32,
+        self.scratch = torch.empty(max(1, _LIBRARY.msm_pages_scratch_ints(n_pages, n_seqs)), dtype=torch.int32,
                                    device=dev)
         kp, self._k_ptrs = _ptr_array([t.data_ptr() for t in k_pages])
         vp, self._v_ptrs = _ptr_array([t.data_ptr() for t in v_pages])
@@ -95,7 +97,7 @@ class PagedCache:
                            _int32(lens, "lens", n_seqs, dev.index), _int32(refs, "refs", n_pages, dev.index),
                            self.status.data_ptr(), self.scratch.data_ptr())
         self._ref = ctypes.byref(self._c)
-        self._lib = lib()
+        self._lib = _LIBRARY
         self._index, self._n_seqs, self._kv_heads, self._head_dim = dev.index, n_seqs, n_kv_heads, head_dim
         self._dtype = first.dtype
         self._bytes = {}      # bytes of the attention's workspace by number of query heads
@@ -120,16 +122,16 @@ class PagedCache:
     def resize(self, new_lens):
         """msm_pages_resize: int32 [n_seqs] on the device, -1 = leave as it is."""
         _check(self._lib.msm_pages_resize(self._ref, _int32(new_lens, "new_lens", self._n_seqs, self._index),
-                                      _stream(self._index)))
+                                      _raw_stream(self._index)))
 
     def fork(self, parent):
         """msm_pages_fork: int32 [n_seqs] on the device, -1 = none."""
         _check(self._lib.msm_pages_fork(self._ref, _int32(parent, "parent", self._n_seqs, self._index),
-                                    _stream(self._index)))
+                                    _raw_stream(self._index)))
 
     def compact(self):
         """msm_pages_compact."""
-        _check(self._lib.msm_pages_compact(self._ref, _stream(self._index)))
+        _check(self._lib.msm_pages_compact(self._ref, _raw_stream(self._index)))
 
     def write(self, layer, k, v, starts):
         """msm_pages_write: k, v [n_tokens, n_kv_heads, head_dim], starts int32 [n_seqs + 1]."""
@@ -138,22 +140,22 @@ class PagedCache:
         kt, kh = _rows(k, "k", shape, self._dtype, i)
         vt, vh = _rows(v, "v", shape, self._dtype, i)
         _check(self._lib.msm_pages_write(self._ref, layer, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh,
-                                     _int32(starts, "starts", self._n_seqs + 1, i), n, _stream(i)))
+                                     _int32(starts, "starts", self._n_seqs + 1, i), n, _raw_stream(i)))
 
     def attention(self, layer, q, window=0, scale=None, out=None):
         """msm_paged_attention: q [n_seqs, n_q_heads, head_dim]; scale defaults to
         1 / sqrt(head_dim).  Returns out."""
-        torch = _torch
-        _need(q.dim() == 3, "q must be [n_seqs, n_q_heads, head_dim]")
+        if q.dim() != 3:
+            raise ValueError("q must be [n_seqs, n_q_heads, head_dim]")
         heads, i, hd = q.shape[1], self._index, self._head_dim
         shape = (self._n_seqs, heads, hd)
         qs, qh = _rows(q, "q", shape, self._dtype, i)
         if out is None:
-            out = torch.empty(shape, dtype=self._dtype, device=self.device)
+            out = _empty(shape, dtype=self._dtype, device=self.device)
             os_, oh = heads * hd, hd
         else:
             os_, oh = _rows(out, "out", shape, self._dtype, i)
-        stream = _stream(i)
+        stream = _raw_stream(i)
         n = self._bytes.get(heads)
         if n is None:
             n = self._lib.msm_paged_attention_workspace(self._ref, heads)
@@ -163,21 +165,23 @@ class PagedCache:
             self._bytes[heads] = n
         # one workspace per stream, and one per call that a graph records (graphs recorded on
         # one stream may be replayed on two)
-        if torch._C._cuda_isCurrentStreamCapturing():
-            ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
+        if _capturing():
+            ws = _torch.zeros(n, dtype=_torch.uint8, device=self.device)
         else:
             ws = self._workspace.get((stream, heads))
             if ws is None:
-                ws = self._workspace[stream, heads] = torch.zeros(n, dtype=torch.uint8, device=self.device)
-        _check(self._lib.msm_paged_attention(self._ref, layer, q.data_ptr(), qs, qh, heads,
-                                         hd ** -0.5 if scale is None else scale, window, out.data_ptr(),
-                                         os_, oh, ws.data_ptr(), n, stream))
+                ws = self._workspace[stream, heads] = _torch.zeros(n, dtype=_torch.uint8, device=self.device)
+        st = self._lib.msm_paged_attention(self._ref, layer, q.data_ptr(), qs, qh, heads,
+                                           (hd or 1) ** -0.5 if scale is None else scale, window, out.data_ptr(), os_, oh,
+                                           ws.data_ptr(), n, stream)
+        if st:
+            _check(st)
         return out
 
     def sync(self):
         """msm_pages_sync: waits for the current stream; raises MsmError for an error that a
         call met on the device (and clears it)."""
-        _check(self._lib.msm_pages_sync(self._ref, _stream(self._index)))
+        _check(self._lib.msm_pages_sync(self._ref, _raw_stream(self._index)))
 
 
 def prompt_attention(q, k, v, q_starts, k_starts=None, window=0, scale=None, out=None):
@@ -191,25 +195,30 @@ def prompt_attention(q, k, v, q_starts, k_starts=None, window=0, scale=None, out
     if _torch is None:
         _load()
     i, dtype, shape, k_shape = q.get_device(), q.dtype, q.shape, k.shape
-    _need(i >= 0, "q must be a CUDA tensor")
-    _need(dtype in _CODES, "expected bfloat16 or float16, got %s" % dtype)
-    _need(len(shape) == 3 and len(k_shape) == 3 and k_shape[2] == shape[2],
-          "q and k must be [tokens, heads, head_dim]")
+    if i < 0:
+        raise ValueError("q must be a CUDA tensor")
+    code = _CODES.get(dtype)
+    if code is None:
+        raise ValueError("expected bfloat16 or float16, got %s" % dtype)
+    if len(shape) != 3 or len(k_shape) != 3 or k_shape[2] != shape[2]:
+        raise ValueError("q and k must be [tokens, heads, head_dim]")
     n_q, heads, hd = shape
     n_k, kv_heads, _ = k_shape
     qt, qh = _rows(q, "q", shape, dtype, i)
     kt, kh = _rows(k, "k", k_shape, dtype, i)
     vt, vh = _rows(v, "v", k_shape, dtype, i)
     if out is None:
-        out = _torch.empty(shape, dtype=dtype, device=q.device)
+        out = _empty(shape, dtype=dtype, device=q.device)
         ot, oh = heads * hd, hd
     else:
         ot, oh = _rows(out, "out", shape, dtype, i)
     n_seqs = q_starts.numel() - 1
     qs = _int32(q_starts, "q_starts", n_seqs + 1, i)
     ks = qs if k_starts is None else _int32(k_starts, "k_starts", n_seqs + 1, i)
-    a = _PROMPT.pack(i, _CODES[dtype], n_seqs, n_q, n_k, heads, kv_heads, hd, window,
-                     hd ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    a = _PROMPT.pack(i, code, n_seqs, n_q, n_k, heads, kv_heads, hd, window,
+                     (hd or 1) ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                      out.data_ptr(), qt, qh, kt, kh, vt, vh, ot, oh, qs, ks)
-    _check(lib().msm_prompt_attention(a, _stream(i)))
+    st = _LIBRARY.msm_prompt_attention(a, _raw_stream(i))
+    if st:
+        _check(st)
     return out
