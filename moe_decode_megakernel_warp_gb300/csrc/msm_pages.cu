@@ -21,9 +21,12 @@ namespace cg = cooperative_groups;
 namespace msm {
 namespace {
 
-constexpr int kMetaThreads = 1024;
-constexpr int kMetaWarps = kMetaThreads / 32;
-constexpr int kMetaBlocks = 8;      // the portable cluster size (one block for small caches: 0.6 us slower)
+// Threads per block (N below): 1,024, or 256 where the eight blocks' 64 warps have a sequence each
+// at most and 16,384 pages are one look -- their barriers cost less (a resize of 32 sequences 8.6
+// -> 7.4 us, a compaction of 150 pages 8.8 -> 7.8) and only larger caches miss the others (a fork of 64 sequences into 256: 7.0 us
+// with 1,024, 9.0 with 256).
+constexpr int kMetaMost = 1024, kMetaFew = 256;
+constexpr int kMetaBlocks = 8;      // the portable cluster size
 constexpr int kPagesPerThread = 8;  // pages one thread looks at per step of a scan
 
 __device__ __forceinline__ void latch(int32_t* status, int code, int call) {
@@ -38,10 +41,11 @@ struct BlockShare {        // what a block tells the others
 struct Share {
   BlockShare mine;
   BlockShare all[kMetaBlocks];
-  int warp_sum[kMetaWarps];
+  int warp_sum[kMetaMost / 32];
 };
 
 // exclusive prefix of x over the block's threads; total = the block's sum
+template <int N>
 __device__ int block_scan(int x, Share& sh, int& total) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   int v = x;
@@ -52,7 +56,7 @@ __device__ int block_scan(int x, Share& sh, int& total) {
   }
   if (lane == 31) sh.warp_sum[wid] = v;
   __syncthreads();
-  int w = lane < kMetaWarps ? sh.warp_sum[lane] : 0, t = w;
+  int w = lane < N / 32 ? sh.warp_sum[lane] : 0, t = w;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, t, o);
@@ -81,24 +85,26 @@ __device__ __forceinline__ void block_range(int n, int rank, int& lo, int& hi) {
 __device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b != 0); }
 
 // pages of [lo, hi) that are free (live = false) or in use
+template <int N>
 __device__ int count_pages(const int32_t* refs, int lo, int hi, bool live, Share& sh) {
   int n = 0;
-  for (int p = lo + (int)threadIdx.x; p < hi; p += kMetaThreads * kPagesPerThread) {
+  for (int p = lo + (int)threadIdx.x; p < hi; p += N * kPagesPerThread) {
     int r[kPagesPerThread];
 #pragma unroll
     for (int q = 0; q < kPagesPerThread; ++q) {
-      const int i = p + q * kMetaThreads;
+      const int i = p + q * N;
       r[q] = i < hi ? __ldcg(refs + i) : (live ? 0 : 1);
     }
 #pragma unroll
     for (int q = 0; q < kPagesPerThread; ++q) n += (r[q] > 0) == live;
   }
   int total;
-  block_scan(n, sh, total);
+  block_scan<N>(n, sh, total);
   return total;
 }
 
-__global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThreads)
+template <int N>
+__global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(N)
     resize_kernel(const PagesMeta p) {
   __shared__ Share sh;
   pdl_launch_dependents();  // the copy launch waits for this one's end itself
@@ -120,11 +126,11 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThrea
 #pragma unroll
   for (int q = 0; q < kPagesPerThread; ++q)
     if (mine + q < p1 && __ldcg(p.refs + mine + q) <= 0) mine_free |= 1u << q;
-  const int p_rest = p0 + kMetaThreads * kPagesPerThread;  // the share's pages behind those
+  const int p_rest = p0 + N * kPagesPerThread;  // the share's pages behind those
 
   // 1. each sequence: are its lengths and the pages it gives up in range, how many pages
   //    does it lack, does it have to leave a shared last page (offset = 2 pages + leave)
-  for (int s = s0 + wid; s < s1; s += kMetaWarps) {
+  for (int s = s0 + wid; s < s1; s += (N / 32)) {
     const int old = p.lens[s], asked = p.arg[s], now = asked == -1 ? old : asked;
     bool bad = old < 0 || old > cap || now < 0 || now > cap;
     int need = 0, leave = 0;
@@ -151,17 +157,17 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThrea
   __syncthreads();
   // 2. prefix of the needs over the block's sequences, free pages of its share of the pool
   int base = 0;
-  for (int c = s0; c < s1; c += kMetaThreads) {
+  for (int c = s0; c < s1; c += N) {
     const int s = c + (int)threadIdx.x;
     const int e = s < s1 ? sc.offset[s] : 0;
     int total;
-    const int before = block_scan(e >> 1, sh, total);
+    const int before = block_scan<N>(e >> 1, sh, total);
     if (s < s1) sc.offset[s] = 2 * (base + before) + (e & 1);
     base += total;
   }
   int n_free;
-  const int mine_rank = block_scan(__popc(mine_free), sh, n_free);
-  if (p_rest < p1) n_free += count_pages(p.refs, p_rest, p1, false, sh);
+  const int mine_rank = block_scan<N>(__popc(mine_free), sh, n_free);
+  if (p_rest < p1) n_free += count_pages<N>(p.refs, p_rest, p1, false, sh);
   if (threadIdx.x == 0) {
     sh.mine.need = base;
     sh.mine.count = n_free;
@@ -198,24 +204,24 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThrea
     int64_t at = free_before;
     if (p_rest < p1) {
       int first_step;
-      block_scan(__popc(mine_free), sh, first_step);
+      block_scan<N>(__popc(mine_free), sh, first_step);
       at += first_step;
     }
-    for (int c = p_rest; c < p1 && at < need_all; c += kMetaThreads * kPagesPerThread) {
+    for (int c = p_rest; c < p1 && at < need_all; c += N * kPagesPerThread) {
       const int q0 = c + (int)threadIdx.x * kPagesPerThread;
       uint32_t mask = 0;
 #pragma unroll
       for (int q = 0; q < kPagesPerThread; ++q)
         if (q0 + q < p1 && __ldcg(p.refs + q0 + q) <= 0) mask |= 1u << q;
       int total;
-      const int before = block_scan(__popc(mask), sh, total);
+      const int before = block_scan<N>(__popc(mask), sh, total);
       give(q0, mask, at + before);
       at += total;
     }
   }
   cl.sync();
   // 4. the tables
-  for (int s = s0 + wid; s < s1; s += kMetaWarps) {
+  for (int s = s0 + wid; s < s1; s += (N / 32)) {
     const int old = p.lens[s], asked = p.arg[s], now = asked == -1 ? old : asked;
     if (now == old) continue;
     int32_t* row = p.table + (size_t)s * p.max_pages;
@@ -248,13 +254,14 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThrea
   }
 }
 
-__global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThreads)
+template <int N>
+__global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(N)
     fork_kernel(const PagesMeta p) {
   __shared__ Share sh;
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int64_t cap = (int64_t)p.max_pages * p.page_rows;
-  const int w0 = rank * kMetaWarps + wid, n_warps = kMetaBlocks * kMetaWarps;
+  const int w0 = rank * (N / 32) + wid, n_warps = kMetaBlocks * (N / 32);
   if (threadIdx.x == 0) sh.mine.bad = 0;
   __syncthreads();
   for (int s = w0; s < p.n_seqs; s += n_warps) {
@@ -298,7 +305,8 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThrea
 // L and above, both ascending.  A page in use with `before` of them in front of it is the
 // (L - 1 - before)-th from the end, so the sources are listed from their end, which needs
 // no count of the pages in use below L; the destinations are listed from the front.
-__global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThreads)
+template <int N>
+__global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(N)
     compact_kernel(const PagesMeta p) {
   __shared__ Share sh;
   pdl_launch_dependents();  // the copy launch waits for this one's end itself
@@ -308,7 +316,7 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThrea
   int32_t* const dst = sc.list + p.n_pages / 2;
   int p0, p1;
   block_range(p.n_pages, rank, p0, p1);
-  const int n_live = count_pages(p.refs, p0, p1, true, sh);
+  const int n_live = count_pages<N>(p.refs, p0, p1, true, sh);
   if (threadIdx.x == 0) {
     sh.mine.count = n_live;
     sh.mine.holes = 0;
@@ -321,14 +329,14 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThrea
     live += sh.all[b].count;
   }
   int holes = 0;
-  for (int c = p0; c < p1; c += kMetaThreads * kPagesPerThread) {
+  for (int c = p0; c < p1; c += N * kPagesPerThread) {
     const int q0 = c + (int)threadIdx.x * kPagesPerThread;
     uint32_t mask = 0;
 #pragma unroll
     for (int q = 0; q < kPagesPerThread; ++q)
       if (q0 + q < p1 && __ldcg(p.refs + q0 + q) > 0) mask |= 1u << q;
     int total;
-    int before = at + block_scan(__popc(mask), sh, total);
+    int before = at + block_scan<N>(__popc(mask), sh, total);
 #pragma unroll
     for (int q = 0; q < kPagesPerThread; ++q) {
       const int pg = q0 + q;
@@ -346,13 +354,13 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(kMetaThrea
     at += total;
   }
   int block_holes;
-  block_scan(holes, sh, block_holes);
+  block_scan<N>(holes, sh, block_holes);
   if (threadIdx.x == 0) sh.mine.holes = block_holes;
   exchange(sh, cl);
   int moves = 0;
 #pragma unroll
   for (int b = 0; b < kMetaBlocks; ++b) moves += sh.all[b].holes;
-  for (int m = rank * kMetaThreads + (int)threadIdx.x; m < moves; m += kMetaBlocks * kMetaThreads) {
+  for (int m = rank * N + (int)threadIdx.x; m < moves; m += kMetaBlocks * N) {
     const int from = __ldcg(sc.list + moves - 1 - m), to = __ldcg(dst + m);
     sc.to[from] = to;
     p.refs[to] = p.refs[from];
@@ -488,18 +496,27 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const PagesWrite p
 
 }  // namespace
 
+namespace {
+bool few(const PagesMeta& p) {
+  return p.n_seqs <= kMetaBlocks * kMetaFew / 32 && p.n_pages <= kMetaBlocks * kMetaFew * kPagesPerThread;
+}
+}  // namespace
+
 cudaError_t launch_pages_resize(const PagesMeta& p, cudaStream_t s) {
-  resize_kernel<<<kMetaBlocks, kMetaThreads, 0, s>>>(p);
+  if (few(p)) resize_kernel<kMetaFew><<<kMetaBlocks, kMetaFew, 0, s>>>(p);
+  else resize_kernel<kMetaMost><<<kMetaBlocks, kMetaMost, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_pages_fork(const PagesMeta& p, cudaStream_t s) {
-  fork_kernel<<<kMetaBlocks, kMetaThreads, 0, s>>>(p);
+  if (few(p)) fork_kernel<kMetaFew><<<kMetaBlocks, kMetaFew, 0, s>>>(p);
+  else fork_kernel<kMetaMost><<<kMetaBlocks, kMetaMost, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_pages_compact(const PagesMeta& p, cudaStream_t s) {
-  compact_kernel<<<kMetaBlocks, kMetaThreads, 0, s>>>(p);
+  if (few(p)) compact_kernel<kMetaFew><<<kMetaBlocks, kMetaFew, 0, s>>>(p);
+  else compact_kernel<kMetaMost><<<kMetaBlocks, kMetaMost, 0, s>>>(p);
   return cudaGetLastError();
 }
 
