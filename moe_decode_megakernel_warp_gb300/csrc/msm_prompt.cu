@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   using C = Cfg<HD>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t b_q[2], b_full[C::kStages], b_empty[C::kStages], b_clean[C::kStages], b_s[2], b_p[2],
-      b_o[2], b_turn[2], b_drain[2];
+      b_o[2], b_used[2], b_turn[2], b_drain[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_dead, s_taken;
   __shared__ Place s_place[kPromptThreads / 32];
@@ -271,6 +271,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       mbar_init(&b_s[t], 1);
       mbar_init(&b_p[t], 4);
       mbar_init(&b_o[t], 1);
+      mbar_init(&b_used[t], 1);
       mbar_init(&b_turn[t], 1);
       mbar_init(&b_drain[t], 1);
     }
@@ -303,8 +304,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       // ---- loads
       int i = 0, q_loads[2] = {0, 0};
       bool ok = true;
-      auto load_q = [&](int t) {  // once the work before is through with the place
-        if (q_loads[t] > 0 && !wait_bar(&b_o[t], (q_loads[t] - 1) & 1, dead)) return false;
+      // once the work before has its last scores: the next Q travels during that step's softmax
+      auto load_q = [&](int t) {
+        if (q_loads[t] > 0 && !wait_bar(&b_used[t], (q_loads[t] - 1) & 1, dead)) return false;
         ++q_loads[t];
         mbar_expect_tx(&b_q[t], C::kTileBytes);
         for (int x = 0; x < C::kBoxes; ++x)
@@ -374,18 +376,28 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       uint32_t clean_phase = 0;
       int steps = 0, loads = 0, turns = 0;  // of this tile's P and Q, and of the two threads, so far
       bool ok = true;
-      while (ok && next_work(p, place, n_work, w)) {
+      Work ahead;
+      for (bool more_work = next_work(p, place, n_work, ahead); ok && more_work;) {
+        w = ahead;
+        int k_st = -1;
+        const bool mine = t == 0 || w.two;  // without a second tile its thread only signs the ring
         if (lane == 0 && w.n > 0) {
-          const bool mine = t == 0 || w.two;  // without a second tile its thread only signs the ring
-          int k_st = ring.next(b_full, dead);
+          k_st = ring.next(b_full, dead);
           ok = k_st >= 0 && (!mine || wait_bar(&b_q[t], loads++ & 1, dead));
           if (ok && mine) {
             tc_fence_after();
             scores(k_st, false);
             tc_commit(&b_empty[k_st]);
+            if (w.n == 1) tc_commit(&b_used[t]);
           } else if (ok) {
             mbar_arrive(&b_empty[k_st], 1);
           }
+        }
+        __syncwarp();
+        // (looked up during the first softmax: behind the last product its loads wait for the
+        // results' stores, 1,500 to 5,000 cycles)
+        more_work = next_work(p, place, n_work, ahead);
+        if (lane == 0 && w.n > 0) {
           for (int j = 0; ok && j < w.n; ++j) {
             const bool more = j + 1 < w.n;
             const int v_st = ring.next(b_full, dead);
@@ -412,6 +424,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               // V(j) and K(j + 1) are used up together: one signal, on K's stage.  (The last V's comes
               // with the next work's first K.)
               tc_commit(&b_empty[k_st]);
+              if (j + 2 == w.n) tc_commit(&b_used[t]);
             } else {
               if (w.two) mbar_arrive(&b_turn[1 - t], 1);
               tc_commit(&b_o[t]);
@@ -441,17 +454,26 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (!w.partial(e >> 1)) continue;
           uint4* const v = reinterpret_cast<uint4*>(s_kv + st * C::kTileBytes);
           bool any = false;
-#pragma unroll 8
-          for (int c = lane; c < C::kTileBytes / 16; c += 32) {
-            const uint4 x = v[c];
+          // (kBatch loads at a time: one by one, as the stores below them would keep them, a tile took
+          // this warp longer than three steps of the products)
+          constexpr int kBatch = 16;
+          for (int c0 = lane; c0 < C::kTileBytes / 16; c0 += 32 * kBatch) {
+            uint4 x[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) x[i] = v[c0 + 32 * i];
             // an exponent of all ones carries into the sign's place
-            const uint32_t m = kE * 0x10001u, a = kLow * 0x10001u;
-            const uint32_t bad = (((x.x & m) + a) | ((x.y & m) + a) | ((x.z & m) + a) | ((x.w & m) + a)) & 0x80008000u;
-            if (bad) {
+            constexpr uint32_t m = kE * 0x10001u, a = kLow * 0x10001u;
+            uint32_t bad = 0;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+              bad |= ((x[i].x & m) + a) | ((x[i].y & m) + a) | ((x[i].z & m) + a) | ((x[i].w & m) + a);
+            if (bad & 0x80008000u) {
               any = true;
-              uint16_t* const el = reinterpret_cast<uint16_t*>(v + c);
-              for (int q = 0; q < 8; ++q)
-                if ((el[q] & kE) == kE) el[q] = 0;
+              for (int i = 0; i < kBatch; ++i) {
+                uint16_t* const el = reinterpret_cast<uint16_t*>(v + c0 + 32 * i);
+                for (int q = 0; q < 8; ++q)
+                  if ((el[q] & kE) == kE) el[q] = 0;
+              }
             }
           }
           if (any) {
@@ -537,12 +559,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
           mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         };
-        if (j == 0) {
-          m = -INFINITY;
+        // the first tile that a row sees (nothing of the row is in O and the sum yet)
+        if (__any_sync(0xffffffffu, m == -INFINITY)) {
+          float own = -INFINITY;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) m = max3(m, __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+            for (int i = 0; i < 32; i += 2) own = max3(own, __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+          if (m == -INFINITY) m = own;
         }
         weights();
         const bool grow = (mx - m) * scale > kGrow;
