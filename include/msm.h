@@ -518,7 +518,7 @@ msm_status msm_graph_create_spec(msm_model* target, msm_model* draft, const void
  * outside [0, n_pages).  Host errors of every call: MSM_ERR_INVALID_ARG (NULL or
  * misaligned pointers, sizes below 1, strides that are no multiple of 8 elements),
  * MSM_ERR_UNSUPPORTED (head_dim other than 64 or 128, n_q_heads / n_kv_heads other
- * than 1, 2, 4 or 8, 2^31 or more table entries, 2^32 or more rows in a pool);
+ * than 1, 2, 4 or 8, more than 65535 kv heads, 2^31 or more table entries, 2^32 or more rows in a pool);
  * nothing is enqueued then.  The calls leave the current device as it was.
  */
 typedef enum { MSM_BF16 = 0, MSM_FP16 = 1 } msm_dtype;
@@ -630,7 +630,7 @@ msm_status msm_pages_sync(const msm_pages* pages, void* stream);
  *            k and v may be NULL.
  * Host errors: MSM_ERR_INVALID_ARG (NULL or misaligned pointers, sizes out of range,
  * strides), MSM_ERR_UNSUPPORTED (head_dim other than 64 or 128, n_q_heads / n_kv_heads
- * other than 1, 2, 4 or 8, n_q or n_k of 2^27 or more).
+ * other than 1, 2, 4 or 8, more than 65535 kv heads, n_q or n_k of 2^27 or more).
  */
 typedef struct {
   int device;

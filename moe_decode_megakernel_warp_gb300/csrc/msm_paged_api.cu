@@ -75,6 +75,8 @@ msm_status check_pages(const msm_pages* c) {
               c->n_seqs > 0 && c->max_pages > 0,
           MSM_ERR_INVALID_ARG, "pages: non-positive size");
   REQUIRE(c->head_dim == 64 || c->head_dim == 128, MSM_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  // (a token's elements are counted in 32 bits)
+  REQUIRE(c->n_kv_heads < 65536, MSM_ERR_UNSUPPORTED, "pages: more than 65535 kv heads");
   REQUIRE((int64_t)c->n_seqs * c->max_pages < (int64_t(1) << 31), MSM_ERR_UNSUPPORTED, "pages: table too large");
   // (the kernels step past a sequence's end by up to a tile in 32 bits)
   REQUIRE((int64_t)c->max_pages * c->page_rows < (int64_t(1) << 31) - 4096, MSM_ERR_UNSUPPORTED,

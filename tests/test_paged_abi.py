@@ -26,7 +26,8 @@ BAD_PAGES = [
     (dict(n_kv_heads=-1), INVALID), (dict(n_seqs=0), INVALID), (dict(max_pages=0), INVALID),
     (dict(head_dim=96), UNSUPPORTED), (dict(head_dim=0), INVALID),
     (dict(n_seqs=1 << 16, max_pages=1 << 16), UNSUPPORTED), (dict(max_pages=1 << 20, page_rows=1 << 11), UNSUPPORTED),
-    (dict(n_pages=1 << 30), UNSUPPORTED), (dict(n_pages=1 << 29, page_rows=16), UNSUPPORTED),
+    (dict(n_kv_heads=1 << 16), UNSUPPORTED), (dict(n_pages=1 << 30), UNSUPPORTED),
+    (dict(n_pages=1 << 29, page_rows=16), UNSUPPORTED),
     (dict(ptrs=[BUF, 0]), INVALID), (dict(ptrs=[BUF + 8, BUF]), INVALID), (dict(k_pages=None), INVALID),
     (dict(table=None), INVALID), (dict(lens=None), INVALID), (dict(refs=None), INVALID), (dict(status=None), INVALID),
     (dict(scratch=None), INVALID), (dict(table=BUF + 2), INVALID), (dict(lens=BUF + 1), INVALID),
