@@ -22,9 +22,9 @@ namespace msm {
 namespace {
 
 // Threads per block (N below): 1,024, or 256 where the eight blocks' 64 warps have a sequence each
-// at most and 16,384 pages are one look -- their barriers cost less (a resize of 32 sequences 8.6
-// -> 7.4 us, a compaction of 150 pages 8.8 -> 7.8) and only larger caches miss the others (a fork of 64 sequences into 256: 7.0 us
-// with 1,024, 9.0 with 256).
+// at most and 16,384 pages are one look: their barriers cost less (a resize of 32 sequences 8.6
+// -> 7.4 us, a compaction of 150 pages 8.8 -> 7.8), and only larger caches miss the others (a fork
+// of 64 sequences into 256: 7.0 us with 1,024, 9.0 with 256).
 constexpr int kMetaMost = 1024, kMetaFew = 256;
 constexpr int kMetaBlocks = 8;      // the portable cluster size
 constexpr int kPagesPerThread = 8;  // pages one thread looks at per step of a scan
