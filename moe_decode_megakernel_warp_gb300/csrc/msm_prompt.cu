@@ -25,9 +25,9 @@
 // at the tensor cores' rate -- Q K^T takes all of shared memory's bandwidth, which the TMA
 // writes share), two tiles of which overlap: about 2,900 cycles for 256 rows x 128 keys, 2,048 of
 // them products.  On one GB300 (1,926 TFLOP/s measured cuBLAS burst), 32 query heads on 8 kv
-// heads of 128, bf16: 16,384 tokens 1.41 ms (1,560 TFLOP/s), 2,048 tokens 37 us, 32,768
-// tokens on a window of 2,048 0.85 ms (1,250 TFLOP/s: two of 17 key tiles are masked, and a
-// piece of work ends every 17); head_dim 64 1.24 ms (890 TFLOP/s: as many exponentials for half
+// heads of 128, bf16: 16,384 tokens 1.39 ms (1,585 TFLOP/s), 2,048 tokens 35 us, 32,768
+// tokens on a window of 2,048 0.84 ms (1,275 TFLOP/s: two of 17 key tiles are masked, 800 cycles
+// each, and the end of a piece of work, every 17, takes 4,500); head_dim 64 1.24 ms (890 TFLOP/s: as many exponentials for half
 // the products).  Tried and slower: P handed over in two or four parts (+5, +13 %), results
 // written by four more warps (+5 %; fewer registers for the softmax) or through shared memory
 // with four stages of the ring instead of five (+4 %), 192 or 208 registers (+7, +2 %).
