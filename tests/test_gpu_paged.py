@@ -568,6 +568,24 @@ def test_many_short_prompts(n_seqs, most):
     assert_close(msm.prompt_attention(q, k, v, ints(st)), want, tol)
 
 
+@pytest.mark.parametrize("group", [1, 8])
+@pytest.mark.parametrize("window", [0, 100, 5000])
+def test_work_of_many_resumed_prompts(window, group):
+    """Prompts of unlike lengths and cached rows, keys missing in some, more than one look at the
+    list of sequences takes in, one look with a single prompt: every row is worked on once."""
+    torch, msm = _mods()
+    rng = np.random.default_rng(window + group)
+    ql = np.concatenate([rng.integers(0, 600, 32), [0] * 7, [333], [0] * 24, rng.integers(0, 90, 9)])
+    kl = np.maximum(0, ql + rng.integers(-40, 700, len(ql)) * rng.integers(0, 2, len(ql)))
+    qs, ks = starts_of(ql), starts_of(kl)
+    q = randn("bf16", qs[-1], group, 64, seed=1).cuda()
+    k, v = (randn("bf16", ks[-1], 1, 64, seed=i).cuda() for i in (2, 3))
+    out = torch.full_like(q, float("nan"))
+    msm.prompt_attention(q, k, v, ints(qs), ints(ks), window=window, out=out)
+    want, tol = prompt_want(q, k, v, qs, ks, window, 0.125, "bf16")
+    assert_close(out, want, tol)
+
+
 def test_prompts_on_two_streams_at_once():
     torch, msm = _mods()
     n = 3000
