@@ -260,9 +260,11 @@ __device__ __forceinline__ bool next_work(const PromptAttn& p, volatile Place* p
 }
 
 // The ring of K and V tiles, in the order K(0), V(0), K(1), V(1), ... of one piece of work
-// after the other, as one of its readers walks it.  Every reader waits for every tile and
-// signs it off, so that none can fall or run a turn of the ring behind or ahead (a barrier only tells
-// neighbouring phases apart).
+// after the other, as one of its readers walks it.  Every reader waits for every tile, so that none
+// can fall or run a turn of the ring behind or ahead (a barrier only tells neighbouring phases
+// apart).  A V has no signal of its own: a reader releases it with the K behind it, which for the last V of a
+// piece of work is the next piece's first K.  That signal therefore has to come after the
+// products that read the V, also from the thread of a tile that the next piece does not have.
 template <int kStages>
 struct Ring {
   int st = 0;
@@ -422,7 +424,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             tc_commit(&b_empty[k_st]);
             if (w.n == 1) tc_commit(&b_used[t]);
           } else if (ok) {
-            mbar_arrive(&b_empty[k_st], 1);
+            // (a commit, not an arrival: this thread's product of the last piece's last V, which this
+            // releases too, may still be under way)
+            tc_commit(&b_empty[k_st]);
           }
         }
         __syncwarp();

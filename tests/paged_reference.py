@@ -147,3 +147,31 @@ def attend(q, k, v, shift, window, scale, kind):
             if kind == "fp16":
                 tol[i, h] += 2.0 ** -25 * np.abs(vv).sum(0) / l
     return out, tol * (1 + 2 * u) + 1e-30
+
+
+def attend_matrix(q, k, v, shift, window, scale, kind):
+    """attend() with a head's queries and keys as one matrix (for batches of many rows)."""
+    nq, hq, hd = q.shape
+    nk, hkv, _ = k.shape
+    group = hq // hkv
+    u = EPS[kind]
+    out, tol = np.zeros((nq, hq, hd)), np.zeros((nq, hq, hd))
+    gap = np.arange(nq)[:, None] + shift - np.arange(nk)
+    see = (gap >= 0) & ((gap < window) if window else True)
+    rows = np.flatnonzero(see.any(1))
+    see = see[rows]
+    if not len(rows):
+        return out, tol + 1e-30
+    for h in range(hq):
+        kk, vv, qq = k[:, h // group], v[:, h // group], q[rows, h]
+        s = np.where(see, qq @ kk.T * scale, -np.inf)
+        e = np.exp(s - s.max(1, keepdims=True))
+        l = e.sum(1, keepdims=True)
+        p = e / l
+        o = p @ vv
+        b = np.where(see, abs(scale) * (np.abs(qq) @ np.abs(kk).T), 0.0).max(1, keepdims=True)
+        t = u * np.abs(o) + (u + 2 * hd * 2.0 ** -23 * b + 2.0 ** -16) * (p @ np.abs(vv))
+        if kind == "fp16":
+            t += 2.0 ** -25 * (see @ np.abs(vv)) / l
+        out[rows, h], tol[rows, h] = o, t
+    return out, tol * (1 + 2 * u) + 1e-30

@@ -3,7 +3,7 @@
 import numpy as np
 import pytest
 
-from paged_reference import Pages, attend
+from paged_reference import Pages, attend, attend_matrix
 
 pytestmark = pytest.mark.gpu
 
@@ -584,6 +584,33 @@ def test_work_of_many_resumed_prompts(window, group):
     msm.prompt_attention(q, k, v, ints(qs), ints(ks), window=window, out=out)
     want, tol = prompt_want(q, k, v, qs, ks, window, 0.125, "bf16")
     assert_close(out, want, tol)
+
+
+@pytest.mark.parametrize("kind,hd", [("bf16", 128), ("fp16", 128), ("bf16", 64)])
+@pytest.mark.parametrize("window", [0, 300])
+def test_blocks_with_several_pieces_of_work(kind, hd, window):
+    """Far more pieces of work than blocks, pieces of two tiles (more than 128 rows) and of one by
+    turns, both with several key tiles: what a block's pieces hand on to one another (the ring's
+    last values, Q, the results in tensor memory) has to be through when the next one takes it."""
+    torch, msm = _mods()
+    rng = np.random.default_rng(hd + window)
+    hkv, group = 8, 4
+    # a block takes 64 tokens: every other prompt's last piece has at most 32
+    ql = [int(64 * rng.integers(0, 3) + rng.integers(1, 33) + (32 if i % 2 else 0)) for i in range(40)]
+    kl = [n + int(rng.integers(0, 500)) for n in ql]
+    qs, ks = starts_of(ql), starts_of(kl)
+    q = randn(kind, qs[-1], hkv * group, hd, seed=1).cuda()
+    k, v = (randn(kind, ks[-1], hkv, hd, seed=i).cuda() for i in (2, 3))
+    pieces = hkv * sum(-(-n // 64) for n in ql)
+    assert pieces > 3 * torch.cuda.get_device_properties(0).multi_processor_count
+    out = torch.full_like(q, float("nan"))
+    msm.prompt_attention(q, k, v, ints(qs), ints(ks), window=window, out=out)
+    for s in range(len(ql)):
+        a, b = slice(qs[s], qs[s + 1]), slice(ks[s], ks[s + 1])
+        want, tol = attend_matrix(f64(q[a]), f64(k[b]), f64(v[b]), kl[s] - ql[s], window, hd ** -0.5, kind)
+        assert_close(out[a], want, tol, "sequence %d" % s)
+    for _ in range(20):
+        assert np.array_equal(bits(msm.prompt_attention(q, k, v, ints(qs), ints(ks), window=window)), bits(out))
 
 
 def test_prompts_on_two_streams_at_once():

@@ -66,3 +66,14 @@ def test_attention_equals_the_masked_softmax(shift, window):
     w = e / np.maximum(e.sum(-1, keepdims=True), 1e-300)
     assert np.allclose(out, np.einsum("hij,jhd->ihd", w, np.repeat(v, 2, 1)))
     assert (tol >= 0).all() and (out[~mask.any(1)] == 0).all()
+
+
+@pytest.mark.parametrize("nq,nk,window,kind", [(40, 40, 0, "bf16"), (33, 90, 20, "fp16"), (50, 20, 0, "bf16"),
+                                               (30, 10, 4, "fp16"), (5, 0, 0, "bf16"), (1, 200, 0, "fp16")])
+def test_the_two_forms_of_the_attention_agree(nq, nk, window, kind):
+    from paged_reference import attend_matrix
+    rng = np.random.default_rng(nq)
+    q, k, v = (rng.standard_normal((n, h, 16)) for n, h in ((nq, 4), (nk, 2), (nk, 2)))
+    for scale in (0.25, -1.0, 0.0):
+        a, b = (f(q, k, v, nk - nq, window, scale, kind) for f in (attend, attend_matrix))
+        assert np.allclose(a[0], b[0], rtol=0, atol=1e-12) and np.allclose(a[1], b[1], rtol=1e-9, atol=1e-30)
