@@ -352,7 +352,9 @@ msm_status msm_prompt_attention(const msm_prompt* a, void* stream) {
   p.n_k = a->n_k;
   p.n_kv_heads = a->n_kv_heads;
   p.group = a->n_q_heads / a->n_kv_heads;
-  p.window = a->window;
+  // (a window of all keys hides none; the kernel's differences of positions and a smaller one stay
+  // far inside 32 bits, also for queries in front of the first key)
+  p.window = a->window < a->n_k ? a->window : 0;
   p.scale_log2 = a->scale * kLog2e;
   CKP(launch_prompt_attn(p, a->dtype, a->head_dim, sms, static_cast<cudaStream_t>(stream)));
   return MSM_OK;

@@ -294,6 +294,15 @@ def test_paged_attention_equals_the_formula(kind, hd, hkv, group, rows):
         assert_close(got, want, tol, "window %d" % window)
 
 
+def test_paged_windows_longer_than_the_sequences():
+    rng = np.random.default_rng(17)
+    c, _, _ = filled(rng, "bf16", LENS, 16, 2, 64)
+    q = randn("bf16", len(LENS), 4, 64, seed=9).cuda()
+    want = bits(c.attention(0, q))
+    for window in (1000, 1001, 2 ** 30, 2 ** 31 - 1):
+        assert np.array_equal(bits(c.attention(0, q, window=window)), want)
+
+
 @pytest.mark.parametrize("kind,lens,rows,window", [
     ("bf16", [40000], 64, 0), ("fp16", [33001, 7], 48, 0), ("bf16", [20000] * 3, 16, 5000),
     ("bf16", [1] * 700, 16, 0), ("fp16", [100 + 3 * i for i in range(300)], 32, 0), ("bf16", [39999, 0, 0, 1], 100, 0)])
@@ -483,6 +492,19 @@ def test_resumed_prompts_and_rows_without_keys(hd, group, qlens, klens):
         got = msm.prompt_attention(q, k, v, ints(qs), ints(ks), window=window)
         want, tol = prompt_want(q, k[:ks[-1]], v[:ks[-1]], qs, ks, window, hd ** -0.5, "bf16")
         assert_close(got, want, tol, "window %d" % window)
+
+
+@pytest.mark.parametrize("qlens,klens", [([70, 20], [30, 0]), ([20], [10]), ([300, 5], [40, 700]), ([40], [40])])
+@pytest.mark.parametrize("window", [40, 45, 700, 740, 2 ** 30, 2 ** 31 - 1])
+def test_windows_longer_than_the_keys(qlens, klens, window):
+    """Up to the largest one, which callers pass for none; queries in front of the first key."""
+    torch, msm = _mods()
+    qs, ks = starts_of(qlens), starts_of(klens)
+    q, k, v = (randn("bf16", n, h, 64, seed=h).cuda() for n, h in ((qs[-1], 4), (ks[-1], 2), (ks[-1], 1)))
+    v = v.expand(-1, 2, 64).contiguous()
+    got = msm.prompt_attention(q, k, v, ints(qs), ints(ks), window=window)
+    want, tol = prompt_want(q, k, v, qs, ks, window, 0.125, "bf16")
+    assert_close(got, want, tol)
 
 
 @pytest.mark.parametrize("kind,n,hq,hkv,hd,window", [("bf16", 1500, 2, 1, 128, 0), ("fp16", 1100, 1, 1, 64, 0),
