@@ -129,7 +129,8 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(N)
   const int p_rest = p0 + N * kPagesPerThread;  // the share's pages behind those
 
   // 1. each sequence: are its lengths and the pages it gives up in range, how many pages
-  //    does it lack, does it have to leave a shared last page (offset = 2 pages + leave)
+  //    does it lack, does it have to leave a shared last page (offset = 2 pages + leave, unsigned:
+  //    the sequences' needs add up to fewer than 2^31 pages, a table's entries)
   for (int s = s0 + wid; s < s1; s += (N / 32)) {
     const int old = p.lens[s], asked = p.arg[s], now = asked == -1 ? old : asked;
     bool bad = old < 0 || old > cap || now < 0 || now > cap;
@@ -152,17 +153,17 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(N)
       sh.mine.bad = 1;
       need = leave = 0;
     }
-    if (lane == 0) sc.offset[s] = 2 * need + leave;
+    if (lane == 0) sc.offset[s] = (int32_t)(2u * (uint32_t)need + (uint32_t)leave);
   }
   __syncthreads();
   // 2. prefix of the needs over the block's sequences, free pages of its share of the pool
   int base = 0;
   for (int c = s0; c < s1; c += N) {
     const int s = c + (int)threadIdx.x;
-    const int e = s < s1 ? sc.offset[s] : 0;
+    const uint32_t e = s < s1 ? (uint32_t)sc.offset[s] : 0u;
     int total;
-    const int before = block_scan<N>(e >> 1, sh, total);
-    if (s < s1) sc.offset[s] = 2 * (base + before) + (e & 1);
+    const int before = block_scan<N>((int)(e >> 1), sh, total);
+    if (s < s1) sc.offset[s] = (int32_t)(2u * (uint32_t)(base + before) + (e & 1u));
     base += total;
   }
   int n_free;
@@ -226,9 +227,9 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(N)
     if (now == old) continue;
     int32_t* row = p.table + (size_t)s * p.max_pages;
     const int n_old = ceil_div(old, p.page_rows), n_new = ceil_div(now, p.page_rows);
-    const int e = sc.offset[s];
-    int off = need_before + (e >> 1);
-    if (e & 1) {
+    const uint32_t e = (uint32_t)sc.offset[s];
+    int off = need_before + (int)(e >> 1);
+    if (e & 1u) {
       if (lane == 0) {
         const int j = old / p.page_rows, from = row[j], to = __ldcg(sc.list + off);
         const int i = atomicAdd(sc.head, 1);

@@ -418,6 +418,28 @@ def test_the_wrappers_refuse_what_does_not_fit():
     c.sync()
 
 
+def test_tables_of_more_than_2_to_the_30_pages():
+    """The needs of sequences whose tables hold more pages than any pool (a 4.3 GB table): no
+    page left, and nothing changed; ordinary lengths in such a table are served."""
+    torch, msm = _mods()
+    for n_seqs, width, new in ((1, (1 << 30) + 64, [(1 << 30) + 1]), (1, (1 << 30) + 64, [1 << 30]),
+                               (2, (1 << 29) + 64, [(1 << 29) + 1, (1 << 29) + 7]), (1, (1 << 30) + 64, [9])):
+        pool = torch.zeros((8, 1, 1, 64), dtype=torch.bfloat16, device="cuda")
+        table = torch.empty((n_seqs, width), dtype=torch.int32, device="cuda")
+        c = msm.PagedCache([pool], [pool.clone()], table, ints([0] * n_seqs), ints([0] * 8))
+        c.resize(ints([3] + [0] * (n_seqs - 1)))
+        c.sync()
+        kept = [c.lens.clone(), c.refs.clone(), table[:, :16].clone()]
+        c.resize(ints(new))
+        with pytest.raises(msm.MsmError, match="no free page"):
+            c.sync()
+        assert all(torch.equal(a, b) for a, b in zip(kept, (c.lens, c.refs, table[:, :16])))
+        c.resize(ints([8] + [0] * (n_seqs - 1)))
+        c.sync()
+        assert table[0, :8].tolist() == list(range(8)) and (c.refs == 1).all()
+        del pool, table, c
+
+
 def test_pools_of_more_than_2_to_the_31_elements():
     """The last pages of a 4.6 GB pool: written, read, copied and moved."""
     torch, msm = _mods()
