@@ -498,7 +498,8 @@ msm_status msm_graph_create_spec(msm_model* target, msm_model* draft, const void
  *                  -1 behind its last page
  *   lens           int32 [n_seqs]: rows of each sequence (0: an unused slot)
  *   refs           int32 [n_pages]: how many sequences hold the page; 0: free
- *   status         int32 [1]: 0, or the first error that a kernel met
+ *   status         int32 [1]: 0, or what msm_pages_sync makes of it: the first error that
+ *                  a kernel met
  *   scratch        int32 [msm_pages_scratch_ints(n_pages, n_seqs)], contents of no
  *                  interest between calls
  * Row r of sequence s is row r % page_rows of page table[s][r / page_rows].  All of
@@ -509,7 +510,11 @@ msm_status msm_graph_create_spec(msm_model* target, msm_model* draft, const void
  * and without a host round trip, so a stream capture records them.  Their results do
  * not depend on timing: pages are always taken in the order of their index, the lowest
  * free one first.  Each of them either does what it was asked or, when it finds an
- * error (below), changes nothing and leaves the error in status.  Calls on one cache
+ * error (below), changes nothing and leaves the error in status.  From a resize or fork that
+ * was not done until msm_pages_sync has returned the error, no call changes the cache:
+ * resize, fork, compact and msm_pages_write do nothing (the lengths are not those
+ * that they were made for; the rows of a write would replace the last ones that are
+ * there), and msm_paged_attention reads the sequences as they stand.  Calls on one cache
  * must be ordered (one stream, or events); msm_pages_write and msm_paged_attention of
  * different layers may overlap each other.
  *
@@ -573,7 +578,7 @@ msm_status msm_pages_compact(const msm_pages* pages, void* stream);
  *   starts  device int32 [n_seqs + 1], ascending from 0; tokens at or behind
  *           starts[n_seqs] are ignored
  * Device error: MSM_ERR_INVALID_ARG for a token without a row, or whose page is free
- * or shared; that token is left out.
+ * or shared; that token is left out (the others are stored, and later calls too).
  */
 msm_status msm_pages_write(const msm_pages* pages, int layer, const void* k, const void* v, int64_t k_token_stride,
                            int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,

@@ -12,8 +12,12 @@ namespace msm {
 msm_status report(msm_status st, const char* msg);
 msm_status report_cuda(cudaError_t e, const char* what);
 
-// device status word of a cache: the msm_status in the low byte, the call above it
+// device status word of a cache: the msm_status of the first error in the low byte, its call in the
+// next one, and whether a resize or fork was refused.  From then on, until msm_pages_sync clears the
+// word, no call changes the cache: the lengths are not those that the following calls
+// count on (a write would store its rows over the last ones of the history).
 enum PagesCall { kCallResize = 1, kCallFork = 2, kCallWrite = 3, kCallAttention = 4 };
+constexpr int kPagesStopped = 1 << 16;
 
 // scratch of a cache: counters, one offset per sequence, a list of row copies (source
 // page, destination page, rows) per sequence, and two page-sized arrays

@@ -291,7 +291,7 @@ msm_status msm_pages_sync(const msm_pages* c, void* stream) {
   if (word == 0) return MSM_OK;
   CKP(cudaMemsetAsync(c->status, 0, sizeof(word), s));
   CKP(cudaStreamSynchronize(s));
-  const int code = word & 0xFF, call = word >> 8;
+  const int code = word & 0xFF, call = word >> 8 & 0xFF;
   const char* const where = call == kCallResize      ? "msm_pages_resize"
                             : call == kCallFork      ? "msm_pages_fork"
                             : call == kCallWrite     ? "msm_pages_write"

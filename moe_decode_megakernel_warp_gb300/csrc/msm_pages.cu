@@ -32,6 +32,13 @@ constexpr int kPagesPerThread = 8;  // pages one thread looks at per step of a s
 __device__ __forceinline__ void latch(int32_t* status, int code, int call) {
   atomicCAS(status, 0, code | (call << 8));
 }
+// a resize or fork that is not done: the calls behind it change nothing either
+__device__ __forceinline__ void refuse(int32_t* status, int code, int call) {
+  latch(status, code, call);
+  atomicOr(status, kPagesStopped);
+}
+// (only ever set by a call that the others are ordered behind, so all threads of a call see the same)
+__device__ __forceinline__ bool stopped(const int32_t* status) { return (__ldcg(status) & kPagesStopped) != 0; }
 
 struct BlockShare {        // what a block tells the others
   int need, count, holes;  // missing pages, free (or live) pages, holes below the live count
@@ -117,6 +124,7 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(N)
   block_range(p.n_pages, rank, p0, p1);
   if (threadIdx.x == 0) sh.mine.bad = 0;
   if (rank == 0 && threadIdx.x == 0) sc.head[0] = 0;
+  const bool stop = stopped(p.status);
   __syncthreads();
 
   // free pages among this thread's first kPagesPerThread of the block's share (their loads
@@ -186,8 +194,8 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(N)
     free_all += sh.all[b].count;
     bad |= sh.all[b].bad;
   }
-  if (bad || need_all > free_all) {
-    if (rank == 0 && threadIdx.x == 0) latch(p.status, bad ? MSM_ERR_INVALID_ARG : MSM_ERR_OOM, kCallResize);
+  if (stop || bad || need_all > free_all) {
+    if (!stop && rank == 0 && threadIdx.x == 0) refuse(p.status, bad ? MSM_ERR_INVALID_ARG : MSM_ERR_OOM, kCallResize);
     cl.sync();  // a block's shared memory stays until the others have read it
     return;
   }
@@ -263,6 +271,7 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(N)
   const int rank = (int)cl.block_rank(), lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int64_t cap = (int64_t)p.max_pages * p.page_rows;
   const int w0 = rank * (N / 32) + wid, n_warps = kMetaBlocks * (N / 32);
+  const bool stop = stopped(p.status);
   if (threadIdx.x == 0) sh.mine.bad = 0;
   __syncthreads();
   for (int s = w0; s < p.n_seqs; s += n_warps) {
@@ -285,8 +294,8 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(N)
 #pragma unroll
   for (int b = 0; b < kMetaBlocks; ++b) bad |= sh.all[b].bad;
   cl.sync();
-  if (bad) {
-    if (rank == 0 && threadIdx.x == 0) latch(p.status, MSM_ERR_INVALID_ARG, kCallFork);
+  if (stop || bad) {
+    if (!stop && rank == 0 && threadIdx.x == 0) refuse(p.status, MSM_ERR_INVALID_ARG, kCallFork);
     return;
   }
   for (int s = w0; s < p.n_seqs; s += n_warps) {
@@ -317,6 +326,7 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(N)
   int32_t* const dst = sc.list + p.n_pages / 2;
   int p0, p1;
   block_range(p.n_pages, rank, p0, p1);
+  const bool stop = stopped(p.status);
   const int n_live = count_pages<N>(p.refs, p0, p1, true, sh);
   if (threadIdx.x == 0) {
     sh.mine.count = n_live;
@@ -360,7 +370,7 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(N)
   exchange(sh, cl);
   int moves = 0;
 #pragma unroll
-  for (int b = 0; b < kMetaBlocks; ++b) moves += sh.all[b].holes;
+  for (int b = 0; b < kMetaBlocks; ++b) moves += stop ? 0 : sh.all[b].holes;
   for (int m = rank * N + (int)threadIdx.x; m < moves; m += kMetaBlocks * N) {
     const int from = __ldcg(sc.list + moves - 1 - m), to = __ldcg(dst + m);
     sc.to[from] = to;
@@ -369,7 +379,7 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(N)
   }
   if (rank == 0 && threadIdx.x == 0) {
     sc.head[0] = moves;
-    sc.head[1] = live;
+    sc.head[1] = stop ? p.n_pages : live;  // pages from here on are renumbered
   }
   cl.sync();  // a block's shared memory stays until the others have read it
 }
@@ -446,6 +456,7 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const PagesWrite p
   const int lane = threadIdx.x & 31;
   const int t = (int)((blockIdx.x * (int64_t)kWriteThreads + threadIdx.x) >> 5);
   if (t >= p.n_tokens || t >= p.starts[p.m.n_seqs]) return;
+  const bool stop = stopped(p.m.status);
   const int half = p.n_kv_heads << p.row_shift, n = 2 * half;
   auto load = [&](int i) -> uint4 {
     const bool v = i >= half;
@@ -464,6 +475,7 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const PagesWrite p
     lo += le ? (31 - __clz(le)) * step : 0;
     hi = min(hi, lo + step);
   }
+  if (stop) return;
   const int first = p.starts[lo], end = p.starts[lo + 1];
   const int64_t pos = (int64_t)p.m.lens[lo] - end + t;
   bool ok = t >= first && t < end && pos >= 0 && pos < (int64_t)p.m.max_pages * p.m.page_rows;

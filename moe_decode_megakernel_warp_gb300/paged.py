@@ -66,7 +66,8 @@ class PagedCache:
     [n_seqs], ``refs`` int32 [n_pages].  ``PagedCache.allocate`` makes an empty one.
 
     ``resize``, ``fork``, ``compact`` and ``write`` change these tensors on the device, in
-    stream order and without a host round trip; ``sync`` waits and raises what they met."""
+    stream order and without a host round trip; ``sync`` waits and raises what they met.  After a
+    ``resize`` or ``fork`` that could not be done none of them changes anything until ``sync``."""
 
     def __init__(self, k_pages, v_pages, table, lens, refs):
         if _torch is None:

@@ -189,6 +189,87 @@ def test_refusals_on_the_device_change_nothing():
     assert c.call("resize", [-1, -1, 64, -1]) is None
 
 
+def contents(c):
+    return [t.clone() for t in [c.table, c.lens, c.refs] + c.k_pages + c.v_pages]
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("what", ["oom", "length", "fork"])
+def test_nothing_changes_between_a_refused_call_and_its_report(what, captured):
+    """Full pages, held once: the rows of a write behind a resize that found no page would
+    replace the last ones of the history."""
+    torch, msm = _mods()
+    c = Both(np.random.default_rng(30), 2, 5, 16, 2, 64, 4, 4)
+    c.call("resize", [32, 16, 0, 0])
+    g = c.gpu
+    kv = randn("bf16", 5, 2, 64, seed=1).cuda()
+    st = ints([0, 4, 5, 5, 5])
+    bad, grow, shrink = ints({"length": [65, 17, -1, -1]}.get(what, [64, 17, -1, -1])), ints([36, 17, 0, 0]), ints([1, 0, 0, 0])
+    parents, wrong = ints([-1, -1, 0, -1]), ints([-1, 0, -1, -1])
+
+    def step():
+        if what == "fork":
+            g.fork(wrong)
+        else:
+            g.resize(bad)
+        for layer in range(2):
+            g.write(layer, kv, kv, st)
+        g.fork(parents)
+        g.write(0, kv, kv, st)
+        g.resize(grow)
+        g.resize(shrink)
+        g.compact()
+        g.write(0, kv[:1], kv[:1], ints_1)
+    ints_1 = ints([0, 1, 1, 1, 1])
+    # a hole in front of the pages in use, for compact
+    c.call("resize", [-1, -1, 5, -1])
+    c.call("resize", [16, -1, -1, -1])
+    c.call("resize", [0, -1, -1, -1])
+    c.call("resize", [16, 16, 0, -1])
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+    before = contents(g)
+    for _ in range(2):
+        graph.replay() if captured else step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(before, contents(g)))
+        q = randn("bf16", 4, 2, 64, seed=2).cuda()
+        seen = g.attention(0, q)  # the sequences as they stand
+        with pytest.raises(msm.MsmError, match="msm_pages_fork" if what == "fork" else "msm_pages_resize") as e:
+            g.sync()
+        assert msm.STATUS_NAMES[e.value.code] == ("MSM_ERR_OOM" if what == "oom" else "MSM_ERR_INVALID_ARG")
+        assert np.array_equal(bits(seen), bits(g.attention(0, q)))
+    # reported: the calls work again
+    c.call("resize", [20, 17, -1, -1])
+    c.write([4, 1, 0, 0], 5)
+    c.call("fork", [-1, -1, 0, -1])
+    c.call("compact")
+
+
+def test_an_earlier_error_does_not_hide_a_refusal():
+    """A write that left a token out stops nothing, but the refused resize behind it does."""
+    torch, msm = _mods()
+    c = Both(np.random.default_rng(31), 1, 3, 16, 2, 64, 2, 4)
+    c.call("resize", [32, 3])
+    g, kv = c.gpu, randn("bf16", 5, 2, 64, seed=1).cuda()
+    g.write(0, kv, kv, ints([0, 0, 5]))   # two of the five tokens have no row
+    g.write(0, kv, kv, ints([0, 1, 1]))   # stored
+    torch.cuda.synchronize()
+    c.ref.write(c.ref.pools[0], bits(kv)[2:], [0, 0, 3])
+    c.ref.write(c.ref.pools[1], bits(kv)[2:], [0, 0, 3])
+    c.ref.write(c.ref.pools[0], bits(kv), [0, 1, 1])
+    c.ref.write(c.ref.pools[1], bits(kv), [0, 1, 1])
+    c.same()
+    g.resize(ints([36, -1]))
+    g.write(0, kv, kv, ints([0, 4, 4]))
+    with pytest.raises(msm.MsmError, match="msm_pages_write"):
+        g.sync()
+    c.same()
+    g.sync()
+
+
 def test_write_leaves_out_tokens_without_a_row_of_their_own():
     torch, msm = _mods()
     rng = np.random.default_rng(7)
