@@ -601,7 +601,7 @@ msm_status msm_pages_write(const msm_pages* pages, int layer, const void* k, con
  *              share a workspace must not overlap on the GPU (neither must graphs that
  *              recorded them), and must have the same n_q_heads, n_kv_heads and head_dim.
  * Device error: MSM_ERR_INVALID_ARG for a row on a page outside the pool; such rows are
- * left out.
+ * left out (a sequence of which no row is left gives zeros).
  */
 size_t msm_paged_attention_workspace(const msm_pages* pages, int n_q_heads);
 msm_status msm_paged_attention(const msm_pages* pages, int layer, const void* q, int64_t q_seq_stride,

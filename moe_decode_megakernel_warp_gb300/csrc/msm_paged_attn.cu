@@ -58,6 +58,13 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   return v;
 }
 
+// The sum of a row's weights where no key took part (every row that a sequence reads lies on pages
+// outside the pool): -0, which stays -0 through sums of such and products with factors, and which
+// becomes 0 with any other sum -- a sum of 0 is that of scores that are all -inf.
+constexpr float kNoKeys = -0.f;
+// 1 / l, and 0 where no key took part
+__device__ __forceinline__ float inverse_sum(float l) { return __float_as_uint(l) == 0x80000000u ? 0.f : 1.f / l; }
+
 // a partial result in the workspace: maxima, sums, outputs
 __host__ __device__ constexpr int part_floats(int group, int hd) { return 2 * kHeads + group * hd; }
 
@@ -168,7 +175,7 @@ __device__ void join_parts(const PagedAttn& p, int b0, int i0, int step, int n, 
   };
   for (int c = threadIdx.x; c < p.group * HD / 4; c += kThreadsA) {  // float4 columns
     const int hd = 4 * c / HD;
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = kNoKeys;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k0 = 0; k0 < n; k0 += kJoinLoads) {
       float mq[kJoinLoads], lq[kJoinLoads];
@@ -176,7 +183,7 @@ __device__ void join_parts(const PagedAttn& p, int b0, int i0, int step, int n, 
 #pragma unroll
       for (int q = 0; q < kJoinLoads; ++q) {
         mq[q] = -INFINITY;
-        lq[q] = 0.f;
+        lq[q] = kNoKeys;
         v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (k0 + q < n) {
           const float* const a = part(k0 + q);
@@ -207,7 +214,7 @@ __device__ void join_parts(const PagedAttn& p, int b0, int i0, int step, int n, 
       m = mn;
     }
     if (final) {
-      const float inv = 1.f / l;
+      const float inv = inverse_sum(l);
       uint2 o;
       o.x = El::pack(x.x * inv, x.y * inv);
       o.y = El::pack(x.z * inv, x.w * inv);
@@ -410,6 +417,7 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
   load_q();
   while (more) {
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2t, 2t + 1
+    uint32_t seen = 0;  // rows that took part
     float o[HD / 16][4];
 #pragma unroll
     for (int i = 0; i < HD / 16; ++i)
@@ -419,6 +427,7 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
       cp_async_wait<kAhead - 1>();
       __syncwarp();
       const uint32_t rows = queue[0];
+      seen |= rows;
       const uint32_t kb = ring + stage * C::kStageBytes, vb = kb + C::kChunk * C::kRowBytes;
       stage = stage + 1 == C::kStages ? 0 : stage + 1;
 #pragma unroll
@@ -506,8 +515,8 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
     if (g == 0) {
       s_m[wid][2 * t] = m0;
       s_m[wid][2 * t + 1] = m1;
-      s_l[wid][2 * t] = l0;
-      s_l[wid][2 * t + 1] = l1;
+      s_l[wid][2 * t] = seen ? l0 : kNoKeys;
+      s_l[wid][2 * t + 1] = seen ? l1 : kNoKeys;
     }
 #pragma unroll
     for (int j = 0; j < VB; ++j)
@@ -531,7 +540,7 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
 #pragma unroll
       for (int q = 0; q < kWarps; ++q) m = fmaxf(m, s_m[q][hd]);
       const float ref = m == -INFINITY ? 0.f : m;
-      float l = 0.f, x = 0.f, y = 0.f;
+      float l = kNoKeys, x = 0.f, y = 0.f;
 #pragma unroll
       for (int q = 0; q < kWarps; ++q) {
         // (a NaN sum passes on; a warp without rows has m = -inf and zeros)
@@ -542,7 +551,7 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
         y += f * v.y;
       }
       if (whole) {
-        const float inv = 1.f / l;
+        const float inv = inverse_sum(l);
         *reinterpret_cast<uint32_t*>(p.out + done.s * p.out_seq + (done.h * p.group + hd) * p.out_head + d) =
             El::pack(x * inv, y * inv);
       } else {

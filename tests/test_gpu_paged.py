@@ -460,6 +460,44 @@ def test_lengths_beyond_the_table_are_cut_off():
     assert (got[0] == 0).all() and np.array_equal(bits(got[1:]), want[1:])
 
 
+@pytest.mark.parametrize("kind,hd", [("bf16", 64), ("fp16", 128)])
+@pytest.mark.parametrize("group", [1, 4, 8])
+def test_sequences_whose_rows_are_all_on_pages_outside_the_pool(kind, hd, group):
+    """Zeros, as for a sequence without rows, in one block's work and in parts that are joined; one
+    row left gives that row; scores that are all -inf stay NaN."""
+    torch, msm = _mods()
+    rng = np.random.default_rng(18)
+    lens = [5, 100, 12000, 200, 40000, 12000, 90, 0]
+    c, rk, rv = filled(rng, kind, lens, 16, 2, hd)
+    q = randn(kind, len(lens), 2 * group, hd, seed=1).cuda().abs()
+    c.table[0, 0] = -1
+    c.table[2] = 1 << 30
+    c.table[4] = -5
+    c.table[5, :700] = c.table.shape[1] * 1000
+    c.k_pages[0][c.table[6, :6].long()] = float("-inf")
+
+    def lost():
+        with pytest.raises(msm.MsmError, match="msm_paged_attention"):
+            c.sync()
+    out = c.attention(0, q)
+    lost()
+    assert all((out[s] == 0).all() for s in (0, 2, 4, 7))
+    assert torch.isnan(out[6]).all()
+    rest = [s for s in range(len(lens)) if s in (1, 3)]
+    want, tol = decode_want(q[rest], [rk[s] for s in rest], [rv[s] for s in rest], 0, hd ** -0.5, kind)
+    assert_close(out[rest], want, tol)
+    want, tol = decode_want(q[5:6], [rk[5][11200:]], [rv[5][11200:]], 0, hd ** -0.5, kind)
+    assert_close(out[5:6], want, tol)
+    # a window that lies on such a page, and one that has one row more
+    c.table[1, 6] = -2   # rows 96 .. 99
+    out = c.attention(0, q, window=4)
+    lost()
+    assert all((out[s] == 0).all() for s in (0, 1, 2, 4, 7))
+    out = c.attention(0, q, window=5)
+    lost()
+    assert np.array_equal(f64(out[1]), np.repeat(f64(rv[1][95]), group, axis=0))
+
+
 @pytest.mark.parametrize("lens", [[0, 0, 0], [0] * 400, [0] * 150 + [77] + [0] * 300 + [200, 0, 1] + [0] * 90])
 def test_batches_of_mostly_empty_slots(lens):
     rng = np.random.default_rng(16)
