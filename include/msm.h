@@ -591,8 +591,8 @@ msm_status msm_pages_write(const msm_pages* pages, int layer, const void* k, con
  * sequence's last row (written before the call); with window > 0 it sees the last
  * `window` rows only, as on the verify step's sliding-window layers.  A sequence
  * without rows gives zeros.  Rows behind a sequence's end or before its window are not
- * read, whatever they hold.  32-bit sums; the weights are rounded to the 16-bit type
- * for their product with v.
+ * read, whatever they hold.  32-bit sums; for their product with v the weights are two
+ * 16-bit terms (bf16 about 15 bits, fp16 about 20).
  *   q, out     device [n_seqs][n_q_heads][head_dim], strides in elements between
  *              sequences and between heads (multiples of 8), 16-byte aligned
  *   workspace  device buffer of msm_paged_attention_workspace bytes (0: an argument is

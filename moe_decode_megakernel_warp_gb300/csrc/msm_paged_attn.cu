@@ -65,6 +65,24 @@ constexpr float kNoKeys = -0.f;
 // 1 / l, and 0 where no key took part
 __device__ __forceinline__ float inverse_sum(float l) { return __float_as_uint(l) == 0x80000000u ? 0.f : 1.f / l; }
 
+// Weights as the B operand.  One 16-bit term is off by up to half a step (2^-8, 2^-11), and equal
+// weights all err the same way, so a weight is split into hi + lo: off by at most 3 half steps
+// squared.  Beside the reads the second product costs nothing (64 sequences of 4,096 rows 165 us
+// either way, one of 2,000 rows 11.3 us).  hi is the weight made smaller by a step before it is
+// rounded, so that lo is above 0, too (down to weights of 2^-125, fp16 2^-28 of the largest): a lo
+// of 0 or below would make NaN of the infinite value of a key that is seen.
+template <class El>
+struct Split {
+  static constexpr float kLess = El::kBf16 ? 1.f - 0x1p-7f : 1.f - 0x1p-10f;
+  // log2 of the largest weight.  fp16 ends at 2^-25 (half its smallest step): with weights up to
+  // 2^14 that is 2^-39 of the largest, so that the many small ones of a long context still count.
+  static constexpr float kTop = El::kBf16 ? 0.f : 14.f;
+  static __device__ __forceinline__ void split(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = El::pack(a * kLess, b * kLess);
+    lo = El::pack(a - El::value((uint16_t)(hi & 0xFFFFu)), b - El::value((uint16_t)(hi >> 16)));
+  }
+};
+
 // a partial result in the workspace: maxima, sums, outputs
 __host__ __device__ constexpr int part_floats(int group, int hd) { return 2 * kHeads + group * hd; }
 
@@ -476,16 +494,21 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
         m0 = n0;
         m1 = n1;
       }
-      const float r0 = m0 == -INFINITY ? 0.f : m0, r1 = m1 == -INFINITY ? 0.f : m1;
+      const float r0 = (m0 == -INFINITY ? 0.f : m0) - Split<El>::kTop, r1 = (m1 == -INFINITY ? 0.f : m1) - Split<El>::kTop;
 #pragma unroll
       for (int u = 0; u < kSub; ++u) {
         const float e0 = exp2_fast(sc[u][0] - r0), e1 = exp2_fast(sc[u][1] - r1), e2 = exp2_fast(sc[u][2] - r0),
                     e3 = exp2_fast(sc[u][3] - r1);
         l0 += e0 + e2;
         l1 += e1 + e3;
-        // P rounded to the 16-bit type for the product (a relative error of half a step per
-        // weight, as V itself carries); its sum keeps 32 bits
-        const uint32_t b0 = transpose8x8(El::pack(e0, e1)), b1 = transpose8x8(El::pack(e2, e3));
+        // P as two 16-bit terms for the product; its sum keeps 32 bits
+        uint32_t h0, h1, w0, w1;
+        Split<El>::split(e0, e1, h0, w0);
+        Split<El>::split(e2, e3, h1, w1);
+        h0 = transpose8x8(h0);
+        h1 = transpose8x8(h1);
+        w0 = transpose8x8(w0);
+        w1 = transpose8x8(w1);
 #pragma unroll
         for (int j = 0; j < VB; ++j) {
           // V rows 2t, 2t + 1, 2t + 8, 2t + 9, elements 8g .. 8g + 7 of the block
@@ -499,8 +522,10 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
           for (int i = 0; i < 4; ++i) {
             const uint32_t v0 = (&v[0].x)[i], v1 = (&v[1].x)[i], v2 = (&v[2].x)[i], v3 = (&v[3].x)[i];
             // element 64 j + 8 g + 2 i in row g of the product, the next one in row g + 8
-            El::mma(o[j * 4 + i], __byte_perm(v0, v1, 0x5410), __byte_perm(v0, v1, 0x7632),
-                    __byte_perm(v2, v3, 0x5410), __byte_perm(v2, v3, 0x7632), b0, b1);
+            const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632),
+                           a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
+            El::mma(o[j * 4 + i], a0, a1, a2, a3, h0, h1);
+            El::mma(o[j * 4 + i], a0, a1, a2, a3, w0, w1);
           }
         }
       }

@@ -460,6 +460,67 @@ def test_lengths_beyond_the_table_are_cut_off():
     assert (got[0] == 0).all() and np.array_equal(bits(got[1:]), want[1:])
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("hd,group,rows", [(64, 4, 16), (128, 8, 64), (128, 1, 7)])
+def test_weights_keep_more_than_16_bits(kind, hd, group, rows):
+    """Random sequences; values that cancel, where equal weights all err the same way; and many
+    small weights beside a large one: within the bound of weights in two terms."""
+    torch, msm = _mods()
+    rng = np.random.default_rng(19)
+    c, rk, rv = filled(rng, kind, LENS + [5000, 5000, 40000], rows, 2, hd)
+    n = len(LENS)
+    q = randn(kind, n + 3, 2 * group, hd, seed=9)
+    q[n:] = 0
+    q[n:, :, 0] = 1
+
+    def put(s, k0, v):   # keys (k0, 0, 0, ...), values v
+        k = torch.zeros((len(k0), 2, hd), dtype=_dtype(kind))
+        k[:, :, 0] = torch.from_numpy(k0).to(_dtype(kind))[:, None]
+        v = torch.from_numpy(v).to(_dtype(kind))[:, None, None].expand(len(k0), 2, hd)
+        rk[s], rv[s] = k, v
+        for r0 in range(0, len(k0), rows):
+            page = int(c.table[s, r0 // rows])
+            c.k_pages[0][page, :, :len(k0) - r0] = k[r0:r0 + rows].transpose(0, 1).cuda()
+            c.v_pages[0][page, :, :len(k0) - r0] = v[r0:r0 + rows].transpose(0, 1).cuda()
+    # scores 0 with value 1, and a score whose weight is far from a 16-bit one with value -1,
+    # as many as make the sum almost zero
+    for s, score in ((n, -0.6875), (n + 1, -2.421875)):
+        e = np.exp(score)
+        one = int(5000 * e / (1 + e))
+        put(s, np.where(np.arange(5000) < one, 0.0, score), np.where(np.arange(5000) < one, 1.0, -1.0))
+    # 39,999 weights of e^-17.75 (2^-25.6) beside one of 1
+    put(n + 2, np.where(np.arange(40000) == 7, 0.0, -17.75), np.where(np.arange(40000) == 7, 0.0, 1.0))
+    q = q.cuda()
+    for window, scale in ((0, hd ** -0.5), (0, 1.0), (300, 1.0)):
+        got = c.attention(0, q, window=window, scale=scale)
+        c.sync()
+        for s in range(n + 3):
+            want, tol = attend_matrix(f64(q[s:s + 1]), f64(rk[s]), f64(rv[s]), len(rk[s]) - 1, window, scale, kind, 2)
+            assert_close(got[s:s + 1], want, tol, "sequence %d window %d scale %g" % (s, window, scale))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+def test_infinite_values_under_small_weights(kind):
+    """Not NaN: every weight above 0 passes an infinite value on."""
+    torch, msm = _mods()
+    c, rk, rv = filled(np.random.default_rng(23), kind, [300], 16, 1, 64)
+    q = torch.zeros((1, 8, 64), dtype=_dtype(kind), device="cuda")
+    q[0, :, 0] = 1
+    for r in (0, 150, 299):
+        for score in (0.0, -0.5, -2.0, -5.5, -9.0, -13.0):
+            k = torch.zeros((300, 64), dtype=_dtype(kind))
+            k[r, 0] = score
+            v = randn(kind, 300, 64, seed=1)
+            v[r, 3], v[r, 4] = float("inf"), float("-inf")
+            for j in range(0, 300, 16):
+                page = int(c.table[0, j // 16])
+                c.k_pages[0][page, 0, :len(k[j:j + 16])] = k[j:j + 16].cuda()
+                c.v_pages[0][page, 0, :len(v[j:j + 16])] = v[j:j + 16].cuda()
+            out = c.attention(0, q, scale=1.0)[0].cpu()
+            assert (out[:, 3] == float("inf")).all() and (out[:, 4] == float("-inf")).all(), (r, score)
+            assert torch.isfinite(out[:, 5:]).all()
+
+
 @pytest.mark.parametrize("kind,hd", [("bf16", 64), ("fp16", 128)])
 @pytest.mark.parametrize("group", [1, 4, 8])
 def test_sequences_whose_rows_are_all_on_pages_outside_the_pool(kind, hd, group):
