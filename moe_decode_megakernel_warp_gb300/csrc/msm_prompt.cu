@@ -11,7 +11,7 @@
 //   A softmax thread owns a row (128 scores in registers), so its maximum and sum need no
 //   exchange.  P takes the place of S (16-bit, half its columns).  P is computed with the
 //   maximum that the row had before the tile; only when the tile's own is larger by more than
-//   a factor 2^12 (P stays below 2^12, well inside fp16) O is rescaled and P computed again.
+//   a factor 2^12 O is rescaled and P computed again.
 //   S(j + 1) being there means that P(j) V is done, the products of a block being issued
 //   and completed in order, so the thread may then change O itself.
 // Warps 0-7: softmax; 8, 10: products of a tile each; 9: TMA loads; 11: finite check of V.
@@ -51,8 +51,15 @@ constexpr int kBoxBytes = kRows * 128;       // 128 rows x 64 elements, one swiz
 // Registers: 384 threads start with 168; warps 8-11 give up 64 each, warps 0-7 take 32
 // (256 x 200 + 128 x 104 = 384 x 168).
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
-constexpr float kGrow = 12.0f;  // log2 of the largest unnormalised weight
 constexpr uint64_t kWaitNs = 2000000000ull;
+
+constexpr float kGrow = 12.0f;  // log2 of how much a row's maximum may be above the one that it works with
+// log2 of the weight of a score that equals the maximum that a row works with.  fp16 ends at 2^16 and
+// rounds to 0 from 2^-25 on, so weights up to 2^15 keep three bits more of the small ones: down to
+// 2^-28 of the largest.  More of them for less growth costs time: 2^-32 and a growth of 2^8 10 %
+// on a window of 2,048 (828 us for 32,768 tokens to 905), 2^-29 and 2^11 1 % at head_dim 64.
+template <class El>
+constexpr float kTop = El::kBf16 ? 0.f : 3.f;
 
 template <int HD>
 struct Cfg {
@@ -572,7 +579,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         float mx;
         uint64_t sum[2];
         auto weights = [&]() {
-          const float neg = m == -INFINITY ? 0.f : -m * scale;
+          const float neg = m == -INFINITY ? 0.f : kTop<El> - m * scale;
           const uint64_t sc2 = pair(scale, scale), neg2 = pair(neg, neg);
           float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           sum[0] = sum[1] = pair(0.f, 0.f);

@@ -149,19 +149,20 @@ def attend(q, k, v, shift, window, scale, kind):
     return out, tol * (1 + 2 * u) + 1e-30
 
 
-def attend_matrix(q, k, v, shift, window, scale, kind, terms=1):
+def attend_matrix(q, k, v, shift, window, scale, kind, terms=1, least=None):
     """attend() with a head's queries and keys as one matrix (for batches of many rows).
 
     terms = 2: the bound where a weight p is held as two 16-bit terms.  The first one is p (1 - 2 u)
     rounded, so the rest is between 0 and p (1 - (1 - 2 u) (1 - u)) < 3 u p, of which its rounding
     takes at most half a step: 3 u^2 p; fp16 weights are at most 2^14 then, so half of their smallest
-    step, 2^-25, is 2^-39 of the largest weight."""
+    step, 2^-25, is 2^-39 of the largest weight.
+    least: half of the smallest fp16 step, as a part of the largest weight (2^-25 where that is 1)."""
     nq, hq, hd = q.shape
     nk, hkv, _ = k.shape
     group = hq // hkv
     u = EPS[kind]
     weight = u if terms == 1 else 3 * u * u
-    least = 2.0 ** (-25 if terms == 1 else -39)
+    least = least or 2.0 ** (-25 if terms == 1 else -39)
     out, tol = np.zeros((nq, hq, hd)), np.zeros((nq, hq, hd))
     gap = np.arange(nq)[:, None] + shift - np.arange(nk)
     see = (gap >= 0) & ((gap < window) if window else True)

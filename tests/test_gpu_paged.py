@@ -34,6 +34,11 @@ def ints(values):
     return torch.tensor(values, dtype=torch.int32, device="cuda")
 
 
+def _dtype_tensor(kind, values):
+    torch, _ = _mods()
+    return torch.from_numpy(np.asarray(values)).to(_dtype(kind))
+
+
 def starts_of(lens):
     return [int(x) for x in np.concatenate([[0], np.cumsum(lens)])]
 
@@ -728,6 +733,45 @@ def test_prompt_scales_and_large_scores():
         q, k, v = (randn("bf16", 333, 2, 64, seed=i, std=std if i == 0 else 1.0).cuda() for i in range(3))
         want, tol = prompt_want(q, k, v, st, st, 0, scale, "bf16")
         assert_close(msm.prompt_attention(q, k, v, ints(st), scale=scale), want, tol, "scale %g" % scale)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("place", ["last", "first", "middle"])
+def test_many_small_weights_beside_a_large_one(kind, hd, place):
+    """Keys of 2^-25.6 of the largest weight each, which together move the result; the largest one
+    in the tile that is worked on first, last, or between."""
+    _, msm = _mods()
+    n, nq = 12000, 200
+    at = dict(last=n - nq, first=3, middle=6000)[place]
+    q, k, v = (randn(kind, m, h, hd, seed=h, std=0.0) for m, h in ((nq, 2), (n, 1), (n, 1)))
+    q[:, :, 0] = 1
+    k[:, :, 0] = -17.75
+    k[at, :, 0] = 0
+    v[:] = 1
+    v[at] = 0
+    got = msm.prompt_attention(q.cuda(), k.cuda(), v.cuda(), ints([0, nq]), ints([0, n]), scale=1.0)
+    # (fp16 weights are at least 2^3 where a score equals the maximum that a row works with)
+    want, tol = attend_matrix(f64(q), f64(k), f64(v), n - nq, 0, 1.0, kind, 1, 2.0 ** -28)
+    assert (want > 2e-4).all() and (tol < 0.25 * want).all()
+    assert_close(got, want, tol)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_growing_scores(kind, hd):
+    """Maxima that grow from key tile to key tile, by less and by more than a row lets them grow."""
+    _, msm = _mods()
+    n = 900
+    rng = np.random.default_rng(hd)
+    q, k, v = (randn(kind, n, h, hd, seed=h) for h in (2, 1, 1))
+    q[:, :, 0] = 1
+    for steps in (3.0, 4.0, 8.0, 13.0):   # in powers of two, per tile from the last key to the first
+        k[:, 0, 1:] *= 0.1
+        k[:, 0, 0] = _dtype_tensor(kind, (n - np.arange(n)) / 128 * steps * np.log(2) + rng.standard_normal(n))
+        got = msm.prompt_attention(q.cuda(), k.cuda(), v.cuda(), ints([0, n]), scale=1.0)
+        want, tol = attend_matrix(f64(q), f64(k), f64(v), 0, 0, 1.0, kind, 1, 2.0 ** -28)
+        assert_close(got, want, tol, "%g" % steps)
 
 
 @pytest.mark.parametrize("hd", [64, 128])
