@@ -534,8 +534,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int t = wid >> 2;
     const uint32_t lanes = (uint32_t)((wid & 3) * 32) << 16;
     const uint32_t ts = t_s(t) + lanes, to = t_o(t) + lanes;
-    // (a negative scale negates Q in the product; a scale of zero must still leave -inf x scale = -inf)
-    const float scale = fmaxf(fabsf(p.scale_log2), 1e-30f);
+    // (a negative scale negates Q in the product; a scale of zero must still leave -inf x scale = -inf: the
+    // smallest number does, and any score times it is less than 2^-20)
+    const float scale = fmaxf(fabsf(p.scale_log2), __int_as_float(1));
     int steps = 0, works = 0;
     Work ahead;
     for (bool more = next_work(p, place, n_work, ahead); more;) {

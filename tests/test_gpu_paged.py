@@ -775,6 +775,24 @@ def test_growing_scores(kind, hd):
 
 
 @pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("scale", [2.0 ** -123, -2.0 ** -123, 2.0 ** -124, 2.0 ** -140, 0.0])
+def test_the_smallest_scales(hd, scale):
+    """Scores near the largest 32-bit number, and a scale that makes ordinary ones of them."""
+    _, msm = _mods()
+    st = [0, 200, 333]
+    q, k, v = (randn("bf16", 333, 2, hd, seed=i, std=2.0 ** 60 if i < 2 else 1.0) for i in range(3))
+    got = msm.prompt_attention(q.cuda(), k.cuda(), v.cuda(), ints(st), scale=scale)
+    want, tol = prompt_want(q, k, v, st, st, 0, scale, "bf16")
+    assert_close(got, want, tol)
+    c, rk, rv = filled(np.random.default_rng(24), "bf16", [200, 1, 33], 16, 2, hd)
+    c.k_pages[0] *= 2.0 ** 60
+    rk = [t * 2.0 ** 60 for t in rk]
+    got = c.attention(0, q[:3].cuda(), scale=scale)
+    want, tol = decode_want(q[:3], rk, rv, 0, scale, "bf16")
+    assert_close(got, want, tol)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
 @pytest.mark.parametrize("bad", ["nan", "inf", "-inf"])
 def test_keys_that_a_query_does_not_see_have_no_part(hd, bad):
     """One row of K or V is not finite: the queries that see it follow the formula, every
