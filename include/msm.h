@@ -636,6 +636,10 @@ msm_status msm_pages_sync(const msm_pages* pages, void* stream);
  * Host errors: MSM_ERR_INVALID_ARG (NULL or misaligned pointers, sizes out of range,
  * strides), MSM_ERR_UNSUPPORTED (head_dim other than 64 or 128, n_q_heads / n_kv_heads
  * other than 1, 2, 4 or 8, more than 65535 kv heads, n_q or n_k of 2^27 or more).
+ * Bounded waits: every wait inside the kernel gives up after 2 s on the clock (a GPU that
+ * does other work meanwhile counts towards it) and lets the launch finish; the rows of that
+ * block that were not done are NaN then, and *status, where it is not NULL and holds 0, becomes
+ * MSM_ERR_DEVICE_TIMEOUT.  Nothing clears it but the caller.
  */
 typedef struct {
   int device;
@@ -648,6 +652,8 @@ typedef struct {
   int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride,
       out_token_stride, out_head_stride;
   const int32_t *q_starts, *k_starts;
+  int32_t* status;  /* device int32 [1], or NULL */
+  uint32_t flags;   /* MSM_FLAG_TEST_DROP_HANDOFF (no key or value is loaded, so that the waits run out), or 0 */
 } msm_prompt;
 msm_status msm_prompt_attention(const msm_prompt* prompt, void* stream);
 

@@ -156,7 +156,8 @@ class MsmPrompt(ctypes.Structure):
         ("scale", ctypes.c_float)] + [(n, ctypes.c_void_p) for n in ("q", "k", "v", "out")] + [
         (n, ctypes.c_int64) for n in (
             "q_token_stride", "q_head_stride", "k_token_stride", "k_head_stride", "v_token_stride", "v_head_stride",
-            "out_token_stride", "out_head_stride")] + [(n, ctypes.c_void_p) for n in ("q_starts", "k_starts")]
+            "out_token_stride", "out_head_stride")] + [
+        (n, ctypes.c_void_p) for n in ("q_starts", "k_starts", "status")] + [("flags", ctypes.c_uint32)]
 
 
 _LIB = None

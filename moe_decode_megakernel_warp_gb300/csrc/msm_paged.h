@@ -84,6 +84,8 @@ struct PromptAttn {
   int n_seqs, n_q, n_k, n_kv_heads, group, window;
   int out_32;        // every row of out starts on a 32-byte boundary
   float scale_log2;  // softmax scale x log2(e)
+  int32_t* status;   // becomes MSM_ERR_DEVICE_TIMEOUT when a wait ran out (may be null)
+  int drop;          // test hook: nothing is loaded
 };
 cudaError_t launch_prompt_attn(const PromptAttn& p, int dtype, int head_dim, int sms, cudaStream_t s);
 

@@ -320,8 +320,9 @@ msm_status msm_prompt_attention(const msm_prompt* a, void* stream) {
   REQUIRE(a->q && a->out && a->q_starts && a->k_starts && (a->n_k == 0 || (a->k && a->v)), MSM_ERR_INVALID_ARG,
           "prompt: NULL pointer");
   REQUIRE(!misaligned(a->q, 16) && !misaligned(a->k, 16) && !misaligned(a->v, 16) && !misaligned(a->out, 16) &&
-              !misaligned(a->q_starts, 4) && !misaligned(a->k_starts, 4),
-          MSM_ERR_INVALID_ARG, "prompt: q, k, v and out must be 16-byte, the starts 4-byte aligned");
+              !misaligned(a->q_starts, 4) && !misaligned(a->k_starts, 4) && !misaligned(a->status, 4),
+          MSM_ERR_INVALID_ARG, "prompt: q, k, v and out must be 16-byte, the starts and status 4-byte aligned");
+  REQUIRE((a->flags & ~MSM_FLAG_TEST_DROP_HANDOFF) == 0, MSM_ERR_INVALID_ARG, "prompt: unknown flags");
   const int64_t strides[] = {a->q_token_stride, a->q_head_stride, a->k_token_stride, a->k_head_stride,
                              a->v_token_stride, a->v_head_stride, a->out_token_stride, a->out_head_stride};
   for (int64_t s : strides)
@@ -356,6 +357,8 @@ msm_status msm_prompt_attention(const msm_prompt* a, void* stream) {
   // far inside 32 bits, also for queries in front of the first key)
   p.window = a->window < a->n_k ? a->window : 0;
   p.scale_log2 = a->scale * kLog2e;
+  p.status = a->status;
+  p.drop = (a->flags & MSM_FLAG_TEST_DROP_HANDOFF) != 0;
   CKP(launch_prompt_attn(p, a->dtype, a->head_dim, sms, static_cast<cudaStream_t>(stream)));
   return MSM_OK;
 }

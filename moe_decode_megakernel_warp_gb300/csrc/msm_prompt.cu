@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                       w.q0 + w.tok0 + t * (kRows / p.group), &b_q[t]);
         return true;
       };
-      while (ok && next_work(p, place, n_work, w)) {
+      while (ok && !p.drop && next_work(p, place, n_work, w)) {
         if (lane == 0) {
           for (int e = 0; ok && e < 2 * w.n; ++e) {
             const int st = i % C::kStages;
@@ -686,6 +686,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && s_dead && p.status) atomicCAS(p.status, 0, MSM_ERR_DEVICE_TIMEOUT);
   if (wid == 8) {
     __syncwarp();
     tc_fence_after();

@@ -14,7 +14,7 @@ import struct
 from . import MSM_BF16, MSM_FP16, MsmPages, MsmPrompt, _check, _ptr_array, lib
 
 # msm_prompt in the C layout (a bytes object takes a third of the time of a ctypes structure)
-_PROMPT = struct.Struct("9if4P8q2P")
+_PROMPT = struct.Struct("9if4P8q3PI4x")
 assert _PROMPT.size == ctypes.sizeof(MsmPrompt)
 
 
@@ -185,14 +185,18 @@ class PagedCache:
         _check(self._lib.msm_pages_sync(self._ref, _raw_stream(self._index)))
 
 
-def prompt_attention(q, k, v, q_starts, k_starts=None, window=0, scale=None, out=None):
+def prompt_attention(q, k, v, q_starts, k_starts=None, window=0, scale=None, out=None, status=None):
     """msm_prompt_attention: causal attention of packed prompts.
 
     q [n_q, n_q_heads, head_dim], k and v [n_k, n_kv_heads, head_dim] (any strides that keep
     rows consecutive; ``cache.transpose(0, 1)`` of a verify-step cache [n_kv_heads, max_ctx,
     head_dim] is read in place), q_starts and k_starts int32 [n_seqs + 1] on the device
     (k_starts defaults to q_starts), scale defaults to 1 / sqrt(head_dim).  Returns out; a new
-    one is uninitialised behind the last sequence."""
+    one is uninitialised behind the last sequence.
+
+    The kernel's own waits end after 2 s, which only a fault or a GPU that is busy elsewhere brings
+    about: the rows that were not done are NaN then, and ``status``, an int32 tensor of one
+    entry that holds 0, becomes MSM_ERR_DEVICE_TIMEOUT."""
     if _torch is None:
         _load()
     i, dtype, shape, k_shape = q.get_device(), q.dtype, q.shape, k.shape
@@ -218,7 +222,8 @@ def prompt_attention(q, k, v, q_starts, k_starts=None, window=0, scale=None, out
     ks = qs if k_starts is None else _int32(k_starts, "k_starts", n_seqs + 1, i)
     a = _PROMPT.pack(i, code, n_seqs, n_q, n_k, heads, kv_heads, hd, window,
                      (hd or 1) ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                     out.data_ptr(), qt, qh, kt, kh, vt, vh, ot, oh, qs, ks)
+                     out.data_ptr(), qt, qh, kt, kh, vt, vh, ot, oh, qs, ks,
+                     0 if status is None else _int32(status, "status", 1, i), 0)
     st = _LIBRARY.msm_prompt_attention(a, _raw_stream(i))
     if st:
         _check(st)

@@ -919,6 +919,32 @@ def test_prompts_on_two_streams_at_once():
             assert np.array_equal(bits(o), want[i])
 
 
+def test_a_wait_that_runs_out_is_reported():
+    """Through the test hook that leaves the loads out (2 s): the launch ends, its rows are NaN, the
+    status says why, and the calls behind it are what they were."""
+    torch, msm = _mods()
+    x = [randn("bf16", 400, 4, 64, seed=i).cuda() for i in range(3)]
+    st, status = ints([0, 300, 400]), ints([0])
+    want = bits(msm.prompt_attention(*x, st, status=status))
+    assert status.item() == 0
+    out = torch.zeros_like(x[0])
+    p = msm.MsmPrompt(0, msm.MSM_BF16, 2, 400, 400, 4, 4, 64, 0, 0.125, *(t.data_ptr() for t in x), out.data_ptr(),
+                      *([256, 64] * 4), st.data_ptr(), st.data_ptr(), status.data_ptr(), msm.MSM_FLAG_TEST_DROP_HANDOFF)
+    assert msm.msm_prompt_attention(p, torch.cuda.current_stream().cuda_stream) == msm.MSM_OK
+    torch.cuda.synchronize()
+    assert torch.isnan(out).all() and status.item() == msm.MSM_ERR_DEVICE_TIMEOUT
+    status.zero_()
+    for _ in range(3):
+        assert np.array_equal(bits(msm.prompt_attention(*x, st, status=status)), want)
+    assert status.item() == 0
+    p.status = None
+    p.flags = 0
+    assert msm.msm_prompt_attention(p, torch.cuda.current_stream().cuda_stream) == msm.MSM_OK
+    assert np.array_equal(bits(out), want)
+    with pytest.raises(ValueError, match="status"):
+        msm.prompt_attention(*x, st, status=status.cpu())
+
+
 def test_prompt_leaves_what_is_not_its_own():
     torch, msm = _mods()
     x = [randn("bf16", 100, 4, 64, seed=i).cuda() for i in range(3)]

@@ -107,6 +107,14 @@ def test_arguments_of_the_prompt_attention():
     assert msm.msm_prompt_attention(msm.MsmPrompt(**{**ok, "n_q": 0, "q": None})) == msm.MSM_OK  # nothing to do
 
 
+def test_status_and_flags_of_the_prompt_attention():
+    ok = dict(device=0, dtype=msm.MSM_BF16, n_seqs=1, n_q=10, n_k=10, n_q_heads=2, n_kv_heads=2, head_dim=64, scale=0.1,
+              q=BUF, k=BUF, v=BUF, out=BUF, q_token_stride=128, q_head_stride=64, k_token_stride=128, k_head_stride=64,
+              v_token_stride=128, v_head_stride=64, out_token_stride=128, out_head_stride=64, q_starts=BUF, k_starts=BUF)
+    for bad in (dict(status=BUF + 2), dict(flags=1), dict(flags=msm.MSM_FLAG_TEST_DROP_HANDOFF | 8)):
+        assert msm.msm_prompt_attention(msm.MsmPrompt(**{**ok, **bad})) == INVALID, bad
+
+
 def test_the_torch_wrappers_check_what_torch_knows():
     torch = pytest.importorskip("torch")
     k = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16)
