@@ -635,7 +635,8 @@ msm_status msm_pages_sync(const msm_pages* pages, void* stream);
  *            k and v may be NULL.
  * Host errors: MSM_ERR_INVALID_ARG (NULL or misaligned pointers, sizes out of range,
  * strides), MSM_ERR_UNSUPPORTED (head_dim other than 64 or 128, n_q_heads / n_kv_heads
- * other than 1, 2, 4 or 8, more than 65535 kv heads, n_q or n_k of 2^27 or more).
+ * other than 1, 2, 4 or 8, more than 65535 kv heads, n_q or n_k of 2^27 or more, or
+ * (n_seqs + n_q * n_q_heads / n_kv_heads / 256) * n_kv_heads of about 2^31 or more).
  * Bounded waits: every wait inside the kernel gives up after 2 s on the clock (a GPU that
  * does other work meanwhile counts towards it) and lets the launch finish; the rows of that
  * block that were not done are NaN then, and *status, where it is not NULL and holds 0, becomes

@@ -87,6 +87,9 @@ struct PromptAttn {
   int32_t* status;   // becomes MSM_ERR_DEVICE_TIMEOUT when a wait ran out (may be null)
   int drop;          // test hook: nothing is loaded
 };
+// most pieces of work that a call can have (its sequences' lengths are on the device); below 2^31 - 2^16
+// for a launch
+int64_t prompt_attn_works(int n_q, int n_seqs, int n_kv_heads, int group);
 cudaError_t launch_prompt_attn(const PromptAttn& p, int dtype, int head_dim, int sms, cudaStream_t s);
 
 cudaError_t launch_pages_resize(const PagesMeta& p, cudaStream_t s);

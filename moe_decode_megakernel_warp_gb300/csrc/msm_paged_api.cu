@@ -314,6 +314,8 @@ msm_status msm_prompt_attention(const msm_prompt* a, void* stream) {
   if (st != MSM_OK) return st;
   REQUIRE(a->n_q < (1 << 27) && a->n_k < (1 << 27) && a->n_kv_heads < 65536, MSM_ERR_UNSUPPORTED,
           "prompt: more than 2^27 tokens or 65535 kv heads");
+  REQUIRE(prompt_attn_works(a->n_q, a->n_seqs, a->n_kv_heads, a->n_q_heads / a->n_kv_heads) < 0x7FFF0000,
+          MSM_ERR_UNSUPPORTED, "prompt: too many sequences times kv heads");
   REQUIRE(a->window >= 0, MSM_ERR_INVALID_ARG, "window is negative");
   REQUIRE(std::isfinite(a->scale * kLog2e), MSM_ERR_INVALID_ARG, "scale must be finite");
   if (a->n_q == 0) return MSM_OK;

@@ -715,9 +715,7 @@ cudaError_t encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
 // rows [tokens][heads][HD] as boxes of 64 elements; Q's heads are split into (group, kv head)
 template <class El, int HD>
 cudaError_t launch(const PromptAttn& p, int sms, cudaStream_t s) {
-  const int64_t tiles = ((int64_t)p.n_q * p.group + kBlockRows - 1) / kBlockRows + p.n_seqs;
-  const int64_t works = tiles * p.n_kv_heads;  // at most
-  if (works > 0x7FFF0000) return cudaErrorInvalidConfiguration;
+  const int64_t works = prompt_attn_works(p.n_q, p.n_seqs, p.n_kv_heads, p.group);
   PFN_cuTensorMapEncodeTiled_v12000 encode;
   cudaError_t e = encoder(&encode);
   if (e != cudaSuccess) return e;
@@ -760,6 +758,10 @@ cudaError_t launch(const PromptAttn& p, int sms, cudaStream_t s) {
 }
 
 }  // namespace
+
+int64_t prompt_attn_works(int n_q, int n_seqs, int n_kv_heads, int group) {
+  return (((int64_t)n_q * group + kBlockRows - 1) / kBlockRows + n_seqs) * n_kv_heads;
+}
 
 cudaError_t launch_prompt_attn(const PromptAttn& p, int dtype, int head_dim, int sms, cudaStream_t s) {
   if (dtype == MSM_BF16) return head_dim == 64 ? launch<Bf16, 64>(p, sms, s) : launch<Bf16, 128>(p, sms, s);

@@ -115,6 +115,18 @@ def test_status_and_flags_of_the_prompt_attention():
         assert msm.msm_prompt_attention(msm.MsmPrompt(**{**ok, **bad})) == INVALID, bad
 
 
+def test_more_work_than_a_launch_of_the_prompt_attention_takes():
+    ok = dict(device=0, dtype=msm.MSM_BF16, n_seqs=1 << 20, n_q=10, n_k=10, n_q_heads=4096, n_kv_heads=4096, head_dim=64,
+              scale=0.1, q=BUF, k=BUF, v=BUF, out=BUF, q_token_stride=1 << 18, q_head_stride=64, k_token_stride=1 << 18,
+              k_head_stride=64, v_token_stride=1 << 18, v_head_stride=64, out_token_stride=1 << 18, out_head_stride=64,
+              q_starts=BUF, k_starts=BUF)
+    assert msm.msm_prompt_attention(msm.MsmPrompt(**ok)) == UNSUPPORTED
+    assert "too many sequences" in msm.msm_last_error()
+    for more in (dict(n_seqs=(1 << 31) - 1, n_q_heads=1, n_kv_heads=1), dict(n_seqs=(1 << 31) - 1),
+                 dict(n_seqs=1, n_q=(1 << 27) - 1, n_q_heads=65528, n_kv_heads=8191)):
+        assert msm.msm_prompt_attention(msm.MsmPrompt(**{**ok, **more})) == UNSUPPORTED, more
+
+
 def test_the_torch_wrappers_check_what_torch_knows():
     torch = pytest.importorskip("torch")
     k = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16)
