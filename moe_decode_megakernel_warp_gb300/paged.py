@@ -59,6 +59,12 @@ def _int32(t, name, n, index):
     return t.data_ptr()
 
 
+def _c_int(x):
+    """x as a C int that says the same: ctypes would take its low 32 bits (a window of 2^32 for none).
+    Every index, and no window, is below the largest one; -1 is refused as any other negative number."""
+    return -1 if x < 0 else x if x < 0x7FFFFFFF else 0x7FFFFFFF
+
+
 class PagedCache:
     """A paged KV cache over the caller's tensors: ``k_pages`` and ``v_pages`` are lists of one
     [n_pages, n_kv_heads, page_rows, head_dim] tensor per layer (bfloat16 or float16),
@@ -137,10 +143,12 @@ class PagedCache:
     def write(self, layer, k, v, starts):
         """msm_pages_write: k, v [n_tokens, n_kv_heads, head_dim], starts int32 [n_seqs + 1]."""
         n, i = len(k), self._index
+        if n > 0x7FFFFFFF:
+            raise ValueError("more than 2^31 - 1 tokens")
         shape = (n, self._kv_heads, self._head_dim)
         kt, kh = _rows(k, "k", shape, self._dtype, i)
         vt, vh = _rows(v, "v", shape, self._dtype, i)
-        _check(self._lib.msm_pages_write(self._ref, layer, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh,
+        _check(self._lib.msm_pages_write(self._ref, _c_int(layer), k.data_ptr(), v.data_ptr(), kt, kh, vt, vh,
                                          _int32(starts, "starts", self._n_seqs + 1, i), n, _raw_stream(i)))
 
     def attention(self, layer, q, window=0, scale=None, out=None):
@@ -148,7 +156,7 @@ class PagedCache:
         1 / sqrt(head_dim).  Returns out."""
         if q.dim() != 3:
             raise ValueError("q must be [n_seqs, n_q_heads, head_dim]")
-        heads, i, hd = q.shape[1], self._index, self._head_dim
+        heads, i, hd, layer = q.shape[1], self._index, self._head_dim, _c_int(layer)
         shape = (self._n_seqs, heads, hd)
         qs, qh = _rows(q, "q", shape, self._dtype, i)
         if out is None:
@@ -173,8 +181,8 @@ class PagedCache:
             if ws is None:
                 ws = self._workspace[stream, heads] = _torch.zeros(n, dtype=_torch.uint8, device=self.device)
         st = self._lib.msm_paged_attention(self._ref, layer, q.data_ptr(), qs, qh, heads,
-                                           (hd or 1) ** -0.5 if scale is None else scale, window, out.data_ptr(), os_, oh,
-                                           ws.data_ptr(), n, stream)
+                                           (hd or 1) ** -0.5 if scale is None else scale, _c_int(window), out.data_ptr(),
+                                           os_, oh, ws.data_ptr(), n, stream)
         if st:
             _check(st)
         return out
@@ -220,7 +228,7 @@ def prompt_attention(q, k, v, q_starts, k_starts=None, window=0, scale=None, out
     n_seqs = q_starts.numel() - 1
     qs = _int32(q_starts, "q_starts", n_seqs + 1, i)
     ks = qs if k_starts is None else _int32(k_starts, "k_starts", n_seqs + 1, i)
-    a = _PROMPT.pack(i, code, n_seqs, n_q, n_k, heads, kv_heads, hd, window,
+    a = _PROMPT.pack(i, code, n_seqs, n_q, n_k, heads, kv_heads, hd, _c_int(window),
                      (hd or 1) ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                      out.data_ptr(), qt, qh, kt, kh, vt, vh, ot, oh, qs, ks,
                      0 if status is None else _int32(status, "status", 1, i), 0)

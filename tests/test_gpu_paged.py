@@ -625,6 +625,34 @@ def test_tables_of_more_than_2_to_the_30_pages():
         del pool, table, c
 
 
+def test_integers_beyond_32_bits():
+    """Windows that hide nothing; layers that are none; not their low 32 bits."""
+    torch, msm = _mods()
+    c, _, _ = filled(np.random.default_rng(25), "bf16", [300, 40], 16, 2, 64)
+    q = randn("bf16", 2, 4, 64).cuda()
+    kv = randn("bf16", 100, 2, 64, seed=1).cuda()
+    qq, st = randn("bf16", 100, 4, 64, seed=2).cuda(), ints([0, 100])
+    want, p_want = bits(c.attention(0, q)), bits(msm.prompt_attention(qq, kv, kv, st))
+    for window in (2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 2 ** 63 - 1, 10 ** 30):
+        assert np.array_equal(bits(c.attention(0, q, window=window)), want)
+        assert np.array_equal(bits(msm.prompt_attention(qq, kv, kv, st, window=window)), p_want)
+    for window in (-1, -2 ** 31, -2 ** 32, 5 - 2 ** 32):
+        with pytest.raises(msm.MsmError, match="window"):
+            c.attention(0, q, window=window)
+        with pytest.raises(msm.MsmError, match="window"):
+            msm.prompt_attention(qq, kv, kv, st, window=window)
+    before = contents(c)
+    for layer in (1, -1, 2 ** 32, -2 ** 32):
+        with pytest.raises(msm.MsmError, match="layer"):
+            c.attention(layer, q)
+        with pytest.raises(msm.MsmError, match="layer"):
+            c.write(layer, kv, kv, ints([0, 100, 100]))
+    with pytest.raises(ValueError, match="tokens"):
+        c.write(0, kv[:1].expand(2 ** 32 + 1, 2, 64), kv[:1].expand(2 ** 32 + 1, 2, 64), ints([0, 1, 1]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a.nan_to_num(), b.nan_to_num()) for a, b in zip(before, contents(c)))
+
+
 def test_pools_of_more_than_2_to_the_31_elements():
     """The last pages of a 4.6 GB pool: written, read, copied and moved."""
     torch, msm = _mods()

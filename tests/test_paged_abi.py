@@ -138,3 +138,11 @@ def test_the_torch_wrappers_check_what_torch_knows():
     x = torch.zeros((3, 2, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         msm.prompt_attention(x, x, x, ints[:2])
+
+
+def test_integers_as_c_ints():
+    from moe_decode_megakernel_warp_gb300.paged import _c_int
+    top = 2 ** 31 - 1
+    for x, want in ((0, 0), (5, 5), (top, top), (top + 1, top), (1 << 32, top), (2 ** 63 - 1, top), (-1, -1), (-7, -1),
+                    (-(1 << 32), -1)):
+        assert _c_int(x) == want
