@@ -43,3 +43,20 @@ def test_single_rank_is_identity():
     import bench
     assert bench.max_over_ranks(3.5, 1) == 3.5
     assert bench.dist_env()[1] >= 1
+
+
+def test_the_traffic_figure_is_void_after_any_edit_that_can_change_it(tmp_path, monkeypatch):
+    """The layer kernel, its packing and the host code that chooses its grid and splits."""
+    import shutil
+    import bench
+    src = os.path.join("moe_decode_megakernel_warp_gb300", "csrc")
+    shutil.copytree(os.path.join(bench.ROOT, src), str(tmp_path / src))
+    whole = bench.kernel_sha256()
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    assert bench.kernel_sha256() == whole
+    for name in ("msm_kernel.cu", "msm_device.cuh", "msm_internal.h", "msm_pack.cu", "msm_api.cu"):
+        p = tmp_path / src / name
+        old = p.read_bytes()
+        p.write_bytes(old + b"\n")
+        assert bench.kernel_sha256() != whole, name
+        p.write_bytes(old)
