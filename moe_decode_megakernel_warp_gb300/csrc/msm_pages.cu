@@ -475,7 +475,6 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const PagesWrite p
     lo += le ? (31 - __clz(le)) * step : 0;
     hi = min(hi, lo + step);
   }
-  if (stop) return;
   const int first = p.starts[lo], end = p.starts[lo + 1];
   const int64_t pos = (int64_t)p.m.lens[lo] - end + t;
   bool ok = t >= first && t < end && pos >= 0 && pos < (int64_t)p.m.max_pages * p.m.page_rows;
@@ -485,8 +484,8 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const PagesWrite p
     ok = pg >= 0 && pg < p.m.n_pages && p.m.refs[pg] == 1;
     at = ((int64_t)pg * p.n_kv_heads * p.m.page_rows + (int)pos % p.m.page_rows) << p.row_shift;
   }
-  if (!ok) {
-    if (lane == 0) latch(p.m.status, MSM_ERR_INVALID_ARG, kCallWrite);
+  if (!ok || stop) {
+    if (lane == 0 && !stop) latch(p.m.status, MSM_ERR_INVALID_ARG, kCallWrite);
     return;
   }
   const int64_t head = (int64_t)p.m.page_rows << p.row_shift;
