@@ -591,8 +591,8 @@ msm_status msm_pages_write(const msm_pages* pages, int layer, const void* k, con
  * sequence's last row (written before the call); with window > 0 it sees the last
  * `window` rows only, as on the verify step's sliding-window layers.  A sequence
  * without rows gives zeros.  Rows behind a sequence's end or before its window are not
- * read, whatever they hold.  32-bit sums; for their product with v the weights are two
- * 16-bit terms (bf16 about 15 bits, fp16 about 20).
+ * read, whatever they hold.  32-bit scores and sums; for their product with v the weights
+ * are two 16-bit terms (off by at most 3 x 2^-16 of themselves, fp16 3 x 2^-22).
  *   q, out     device [n_seqs][n_q_heads][head_dim], strides in elements between
  *              sequences and between heads (multiples of 8), 16-byte aligned
  *   workspace  device buffer of msm_paged_attention_workspace bytes (0: an argument is
@@ -621,8 +621,8 @@ msm_status msm_pages_sync(const msm_pages* pages, void* stream);
  * i + (nk - nq) - j < window (the verify step's sliding window).  nk > nq resumes a
  * prompt whose first rows are cached already; a query that sees no key gives zeros.
  *   out[i][h] = sum_j softmax_j(scale q[i][h] . k[j]) v[j]
- * with kv head h / (n_q_heads / n_kv_heads).  32-bit sums; the weights are rounded to
- * the 16-bit type for their product with v.  Keys that a query does not see have no
+ * with kv head h / (n_q_heads / n_kv_heads).  32-bit scores and sums; the weights are rounded
+ * to the 16-bit type for their product with v (fp16: to 0 below 2^-28 of the largest).  Keys that a query does not see have no
  * part in its result, whatever they hold.
  *   q, out   device [n_q][n_q_heads][head_dim]; k, v device [n_k][n_kv_heads][head_dim]:
  *            strides in elements between tokens and between heads (multiples of 8, at
@@ -631,7 +631,8 @@ msm_status msm_pages_sync(const msm_pages* pages, void* stream);
  *            overlap the inputs.
  *   q_starts, k_starts  device int32 [n_seqs + 1], ascending from 0, at most n_q and n_k
  *            (larger values are cut off there); rows of out at or behind
- *            q_starts[n_seqs] are left as they are.  n_q = 0 does nothing; with n_k = 0
+ *            q_starts[n_seqs] are left as they are.  A sequence without queries stands for
+ *            keys to be passed over, as the rows that a cache has to spare.  n_q = 0 does nothing; with n_k = 0
  *            k and v may be NULL.
  * Host errors: MSM_ERR_INVALID_ARG (NULL or misaligned pointers, sizes out of range,
  * strides), MSM_ERR_UNSUPPORTED (head_dim other than 64 or 128, n_q_heads / n_kv_heads

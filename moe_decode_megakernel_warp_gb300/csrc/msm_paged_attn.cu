@@ -22,7 +22,7 @@
 // 6,550; one block of eight warps per SM is as fast on long sequences and 1.7 times slower on short ones.)
 //
 // On one GB300 (6,691 GB/s measured copy rate), 32 query heads on 8 kv heads of 128, bf16: 64
-// sequences of 4,096 rows 164 us (6,570 GB/s from DRAM), one of 131,071 rows 88 us, 64 of 1
+// sequences of 4,096 rows 165 us (6,500 GB/s from DRAM), one of 131,071 rows 89 us, 64 of 1
 // to 8,192 rows 61 us; one of 200 rows (8 heads on 2 of 64) 7 us.
 
 #include <atomic>

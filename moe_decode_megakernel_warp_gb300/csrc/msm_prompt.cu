@@ -25,10 +25,11 @@
 // at the tensor cores' rate -- Q K^T takes all of shared memory's bandwidth, which the TMA
 // writes share), two tiles of which overlap: about 2,900 cycles for 256 rows x 128 keys, 2,048 of
 // them products.  On one GB300 (1,926 TFLOP/s measured cuBLAS burst), 32 query heads on 8 kv
-// heads of 128, bf16: 16,384 tokens 1.39 ms (1,585 TFLOP/s), 2,048 tokens 35 us, 32,768
-// tokens on a window of 2,048 0.84 ms (1,275 TFLOP/s: two of 17 key tiles are masked, 800 cycles
-// each, and the end of a piece of work, every 17, takes 4,500); head_dim 64 1.24 ms (890 TFLOP/s: as many exponentials for half
-// the products).  Tried and slower: P handed over in two or four parts (+5, +13 %), results
+// heads of 128, bf16: 16,384 tokens 1.39 ms alone (1,580 TFLOP/s) and 1.50 in a row (power), 2,048
+// tokens 36 us, 32,768 tokens on a window of 2,048 0.83 ms (1,290 TFLOP/s: two of 17 key tiles are
+// masked, 800 cycles each, and the end of a piece of work, every 17, takes 4,500).  At head_dim 64
+// the chain is what bounds it still more: 16,384 tokens 1.23 ms (895 TFLOP/s), some 2,740 cycles a
+// step of which the products need 1,024; tensor pipe 34 %, exponentials 34 %, issue 41 %.  Tried and slower: P handed over in two or four parts (+5, +13 %), results
 // written by four more warps (+5 %; fewer registers for the softmax) or through shared memory
 // with four stages of the ring instead of five (+4 %), 192 or 208 registers (+7, +2 %).
 #include <cuda.h>
@@ -163,7 +164,9 @@ struct Place {
 // end (cached ones too), highest first: that is by the keys that they see, the most first (four prompts of
 // 2,048 tokens 132 us, listed sequence by sequence 154).  Where the window makes tiles alike, or there is
 // one sequence, they are listed sequence by sequence: neighbours share keys, and there is nothing to
-// search (12 resumed prompts on a window of 2,048 170 us, by level 175).
+// search (12 resumed prompts on a window of 2,048 170 us, by level 175; the one windowed batch measured.
+// One sequence with more keys than the window decides it for its 32, so a window that hides few keys of long
+// ones gives the order by level up as well).
 __device__ bool find_tile(const PromptAttn& p, volatile Place* place, int t, int& seq, int& tile) {
   const int lane = threadIdx.x & 31;
   int c = place->c, before = place->before;
@@ -596,7 +599,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
               e0 = exp2_fast(e0);
               e1 = exp2_fast(e1);
               sum[i & 1] = add2(sum[i & 1], pair(e0, e1));
-              // rounded to the 16-bit type for the product with V; the sum keeps 32 bits
+              // Rounded to the 16-bit type for the product with V; the sum keeps 32 bits.  (The rest as a
+              // second term, a second product: relative L2 error 2.1e-3 -> 1.6e-3, what the
+              // result's own rounding leaves, fp16 2.6e-4 -> 2.0e-4, but 16,384 tokens 1.39 -> 2.39 ms.)
               pk[i] = El::pack(e0, e1);
             }
             tmem_st16(ts + c * 16, pk);

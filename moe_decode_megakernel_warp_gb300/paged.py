@@ -199,7 +199,8 @@ def prompt_attention(q, k, v, q_starts, k_starts=None, window=0, scale=None, out
     q [n_q, n_q_heads, head_dim], k and v [n_k, n_kv_heads, head_dim] (any strides that keep
     rows consecutive; ``cache.transpose(0, 1)`` of a verify-step cache [n_kv_heads, max_ctx,
     head_dim] is read in place), q_starts and k_starts int32 [n_seqs + 1] on the device
-    (k_starts defaults to q_starts), scale defaults to 1 / sqrt(head_dim).  Returns out; a new
+    (k_starts defaults to q_starts; a sequence without queries passes over keys, as the rows that a
+    cache has to spare), scale defaults to 1 / sqrt(head_dim).  Returns out; a new
     one is uninitialised behind the last sequence.
 
     The kernel's own waits end after 2 s, which only a fault or a GPU that is busy elsewhere brings

@@ -927,6 +927,30 @@ def test_blocks_with_several_pieces_of_work(kind, hd, window):
         assert np.array_equal(bits(msm.prompt_attention(q, k, v, ints(qs), ints(ks), window=window)), bits(out))
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("window", [0, 50])
+def test_a_batch_of_caches_with_rows_to_spare(hd, window):
+    """Contiguous caches side by side, filled in part (NaN behind), each with a turn that continues it: the
+    spare rows as sequences without queries."""
+    torch, msm = _mods()
+    room, have, new = 300, [120, 300, 0, 7, 299], [33, 5, 0, 7, 130]
+    k, v = (randn("bf16", 2, room * len(have), hd, seed=i).cuda() for i in (1, 2))
+    qs, ks, at = [0], [0], 0
+    for s, (h, n) in enumerate(zip(have, new)):
+        at += n
+        qs += [at, at]
+        ks += [room * s + h, room * (s + 1)]
+        k[:, room * s + h:room * (s + 1)] = float("nan")
+        v[:, room * s + h:room * (s + 1)] = float("nan")
+    k, v = k.transpose(0, 1), v.transpose(0, 1)
+    q = randn("bf16", at, 8, hd, seed=3).cuda()
+    got = msm.prompt_attention(q, k, v, ints(qs), ints(ks), window=window)
+    for s, (h, n) in enumerate(zip(have, new)):
+        a, b = slice(qs[2 * s], qs[2 * s] + n), slice(room * s, room * s + h)
+        want, tol = attend_matrix(f64(q[a]), f64(k[b]), f64(v[b]), h - n, window, hd ** -0.5, "bf16")
+        assert_close(got[a], want, tol, "cache %d" % s)
+
+
 def test_prompts_on_two_streams_at_once():
     torch, msm = _mods()
     n = 3000
