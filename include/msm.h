@@ -621,9 +621,9 @@ msm_status msm_pages_sync(const msm_pages* pages, void* stream);
  * i + (nk - nq) - j < window (the verify step's sliding window).  nk > nq resumes a
  * prompt whose first rows are cached already; a query that sees no key gives zeros.
  *   out[i][h] = sum_j softmax_j(scale q[i][h] . k[j]) v[j]
- * with kv head h / (n_q_heads / n_kv_heads).  32-bit scores and sums; the weights are rounded
- * to the 16-bit type for their product with v (fp16: to 0 below 2^-28 of the largest).  Keys that a query does not see have no
- * part in its result, whatever they hold.
+ * with kv head h / (n_q_heads / n_kv_heads).  32-bit scores and sums; the weights are
+ * rounded to the 16-bit type for their product with v (fp16: to 0 below 2^-28 of the
+ * largest).  Keys that a query does not see have no part in its result, whatever they hold.
  *   q, out   device [n_q][n_q_heads][head_dim]; k, v device [n_k][n_kv_heads][head_dim]:
  *            strides in elements between tokens and between heads (multiples of 8, at
  *            least head_dim, below 2^31), 16-byte aligned.  A verify-step cache is read in
@@ -632,8 +632,8 @@ msm_status msm_pages_sync(const msm_pages* pages, void* stream);
  *   q_starts, k_starts  device int32 [n_seqs + 1], ascending from 0, at most n_q and n_k
  *            (larger values are cut off there); rows of out at or behind
  *            q_starts[n_seqs] are left as they are.  A sequence without queries stands for
- *            keys to be passed over, as the rows that a cache has to spare.  n_q = 0 does nothing; with n_k = 0
- *            k and v may be NULL.
+ *            keys to be passed over, as the rows that a cache has to spare.  n_q = 0 does
+ *            nothing; with n_k = 0 k and v may be NULL.
  * Host errors: MSM_ERR_INVALID_ARG (NULL or misaligned pointers, sizes out of range,
  * strides), MSM_ERR_UNSUPPORTED (head_dim other than 64 or 128, n_q_heads / n_kv_heads
  * other than 1, 2, 4 or 8, more than 65535 kv heads, n_q or n_k of 2^27 or more, or

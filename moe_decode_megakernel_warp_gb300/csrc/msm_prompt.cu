@@ -29,9 +29,10 @@
 // tokens 36 us, 32,768 tokens on a window of 2,048 0.83 ms (1,290 TFLOP/s: two of 17 key tiles are
 // masked, 800 cycles each, and the end of a piece of work, every 17, takes 4,500).  At head_dim 64
 // the chain is what bounds it still more: 16,384 tokens 1.23 ms (895 TFLOP/s), some 2,740 cycles a
-// step of which the products need 1,024; tensor pipe 34 %, exponentials 34 %, issue 41 %.  Tried and slower: P handed over in two or four parts (+5, +13 %), results
-// written by four more warps (+5 %; fewer registers for the softmax) or through shared memory
-// with four stages of the ring instead of five (+4 %), 192 or 208 registers (+7, +2 %).
+// step of which the products need 1,024; tensor pipe 34 %, exponentials 34 %, issue 41 %.  Tried
+// and slower: P handed over in two or four parts (+5, +13 %), results written by four more warps
+// (+5 %; fewer registers for the softmax) or through shared memory with four stages of the ring
+// instead of five (+4 %), 192 or 208 registers (+7, +2 %).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
