@@ -526,11 +526,11 @@ msm_status msm_graph_create_spec(msm_model* target, msm_model* draft, const void
  * than 1, 2, 4 or 8, more than 65535 kv heads, 2^31 or more table entries, 2^32 or more rows in a pool);
  * nothing is enqueued then.  The calls leave the current device as it was.
  */
-typedef enum { MSM_BF16 = 0, MSM_FP16 = 1 } msm_dtype;
+typedef enum { MSM_BF16 = 0, MSM_FP16 = 1, MSM_E4M3 = 2, MSM_FP32 = 3 } msm_dtype;
 
 typedef struct {
   int device;
-  int dtype;                   /* msm_dtype of the pools, and of the rows and queries used with them */
+  int dtype;                   /* MSM_BF16 or MSM_FP16: the pools, and the rows and queries used with them */
   int n_layers, n_pages, page_rows, n_kv_heads, head_dim;
   int n_seqs, max_pages;       /* rows and columns of the table */
   void* const* k_pages;        /* host arrays [n_layers] of device pointers, 16-byte aligned */
@@ -609,8 +609,71 @@ msm_status msm_paged_attention(const msm_pages* pages, int layer, const void* q,
                                int64_t out_seq_stride, int64_t out_head_stride, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/*
+ * msm_paged_attention with sinks: on a sliding-window layer (window > 0) the first `sinks` rows of a
+ * sequence stay visible behind the window, row r of n being seen if n - 1 - r < window or
+ * r < sinks.  Without a window every row is seen anyway.  Rows between the sinks and the window are
+ * not read.  Workspace, errors and arithmetic are those of msm_paged_attention, which is this
+ * call with sinks = 0; a negative number of sinks is MSM_ERR_INVALID_ARG.
+ */
+msm_status msm_paged_attention_sinks(const msm_pages* pages, int layer, const void* q, int64_t q_seq_stride,
+                                     int64_t q_head_stride, int n_q_heads, float scale, int window, int sinks,
+                                     void* out, int64_t out_seq_stride, int64_t out_head_stride, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
 /* Wait for `stream`, then return (and clear) the device status of the cache. */
 msm_status msm_pages_sync(const msm_pages* pages, void* stream);
+
+/*
+ * Paged KV cache in 8 bits: the pools hold e4m3 codes, and every block of block_rows rows of one
+ * page and head has a 32-bit scale, K and V apart.  Row r of a page belongs to block r / block_rows of
+ * the page; where block_rows does not divide page_rows the page's last block is shorter.  A value is
+ * code x scale.
+ *   pages      as for a cache of 16 bits, with dtype = MSM_E4M3 and pools e4m3
+ *              [n_pages][n_kv_heads][page_rows][head_dim]
+ *   block_rows 1 .. page_rows
+ *   k_scales, v_scales  host arrays [n_layers] of device pointers, fp32
+ *              [n_pages][n_kv_heads][ceil(page_rows / block_rows)], finite and not negative (0: the block's
+ *              values are 0)
+ * Tables, errors and the order of calls are those of the calls on msm_pages; the calls that move rows
+ * move their scales too.
+ */
+typedef struct {
+  msm_pages pages;
+  int block_rows;
+  float* const* k_scales;
+  float* const* v_scales;
+} msm_qpages;
+
+msm_status msm_qpages_resize(const msm_qpages* pages, const int32_t* new_lens, void* stream);
+msm_status msm_qpages_fork(const msm_qpages* pages, const int32_t* parent, void* stream);
+msm_status msm_qpages_compact(const msm_qpages* pages, void* stream);
+msm_status msm_qpages_sync(const msm_qpages* pages, void* stream);
+
+/*
+ * msm_pages_write into 8 bits: k and v hold dtype (MSM_BF16 or MSM_FP16) elements.  For each head and block
+ * of rows, with amax the largest finite magnitude among the block's new rows, the least power of two s >= 2^-126
+ * with amax <= 448 s (0 for amax = 0) is what they need.  A block whose first row is new takes it as its scale.
+ * In one that begins with older rows of the sequence the scale becomes the larger of it and the old one,
+ * and where that is larger than the old one the older codes are multiplied by old / new in 32 bits and rounded
+ * again.  New elements are divided by the scale and rounded to nearest even, infinities to +-448, NaN stays
+ * NaN.  (Between powers of two the older codes lose bits below 2^-6 of the scale only.)
+ */
+msm_status msm_qpages_write(const msm_qpages* pages, int layer, int dtype, const void* k, const void* v,
+                            int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                            int64_t v_head_stride, const int32_t* starts, int n_tokens, void* stream);
+
+/*
+ * msm_paged_attention_sinks over a cache in 8 bits; q and out hold dtype (MSM_BF16 or MSM_FP16) elements.
+ * The codes are exact in the products with q and the weights, 16-bit floats (fp16, the head's q scaled by a power of
+ * two); scores and sums have 32 bits, and a weight times V's scale is two 16-bit terms (off by at most
+ * 3 x 2^-22 of itself or 2^-39 of the largest).
+ */
+size_t msm_qpages_attention_workspace(const msm_qpages* pages, int n_q_heads);
+msm_status msm_qpages_attention(const msm_qpages* pages, int layer, int dtype, const void* q, int64_t q_seq_stride,
+                                int64_t q_head_stride, int n_q_heads, float scale, int window, int sinks, void* out,
+                                int64_t out_seq_stride, int64_t out_head_stride, void* workspace,
+                                size_t workspace_bytes, void* stream);
 
 /*
  * Causal attention of whole prompts, packed one behind the other: the pass that fills
@@ -658,6 +721,55 @@ typedef struct {
   uint32_t flags;   /* MSM_FLAG_TEST_DROP_HANDOFF (no key or value is loaded, so that the waits run out), or 0 */
 } msm_prompt;
 msm_status msm_prompt_attention(const msm_prompt* prompt, void* stream);
+
+/*
+ * msm_prompt_attention with sinks: with window > 0 the first `sinks` keys of a sequence stay visible
+ * behind the window, key j being seen by the query at position i' = i + (nk - nq) if j <= i' and
+ * (i' - j < window or j < sinks).  msm_prompt_attention is this call with sinks = 0; a negative number
+ * of sinks is MSM_ERR_INVALID_ARG.
+ */
+msm_status msm_prompt_attention_sinks(const msm_prompt* prompt, int sinks, void* stream);
+
+/*
+ * Drawing one token per row of logits, from given random numbers: the step from the LM head's logits
+ * (those of msm_verify_step and msm_draft_step among them) to the next tokens where msm_accept's greedy
+ * choice is not wanted.  With x a row, M its maximum, T its temperature and w_i = exp((x_i - M) / T):
+ *   - the tokens are ordered by x, the larger first, among equals the lower index first; -inf and NaN are
+ *     never drawn;
+ *   - top_k > 0 keeps the first top_k of them;
+ *   - top_p < 1 keeps of these the shortest beginning whose weights add up to at least top_p times theirs
+ *     (at least one token);
+ *   - min_p keeps of these the ones with w >= min_p;
+ *   - the token is the lowest index whose weight, added to those of the kept lower indices, exceeds
+ *     random x the sum over all that are kept (random = 1: the last one that has a weight).
+ * T = 0 takes the largest logit (the lowest index among equals).  Where x is +inf its w is 1, and those of
+ * finite ones are 0.  Weights are held as multiples of 2^-42, so sums are exact and do not depend on timing.
+ *   logits     device MSM_FP32, MSM_BF16 or MSM_FP16 [n_rows][vocab], row_stride elements between rows (0:
+ *              every row is the same one), aligned to their type
+ *   temperature, top_k, top_p, min_p  device [n_rows], fp32 and int32, or NULL for 1, 0 (no limit), 1 and 0
+ *   random     device fp32 [n_rows], 0 .. 1
+ *   tokens     device int32 [n_rows]: the tokens; -1 for a row without a token that can be drawn, and for one
+ *              whose temperature is negative or not finite, or whose top_p, min_p or random is outside 0 .. 1
+ *   probs      device fp32 [n_rows] or NULL: the token's probability among those kept (0 beside -1)
+ *   kept       device int32 [n_rows] or NULL: how many tokens are kept (0 beside -1)
+ * Host errors: MSM_ERR_INVALID_ARG (NULL or misaligned pointers, sizes below 1 - n_rows = 0 does nothing -,
+ * a negative stride, another dtype), MSM_ERR_UNSUPPORTED (vocab above 2^20, 2^24 rows or more).
+ * One launch, no workspace; the logits are read once up to 409,600 of them.
+ */
+typedef struct {
+  int device;
+  int dtype; /* msm_dtype of the logits */
+  int n_rows, vocab;
+  const void* logits;
+  int64_t row_stride;
+  const float* temperature;
+  const int32_t* top_k;
+  const float *top_p, *min_p, *random;
+  int32_t* tokens;
+  float* probs;
+  int32_t* kept;
+} msm_sampling;
+msm_status msm_sample(const msm_sampling* sampling, void* stream);
 
 /* Message of the last error on the calling thread ("" if none). */
 const char* msm_last_error(void);

@@ -22,8 +22,8 @@ _ROOT = os.path.dirname(_HERE)
 _INCLUDE = os.path.join(_ROOT, "include")
 LIB_PATH = os.path.join(_BUILD, "libmsm.so")
 _SOURCES = ["msm_kernel.cu", "msm_pack.cu", "msm_api.cu", "msm_accept.cu", "msm_pages.cu", "msm_paged_attn.cu",
-            "msm_prompt.cu", "msm_paged_api.cu"]
-_HEADERS = ["msm_device.cuh", "msm_internal.h", "msm_paged.h", "msm_attn.cuh"]
+            "msm_prompt.cu", "msm_paged_api.cu", "msm_qpages.cu", "msm_sample.cu"]
+_HEADERS = ["msm_device.cuh", "msm_internal.h", "msm_paged.h", "msm_attn.cuh", "msm_sample.h"]
 NVCC_ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 MSM_OK, MSM_ERR_INVALID_ARG, MSM_ERR_CUDA, MSM_ERR_OOM, MSM_ERR_DEVICE_TIMEOUT, MSM_ERR_UNSUPPORTED = range(6)
@@ -36,8 +36,9 @@ MSM_FLAG_PDL = 0x8
 MSM_FLAG_DRAFT = 0x20
 MSM_FLAG_TEST_DROP_HANDOFF = 0x10000
 MSM_TIMING_EVENTS = 192
-# msm_dtype: the 16-bit types of a paged cache and of the prompt attention
-MSM_BF16, MSM_FP16 = 0, 1
+# msm_dtype: the 16-bit types of a paged cache and of the prompt attention, the codes of a cache in 8 bits,
+# and (with the 16-bit ones) logits
+MSM_BF16, MSM_FP16, MSM_E4M3, MSM_FP32 = 0, 1, 2, 3
 # entries of msm_accept's result buffer (MSM_ACCEPT_RESULT_INTS)
 MSM_ACCEPT_RESULT_INTS = 34
 # entries of the device-resident step state (MSM_STEP_STATE_INTS): pos0, parent[16], tokens[16], spare
@@ -67,7 +68,10 @@ EXPORTED = ["msm_model_create", "msm_model_destroy", "msm_verify_step", "msm_ver
             "msm_graph_launch", "msm_graph_destroy", "msm_verify_step_dev", "msm_accept_dev",
             "msm_graph_create_dev", "msm_draft_step_dev", "msm_embed_dev", "msm_graph_create_spec",
             "msm_pages_scratch_ints", "msm_pages_resize", "msm_pages_fork", "msm_pages_compact", "msm_pages_write",
-            "msm_pages_sync", "msm_paged_attention_workspace", "msm_paged_attention", "msm_prompt_attention"]
+            "msm_pages_sync", "msm_paged_attention_workspace", "msm_paged_attention", "msm_prompt_attention",
+            "msm_paged_attention_sinks", "msm_prompt_attention_sinks", "msm_qpages_resize", "msm_qpages_fork",
+            "msm_qpages_compact", "msm_qpages_sync", "msm_qpages_write", "msm_qpages_attention_workspace",
+            "msm_qpages_attention", "msm_sample"]
 # capacity of the static scratch array behind msm_verify_step_noalloc (MSM_NOALLOC_SCRATCH_BYTES)
 MSM_NOALLOC_SCRATCH_BYTES = 10 << 20
 
@@ -160,6 +164,18 @@ class MsmPrompt(ctypes.Structure):
         (n, ctypes.c_void_p) for n in ("q_starts", "k_starts", "status")] + [("flags", ctypes.c_uint32)]
 
 
+class MsmQPages(ctypes.Structure):
+    """msm_qpages: the description of a paged KV cache in 8 bits."""
+    _fields_ = [("pages", MsmPages), ("block_rows", ctypes.c_int), ("k_scales", _PP), ("v_scales", _PP)]
+
+
+class MsmSampling(ctypes.Structure):
+    """msm_sampling: the arguments of msm_sample."""
+    _fields_ = [(n, ctypes.c_int) for n in ("device", "dtype", "n_rows", "vocab")] + [
+        ("logits", ctypes.c_void_p), ("row_stride", ctypes.c_int64)] + [
+        (n, ctypes.c_void_p) for n in ("temperature", "top_k", "top_p", "min_p", "random", "tokens", "probs", "kept")]
+
+
 _LIB = None
 _LOCK = threading.Lock()
 
@@ -239,6 +255,31 @@ def lib():
             L.msm_paged_attention.restype = st
             L.msm_prompt_attention.argtypes = [vp, vp]
             L.msm_prompt_attention.restype = st
+            L.msm_paged_attention_sinks.argtypes = [pp, ctypes.c_int, vp, i64, i64, ctypes.c_int, ctypes.c_float,
+                                                    ctypes.c_int, ctypes.c_int, vp, i64, i64, vp, ctypes.c_size_t, vp]
+            L.msm_paged_attention_sinks.restype = st
+            L.msm_prompt_attention_sinks.argtypes = [vp, ctypes.c_int, vp]
+            L.msm_prompt_attention_sinks.restype = st
+            qp = ctypes.POINTER(MsmQPages)
+            L.msm_qpages_resize.argtypes = [qp, vp, vp]
+            L.msm_qpages_resize.restype = st
+            L.msm_qpages_fork.argtypes = [qp, vp, vp]
+            L.msm_qpages_fork.restype = st
+            L.msm_qpages_compact.argtypes = [qp, vp]
+            L.msm_qpages_compact.restype = st
+            L.msm_qpages_sync.argtypes = [qp, vp]
+            L.msm_qpages_sync.restype = st
+            L.msm_qpages_write.argtypes = [qp, ctypes.c_int, ctypes.c_int, vp, vp, i64, i64, i64, i64, vp, ctypes.c_int,
+                                           vp]
+            L.msm_qpages_write.restype = st
+            L.msm_qpages_attention_workspace.argtypes = [qp, ctypes.c_int]
+            L.msm_qpages_attention_workspace.restype = ctypes.c_size_t
+            L.msm_qpages_attention.argtypes = [qp, ctypes.c_int, ctypes.c_int, vp, i64, i64, ctypes.c_int,
+                                               ctypes.c_float, ctypes.c_int, ctypes.c_int, vp, i64, i64, vp,
+                                               ctypes.c_size_t, vp]
+            L.msm_qpages_attention.restype = st
+            L.msm_sample.argtypes = [vp, vp]
+            L.msm_sample.restype = st
             L.msm_last_error.argtypes = []
             L.msm_last_error.restype = ctypes.c_char_p
             _LIB = L
@@ -457,8 +498,57 @@ def msm_paged_attention(pages: MsmPages, layer, q, q_strides, n_q_heads, scale, 
                                      out_strides[0], out_strides[1], workspace, workspace_bytes, stream)
 
 
+def msm_paged_attention_sinks(pages: MsmPages, layer, q, q_strides, n_q_heads, scale, window, sinks, out, out_strides,
+                              workspace, workspace_bytes, stream=0) -> int:
+    """q_strides, out_strides: (sequence, head) strides in elements."""
+    return lib().msm_paged_attention_sinks(pages, layer, q, q_strides[0], q_strides[1], n_q_heads, scale, window, sinks,
+                                           out, out_strides[0], out_strides[1], workspace, workspace_bytes, stream)
+
+
 def msm_prompt_attention(prompt: MsmPrompt, stream=0) -> int:
     return lib().msm_prompt_attention(ctypes.byref(prompt), stream)
+
+
+def msm_prompt_attention_sinks(prompt: MsmPrompt, sinks, stream=0) -> int:
+    return lib().msm_prompt_attention_sinks(ctypes.byref(prompt), sinks, stream)
+
+
+def msm_qpages_resize(pages: MsmQPages, new_lens, stream=0) -> int:
+    return lib().msm_qpages_resize(pages, new_lens, stream)
+
+
+def msm_qpages_fork(pages: MsmQPages, parent, stream=0) -> int:
+    return lib().msm_qpages_fork(pages, parent, stream)
+
+
+def msm_qpages_compact(pages: MsmQPages, stream=0) -> int:
+    return lib().msm_qpages_compact(pages, stream)
+
+
+def msm_qpages_write(pages: MsmQPages, layer, dtype, k, v, k_strides, v_strides, starts, n_tokens, stream=0) -> int:
+    """dtype: msm_dtype of k and v; k_strides, v_strides: (token, head) strides in elements."""
+    return lib().msm_qpages_write(pages, layer, dtype, k, v, k_strides[0], k_strides[1], v_strides[0], v_strides[1],
+                                  starts, n_tokens, stream)
+
+
+def msm_qpages_sync(pages: MsmQPages, stream=0) -> int:
+    return lib().msm_qpages_sync(pages, stream)
+
+
+def msm_qpages_attention_workspace(pages: MsmQPages, n_q_heads) -> int:
+    """Bytes of the workspace; 0 if an argument is wrong (see msm_last_error)."""
+    return lib().msm_qpages_attention_workspace(pages, n_q_heads)
+
+
+def msm_qpages_attention(pages: MsmQPages, layer, dtype, q, q_strides, n_q_heads, scale, window, sinks, out, out_strides,
+                         workspace, workspace_bytes, stream=0) -> int:
+    """dtype: msm_dtype of q and out; q_strides, out_strides: (sequence, head) strides in elements."""
+    return lib().msm_qpages_attention(pages, layer, dtype, q, q_strides[0], q_strides[1], n_q_heads, scale, window, sinks,
+                                      out, out_strides[0], out_strides[1], workspace, workspace_bytes, stream)
+
+
+def msm_sample(sampling: MsmSampling, stream=0) -> int:
+    return lib().msm_sample(ctypes.byref(sampling), stream)
 
 
 # ---------------------------------------------------------------- torch-facing wrapper
@@ -684,4 +774,5 @@ class StepGraph:
             pass
 
 
-from .paged import PagedCache, prompt_attention  # noqa: E402  (uses the definitions above)
+from .paged import PagedCache, prompt_attention  # noqa: E402
+from .sampling import sample  # noqa: E402  (uses the definitions above)

@@ -46,8 +46,11 @@ struct PagesCopy {
   PagesMeta m;
   int n_layers, n_kv_heads, row_vecs;  // 16-byte vectors per row
   int renumber;                        // compact: this launch also renumbers the tables
+  int block_rows, page_blocks;         // a cache in 8 bits: rows of a scale, scales of a page and head (else 0)
   uint4* k[kPagesLayers];
   uint4* v[kPagesLayers];
+  float* k_scales[kPagesLayers];
+  float* v_scales[kPagesLayers];
 };
 
 struct PagesWrite {
@@ -59,12 +62,30 @@ struct PagesWrite {
   const int32_t* starts;
 };
 
+// new rows of a cache in 8 bits (msm_qpages.cu)
+struct QPagesWrite {
+  PagesMeta m;
+  int n_kv_heads, n_tokens, block_rows, page_blocks;
+  int group;  // tokens that one unit of threads looks at
+  uint8_t *pool_k, *pool_v;
+  float *k_scales, *v_scales;
+  const uint16_t *k, *v;
+  int64_t k_token, k_head, v_token, v_head;  // strides in elements
+  const int32_t* starts;
+};
+cudaError_t launch_qpages_write(const QPagesWrite& p, int dtype, int head_dim, cudaStream_t s);
+
 // attention of one new token per sequence (msm_paged_attn.cu)
 struct PagedAttn {
   const int32_t *table, *lens;
   int32_t* status;
   int n_seqs, max_pages, n_pages, page_rows, n_kv_heads, group, window;
-  const uint16_t *q, *k, *v;  // k, v: the layer's pools
+  int sinks;  // rows at the front that stay visible (0 without a window)
+  const uint16_t* q;
+  const void *k, *v;  // the layer's pools
+  // a cache in 8 bits (else null): fp32 [n_pages][n_kv_heads][page_blocks], a scale for block_rows rows each
+  const float *k_scales, *v_scales;
+  int block_rows, page_blocks;
   uint16_t* out;
   int64_t q_seq, q_head, out_seq, out_head;  // strides in elements
   float scale_log2;                          // softmax scale x log2(e)
@@ -75,6 +96,15 @@ constexpr int kPagedAttnPerSm = 2;  // blocks per SM
 size_t paged_attn_workspace(int blocks, int group, int head_dim);
 cudaError_t launch_paged_attn(const PagedAttn& p, int dtype, int head_dim, int blocks, cudaStream_t s);
 
+// what the page operations share: the status word
+#ifdef __CUDACC__
+__device__ __forceinline__ void latch(int32_t* status, int code, int call) {
+  atomicCAS(status, 0, code | (call << 8));
+}
+// (only ever set by a call that the others are ordered behind, so all threads of a call see the same)
+__device__ __forceinline__ bool stopped(const int32_t* status) { return (__ldcg(status) & kPagesStopped) != 0; }
+#endif
+
 // causal attention of packed prompts (msm_prompt.cu)
 struct PromptAttn {
   const uint16_t *q, *k, *v;
@@ -82,6 +112,7 @@ struct PromptAttn {
   int64_t q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;  // strides in elements
   const int32_t *q_starts, *k_starts;
   int n_seqs, n_q, n_k, n_kv_heads, group, window;
+  int sinks;         // keys at a sequence's front that stay visible behind the window (0 without a window; at most n_k)
   int out_32;        // every row of out starts on a 32-byte boundary
   float scale_log2;  // softmax scale x log2(e)
   int32_t* status;   // becomes MSM_ERR_DEVICE_TIMEOUT when a wait ran out (may be null)

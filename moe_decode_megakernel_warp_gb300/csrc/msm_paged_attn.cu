@@ -26,6 +26,7 @@
 // to 8,192 rows 61 us; one of 200 rows (8 heads on 2 of 64) 7 us.
 
 #include <atomic>
+#include <type_traits>
 
 #include "msm_attn.cuh"
 #include "msm_paged.h"
@@ -86,11 +87,15 @@ struct Split {
 // a partial result in the workspace: maxima, sums, outputs
 __host__ __device__ constexpr int part_floats(int group, int hd) { return 2 * kHeads + group * hd; }
 
-// The rows of one sequence that a call reads: [lo, hi), in tiles from base (lo rounded down to
-// a chunk).  An item costs its block one unit more than its tiles: finishing it takes about as long
-// as a tile (64 sequences of 1 to 8,192 rows: 80 us without that unit, 60 us with it).
+// The rows of one sequence that a call reads: the sinks [0, first) and the window [lo, hi), in
+// tiles.  Places count them through: without sinks a place is its row, from base (lo rounded down to a
+// chunk) to hi.  With sinks in front of the window the tiles that hold them come first, from place 0,
+// and the places from `pad` on are the rows `skip` further on, from base.  (Where those tiles reach the
+// window there is nothing to skip.)  An item costs its block one unit more than its tiles: finishing it
+// takes about as long as a tile (64 sequences of 1 to 8,192 rows: 80 us without that unit, 60 us with it).
 struct Rows {
-  int lo, hi, base, tiles, units;
+  int lo, hi, base, tiles, units;  // hi, base: places
+  int first, pad, skip;
 };
 __device__ __forceinline__ Rows seq_rows(const PagedAttn& p, int s) {
   Rows r;
@@ -98,17 +103,29 @@ __device__ __forceinline__ Rows seq_rows(const PagedAttn& p, int s) {
   r.hi = (int)min((int64_t)max(p.lens[s], 0), cap);
   r.lo = p.window > 0 ? max(0, r.hi - p.window) : 0;
   r.base = r.lo & ~31;
+  r.first = min(p.sinks, r.lo);
+  r.pad = r.skip = 0;
+  if (r.first > 0) {
+    r.pad = (r.first + kTile - 1) / kTile * kTile;
+    r.skip = max(0, r.base - r.pad);
+    r.hi -= r.skip;
+    r.base = 0;
+  }
   r.tiles = (r.hi - r.base + kTile - 1) / kTile;
   r.units = r.tiles > 0 ? r.tiles + 1 : 0;
   return r;
 }
 
-// The work of one block on one (sequence, head): tiles [ta, tb), rows [first, end).
+// The work of one block on one (sequence, head): tiles [ta, tb), places [first, end).
 struct Segment {
   int s, h;
-  int lo, end, first;  // rows below lo are not seen
+  int lo, sinks;       // rows below lo are not seen, but for the first `sinks`
+  int pad, skip;       // as in Rows
+  int end, first;
   int ta, tb, tiles;   // its tiles of the item's
   int64_t unit0;       // the batch's unit that holds the item's first tile
+  __device__ __forceinline__ int row(int place) const { return place < pad ? place : place + skip; }
+  __device__ __forceinline__ bool sees(int row) const { return row >= lo || row < sinks; }
 };
 
 // Walks the segments of a block's run of units [u, u1) (a whole warp together).  Unit 0 of an item
@@ -148,6 +165,9 @@ struct Walk {
       g.tb = (int)min((int64_t)rw.tiles, u1 - g.unit0);
       g.tiles = rw.tiles;
       g.lo = rw.lo;
+      g.sinks = rw.first;
+      g.pad = rw.pad;
+      g.skip = rw.skip;
       g.first = rw.base + g.ta * kTile;
       g.end = min(rw.hi, rw.base + g.tb * kTile);
       u = g.unit0 + g.tb;
@@ -157,25 +177,59 @@ struct Walk {
   }
 };
 
-template <int HD>
+template <int HD, bool kHeld8>
 struct Cfg {
-  static constexpr int kRowBytes = HD * 2;
-  static constexpr int kChunk = HD == 128 ? 16 : 32;          // rows of one warp step: 8 KB of K and V
+  static constexpr int kRowBytes = HD * (kHeld8 ? 1 : 2);
+  static constexpr int kChunk = HD == 128 && !kHeld8 ? 16 : 32;  // rows of one warp step: 8 KB of K and V (8 bits of 64: 4 KB)
   static constexpr int kStep = kWarps * kChunk;               // rows of one step of the block
   static constexpr int kStageBytes = 2 * kChunk * kRowBytes;
   // One step on the way while another one is worked on: 64 KB per SM cover the latency, and
   // more of them cost DRAM locality (head_dim 128, 64 sequences of 16,384 rows: two stages
   // 6,736 GB/s, three 6,457).
-  static constexpr int kStages = 2;
+  static constexpr int kStages = HD == 64 && kHeld8 ? 3 : 2;
   static constexpr int kOutStride = HD + 4;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
   static constexpr int kSmem = kRingBytes + kWarps * kHeads * kOutStride * 4;
 };
 
-// 16-byte piece c of row r of a chunk: the permutation keeps the eight lanes of a phase on
+// Where 16-byte piece c of row r of a chunk stands: the permutation keeps the lanes of a phase on
 // different banks for the K reads (two rows x four pieces) and the V reads (four rows of one
-// parity x two pieces) alike
-__device__ __forceinline__ int swizzle(int r, int c) { return c ^ (((r >> 1) & 3) << 1) ^ ((r & 1) << 2); }
+// parity x two pieces) alike.  Rows of 64 bytes share a line of 128 in pairs.
+template <int kRowBytes>
+__device__ __forceinline__ int at_piece(int r, int c) {
+  if constexpr (kRowBytes == 64) return (r >> 1) * 128 + ((((r & 1) << 2) + c) ^ (((r >> 1) & 3) << 1)) * 16;
+  else return r * kRowBytes + (c ^ (((r >> 1) & 3) << 1) ^ ((r & 1) << 2)) * 16;
+}
+// two e4m3 values (the low or the high half of x) as two fp16, which hold every one of them
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {
+  uint32_t r;
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l; }" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
+  uint32_t r;
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+// The scales of a row of a cache in 8 bits: K's, and V's as f 2^e.  e is a float, -inf for a scale of 0.
+struct RowScale {
+  float k, f, e;
+};
+__device__ __forceinline__ RowScale row_scale(float k, float v) {
+  RowScale s;
+  const bool tiny = fabsf(v) < 0x1p-126f;
+  const uint32_t b = __float_as_uint(tiny ? v * 0x1p64f : v), x = b >> 23 & 255u;
+  s.k = k;
+  s.f = x == 255u ? NAN : __uint_as_float((b & 0x807FFFFFu) | 0x3F800000u);
+  s.e = x == 0u ? -INFINITY : (float)((int)x - (tiny ? 127 + 64 : 127));
+  return s;
+}
 
 // Parts of an item, in the order of its tiles: part i stands in slot 1 of block b0 (i = 0) or
 // in slot 0 of block b0 + i.  Joins parts i0, i0 + step, ... (n of them, at most kJoinGroup
@@ -270,13 +324,16 @@ __device__ bool arrive_last(uint32_t* counter, int n, int* s_flag) {
   return last;
 }
 
-template <class El, int HD>
+template <class El, int HD, bool kHeld8>
 __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(const PagedAttn p) {
-  using C = Cfg<HD>;
+  using C = Cfg<HD, kHeld8>;
+  // 8-bit rows become fp16 on their way into the products (exactly), and so do q and the weights
+  using Mul = typename std::conditional<kHeld8, Fp16, El>::type;
   constexpr int KB = HD / 32;  // 32-element blocks of a K row
   constexpr int VB = HD / 64;  // 64-element blocks of a V row
   constexpr int kAhead = C::kStages - 1;
   constexpr int kSub = C::kChunk / 16;
+  constexpr float kSumTop = kHeld8 ? 0.f : Split<Mul>::kTop;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int64_t s_sum[kWarps];
   __shared__ int64_t s_find[2];  // first sequence of the block's run, units before it
@@ -357,12 +414,12 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
   // ---- loads: every warp keeps kAhead chunks of its own on the way, across the ends of items
   Walk ahead{u0, u1, s_find[1], (int)s_find[0]};
   Segment fs{};
-  int fc = 0;  // the next chunk to fetch: row of its first row; -1: none left
+  int fc = 0;  // the next chunk to fetch: place of its first row; -1: none left
   int page = 0;
   // the page of row lane % kChunk of the next chunk
   auto look = [&]() {
     const int r = fc + lane % C::kChunk;
-    page = fc >= 0 && r < fs.end ? p.table[(size_t)fs.s * p.max_pages + r / p.page_rows] : -1;
+    page = fc >= 0 && r < fs.end ? p.table[(size_t)fs.s * p.max_pages + fs.row(r) / p.page_rows] : -1;
   };
   // the next chunk of this warp, in this or a later segment
   auto find_chunk = [&]() {
@@ -377,30 +434,35 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
   int f_stage = 0;
   bool lost = false;  // a table entry outside the pool
   // fetches a chunk and returns which of its rows take part (0 when none is left)
-  auto fetch = [&]() -> uint32_t {
+  auto fetch = [&](RowScale& rs) -> uint32_t {
     uint32_t rows = 0;
     if (fc >= 0) {
-      const int r = fc + lane % C::kChunk;
-      bool ok = r >= fs.lo && r < fs.end;
+      const int place = fc + lane % C::kChunk, r = fs.row(place);
+      bool ok = fs.sees(r) && place < fs.end;
       if (ok && (page < 0 || page >= p.n_pages)) {
         lost = true;
         ok = false;
       }
       rows = __ballot_sync(0xffffffffu, ok);
       // pool row of row lane % kChunk
-      const uint32_t at = ((uint32_t)page * p.n_kv_heads + fs.h) * p.page_rows + r % p.page_rows;
+      const uint32_t head = (uint32_t)page * p.n_kv_heads + fs.h, in_page = r % p.page_rows;
+      const uint32_t at = head * p.page_rows + in_page;
+      if constexpr (kHeld8) {
+        const uint32_t i = head * p.page_blocks + in_page / (uint32_t)p.block_rows;
+        rs = row_scale(ok ? __ldg(p.k_scales + i) : 0.f, ok ? __ldg(p.v_scales + i) : 0.f);
+      }
       const uint32_t dst = ring + f_stage * C::kStageBytes;
-      constexpr int kPieces = HD / 8, kRowsAtOnce = 32 / kPieces;  // 16-byte pieces of a row
+      constexpr int kPieces = C::kRowBytes / 16, kRowsAtOnce = 32 / kPieces;  // 16-byte pieces of a row
       const int c = lane % kPieces, sub = lane / kPieces;
 #pragma unroll
       for (int i = 0; i < C::kChunk / kRowsAtOnce; ++i) {
         const int row = i * kRowsAtOnce + sub;
         const uint32_t pr = __shfl_sync(0xffffffffu, at, row);
         const bool in = rows >> row & 1;
-        const size_t off = in ? (size_t)pr * HD + c * 8 : 0;
-        const uint32_t d = dst + row * C::kRowBytes + swizzle(row, c) * 16;
-        cp_async16(d, p.k + off, in ? 16 : 0);
-        cp_async16(d + C::kChunk * C::kRowBytes, p.v + off, in ? 16 : 0);
+        const size_t off = in ? (size_t)pr * C::kRowBytes + c * 16 : 0;
+        const uint32_t d = dst + at_piece<C::kRowBytes>(row, c);
+        cp_async16(d, static_cast<const char*>(p.k) + off, in ? 16 : 0);
+        cp_async16(d + C::kChunk * C::kRowBytes, static_cast<const char*>(p.v) + off, in ? 16 : 0);
       }
       f_stage = f_stage + 1 == C::kStages ? 0 : f_stage + 1;
       fc += C::kStep;
@@ -414,8 +476,9 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
   find_chunk();
   look();
   uint32_t queue[kAhead];
+  RowScale scales[kAhead] = {};  // of row `lane`
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) queue[i] = fetch();
+  for (int i = 0; i < kAhead; ++i) queue[i] = fetch(scales[i]);
 
   Walk walk{u0, u1, s_find[1], (int)s_find[0]};
   Segment sg;
@@ -423,18 +486,48 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
   // q of the group as the B operand: column g = query head, the contraction index in the
   // order of the K reads
   uint4 qf[KB];
+  float q0 = 1.f, q1 = 1.f;  // what the products with q of heads 2t, 2t + 1 are times too small
   auto load_q = [&]() {
 #pragma unroll
     for (int j = 0; j < KB; ++j) {
       qf[j] = make_uint4(0u, 0u, 0u, 0u);
-      if (g < p.group)
-        qf[j] = *reinterpret_cast<const uint4*>(p.q + sg.s * p.q_seq + (sg.h * p.group + g) * p.q_head + j * 32 + t * 8);
+      // (8 bits: 16 consecutive elements of a K row a lane, in blocks of 64)
+      const int at = kHeld8 ? (j / 2) * 64 + t * 16 + (j & 1) * 8 : j * 32 + t * 8;
+      if (g < p.group) qf[j] = *reinterpret_cast<const uint4*>(p.q + sg.s * p.q_seq + (sg.h * p.group + g) * p.q_head + at);
+    }
+    if constexpr (kHeld8 && El::kBf16) {
+      // bf16 to fp16: the head's largest finite element to 2^14 .. 2^15 by a power of two.  Elements down to 2^-31
+      // of it stay exact, and what is lost of smaller ones is 2^-39 of it at most.
+      uint32_t most = 0;
+#pragma unroll
+      for (int j = 0; j < KB; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t x = ((&qf[j].x)[i >> 1] >> (16 * (i & 1))) & 0x7FFFu;
+          most = x < El::kExponent ? max(most, x) : most;
+        }
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      // (elements below 2^-98 keep fewer bits: the factor has to be a number)
+      const int up = most ? min(112, 127 + 14 - (int)(most >> 7)) : 0;
+      const float f = __uint_as_float((uint32_t)(127 + up) << 23), back = __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+      for (int j = 0; j < KB; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t& x = (&qf[j].x)[i];
+          x = Fp16::pack(El::value((uint16_t)(x & 0xFFFFu)) * f, El::value((uint16_t)(x >> 16)) * f);
+        }
+      q0 = __shfl_sync(0xffffffffu, back, 8 * t);
+      q1 = __shfl_sync(0xffffffffu, back, 8 * t + 4);
     }
   };
   bool more = walk.next(p, sg);
   load_q();
   while (more) {
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2t, 2t + 1
+    // 8 bits: the largest score + log2 of V's scale.  What V is multiplied with is relative to this one.
+    float v0 = -INFINITY, v1 = -INFINITY;
     uint32_t seen = 0;  // rows that took part
     float o[HD / 16][4];
 #pragma unroll
@@ -445,89 +538,179 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
       cp_async_wait<kAhead - 1>();
       __syncwarp();
       const uint32_t rows = queue[0];
+      const RowScale rs = scales[0];
       seen |= rows;
       const uint32_t kb = ring + stage * C::kStageBytes, vb = kb + C::kChunk * C::kRowBytes;
       stage = stage + 1 == C::kStages ? 0 : stage + 1;
 #pragma unroll
-      for (int i = 0; i + 1 < kAhead; ++i) queue[i] = queue[i + 1];
-      queue[kAhead - 1] = fetch();  // into the stage that the previous step read
+      for (int i = 0; i + 1 < kAhead; ++i) {
+        queue[i] = queue[i + 1];
+        scales[i] = scales[i + 1];
+      }
+      queue[kAhead - 1] = fetch(scales[kAhead - 1]);  // into the stage that the previous step read
       // 16 rows at a time: rows g (sc[0], sc[1]) and g + 8 (sc[2], sc[3]); heads 2t and 2t + 1
       float sc[kSub][4];
-      float x0 = -INFINITY, x1 = -INFINITY;
+      float f_a[kSub], f_b[kSub], e_a[kSub], e_b[kSub];  // V's scales of rows g and g + 8
+      float x0 = -INFINITY, x1 = -INFINITY, y0 = -INFINITY, y1 = -INFINITY;
 #pragma unroll
       for (int u = 0; u < kSub; ++u) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) sc[u][q] = 0.f;
-        const uint32_t k0 = kb + (u * 16 + g) * C::kRowBytes, k1 = k0 + 8 * C::kRowBytes;
+        const int ra = u * 16 + g, rb = ra + 8;
+        const bool ok0 = rows >> ra & 1, ok1 = rows >> rb & 1;
+        if constexpr (kHeld8) {
 #pragma unroll
-        for (int j = 0; j < KB; ++j) {
-          const uint4 a = lds128(k0 + swizzle(g, j * 4 + t) * 16), c = lds128(k1 + swizzle(g, j * 4 + t) * 16);
-          El::mma(sc[u], a.x, c.x, a.y, c.y, qf[j].x, qf[j].y);
-          El::mma(sc[u], a.z, c.z, a.w, c.w, qf[j].z, qf[j].w);
+          for (int j = 0; j < HD / 64; ++j) {
+            const uint4 a = lds128(kb + at_piece<C::kRowBytes>(ra, j * 4 + t)),
+                        c = lds128(kb + at_piece<C::kRowBytes>(rb, j * 4 + t));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t aw = (&a.x)[i], cw = (&c.x)[i];
+              const uint4& q = qf[2 * j + (i >> 1)];
+              Mul::mma(sc[u], e4m3_lo(aw), e4m3_lo(cw), e4m3_hi(aw), e4m3_hi(cw), i & 1 ? q.z : q.x, i & 1 ? q.w : q.y);
+            }
+          }
+          const float ka = __shfl_sync(0xffffffffu, rs.k, ra), kc = __shfl_sync(0xffffffffu, rs.k, rb);
+          f_a[u] = __shfl_sync(0xffffffffu, rs.f, ra);
+          f_b[u] = __shfl_sync(0xffffffffu, rs.f, rb);
+          e_a[u] = __shfl_sync(0xffffffffu, rs.e, ra);
+          e_b[u] = __shfl_sync(0xffffffffu, rs.e, rb);
+          sc[u][0] = sc[u][0] * q0 * ka;
+          sc[u][1] = sc[u][1] * q1 * ka;
+          sc[u][2] = sc[u][2] * q0 * kc;
+          sc[u][3] = sc[u][3] * q1 * kc;
+        } else {
+#pragma unroll
+          for (int j = 0; j < KB; ++j) {
+            const uint4 a = lds128(kb + at_piece<C::kRowBytes>(ra, j * 4 + t)),
+                        c = lds128(kb + at_piece<C::kRowBytes>(rb, j * 4 + t));
+            Mul::mma(sc[u], a.x, c.x, a.y, c.y, qf[j].x, qf[j].y);
+            Mul::mma(sc[u], a.z, c.z, a.w, c.w, qf[j].z, qf[j].w);
+          }
         }
-        const bool ok0 = rows >> (u * 16 + g) & 1, ok1 = rows >> (u * 16 + g + 8) & 1;
         sc[u][0] = ok0 ? sc[u][0] * p.scale_log2 : -INFINITY;
         sc[u][1] = ok0 ? sc[u][1] * p.scale_log2 : -INFINITY;
         sc[u][2] = ok1 ? sc[u][2] * p.scale_log2 : -INFINITY;
         sc[u][3] = ok1 ? sc[u][3] * p.scale_log2 : -INFINITY;
         x0 = fmaxf(x0, fmaxf(sc[u][0], sc[u][2]));
         x1 = fmaxf(x1, fmaxf(sc[u][1], sc[u][3]));
+        if constexpr (kHeld8) {
+          y0 = fmaxf(y0, fmaxf(sc[u][0] + e_a[u], sc[u][2] + e_b[u]));
+          y1 = fmaxf(y1, fmaxf(sc[u][1] + e_a[u], sc[u][3] + e_b[u]));
+        }
       }
 #pragma unroll
       for (int q = 4; q <= 16; q <<= 1) {
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, q));
         x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, q));
+        if constexpr (kHeld8) {
+          y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, q));
+          y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, q));
+        }
       }
       const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-      if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
+      const float w0 = fmaxf(v0, y0), w1 = fmaxf(v1, y1);
+      if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1 || (kHeld8 && (w0 > v0 || w1 > v1)))) {
         // (with no score above -inf yet there is nothing to scale)
         const float a0 = m0 == n0 ? 1.f : exp2_fast(m0 - n0), a1 = m1 == n1 ? 1.f : exp2_fast(m1 - n1);
+        const float b0 = !kHeld8 ? a0 : v0 == w0 ? 1.f : exp2_fast(v0 - w0);
+        const float b1 = !kHeld8 ? a1 : v1 == w1 ? 1.f : exp2_fast(v1 - w1);
         l0 *= a0;
         l1 *= a1;
 #pragma unroll
         for (int i = 0; i < HD / 16; ++i) {
-          o[i][0] *= a0;
-          o[i][1] *= a1;
-          o[i][2] *= a0;
-          o[i][3] *= a1;
+          o[i][0] *= b0;
+          o[i][1] *= b1;
+          o[i][2] *= b0;
+          o[i][3] *= b1;
         }
         m0 = n0;
         m1 = n1;
+        v0 = w0;
+        v1 = w1;
       }
-      const float r0 = (m0 == -INFINITY ? 0.f : m0) - Split<El>::kTop, r1 = (m1 == -INFINITY ? 0.f : m1) - Split<El>::kTop;
+      // what scores are relative to in the sum, and for their product with V
+      const float r0 = (m0 == -INFINITY ? 0.f : m0) - kSumTop, r1 = (m1 == -INFINITY ? 0.f : m1) - kSumTop;
+      const float s0 = (v0 == -INFINITY ? 0.f : v0) - Split<Mul>::kTop + 1.f,
+                  s1 = (v1 == -INFINITY ? 0.f : v1) - Split<Mul>::kTop + 1.f;
 #pragma unroll
       for (int u = 0; u < kSub; ++u) {
-        const float e0 = exp2_fast(sc[u][0] - r0), e1 = exp2_fast(sc[u][1] - r1), e2 = exp2_fast(sc[u][2] - r0),
-                    e3 = exp2_fast(sc[u][3] - r1);
+        float e0 = exp2_fast(sc[u][0] - r0), e1 = exp2_fast(sc[u][1] - r1), e2 = exp2_fast(sc[u][2] - r0),
+              e3 = exp2_fast(sc[u][3] - r1);
         l0 += e0 + e2;
         l1 += e1 + e3;
+        if constexpr (kHeld8) {
+          // weight x V's scale, at most 2^14 (the scale's power of two is in the exponent: neither factor can leave
+          // the range)
+          e0 = exp2_fast(sc[u][0] + e_a[u] - s0) * f_a[u];
+          e1 = exp2_fast(sc[u][1] + e_a[u] - s1) * f_a[u];
+          e2 = exp2_fast(sc[u][2] + e_b[u] - s0) * f_b[u];
+          e3 = exp2_fast(sc[u][3] + e_b[u] - s1) * f_b[u];
+        }
         // P as two 16-bit terms for the product; its sum keeps 32 bits
         uint32_t h0, h1, w0, w1;
-        Split<El>::split(e0, e1, h0, w0);
-        Split<El>::split(e2, e3, h1, w1);
+        Split<Mul>::split(e0, e1, h0, w0);
+        Split<Mul>::split(e2, e3, h1, w1);
         h0 = transpose8x8(h0);
         h1 = transpose8x8(h1);
         w0 = transpose8x8(w0);
         w1 = transpose8x8(w1);
-#pragma unroll
-        for (int j = 0; j < VB; ++j) {
-          // V rows 2t, 2t + 1, 2t + 8, 2t + 9, elements 8g .. 8g + 7 of the block
-          uint4 v[4];
+        if constexpr (kHeld8) {
+          // V rows 2t, 2t + 1, 2t + 8, 2t + 9, elements HD / 8 g .. + HD / 8
+          uint32_t v[4][HD / 32];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int i = 2 * t + (q & 1) + 8 * (q >> 1);
-            v[q] = lds128(vb + (u * 16 + i) * C::kRowBytes + swizzle(i, j * 8 + g) * 16);
+            const int i = u * 16 + 2 * t + (q & 1) + 8 * (q >> 1);
+            if constexpr (HD == 128) {
+              const uint4 x = lds128(vb + at_piece<C::kRowBytes>(i, g));
+              v[q][0] = x.x, v[q][1] = x.y, v[q][2] = x.z, v[q][3] = x.w;
+            } else {
+              const uint2 x = lds64(vb + at_piece<C::kRowBytes>(i, g >> 1) + (g & 1) * 8);
+              v[q][0] = x.x, v[q][1] = x.y;
+            }
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t v0 = (&v[0].x)[i], v1 = (&v[1].x)[i], v2 = (&v[2].x)[i], v3 = (&v[3].x)[i];
-            // element 64 j + 8 g + 2 i in row g of the product, the next one in row g + 8
-            const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632),
-                           a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
-            El::mma(o[j * 4 + i], a0, a1, a2, a3, h0, h1);
-            El::mma(o[j * 4 + i], a0, a1, a2, a3, w0, w1);
+          for (int i = 0; i < HD / 32; ++i)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              // elements 4 i + 2 half and the next one of two rows, then of the other two
+              const uint32_t a = __byte_perm(v[0][i], v[1][i], half ? 0x7362 : 0x5140),
+                             c = __byte_perm(v[2][i], v[3][i], half ? 0x7362 : 0x5140);
+              const uint32_t a0 = e4m3_lo(a), a1 = e4m3_hi(a), a2 = e4m3_lo(c), a3 = e4m3_hi(c);
+              Mul::mma(o[2 * i + half], a0, a1, a2, a3, h0, h1);
+              Mul::mma(o[2 * i + half], a0, a1, a2, a3, w0, w1);
+            }
+        } else {
+#pragma unroll
+          for (int j = 0; j < VB; ++j) {
+            // V rows 2t, 2t + 1, 2t + 8, 2t + 9, elements 8g .. 8g + 7 of the block
+            uint4 v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              v[q] = lds128(vb + at_piece<C::kRowBytes>(u * 16 + 2 * t + (q & 1) + 8 * (q >> 1), j * 8 + g));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t v0 = (&v[0].x)[i], v1 = (&v[1].x)[i], v2 = (&v[2].x)[i], v3 = (&v[3].x)[i];
+              // element 64 j + 8 g + 2 i in row g of the product, the next one in row g + 8
+              const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632),
+                             a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
+              Mul::mma(o[j * 4 + i], a0, a1, a2, a3, h0, h1);
+              Mul::mma(o[j * 4 + i], a0, a1, a2, a3, w0, w1);
+            }
           }
         }
+      }
+    }
+    if constexpr (kHeld8) {
+      // the output relative to the scores' maximum, as its sum is (two factors: neither leaves the range)
+      const float h0 = v0 == -INFINITY ? 0.f : exp2_fast((v0 - Split<Mul>::kTop + 1.f - m0) * 0.5f),
+                  h1 = v1 == -INFINITY ? 0.f : exp2_fast((v1 - Split<Mul>::kTop + 1.f - m1) * 0.5f);
+#pragma unroll
+      for (int i = 0; i < HD / 16; ++i) {
+        o[i][0] = o[i][0] * h0 * h0;
+        o[i][1] = o[i][1] * h1 * h1;
+        o[i][2] = o[i][2] * h0 * h0;
+        o[i][3] = o[i][3] * h1 * h1;
       }
     }
 
@@ -544,13 +727,11 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
       s_l[wid][2 * t + 1] = seen ? l1 : kNoKeys;
     }
 #pragma unroll
-    for (int j = 0; j < VB; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = j * 64 + 8 * g + 2 * i;
-        *reinterpret_cast<float2*>(&s_o[wid][2 * t][d]) = make_float2(o[j * 4 + i][0], o[j * 4 + i][2]);
-        *reinterpret_cast<float2*>(&s_o[wid][2 * t + 1][d]) = make_float2(o[j * 4 + i][1], o[j * 4 + i][3]);
-      }
+    for (int i = 0; i < HD / 16; ++i) {
+      const int d = kHeld8 ? HD / 8 * g + 2 * i : i / 4 * 64 + 8 * g + 2 * (i % 4);
+      *reinterpret_cast<float2*>(&s_o[wid][2 * t][d]) = make_float2(o[i][0], o[i][2]);
+      *reinterpret_cast<float2*>(&s_o[wid][2 * t + 1][d]) = make_float2(o[i][1], o[i][3]);
+    }
     const Segment done = sg;
     more = walk.next(p, sg);
     if (more) load_q();
@@ -608,20 +789,25 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
   if (lost) atomicCAS(p.status, 0, MSM_ERR_INVALID_ARG | (kCallAttention << 8));
 }
 
-template <class El, int HD>
+template <class El, int HD, bool kHeld8>
 cudaError_t launch(const PagedAttn& p, int blocks, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit for this kernel is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(paged_attn_kernel<El, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Cfg<HD>::kSmem);
+    e = cudaFuncSetAttribute(paged_attn_kernel<El, HD, kHeld8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cfg<HD, kHeld8>::kSmem);
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  paged_attn_kernel<El, HD><<<blocks, kThreadsA, Cfg<HD>::kSmem, s>>>(p);
+  paged_attn_kernel<El, HD, kHeld8><<<blocks, kThreadsA, Cfg<HD, kHeld8>::kSmem, s>>>(p);
   return cudaGetLastError();
+}
+template <class El>
+cudaError_t launch_as(const PagedAttn& p, int head_dim, int blocks, cudaStream_t s) {
+  if (p.k_scales) return head_dim == 64 ? launch<El, 64, true>(p, blocks, s) : launch<El, 128, true>(p, blocks, s);
+  return head_dim == 64 ? launch<El, 64, false>(p, blocks, s) : launch<El, 128, false>(p, blocks, s);
 }
 }  // namespace
 
@@ -630,8 +816,7 @@ size_t paged_attn_workspace(int blocks, int group, int head_dim) {
 }
 
 cudaError_t launch_paged_attn(const PagedAttn& p, int dtype, int head_dim, int blocks, cudaStream_t s) {
-  if (dtype == MSM_BF16) return head_dim == 64 ? launch<Bf16, 64>(p, blocks, s) : launch<Bf16, 128>(p, blocks, s);
-  return head_dim == 64 ? launch<Fp16, 64>(p, blocks, s) : launch<Fp16, 128>(p, blocks, s);
+  return dtype == MSM_BF16 ? launch_as<Bf16>(p, head_dim, blocks, s) : launch_as<Fp16>(p, head_dim, blocks, s);
 }
 
 }  // namespace msm

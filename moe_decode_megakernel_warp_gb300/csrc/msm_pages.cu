@@ -29,16 +29,11 @@ constexpr int kMetaMost = 1024, kMetaFew = 256;
 constexpr int kMetaBlocks = 8;      // the portable cluster size
 constexpr int kPagesPerThread = 8;  // pages one thread looks at per step of a scan
 
-__device__ __forceinline__ void latch(int32_t* status, int code, int call) {
-  atomicCAS(status, 0, code | (call << 8));
-}
 // a resize or fork that is not done: the calls behind it change nothing either
 __device__ __forceinline__ void refuse(int32_t* status, int code, int call) {
   latch(status, code, call);
   atomicOr(status, kPagesStopped);
 }
-// (only ever set by a call that the others are ordered behind, so all threads of a call see the same)
-__device__ __forceinline__ bool stopped(const int32_t* status) { return (__ldcg(status) & kPagesStopped) != 0; }
 
 struct BlockShare {        // what a block tells the others
   int need, count, holes;  // missing pages, free (or live) pages, holes below the live count
@@ -387,7 +382,8 @@ __global__ void __cluster_dims__(kMetaBlocks, 1, 1) __launch_bounds__(N)
 // ---------------------------------------------------------------- row copies
 // Bound by memory: each byte is read once and written once.  blockIdx.y = (layer, K or V); the
 // warps of a row of blocks share out the pieces of up to 8 KB, 16 loads of 16 bytes in flight
-// per lane (8: 20 % slower on short runs).
+// per lane (8: 20 % slower on short runs).  The scales of a cache in 8 bits are behind its rows in
+// blockIdx.y, an entry per warp.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyVecs = 16;  // 16-byte vectors per lane
 constexpr int kPieceVecs = 32 * kCopyVecs;
@@ -400,6 +396,22 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const PagesCopy p) {
   const int lane = threadIdx.x & 31;
   const uint32_t warp = (blockIdx.x * kCopyThreads + threadIdx.x) >> 5, warps = (gridDim.x * kCopyThreads) >> 5;
   const uint32_t entries = sc.head[0];
+  if ((int)blockIdx.y >= 2 * p.n_layers) {
+    const int layer = (blockIdx.y >> 1) - p.n_layers;
+    float* const scales = blockIdx.y & 1 ? p.v_scales[layer] : p.k_scales[layer];
+    const int64_t page_scales = (int64_t)p.n_kv_heads * p.page_blocks;
+    for (uint32_t e = warp; e < entries; e += warps) {
+      const int from = kCompact ? sc.list[entries - 1 - e] : sc.copies[3 * (size_t)e];
+      const int to = kCompact ? dst[e] : sc.copies[3 * (size_t)e + 1];
+      // those of the rows that are copied
+      const int blocks = kCompact ? p.page_blocks : ceil_div(sc.copies[3 * (size_t)e + 2], p.block_rows);
+      for (int64_t i = lane; i < (int64_t)p.n_kv_heads * blocks; i += 32) {
+        const int64_t at = i / blocks * p.page_blocks + i % blocks;
+        scales[to * page_scales + at] = scales[from * page_scales + at];
+      }
+    }
+    return;
+  }
   // a page is n_kv_heads runs of page_rows rows; all of it is one run when it moves whole
   const int64_t head_vecs = (int64_t)p.m.page_rows * p.row_vecs, page_vecs = head_vecs * p.n_kv_heads;
   const int64_t run_vecs = kCompact ? page_vecs : head_vecs;
@@ -538,9 +550,10 @@ cudaError_t launch_pages_copy(const PagesCopy& p, bool compact, int sms, cudaStr
   const int64_t pieces = (vecs - 1) / kPieceVecs + 1;
   const int64_t entries = compact ? p.m.n_pages / 2 : p.m.n_seqs;
   const int64_t warps = entries * pieces * (compact ? 1 : p.n_kv_heads);
+  const int ys = 2 * p.n_layers * (p.page_blocks ? 2 : 1);
   const int64_t blocks = (warps - 1) / (kCopyThreads / 32) + 1, most = (16 * sms - 1) / (2 * p.n_layers) + 1;
   cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min(blocks, most)), 2 * p.n_layers);
+  lc.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min(blocks, most)), ys);
   lc.blockDim = dim3(kCopyThreads);
   lc.stream = s;
   cudaLaunchAttribute attr[1];

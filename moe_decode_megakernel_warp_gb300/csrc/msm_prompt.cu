@@ -226,20 +226,28 @@ __device__ bool find_tile(const PromptAttn& p, volatile Place* place, int t, int
   return false;
 }
 
-// 256 rows of one kv head
+// 256 rows of one kv head.  With sinks (kSinks) the tiles that hold them follow those of the window,
+// where they are not among these.
+template <bool kSinks>
 struct Work {
   int h, q0, nq, k0, shift, window;
   int row0, tok0, tok1;  // first row, its token, one past the last token
-  int t_lo, n;           // first key tile, their number (0: no row sees a key)
+  int t_lo, n;           // first key tile, number of tiles (0: no row sees a key)
+  int n_win, sinks;      // (kSinks) tiles of the window, keys at the front that stay visible
   bool two;              // the second tile has rows
-  __device__ int tile(int j) const { return t_lo + n - 1 - j; }
+  __device__ int tile(int j) const {
+    if (kSinks) return j < n_win ? t_lo + n_win - 1 - j : n - 1 - j;
+    return t_lo + n - 1 - j;
+  }
   // does some row see only a part of tile j?
   __device__ bool partial(int j) const {
     const int a = tile(j) * kKeys;
-    return a + kKeys - 1 > tok0 + shift || (window > 0 && a < tok1 + shift - window);
+    return a + kKeys - 1 > tok0 + shift ||
+           (window > 0 && a < tok1 + shift - window && (!kSinks || a + kKeys > sinks));
   }
 };
-__device__ bool find_work(const PromptAttn& p, volatile Place* place, int idx, Work& w) {
+template <bool kSinks>
+__device__ bool find_work(const PromptAttn& p, volatile Place* place, int idx, Work<kSinks>& w) {
   int seq, tile;
   w.h = idx % p.n_kv_heads;
   if (!find_tile(p, place, idx / p.n_kv_heads, seq, tile)) return false;
@@ -255,6 +263,11 @@ __device__ bool find_work(const PromptAttn& p, volatile Place* place, int idx, W
   const int hi = max(0, w.tok1 + w.shift), lo = p.window > 0 ? max(0, w.tok0 + w.shift - p.window + 1) : 0;
   w.t_lo = lo / kKeys;
   w.n = hi > 0 ? (hi + kKeys - 1) / kKeys - w.t_lo : 0;
+  if (kSinks) {
+    w.n_win = w.n;
+    w.sinks = p.sinks;
+    if (w.n > 0) w.n += min(w.t_lo, (p.sinks + kKeys - 1) / kKeys);
+  }
   w.two = w.row0 + kRows < sq.nq * p.group;
   return true;
 }
@@ -262,7 +275,8 @@ __device__ bool find_work(const PromptAttn& p, volatile Place* place, int idx, W
 // A block's pieces of work: one of every round of gridDim.x, the rounds alternately from the front
 // and from the back.  (The work is listed from the longest to the shortest: the
 // block that got the longest piece of a round gets the shortest of the next.)
-__device__ __forceinline__ bool next_work(const PromptAttn& p, volatile Place* place, int n_work, Work& w) {
+template <bool kSinks>
+__device__ __forceinline__ bool next_work(const PromptAttn& p, volatile Place* place, int n_work, Work<kSinks>& w) {
   const int round = place->round;
   __syncwarp();
   if ((threadIdx.x & 31) == 0) place->round = round + 1;
@@ -292,7 +306,7 @@ struct Ring {
   }
 };
 
-template <class El, int HD>
+template <class El, int HD, bool kSinks>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     prompt_kernel(const __grid_constant__ Maps maps, const PromptAttn p, const int n_work) {
   using C = Cfg<HD>;
@@ -341,7 +355,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   auto t_s = [&](int t) { return tmem + t * 128; };
   auto t_o = [&](int t) { return tmem + 256 + t * HD; };
   volatile int* const dead = &s_dead;
-  Work w;
+  Work<kSinks> w;
 
   if (wid >= 8) {
     set_max_regs_down<kOtherRegs>();
@@ -421,7 +435,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       uint32_t clean_phase = 0;
       int steps = 0, loads = 0, turns = 0;  // of this tile's P and Q, and of the two threads, so far
       bool ok = true;
-      Work ahead;
+      Work<kSinks> ahead;
       for (bool more_work = next_work(p, place, n_work, ahead); ok && more_work;) {
         w = ahead;
         int k_st = -1;
@@ -542,7 +556,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     // smallest number does, and any score times it is less than 2^-20)
     const float scale = fmaxf(fabsf(p.scale_log2), __int_as_float(1));
     int steps = 0, works = 0;
-    Work ahead;
+    Work<kSinks> ahead;
     for (bool more = next_work(p, place, n_work, ahead); more;) {
       w = ahead;
       if (w.n > 0 && t == 1 && !w.two) {
@@ -575,7 +589,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const int a = first - w.tile(j) * kKeys, b = last - w.tile(j) * kKeys;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const uint32_t see = bits_upto(b - c * 32) & ~bits_upto(a - 1 - c * 32);
+            uint32_t see = ~bits_upto(a - 1 - c * 32);
+            if (kSinks) see |= bits_upto(w.sinks - 1 - w.tile(j) * kKeys - c * 32);
+            see &= bits_upto(b - c * 32);
 #pragma unroll
             for (int i = 0; i < 32; ++i) s[c][i] = see >> i & 1 ? s[c][i] : 0xFF800000u;
           }
@@ -663,8 +679,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (taken && tok < w.nq) {
           for (int j = 0; j < w.n; ++j) {
             if (!w.partial(j)) continue;
-            const int a = max(first, w.tile(j) * kKeys), b = min(last, w.tile(j) * kKeys + kKeys - 1);
+            const int a0 = w.tile(j) * kKeys, a = kSinks ? a0 : max(first, a0), b = min(last, a0 + kKeys - 1);
             for (int key = a; key <= b; ++key) {
+              if (kSinks && key < first && key >= w.sinks) continue;
               const uint16_t* const v = p.v + (int64_t)(w.k0 + key) * p.v_token + w.h * p.v_head + c * 32;
 #pragma unroll
               for (int i = 0; i < 32; ++i)
@@ -719,7 +736,7 @@ cudaError_t encoder(PFN_cuTensorMapEncodeTiled_v12000* out) {
 }
 
 // rows [tokens][heads][HD] as boxes of 64 elements; Q's heads are split into (group, kv head)
-template <class El, int HD>
+template <class El, int HD, bool kSinks>
 cudaError_t launch(const PromptAttn& p, int sms, cudaStream_t s) {
   const int64_t works = prompt_attn_works(p.n_q, p.n_seqs, p.n_kv_heads, p.group);
   PFN_cuTensorMapEncodeTiled_v12000 encode;
@@ -752,14 +769,14 @@ cudaError_t launch(const PromptAttn& p, int sms, cudaStream_t s) {
     // the warps' register shares must add up to what a block starts with, or they would wait
     // for registers that never come
     cudaFuncAttributes at;
-    if ((e = cudaFuncGetAttributes(&at, prompt_kernel<El, HD>)) != cudaSuccess) return e;
+    if ((e = cudaFuncGetAttributes(&at, prompt_kernel<El, HD, kSinks>)) != cudaSuccess) return e;
     if (at.numRegs * kPromptThreads < 256 * kSoftmaxRegs + (kPromptThreads - 256) * kOtherRegs)
       return cudaErrorLaunchOutOfResources;
-    e = cudaFuncSetAttribute(prompt_kernel<El, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<HD>::kSmem);
+    e = cudaFuncSetAttribute(prompt_kernel<El, HD, kSinks>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<HD>::kSmem);
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  prompt_kernel<El, HD><<<(unsigned)std::min<int64_t>(works, sms), kPromptThreads, Cfg<HD>::kSmem, s>>>(maps, p, (int)works);
+  prompt_kernel<El, HD, kSinks><<<(unsigned)std::min<int64_t>(works, sms), kPromptThreads, Cfg<HD>::kSmem, s>>>(maps, p, (int)works);
   return cudaGetLastError();
 }
 
@@ -769,9 +786,13 @@ int64_t prompt_attn_works(int n_q, int n_seqs, int n_kv_heads, int group) {
   return (((int64_t)n_q * group + kBlockRows - 1) / kBlockRows + n_seqs) * n_kv_heads;
 }
 
+template <class El>
+static cudaError_t launch_as(const PromptAttn& p, int head_dim, int sms, cudaStream_t s) {
+  if (p.sinks > 0) return head_dim == 64 ? launch<El, 64, true>(p, sms, s) : launch<El, 128, true>(p, sms, s);
+  return head_dim == 64 ? launch<El, 64, false>(p, sms, s) : launch<El, 128, false>(p, sms, s);
+}
 cudaError_t launch_prompt_attn(const PromptAttn& p, int dtype, int head_dim, int sms, cudaStream_t s) {
-  if (dtype == MSM_BF16) return head_dim == 64 ? launch<Bf16, 64>(p, sms, s) : launch<Bf16, 128>(p, sms, s);
-  return head_dim == 64 ? launch<Fp16, 64>(p, sms, s) : launch<Fp16, 128>(p, sms, s);
+  return dtype == MSM_BF16 ? launch_as<Bf16>(p, head_dim, sms, s) : launch_as<Fp16>(p, head_dim, sms, s);
 }
 
 }  // namespace msm

@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes
 import struct
 
-from . import MSM_BF16, MSM_FP16, MsmPages, MsmPrompt, _check, _ptr_array, lib
+from . import MSM_BF16, MSM_E4M3, MSM_FP16, MsmPages, MsmPrompt, MsmQPages, _check, _ptr_array, lib
 
 # msm_prompt in the C layout (a bytes object takes a third of the time of a ctypes structure)
 _PROMPT = struct.Struct("9if4P8q3PI4x")
@@ -59,6 +59,13 @@ def _int32(t, name, n, index):
     return t.data_ptr()
 
 
+def _sixteen(t):
+    """The tensor's type, which must be one of the 16-bit ones."""
+    if t.dtype not in _CODES:
+        raise ValueError("expected bfloat16 or float16, got %s" % t.dtype)
+    return t.dtype
+
+
 def _c_int(x):
     """x as a C int that says the same: ctypes would take its low 32 bits (a window of 2^32 for none).
     Every index, and no window, is below the largest one; -1 is refused as any other negative number."""
@@ -71,11 +78,16 @@ class PagedCache:
     ``table`` int32 [n_seqs, max_pages] (-1 behind a sequence's last page), ``lens`` int32
     [n_seqs], ``refs`` int32 [n_pages].  ``PagedCache.allocate`` makes an empty one.
 
+    Pools of torch.float8_e4m3fn hold the rows in 8 bits, with a scale for each block of
+    ``block_rows`` rows (page_rows by default) of a page and head: ``k_scales`` and ``v_scales`` are lists of
+    one float32 [n_pages, n_kv_heads, ceil(page_rows / block_rows)] tensor per layer.  What is written and the
+    queries are bfloat16 or float16 then.
+
     ``resize``, ``fork``, ``compact`` and ``write`` change these tensors on the device, in
     stream order and without a host round trip; ``sync`` waits and raises what they met.  After a
     ``resize`` or ``fork`` that could not be done none of them changes anything until ``sync``."""
 
-    def __init__(self, k_pages, v_pages, table, lens, refs):
+    def __init__(self, k_pages, v_pages, table, lens, refs, k_scales=None, v_scales=None, block_rows=None):
         if _torch is None:
             _load()
         torch = _torch
@@ -88,7 +100,10 @@ class PagedCache:
             _need(t.shape == first.shape and t.dtype == first.dtype and t.device == first.device and t.is_contiguous(),
                   "the pools must be contiguous and alike in shape, type and device")
         _need(table.dim() == 2, "table is [n_seqs, max_pages]")
-        _need(first.dtype in _CODES, "the pools must be bfloat16 or float16, got %s" % first.dtype)
+        held8 = first.dtype == torch.float8_e4m3fn
+        _need(held8 or first.dtype in _CODES, "the pools must be bfloat16, float16 or float8_e4m3fn, got %s" % first.dtype)
+        _need(held8 == (k_scales is not None) == (v_scales is not None) and (held8 or block_rows is None),
+              "pools of 8 bits, and only those, have scales")
         n_pages, n_kv_heads, page_rows, head_dim = first.shape
         n_seqs, max_pages = table.shape
         dev = first.device
@@ -99,20 +114,39 @@ class PagedCache:
                                    device=dev)
         kp, self._k_ptrs = _ptr_array([t.data_ptr() for t in k_pages])
         vp, self._v_ptrs = _ptr_array([t.data_ptr() for t in v_pages])
-        self._c = MsmPages(dev.index, _CODES[first.dtype], len(k_pages), n_pages, page_rows, n_kv_heads, head_dim, n_seqs,
+        self._c = MsmPages(dev.index, MSM_E4M3 if held8 else _CODES[first.dtype], len(k_pages), n_pages, page_rows, n_kv_heads, head_dim, n_seqs,
                            max_pages, kp, vp, _int32(table, "table", n_seqs * max_pages, dev.index),
                            _int32(lens, "lens", n_seqs, dev.index), _int32(refs, "refs", n_pages, dev.index),
                            self.status.data_ptr(), self.scratch.data_ptr())
-        self._ref = ctypes.byref(self._c)
         self._lib = _LIBRARY
+        self._held8 = held8
+        if held8:
+            self.k_scales, self.v_scales = list(k_scales), list(v_scales)
+            self.block_rows = page_rows if block_rows is None else block_rows
+            _need(1 <= self.block_rows <= page_rows, "block_rows must be 1 to page_rows")
+            shape = (n_pages, n_kv_heads, -(-page_rows // self.block_rows))
+            _need(len(self.k_scales) == len(self.v_scales) == len(k_pages), "one tensor of K's and one of V's scales per layer")
+            for t in self.k_scales + self.v_scales:
+                _need(t.shape == shape and t.dtype == torch.float32 and t.device == dev and t.is_contiguous(),
+                      "the scales must be contiguous float32 %s on %s" % (list(shape), dev))
+            ks, self._ks_ptrs = _ptr_array([t.data_ptr() for t in self.k_scales])
+            vs, self._vs_ptrs = _ptr_array([t.data_ptr() for t in self.v_scales])
+            self._c = MsmQPages(self._c, self.block_rows, ks, vs)
+            calls = "msm_qpages_"
+        else:
+            calls = "msm_pages_"
+        self._resize, self._fork, self._compact, self._write, self._sync = (
+            getattr(_LIBRARY, calls + n) for n in ("resize", "fork", "compact", "write", "sync"))
+        self._ref = ctypes.byref(self._c)
         self._index, self._n_seqs, self._kv_heads, self._head_dim = dev.index, n_seqs, n_kv_heads, head_dim
-        self._dtype = first.dtype
+        self._dtype = None if held8 else first.dtype  # of rows and queries (8 bits: each call's own)
         self._bytes = {}      # bytes of the attention's workspace by number of query heads
         self._workspace = {}  # workspaces by (stream, number of query heads)
 
     @classmethod
-    def allocate(cls, n_layers, n_pages, page_rows, n_kv_heads, head_dim, n_seqs, max_pages, dtype=None, device=None):
-        """An empty cache (bfloat16 by default)."""
+    def allocate(cls, n_layers, n_pages, page_rows, n_kv_heads, head_dim, n_seqs, max_pages, dtype=None, device=None,
+                 block_rows=None):
+        """An empty cache (bfloat16 by default; torch.float8_e4m3fn: in 8 bits)."""
         if _torch is None:
             _load()
         torch = _torch
@@ -124,53 +158,63 @@ class PagedCache:
 
         def ints(*shape):
             return torch.zeros(shape, dtype=torch.int32, device=dev)
-        return cls(pools(), pools(), ints(n_seqs, max_pages).fill_(-1), ints(n_seqs), ints(n_pages))
+        scales = {}
+        if dtype == torch.float8_e4m3fn:
+            block_rows = page_rows if block_rows is None else block_rows
+            _need(1 <= block_rows <= page_rows, "block_rows must be 1 to page_rows")
+            for name in ("k_scales", "v_scales"):
+                scales[name] = [torch.zeros((n_pages, n_kv_heads, -(-page_rows // block_rows)), device=dev)
+                                for _ in range(n_layers)]
+        return cls(pools(), pools(), ints(n_seqs, max_pages).fill_(-1), ints(n_seqs), ints(n_pages),
+                   block_rows=block_rows, **scales)
 
     def resize(self, new_lens):
         """msm_pages_resize: int32 [n_seqs] on the device, -1 = leave as it is."""
-        _check(self._lib.msm_pages_resize(self._ref, _int32(new_lens, "new_lens", self._n_seqs, self._index),
-                                          _raw_stream(self._index)))
+        _check(self._resize(self._ref, _int32(new_lens, "new_lens", self._n_seqs, self._index), _raw_stream(self._index)))
 
     def fork(self, parent):
         """msm_pages_fork: int32 [n_seqs] on the device, -1 = none."""
-        _check(self._lib.msm_pages_fork(self._ref, _int32(parent, "parent", self._n_seqs, self._index),
-                                        _raw_stream(self._index)))
+        _check(self._fork(self._ref, _int32(parent, "parent", self._n_seqs, self._index), _raw_stream(self._index)))
 
     def compact(self):
         """msm_pages_compact."""
-        _check(self._lib.msm_pages_compact(self._ref, _raw_stream(self._index)))
+        _check(self._compact(self._ref, _raw_stream(self._index)))
 
     def write(self, layer, k, v, starts):
-        """msm_pages_write: k, v [n_tokens, n_kv_heads, head_dim], starts int32 [n_seqs + 1]."""
+        """msm_pages_write (8 bits: msm_qpages_write): k, v [n_tokens, n_kv_heads, head_dim], starts int32
+        [n_seqs + 1]."""
         n, i = len(k), self._index
         if n > 0x7FFFFFFF:
             raise ValueError("more than 2^31 - 1 tokens")
         shape = (n, self._kv_heads, self._head_dim)
-        kt, kh = _rows(k, "k", shape, self._dtype, i)
-        vt, vh = _rows(v, "v", shape, self._dtype, i)
-        _check(self._lib.msm_pages_write(self._ref, _c_int(layer), k.data_ptr(), v.data_ptr(), kt, kh, vt, vh,
-                                         _int32(starts, "starts", self._n_seqs + 1, i), n, _raw_stream(i)))
+        dtype = self._dtype or _sixteen(k)
+        kt, kh = _rows(k, "k", shape, dtype, i)
+        vt, vh = _rows(v, "v", shape, dtype, i)
+        code = (_CODES[dtype],) if self._held8 else ()
+        _check(self._write(self._ref, _c_int(layer), *code, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh,
+                           _int32(starts, "starts", self._n_seqs + 1, i), n, _raw_stream(i)))
 
-    def attention(self, layer, q, window=0, scale=None, out=None):
-        """msm_paged_attention: q [n_seqs, n_q_heads, head_dim]; scale defaults to
-        1 / sqrt(head_dim).  Returns out."""
+    def attention(self, layer, q, window=0, scale=None, out=None, sinks=0):
+        """msm_paged_attention_sinks (8 bits: msm_qpages_attention): q [n_seqs, n_q_heads, head_dim]; scale
+        defaults to 1 / sqrt(head_dim); with a window the first ``sinks`` rows stay visible.  Returns out."""
         if q.dim() != 3:
             raise ValueError("q must be [n_seqs, n_q_heads, head_dim]")
+        dtype = self._dtype or _sixteen(q)
         heads, i, hd, layer = q.shape[1], self._index, self._head_dim, _c_int(layer)
         shape = (self._n_seqs, heads, hd)
-        qs, qh = _rows(q, "q", shape, self._dtype, i)
+        qs, qh = _rows(q, "q", shape, dtype, i)
         if out is None:
-            out = _empty(shape, dtype=self._dtype, device=self.device)
+            out = _empty(shape, dtype=dtype, device=self.device)
             os_, oh = heads * hd, hd
         else:
-            os_, oh = _rows(out, "out", shape, self._dtype, i)
+            os_, oh = _rows(out, "out", shape, dtype, i)
         stream = _raw_stream(i)
         n = self._bytes.get(heads)
         if n is None:
-            n = self._lib.msm_paged_attention_workspace(self._ref, heads)
+            of = self._lib.msm_qpages_attention_workspace if self._held8 else self._lib.msm_paged_attention_workspace
+            n = of(self._ref, heads)
             if n == 0:  # the call says what is wrong
-                _check(self._lib.msm_paged_attention(self._ref, layer, None, qs, qh, heads, 1.0, 0, None, os_, oh, None,
-                                                     0, None))
+                self._attend(layer, dtype, None, qs, qh, heads, 1.0, 0, 0, None, os_, oh, None, 0, None)
             self._bytes[heads] = n
         # one workspace per stream, and one per call that a graph records (graphs recorded on
         # one stream may be replayed on two)
@@ -180,21 +224,27 @@ class PagedCache:
             ws = self._workspace.get((stream, heads))
             if ws is None:
                 ws = self._workspace[stream, heads] = _torch.zeros(n, dtype=_torch.uint8, device=self.device)
-        st = self._lib.msm_paged_attention(self._ref, layer, q.data_ptr(), qs, qh, heads,
-                                           (hd or 1) ** -0.5 if scale is None else scale, _c_int(window), out.data_ptr(),
-                                           os_, oh, ws.data_ptr(), n, stream)
+        self._attend(layer, dtype, q.data_ptr(), qs, qh, heads, (hd or 1) ** -0.5 if scale is None else scale,
+                     _c_int(window), _c_int(sinks), out.data_ptr(), os_, oh, ws.data_ptr(), n, stream)
+        return out
+
+    def _attend(self, layer, dtype, *args):
+        if self._held8:
+            st = self._lib.msm_qpages_attention(self._ref, layer, _CODES[dtype], *args)
+        else:
+            st = self._lib.msm_paged_attention_sinks(self._ref, layer, *args)
         if st:
             _check(st)
-        return out
 
     def sync(self):
         """msm_pages_sync: waits for the current stream; raises MsmError for an error that a
         call met on the device (and clears it)."""
-        _check(self._lib.msm_pages_sync(self._ref, _raw_stream(self._index)))
+        _check(self._sync(self._ref, _raw_stream(self._index)))
 
 
-def prompt_attention(q, k, v, q_starts, k_starts=None, window=0, scale=None, out=None, status=None):
-    """msm_prompt_attention: causal attention of packed prompts.
+def prompt_attention(q, k, v, q_starts, k_starts=None, window=0, scale=None, out=None, status=None, sinks=0):
+    """msm_prompt_attention_sinks: causal attention of packed prompts; with a window the first
+    ``sinks`` keys of a sequence stay visible.
 
     q [n_q, n_q_heads, head_dim], k and v [n_k, n_kv_heads, head_dim] (any strides that keep
     rows consecutive; ``cache.transpose(0, 1)`` of a verify-step cache [n_kv_heads, max_ctx,
@@ -233,7 +283,7 @@ def prompt_attention(q, k, v, q_starts, k_starts=None, window=0, scale=None, out
                      (hd or 1) ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                      out.data_ptr(), qt, qh, kt, kh, vt, vh, ot, oh, qs, ks,
                      0 if status is None else _int32(status, "status", 1, i), 0)
-    st = _LIBRARY.msm_prompt_attention(a, _raw_stream(i))
+    st = _LIBRARY.msm_prompt_attention_sinks(a, _c_int(sinks), _raw_stream(i))
     if st:
         _check(st)
     return out
