@@ -10,22 +10,23 @@
 //
 // Weights are whole multiples of 2^-42 (of the largest weight), so their sums are exact in 64 bits whatever
 // their order: which token is drawn depends on no thread's timing, and the sums say the same as the
-// definition in 64-bit floating point but for the weights' own rounding.  That matters: a row's 100,000
-// borders between tokens lie so close that sums in 32-bit floating point draw another token once in some
-// thousand rows.  exp2 is computed to 2^-42: the argument as two floats, its leading 10 fractional bits
-// through a table of 1,024 entries (products of two 64-bit constants), the rest by a polynomial
-// of third degree.
+// definition in 64-bit floating point but for the weights' own rounding, 2^-31 of each.  That matters: a
+// row's 100,000 borders between tokens lie so close that weights of 32-bit floating point draw another token
+// in one of some thousand rows.  w = 2^-t, t = (M - x) log2(e) / T as two floats: t = k + j / 1024 + r, a
+// table of 1,024 entries for j, a polynomial of third degree for r, two logits per instruction.
 //
 // A row belongs to one cluster of up to eight blocks, each with a slice of it in shared memory, so the
 // logits are read once.  The order's border is found without sorting the row: a histogram over 1,024
-// classes of the scaled logit (counts and, where top-p needs them, weights), of which only the class that
-// holds the border goes on: gathered and sorted by the cluster's first block when it is small (top-k: with all
-// classes in front of it), else divided into 1,024 finer classes, down to single values, whose equals are
-// told apart by index.  Between the steps the blocks exchange sums through distributed shared memory.
+// classes of t below 16 (counts and, where top-p needs them, weights), of which only the class that holds the
+// border goes on: gathered and sorted by the cluster's first block when it is small (top-k: with all classes
+// in front of it), else divided into 1,024 finer classes, down to single values, whose equals are told apart
+// by index.  Between the steps the blocks exchange sums through distributed shared memory.
 #include <cooperative_groups.h>
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
+#include <climits>
 
 #include "msm_attn.cuh"
 #include "msm_sample.h"
@@ -39,11 +40,11 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr int kBinsPerThread = kBins / kThreads;
-constexpr float kBinsPerLog2 = 16.f;  // classes of the first histogram per factor of two of the weight
-constexpr int kList = 1024;           // candidates that are sorted
+constexpr int kList = 512;            // candidates that are sorted
 constexpr int kSegs = 128;            // segments of a slice, in the order of the index
 constexpr int kMaxCluster = 8;
-constexpr int kOneBits = 42;          // a weight of 1
+constexpr int kBits = 42;             // weights are multiples of 2^-42 ...
+constexpr uint64_t kOne = 0x7FFFFFFFull << (kBits - 31);  // ... of this one, the largest logit's (2^-31 short of 1)
 constexpr uint32_t kLowestKey = 0x00800000u;  // of the lowest finite value
 
 // 2^(-i / 32) in units of 2^-63 and 2^(-i / 1024) in units of 2^-64 (its first one a unit short of 1)
@@ -66,32 +67,37 @@ __constant__ uint64_t c_fine[32] = {
     0xfbdfed6ce5f09c49ull, 0xfbb44bafad642efdull, 0xfb88b1815ea93211ull, 0xfb5d1ee0aa913025ull,
     0xfb3193cc4227c3f4ull, 0xfb061042d6b28e41ull, 0xfada944319b12bcaull, 0xfaaf1fcbbcdd2b40ull};
 
-struct Share {  // what a block tells the others
+struct __align__(16) Share {  // what a block tells the others
   uint64_t sum;
-  uint32_t count, top;
+  uint32_t count;
+  float top;
 };
-enum Op { kGather, kRefine, kTies, kDone };
+enum Op { kGather, kRefine, kTies, kDone, kDrawn };
 struct Message {  // what the first block tells the others
   int op;
-  uint32_t lo, hi;   // keys of the candidates
-  uint64_t border;   // kTies: how many of the equals are kept; kDone: the last kept token's order
+  uint32_t lo, hi;   // classes of the first histogram, or keys, of the candidates
+  int by_bin;
+  uint64_t border;   // kTies: how many of the equals are kept; kDone: the last kept token's order (kDrawn: all is done)
 };
 
 struct Shared {
-  uint64_t table[1024];
+  uint32_t table[1024];  // 2^(-j / 1024) in units of 2^-31
   union {
     struct {
-      uint32_t n[kBins], lo[kBins], hi[kBins];
+      uint32_t n[kBins], lo[kBins], hi[kBins];  // counts, weights; then their running sums (of later histograms)
     } bins;
-    uint64_t list[kList];
+    struct {
+      uint64_t list[kList], other[kList], sums[kList];
+    };
   };
-  // sums up to and including a class, of the whole row: of the first histogram, of the last one or of the list
-  uint32_t first_n[kBins], last_n[kBins];
-  uint64_t first_w[kBins], last_w[kBins];
+  // running sums of the first histogram over the whole row, up to and including a class
+  uint32_t first_n[kBins];
+  uint64_t first_w[kBins];
   uint64_t seg_sum[kSegs];
   uint32_t seg_n[kSegs];
   uint64_t warp_w[kWarps];
-  uint32_t warp_n[kWarps], warp_top[kWarps];
+  uint32_t warp_n[kWarps];
+  float warp_top[kWarps];
   Share share[2];
   Message message[2];
   uint32_t n_list;
@@ -99,72 +105,122 @@ struct Shared {
   uint32_t found;
 };
 
-// ---- order of logits: larger keys are larger logits; 0: never drawn (-inf, NaN)
+// ---- order of logits: larger keys are larger logits
 __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t b = __float_as_uint(x + 0.f);  // (-0 becomes 0)
-  const uint32_t k = b & 0x80000000u ? ~b : b | 0x80000000u;
-  return x > -INFINITY ? k : 0u;
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float value_of(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 __device__ __forceinline__ uint64_t order_of(uint32_t key, uint32_t index) { return (uint64_t)key << 32 | (0xFFFFFFFFu - index); }
+// is it one that can be drawn (no NaN, not -inf)?
+__device__ __forceinline__ bool drawable(float x) { return x > -INFINITY; }
+
+// ---- two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 // ---- weights
 struct Scale {
-  uint32_t top;  // key of the largest logit
-  float max;     // and its value
+  float max;     // the largest logit
   float hi, lo;  // log2(e) / temperature
 };
-__device__ __forceinline__ Scale scale_of(uint32_t top, float temperature) {
+__device__ __forceinline__ Scale scale_of(float max, float temperature) {
   Scale s;
-  s.top = top;
-  s.max = value_of(top);
+  s.max = max;
   constexpr float kHi = 1.44269502162933349609375f, kLo = 1.925963033500011e-8f;  // log2(e)
   s.hi = kHi / temperature;
   s.lo = (fmaf(-s.hi, temperature, kHi) + kLo) / temperature;
+  if (!(s.hi <= FLT_MAX)) {  // (a temperature below 2^-127: differences of logits above 2^-120 count as they should)
+    s.hi = FLT_MAX;
+    s.lo = 0.f;
+  }
   return s;
 }
-// (max - x) log2(e) / T as hi + lo; hi is infinite (and lo means nothing) where the difference is
-__device__ __forceinline__ void log2_below(const Scale& s, uint32_t key, float& hi, float& lo) {
-  const float x = value_of(key);
-  const float d = s.max - x, b = d - s.max, e = (s.max - (d - b)) + (-x - b);  // d + e = max - x exactly
-  hi = d * s.hi;
-  lo = fmaf(d, s.hi, -hi) + fmaf(d, s.lo, e * s.hi);
-}
-// 2^42 exp((x - max) / T), rounded
-__device__ __forceinline__ uint64_t weight_of(const Scale& s, const uint64_t* table, uint32_t key) {
-  if (key == s.top) return 1ull << kOneBits;
-  float h, l;
-  log2_below(s, key, h, l);
-  if (!(h < 43.f)) return 0;
-  const int n = __float2int_rz(h * 1024.f);
-  const float f = fmaf((float)n, -1.f / 1024.f, h);  // exact: 0 <= f < 2^-10
-  const float r = f + l, rl = (f - r) + l;
-  // 2^-r = 1 - (u - u^2 / 2 + u^3 / 6 - ...), u = r ln 2 < 2^-10.5; the next term is below 2^-46
-  constexpr float kHi = 0.693147182464599609375f, kLo = -1.904654299957768e-9f;  // ln 2
-  const float u = r * kHi, ul = fmaf(r, kHi, -u) + fmaf(r, kLo, rl * kHi);
-  const float g = ul - u * u * fmaf(u, -1.f / 6.f, 0.5f);
-  const int qu = __float2int_rn(u * 0x1p41f);
-  const int64_t q = 2 * (int64_t)qu + __float2int_rn((g + fmaf((float)qu, -0x1p-41f, u)) * 0x1p42f);
-  const uint64_t a = table[n & 1023];
-  const int64_t less = (int64_t)((a + 0x80000000ull) >> 32) * q;  // 2^-31 x 2^-42
-  const int shift = 63 - kOneBits + (n >> 10);
-  return (a - (uint64_t)(less >> 10) + (1ull << (shift - 1))) >> shift;
-}
+// t is rounded to a multiple of 2^-10 by adding 3 x 2^12: the sum's last bits are that multiple
+constexpr float kRound = 12288.f;
+constexpr int kRoundBits = 0x46400000;
 
-// class of the first histogram; rises as the key falls
-__device__ __forceinline__ int bin_of(const Scale& s, uint32_t key) {
-  if (key == s.top) return 0;
-  const float z = (s.max - value_of(key)) * (s.hi * kBinsPerLog2);
-  return (int)min(__float2uint_rz(z), (uint32_t)kBins - 1u);
+// Weights of two logits, and their t in units of 2^-10.  Beyond t = 43, and for -inf and NaN (whose t are as
+// large as can be, or NaN, with bits as large), the weight is 0.
+__device__ __forceinline__ void weights_of(const Scale& s, const uint32_t* table, float x0, float x1, uint64_t& w0,
+                                           uint64_t& w1, int& i0, int& i1) {
+  const uint64_t x = pair(x0, x1), m = pair(s.max, s.max), minus = pair(-1.f, -1.f);
+  const uint64_t c_hi = pair(s.hi, s.hi), n_hi = pair(-s.hi, -s.hi), n_lo = pair(-s.lo, -s.lo);
+  // d + e = max - x exactly
+  const uint64_t d = fma2(x, minus, m), b = fma2(m, minus, d);
+  const uint64_t e = fma2(add2(x, b), minus, fma2(fma2(b, minus, d), minus, m));
+  // t = h - q
+  const uint64_t h = mul2(d, c_hi);
+  const uint64_t q = fma2(e, n_hi, fma2(d, n_lo, fma2(d, n_hi, h)));
+  const uint64_t y = add2(h, pair(kRound, kRound));
+  const uint64_t f = fma2(add2(y, pair(-kRound, -kRound)), minus, h);  // exact, at most 2^-11
+  const uint64_t r = fma2(q, minus, f);
+  // 2^-r = 1 - g, g = u - u^2 / 2 + u^3 / 6, u = r ln 2 < 2^-11.5; the next term is below 2^-50
+  constexpr float k1 = 0.693147180559945f, k2 = -0.240226506959101f, k3 = 0.0555041086648216f;
+  const uint64_t g = mul2(r, fma2(r, fma2(r, pair(k3, k3), pair(k2, k2)), pair(k1, k1)));
+  float y0, y1, g0, g1;
+  unpair(y, y0, y1);
+  unpair(g, g0, g1);
+  i0 = __float_as_int(y0) - kRoundBits;
+  i1 = __float_as_int(y1) - kRoundBits;
+  const uint32_t a0 = table[__float_as_int(y0) & 1023], a1 = table[__float_as_int(y1) & 1023];
+  // a (1 - g) in units of 2^-31: a has its leading bit at 2^30, so that its bits are a float's; the product, at
+  // most 2^20, is rounded by adding 3 x 2^22
+  const float p0 = fmaf(__uint_as_float(0x4E800000u | (a0 & 0x3FFFFFFFu) >> 7), g0, 12582912.f),
+              p1 = fmaf(__uint_as_float(0x4E800000u | (a1 & 0x3FFFFFFFu) >> 7), g1, 12582912.f);
+  const uint32_t v0 = a0 + (0x4B400000u - __float_as_uint(p0)), v1 = a1 + (0x4B400000u - __float_as_uint(p1));
+  // 2^42 2^-k v 2^-31, rounded
+  w0 = ((((uint64_t)v0 << (kBits - 30)) >> min(i0 >> 10, 63)) + 1) >> 1;
+  w1 = ((((uint64_t)v1 << (kBits - 30)) >> min(i1 >> 10, 63)) + 1) >> 1;
 }
+__device__ __forceinline__ uint64_t weight_of(const Scale& s, const uint32_t* table, float x) {
+  uint64_t w, unused;
+  int i, j;
+  weights_of(s, table, x, -INFINITY, w, unused, i, j);
+  return w;
+}
+// t in units of 2^-10, as weights_of has it (one rounding each)
+__device__ __forceinline__ int log2_below(const Scale& s, float x) {
+  return __float_as_int(__fadd_rn(__fmul_rn(s.max - x, s.hi), kRound)) - kRoundBits;
+}
+// class of the first histogram; rises as the logit falls
+__device__ __forceinline__ int bin_of(int i) { return min(i >> 4, kBins - 1); }
+__device__ __forceinline__ int bin_of(const Scale& s, float x) { return bin_of(log2_below(s, x)); }
 
-// ---- a block's sums
+// ---- sums
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
+}
+// of lanes' weights of a few logits each (below 2^44)
+__device__ __forceinline__ uint64_t warp_sum_few(uint64_t w) {
+  const uint32_t low = __reduce_add_sync(0xffffffffu, (uint32_t)w & 0x3FFFFFu),
+                 high = __reduce_add_sync(0xffffffffu, (uint32_t)(w >> 22));
+  return ((uint64_t)high << 22) + low;
 }
 // sums over the block's threads up to and including this one's
 __device__ void block_scan(uint32_t& n, uint64_t& w, Shared& sh) {
@@ -183,23 +239,45 @@ __device__ void block_scan(uint32_t& n, uint64_t& w, Shared& sh) {
     sh.warp_w[wid] = w;
   }
   __syncthreads();
-  for (int i = 0; i < wid; ++i) {
-    n += sh.warp_n[i];
-    w += sh.warp_w[i];
-  }
+  n += __reduce_add_sync(0xffffffffu, lane < wid ? sh.warp_n[lane] : 0u);
+  w += warp_sum(lane < wid ? sh.warp_w[lane] : 0ull);
   __syncthreads();
 }
 
-// A row's slice in one block of its cluster, and the steps that all blocks take together.
+// ---- A row's slice in one block of its cluster: pairs of logits, the first of them `skew` in front of the slice
+// (so that a pair stands as it does within 16 bytes of the row); logits outside the slice read as -inf.
+__device__ __forceinline__ float2 floats(uint2 v, const float*) { return make_float2(__uint_as_float(v.x), __uint_as_float(v.y)); }
+__device__ __forceinline__ float2 floats(uint32_t v, const __nv_bfloat16*) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 floats(uint32_t v, const __half*) { return __half22float2(*reinterpret_cast<__half2*>(&v)); }
+template <class T>
+struct Pair {
+  using Bits = uint32_t;
+};
+template <>
+struct Pair<float> {
+  using Bits = uint2;
+};
+
 template <class T>
 struct Slice {
-  const T* x;        // the row
-  int begin, n;      // the slice's first index, its length
-  const uint32_t* keys;
-  int held;          // so many of its keys are in shared memory
-  __device__ __forceinline__ uint32_t key(int i) const {
-    return i < held ? keys[i] : key_of((float)x[begin + i]);
+  using Bits = typename Pair<T>::Bits;
+  const T* x;        // the slice in the row
+  int begin, n;      // its first index, its length
+  int skew, pairs;   // pairs, with those that begin in front of it or end behind it
+  const Bits* room;
+  int held;          // so many of the pairs are in shared memory
+  bool infinite;     // the row has an infinite logit: such read as 0, all others as -inf
+  __device__ __forceinline__ float2 operator()(int i) const {
+    if (i < held) return floats(room[i], x);
+    return make_float2(far(2 * i - skew), far(2 * i + 1 - skew));
   }
+  __device__ float far(int e) const {
+    const float v = e >= 0 && e < n ? (float)x[e] : -INFINITY;
+    return !infinite ? v : v == INFINITY ? 0.f : -INFINITY;
+  }
+  __device__ __forceinline__ int index(int i) const { return begin + 2 * i - skew; }  // of a pair's first logit
 };
 
 struct Cluster {
@@ -207,24 +285,28 @@ struct Cluster {
   Shared& sh;
   int rank, size;
   int shares, messages;  // exchanges so far: two buffers each, so that one barrier is enough
-  // every block's share; returns the sums over all of them and over those in front of this one
+  // every block's share; returns the sums over all of them, and over those in front of this one
   __device__ Share exchange(const Share& mine, Share& before) {
     Share* const buf = &sh.share[shares++ & 1];
     if (threadIdx.x == 0) *buf = mine;
     group.sync();
-    Share all{0, 0, 0};
-    before = all;
-    for (int r = 0; r < size; ++r) {
-      const Share s = *group.map_shared_rank(buf, r);
-      if (r < rank) {
-        before.sum += s.sum;
-        before.count += s.count;
-      }
-      all.sum += s.sum;
-      all.count += s.count;
-      all.top = max(all.top, s.top);
+    const int lane = threadIdx.x & 31;
+    Share s{0, 0, -INFINITY};
+    if (lane < size) {
+      const Share* const from = group.map_shared_rank(buf, lane);
+      s = *from;
     }
-    return all;
+    Share front{lane < rank ? s.sum : 0, lane < rank ? s.count : 0, 0.f};
+#pragma unroll
+    for (int o = kMaxCluster / 2; o >= 1; o >>= 1) {
+      s.sum += __shfl_xor_sync(0xffffffffu, s.sum, o);
+      s.count += __shfl_xor_sync(0xffffffffu, s.count, o);
+      s.top = fmaxf(s.top, __shfl_xor_sync(0xffffffffu, s.top, o));
+      front.sum += __shfl_xor_sync(0xffffffffu, front.sum, o);
+      front.count += __shfl_xor_sync(0xffffffffu, front.count, o);
+    }
+    before = Share{__shfl_sync(0xffffffffu, front.sum, 0), __shfl_sync(0xffffffffu, front.count, 0), 0.f};
+    return Share{__shfl_sync(0xffffffffu, s.sum, 0), __shfl_sync(0xffffffffu, s.count, 0), __shfl_sync(0xffffffffu, s.top, 0)};
   }
   // what the first block wrote to the message buffer
   __device__ Message* message() { return &sh.message[messages & 1]; }
@@ -236,117 +318,202 @@ struct Cluster {
   }
 };
 
-// Counts (and weights) of the keys lo .. hi of the slice by class.  shift < 0: the first histogram.
-template <class T>
-__device__ void histogram(const Slice<T>& sl, const Scale& sc, Shared& sh, uint32_t lo, uint32_t hi, int shift,
-                          bool weights) {
-  for (int i = threadIdx.x; i < kBins; i += kThreads) sh.bins.n[i] = sh.bins.lo[i] = sh.bins.hi[i] = 0;
-  __syncthreads();
-  const int steps = (sl.n + kThreads - 1) / kThreads;
-  for (int s = 0; s < steps; ++s) {
-    const int i = s * kThreads + threadIdx.x;
-    const uint32_t k = i < sl.n ? sl.key(i) : 0u;
-    const bool in = k >= lo && k <= hi;
-    const uint32_t lanes = __ballot_sync(0xffffffffu, in);
-    if (!lanes) continue;
-    const int b = !in ? 0 : shift < 0 ? bin_of(sc, k) : (int)((hi - k) >> shift);
-    const uint64_t w = in && weights ? weight_of(sc, sh.table, k) : 0;
-    // (equal logits, or a high temperature: a warp's elements in one class would queue up)
-    const int b0 = __shfl_sync(0xffffffffu, b, __ffs(lanes) - 1);
-    if (__all_sync(0xffffffffu, !in || b == b0)) {
-      const uint32_t low = __reduce_add_sync(0xffffffffu, (uint32_t)w & 0x3FFFFFu),
-                     high = __reduce_add_sync(0xffffffffu, (uint32_t)(w >> 22));
-      if ((threadIdx.x & 31) == 0) {
-        const uint64_t sum = ((uint64_t)high << 22) + low;
-        atomicAdd(&sh.bins.n[b0], __popc(lanes));
-        const uint32_t was = atomicAdd(&sh.bins.lo[b0], (uint32_t)sum);
-        atomicAdd(&sh.bins.hi[b0], (uint32_t)(sum >> 32) + (was + (uint32_t)sum < was));
-      }
-    } else if (in) {
-      atomicAdd(&sh.bins.n[b], 1u);
-      if (w) {
-        const uint32_t was = atomicAdd(&sh.bins.lo[b], (uint32_t)w), up = (uint32_t)(w >> 32) + (was + (uint32_t)w < was);
-        if (up) atomicAdd(&sh.bins.hi[b], up);
-      }
+// Calls f(i, pair) for this thread's pairs of the slice, kAtOnce of them at a time; whole warps together.
+template <int kAtOnce, class T, class F>
+__device__ __forceinline__ void each_pair(const Slice<T>& sl, F f) {
+  for (int i0 = threadIdx.x & ~31; i0 < sl.pairs; i0 += kThreads * kAtOnce) {
+    float2 x[kAtOnce];
+#pragma unroll
+    for (int q = 0; q < kAtOnce; ++q) {
+      const int i = i0 + q * kThreads + (threadIdx.x & 31);
+      x[q] = i < sl.pairs ? sl(i) : make_float2(-INFINITY, -INFINITY);
+    }
+    f(i0 + (threadIdx.x & 31), x);
+  }
+}
+
+// Adds to a class (all lanes; lanes without `in` add nothing).
+__device__ __forceinline__ void add_to_bin(Shared& sh, bool in, int b, uint64_t w, bool weights) {
+  if (in) {
+    atomicAdd(&sh.bins.n[b], 1u);
+    if (weights) {
+      const uint32_t was = atomicAdd(&sh.bins.lo[b], (uint32_t)w), up = (uint32_t)(w >> 32) + (was + (uint32_t)w < was);
+      if (up) atomicAdd(&sh.bins.hi[b], up);
     }
   }
+}
+// The same where a whole warp's elements may be in one class and would queue up.
+__device__ __forceinline__ void add_to_one_bin(Shared& sh, bool in, int b, uint64_t w, bool weights) {
+  const uint32_t lanes = __ballot_sync(0xffffffffu, in);
+  if (!lanes) return;
+  const int b0 = __shfl_sync(0xffffffffu, b, __ffs(lanes) - 1);
+  if (__all_sync(0xffffffffu, !in || b == b0)) {
+    const uint64_t sum = weights ? warp_sum_few(in ? w : 0ull) : 0ull;
+    if ((threadIdx.x & 31) == 0) {
+      atomicAdd(&sh.bins.n[b0], __popc(lanes));
+      const uint32_t was = atomicAdd(&sh.bins.lo[b0], (uint32_t)sum);
+      atomicAdd(&sh.bins.hi[b0], (uint32_t)(sum >> 32) + (was + (uint32_t)sum < was));
+    }
+  } else {
+    add_to_bin(sh, in, b, w, weights);
+  }
+}
+__device__ __forceinline__ void clear_bins(Shared& sh) {
+  for (int i = threadIdx.x; i < kBins; i += kThreads) sh.bins.n[i] = sh.bins.lo[i] = sh.bins.hi[i] = 0;
+  __syncthreads();
+}
+
+// The first histogram of the slice.  Its last class, most of the logits, is summed up in registers.
+template <class T>
+__device__ void first_histogram(const Slice<T>& sl, const Scale& sc, Shared& sh, bool weights) {
+  constexpr int kAtOnce = 2;
+  uint64_t tail_w = 0;
+  uint32_t tail_n = 0;
+  each_pair<kAtOnce>(sl, [&](int, const float2 (&x)[kAtOnce]) {
+    uint64_t w[kAtOnce][2];
+    int b[kAtOnce][2];
+    bool all_in = true, one = true;  // a row of logits that lie close: whole warps in one class
+#pragma unroll
+    for (int q = 0; q < kAtOnce; ++q) {
+      int i0, i1;
+      if (weights) {
+        weights_of(sc, sh.table, x[q].x, x[q].y, w[q][0], w[q][1], i0, i1);
+      } else {
+        w[q][0] = w[q][1] = 0;
+        i0 = log2_below(sc, x[q].x);
+        i1 = log2_below(sc, x[q].y);
+      }
+      b[q][0] = bin_of(i0);
+      b[q][1] = bin_of(i1);
+      one = one && b[q][0] == b[q][1] && b[q][0] == b[0][0];
+      all_in = all_in && b[q][0] < kBins - 1;
+    }
+    const bool queue = __all_sync(0xffffffffu, one && all_in);
+#pragma unroll
+    for (int q = 0; q < kAtOnce; ++q)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const bool in = b[q][e] < kBins - 1;
+        if (!in && drawable(e ? x[q].y : x[q].x)) {
+          ++tail_n;
+          tail_w += w[q][e];
+        }
+        if (queue) add_to_one_bin(sh, in, b[q][e], w[q][e], weights);
+        else add_to_bin(sh, in, b[q][e], w[q][e], weights);
+      }
+  });
+  block_scan(tail_n, tail_w, sh);
+  if (threadIdx.x == kThreads - 1) {
+    sh.bins.n[kBins - 1] = tail_n;
+    sh.bins.lo[kBins - 1] = (uint32_t)tail_w;
+    sh.bins.hi[kBins - 1] = (uint32_t)(tail_w >> 32);
+  }
+}
+
+// A later one, over the keys lo .. hi, in classes of 2^shift keys from hi down.
+template <class T>
+__device__ void histogram(const Slice<T>& sl, const Scale& sc, Shared& sh, uint32_t lo, uint32_t hi, int shift, bool weights) {
+  each_pair<1>(sl, [&](int, const float2 (&x)[1]) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float v = e ? x[0].y : x[0].x;
+      const uint32_t k = key_of(v);
+      const bool in = drawable(v) && k >= lo && k <= hi;
+      if (!__any_sync(0xffffffffu, in)) continue;
+      const uint64_t w = weights ? weight_of(sc, sh.table, v) : 0;
+      add_to_one_bin(sh, in, in ? (int)((hi - k) >> shift) : 0, w, weights);
+    }
+  });
 }
 
 // What the first block knows of the search for a border.
 struct Search {
   bool by_weight;     // the goal is a sum of weights (else a count)
+  bool first;         // the last histogram is the first one
   uint64_t goal;      // the border is the first token in the order with which the sum reaches it
   uint32_t lo, hi;    // keys of the classes of the last histogram
-  int shift;          // -1: the first histogram
+  int shift;
   uint32_t n_before;  // tokens and weights in front of them
   uint64_t w_before;
 };
 
-// Smallest or largest key of a class of the first histogram (a warp together): the classes rise as keys fall.
-__device__ uint32_t first_key(const Scale& sc, int bin, bool largest) {
-  // largest: the last key with bin_of >= bin, else the first with bin_of <= bin
-  uint32_t lo = kLowestKey, hi = sc.top;
+// The largest key whose class of the first histogram is at least `bin`, or the smallest whose is at most that (a warp
+// together): the classes rise as keys fall.
+__device__ uint32_t key_at(const Scale& sc, int bin, bool largest) {
+  uint32_t lo = kLowestKey, hi = key_of(sc.max);
   const int lane = threadIdx.x & 31;
+  if (!largest && bin_of(sc, value_of(lo)) <= bin) return lo;
   while (lo < hi) {
     const uint32_t step = (hi - lo) / 32 + 1;  // probes lo + step, lo + 2 step, ...
     const uint64_t at = (uint64_t)lo + (uint64_t)step * (lane + 1);
     const bool in = at <= hi;
-    const int b = in ? bin_of(sc, (uint32_t)at) : 0;
+    const int b = in ? bin_of(sc, value_of((uint32_t)at)) : 0;
     if (largest) {  // true for the keys up to the one sought
-      const uint32_t yes = __ballot_sync(0xffffffffu, in && b >= bin);
-      const int n = __popc(yes);
+      const int n = __popc(__ballot_sync(0xffffffffu, in && b >= bin));
       hi = (uint32_t)min((uint64_t)hi, (uint64_t)lo + (uint64_t)step * (n + 1) - 1);
       lo += step * n;
-    } else {  // false for the keys in front of the one sought; the last key of the range is true
-      const int b_lo = bin_of(sc, lo);
-      if (b_lo <= bin) return lo;
-      const uint32_t no = __ballot_sync(0xffffffffu, in && b > bin);
-      const int n = __popc(no);
+    } else {  // lo's class is above, hi's is not
+      const int n = __popc(__ballot_sync(0xffffffffu, in && b > bin));
       hi = (uint32_t)min((uint64_t)hi, (uint64_t)lo + (uint64_t)step * (n + 1));
-      lo += step * n + 1;
+      lo += step * n;
+      if (hi - lo <= 1) return hi;
     }
   }
   return lo;
 }
 
-// The first block: sums the cluster's histograms and keeps the running sums.
-__device__ void merge(Cluster& cl, Shared& sh, uint32_t* cum_n, uint64_t* cum_w) {
-  uint32_t n[kBinsPerThread];
-  uint64_t w[kBinsPerThread];
-  uint32_t tn = 0;
-  uint64_t tw = 0;
+// The first block: sums the cluster's histograms, two classes a thread, as running sums.
+__device__ void merge(Cluster& cl, Shared& sh, bool first) {
+  static_assert(kBinsPerThread == 2, "");
+  uint32_t n[2] = {0, 0};
+  uint64_t w[2] = {0, 0};
+  constexpr int kRanks = 8;  // whose loads travel together
+  for (int r0 = 0; r0 < cl.size; r0 += kRanks) {
+    uint2 v[kRanks][3];
 #pragma unroll
-  for (int q = 0; q < kBinsPerThread; ++q) n[q] = 0, w[q] = 0;
-  for (int r = 0; r < cl.size; ++r) {
-    const Shared* const o = cl.group.map_shared_rank(&sh, r);
+    for (int r = 0; r < kRanks; ++r) {
 #pragma unroll
-    for (int q = 0; q < kBinsPerThread; ++q) {
-      const int b = threadIdx.x * kBinsPerThread + q;
-      n[q] += o->bins.n[b];
-      w[q] += (uint64_t)o->bins.hi[b] << 32 | o->bins.lo[b];
+      for (int q = 0; q < 3; ++q) v[r][q] = make_uint2(0u, 0u);
+      if (r0 + r < cl.size) {
+        const Shared* const o = cl.group.map_shared_rank(&sh, r0 + r);
+        v[r][0] = reinterpret_cast<const uint2*>(o->bins.n)[threadIdx.x];
+        v[r][1] = reinterpret_cast<const uint2*>(o->bins.lo)[threadIdx.x];
+        v[r][2] = reinterpret_cast<const uint2*>(o->bins.hi)[threadIdx.x];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kRanks; ++r) {
+      n[0] += v[r][0].x;
+      n[1] += v[r][0].y;
+      w[0] += (uint64_t)v[r][2].x << 32 | v[r][1].x;
+      w[1] += (uint64_t)v[r][2].y << 32 | v[r][1].y;
     }
   }
-#pragma unroll
-  for (int q = 0; q < kBinsPerThread; ++q) {
-    tn += n[q];
-    tw += w[q];
-  }
-  block_scan(tn, tw, sh);
-#pragma unroll
-  for (int q = kBinsPerThread - 1; q >= 0; --q) {
-    cum_n[threadIdx.x * kBinsPerThread + q] = tn;
-    cum_w[threadIdx.x * kBinsPerThread + q] = tw;
-    tn -= n[q];
-    tw -= w[q];
+  uint32_t tn = n[0] + n[1];
+  uint64_t tw = w[0] + w[1];
+  block_scan(tn, tw, sh);  // (its barriers: everybody has read this block's own counts)
+  const int b = threadIdx.x * 2;
+  if (first) {
+    sh.first_n[b] = tn - n[1];
+    sh.first_n[b + 1] = tn;
+    sh.first_w[b] = tw - w[1];
+    sh.first_w[b + 1] = tw;
+  } else {
+    sh.bins.n[b] = tn - n[1];
+    sh.bins.n[b + 1] = tn;
+    sh.bins.lo[b] = (uint32_t)(tw - w[1]);
+    sh.bins.hi[b] = (uint32_t)((tw - w[1]) >> 32);
+    sh.bins.lo[b + 1] = (uint32_t)tw;
+    sh.bins.hi[b + 1] = (uint32_t)(tw >> 32);
   }
   __syncthreads();
 }
 
-// The first place of a rising array of running sums that reaches the goal (the block together).
-template <class V>
-__device__ int reaches(const V* cum, int n, uint64_t goal, Shared& sh) {
+// The first place of rising running sums cum(0) .. cum(n - 1) that reaches the goal (the block together).
+template <class F>
+__device__ int reaches(int n, uint64_t goal, Shared& sh, F cum) {
   for (int i = threadIdx.x; i < n; i += kThreads)
-    if (cum[i] >= goal && (i == 0 || cum[i - 1] < goal)) sh.bin = i;
+    if (cum(i) >= goal && (i == 0 || cum(i - 1) < goal)) sh.bin = i;
   __syncthreads();
   const int b = sh.bin;
   __syncthreads();
@@ -355,165 +522,234 @@ __device__ int reaches(const V* cum, int n, uint64_t goal, Shared& sh) {
 
 // The first block: what to do about the class that holds the border.
 __device__ void next_step(Search& s, const Scale& sc, Shared& sh, Message* out) {
-  const bool first = s.shift < 0;
-  const uint32_t* const cum_n = first ? sh.first_n : sh.last_n;
-  const uint64_t* const cum_w = first ? sh.first_w : sh.last_w;
-  const int b = s.by_weight ? reaches(cum_w, kBins, s.goal - s.w_before, sh) : reaches(cum_n, kBins, s.goal - s.n_before, sh);
-  const uint32_t upto = cum_n[b], in_front = b ? cum_n[b - 1] : 0u;
-  const uint64_t w_front = b ? cum_w[b - 1] : 0;
-  uint32_t lo, hi;
-  if (first) {
-    hi = first_key(sc, b, true);
-    lo = first_key(sc, b, false);
-  } else {
-    hi = s.hi - ((uint32_t)b << s.shift);
-    lo = max(s.lo, hi - ((1u << s.shift) - 1u));
-  }
+  auto cum_n = [&](int i) { return s.first ? sh.first_n[i] : sh.bins.n[i]; };
+  auto cum_w = [&](int i) { return s.first ? sh.first_w[i] : (uint64_t)sh.bins.hi[i] << 32 | sh.bins.lo[i]; };
+  const int b = s.by_weight ? reaches(kBins, s.goal - s.w_before, sh, cum_w) : reaches(kBins, s.goal - s.n_before, sh, cum_n);
+  const uint32_t upto = cum_n(b), in_front = b ? cum_n(b - 1) : 0u;
+  const uint64_t w_front = b ? cum_w(b - 1) : 0;
   Message m{};
-  m.lo = lo;
-  m.hi = hi;
-  if (first && upto <= kList) {  // with all in front: a limit to the rest of top-k is among them, too
+  if (s.first && upto <= kList) {  // with all in front: a limit to the rest of top-k is among them, too
     m.op = kGather;
-    m.hi = sc.top;
+    m.by_bin = 1;
+    m.hi = (uint32_t)b;
   } else {
+    const bool first = s.first;
     s.n_before += in_front;
     s.w_before += w_front;
-    s.lo = lo;
-    s.hi = hi;
-    if (upto - in_front <= kList) {
+    if (first && upto - in_front <= kList) {
       m.op = kGather;
-    } else if (lo == hi) {
-      m.op = kTies;
-      const uint64_t w = weight_of(sc, sh.table, lo);
-      m.border = s.by_weight ? (s.goal - s.w_before + w - 1) / w : s.goal - s.n_before;
+      m.by_bin = 1;
+      m.lo = m.hi = (uint32_t)b;
     } else {
-      m.op = kRefine;
-      s.shift = max(0, 22 - __clz(hi - lo));
+      if (first) {
+        m.hi = key_at(sc, b, true);
+        m.lo = key_at(sc, b, false);
+      } else {
+        m.hi = s.hi - ((uint32_t)b << s.shift);
+        m.lo = max(s.lo, m.hi - ((1u << s.shift) - 1u));
+      }
+      if (upto - in_front <= kList) {
+        m.op = kGather;
+      } else if (m.lo == m.hi) {
+        m.op = kTies;
+        const uint64_t w = weight_of(sc, sh.table, value_of(m.lo));
+        m.border = s.by_weight ? (s.goal - s.w_before + w - 1) / w : s.goal - s.n_before;
+      } else {
+        m.op = kRefine;
+        s.first = false;
+        s.lo = m.lo;
+        s.hi = m.hi;
+        s.shift = max(0, 22 - __clz(m.hi - m.lo));
+      }
     }
   }
+  __syncthreads();  // (the running sums may give way to a list)
   if (threadIdx.x == 0) *out = m;
 }
 
-// Descending order of n entries (a power of two, at most kList), the block together
-__device__ void sort_list(uint64_t* list, int n) {
-  for (int size = 2; size <= n; size <<= 1)
-    for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      for (int i = threadIdx.x; i < n / 2; i += kThreads) {
-        const int a = 2 * i - (i & (stride - 1)), b = a + stride;
-        const uint64_t x = list[a], y = list[b];
-        if ((x < y) == ((a & size) == 0)) {
-          list[a] = y;
-          list[b] = x;
-        }
-      }
-      __syncthreads();
-    }
+// The first block: its list of n candidates in falling order, with the running sums of their weights.
+__device__ void sort_list(const Scale& sc, Shared& sh, int n) {
+  static_assert(kList <= kThreads, "");
+  const int i = threadIdx.x;
+  uint64_t mine = 0;
+  if (i < n) {
+    mine = sh.list[i];
+    int place = 0;
+    for (int j = 0; j < n; ++j) place += sh.list[j] > mine;
+    sh.other[place] = mine;
+  }
+  __syncthreads();
+  uint64_t w = 0;
+  uint32_t unused = 0;
+  if (i < n) {
+    mine = sh.other[i];
+    w = weight_of(sc, sh.table, value_of((uint32_t)(mine >> 32)));
+    sh.list[i] = mine;
+  }
+  block_scan(unused, w, sh);
+  if (i < n) sh.sums[i] = w;
+  __syncthreads();
 }
 
-// Sums of a slice by segment in the order of the index: f(key, index) gives what counts of an element.
-// Afterwards `find` gives the index with which the sum over the row exceeds `target`.
-template <class T, class F>
-__device__ Share segments(const Slice<T>& sl, Shared& sh, Cluster& cl, Share& before, F f) {
+// Sums of a slice by segment in the order of the index: in(x, index) says whether a logit counts, weigh(x, w) gives
+// two logits' weights and how many of them count after all.  Few of a row's logits do, as a rule: each lane first
+// marks those of its pairs, then weighs them two at a time.  Afterwards `find` gives the index with which the sum over
+// the row exceeds `target`.
+constexpr int kStep = 4;  // pairs of a lane at a time
+template <class T>
+__device__ __forceinline__ int segment_pairs(const Slice<T>& sl) {
+  return ((sl.pairs + kSegs - 1) / kSegs + 32 * kStep - 1) / (32 * kStep) * (32 * kStep);
+}
+template <class T, class In, class Weigh>
+__device__ Share segments(const Slice<T>& sl, Shared& sh, Cluster& cl, Share& before, In in, Weigh weigh) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int len = ((sl.n + kSegs - 1) / kSegs + 31) & ~31;
+  const int len = segment_pairs(sl);
   for (int s = wid; s < kSegs; s += kWarps) {
     uint64_t w = 0;
     uint32_t n = 0;
-    const int end = min(sl.n, (s + 1) * len);
-    for (int i = s * len; i < end; i += 32)
-      if (i + lane < end) {
-        uint64_t add = 0;
-        if (f(sl.key(i + lane), sl.begin + i + lane, add)) ++n;
-        w += add;
+    const int end = min(sl.pairs, (s + 1) * len);
+    for (int i0 = s * len; i0 < end; i0 += 32 * kStep) {
+      uint32_t marks = 0;
+#pragma unroll
+      for (int q = 0; q < kStep; ++q) {
+        const int i = i0 + 32 * q + lane;
+        const float2 x = i < end ? sl(i) : make_float2(-INFINITY, -INFINITY);
+        marks |= (uint32_t)in(x.x, sl.index(i)) << (2 * q) | (uint32_t)in(x.y, sl.index(i) + 1) << (2 * q + 1);
       }
+      while (__any_sync(0xffffffffu, marks != 0)) {
+        float2 x = make_float2(-INFINITY, -INFINITY);
+        if (marks) {
+          const int e = __ffs(marks) - 1;
+          marks &= marks - 1;
+          const float2 v = sl(i0 + 32 * (e >> 1) + lane);
+          x.x = e & 1 ? v.y : v.x;
+        }
+        if (marks) {
+          const int e = __ffs(marks) - 1;
+          marks &= marks - 1;
+          const float2 v = sl(i0 + 32 * (e >> 1) + lane);
+          x.y = e & 1 ? v.y : v.x;
+        }
+        uint64_t a, b;
+        n += weigh(x, a, b);
+        w += a + b;
+      }
+    }
     n = __reduce_add_sync(0xffffffffu, n);
-    if (__any_sync(0xffffffffu, w != 0)) w = warp_sum(w);
+    w = __any_sync(0xffffffffu, w != 0) ? warp_sum(w) : 0;
     if (lane == 0) {
       sh.seg_sum[s] = w;
       sh.seg_n[s] = n;
     }
   }
   __syncthreads();
-  if (wid == 0) {  // running sums over the segments
-    uint64_t w = 0;
+  if (wid == 0) {  // running sums over the segments, four to a lane
+    static_assert(kSegs == 128, "");
+    uint64_t v[4], sum = 0;
     uint32_t n = 0;
-    for (int c = 0; c < kSegs; c += 32) {
-      uint64_t x = sh.seg_sum[c + lane];
-      n += __reduce_add_sync(0xffffffffu, sh.seg_n[c + lane]);
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      x += w;
-      sh.seg_sum[c + lane] = x;
-      w = __shfl_sync(0xffffffffu, x, 31);
+    for (int q = 0; q < 4; ++q) {
+      v[q] = sum += sh.seg_sum[4 * lane + q];
+      n += sh.seg_n[4 * lane + q];
     }
-    if (lane == 0) {
-      sh.warp_w[0] = w;
+    n = __reduce_add_sync(0xffffffffu, n);
+    uint64_t up = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t y = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += y;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sh.seg_sum[4 * lane + q] = v[q] + up - sum;
+    if (lane == 31) {
+      sh.warp_w[0] = up;
       sh.warp_n[0] = n;
     }
   }
   __syncthreads();
-  const Share all = cl.exchange(Share{sh.warp_w[0], sh.warp_n[0], 0}, before);
-  return all;
+  return cl.exchange(Share{sh.warp_w[0], sh.warp_n[0], 0.f}, before);
 }
 // (the first warp of the block that holds it; else -1)
-template <class T, class F>
-__device__ int find(const Slice<T>& sl, Shared& sh, const Share& before, uint64_t target, F f) {
+template <class T, class In, class Weigh>
+__device__ int find(const Slice<T>& sl, Shared& sh, const Share& before, uint64_t target, In in, Weigh weigh) {
   const int lane = threadIdx.x & 31;
   if (threadIdx.x >= 32 || target < before.sum || target - before.sum >= sh.seg_sum[kSegs - 1]) return -1;
   const uint64_t rest = target - before.sum;
   int s = 0;
+#pragma unroll
   for (int c = 0; c < kSegs; c += 32) s += __popc(__ballot_sync(0xffffffffu, sh.seg_sum[c + lane] <= rest));
-  const int len = ((sl.n + kSegs - 1) / kSegs + 31) & ~31;
+  const int len = segment_pairs(sl);
   uint64_t sum = s ? sh.seg_sum[s - 1] : 0;
-  const int end = min(sl.n, (s + 1) * len);
+  const int end = min(sl.pairs, (s + 1) * len);
   for (int i = s * len; i < end; i += 32) {
-    uint64_t w = 0;
-    if (i + lane < end) f(sl.key(i + lane), sl.begin + i + lane, w);
+    float2 x = i + lane < end ? sl(i + lane) : make_float2(-INFINITY, -INFINITY);
+    if (!in(x.x, sl.index(i + lane))) x.x = -INFINITY;
+    if (!in(x.y, sl.index(i + lane) + 1)) x.y = -INFINITY;
+    if (!__any_sync(0xffffffffu, drawable(x.x) || drawable(x.y))) continue;
+    uint64_t a, b;
+    weigh(x, a, b);
+    uint64_t w = a + b;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint64_t y = __shfl_up_sync(0xffffffffu, w, o);
       if (lane >= o) w += y;
     }
     const uint32_t over = __ballot_sync(0xffffffffu, sum + w > rest);
-    if (over) return i + __ffs(over) - 1;
+    if (over) {
+      const int l = __ffs(over) - 1;
+      // the pair's second logit, if the sum without it does not exceed
+      const bool second = sum + w - b <= rest;
+      return 2 * (i + l) - sl.skew + __shfl_sync(0xffffffffu, (int)second, l);
+    }
     sum += __shfl_sync(0xffffffffu, w, 31);
   }
   return -1;
 }
 
-// The index of the m-th key (from 1) that equals k.
+// The index of the m-th logit (from 1) that equals v.
 template <class T>
-__device__ uint32_t tie(const Slice<T>& sl, Shared& sh, Cluster& cl, uint32_t k, uint64_t m) {
-  auto equal = [&](uint32_t key, int, uint64_t& w) {
-    w = key == k;
-    return key == k;
+__device__ uint32_t tie(const Slice<T>& sl, Shared& sh, Cluster& cl, float v, uint64_t m) {
+  auto equal = [&](float x, int) { return x == v; };
+  auto one = [&](float2 x, uint64_t& a, uint64_t& b) {
+    a = x.x == v;
+    b = x.y == v;
+    return (uint32_t)(a + b);
   };
-  Share before;
-  segments(sl, sh, cl, before, equal);
-  const int i = find(sl, sh, before, m - 1, equal);
-  Share found{0, 0, 0};
+  Share before, unused;
+  segments(sl, sh, cl, before, equal, one);
+  const int i = find(sl, sh, before, m - 1, equal, one);
   if (threadIdx.x == 0) sh.found = i >= 0 ? (uint32_t)(sl.begin + i) + 1u : 0u;
   __syncthreads();
-  found.top = sh.found;
-  Share unused;
-  return cl.exchange(found, unused).top - 1u;
+  return cl.exchange(Share{0, sh.found, 0.f}, unused).count - 1u;
 }
 
-// 16 bytes of logits as values
-__device__ __forceinline__ void values_of(const uint4& v, float (&x)[4], const float*) {
-  x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+// the larger of each half's elements; NaN counts for nothing
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b, const float*) {
+  return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
 }
-template <class H>
-__device__ __forceinline__ void values_of(const uint4& v, float (&x)[8], const H*) {
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const uint16_t b = (uint16_t)((&v.x)[q >> 1] >> (16 * (q & 1)));
-    x[q] = (float)*reinterpret_cast<const H*>(&b);
-  }
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b, const __nv_bfloat16*) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b, const __half*) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <class T>
+__device__ __forceinline__ float largest_of(uint32_t a, const T* t) {
+  const float2 f = floats(a, t);
+  return fmaxf(f.x, f.y);
+}
+__device__ __forceinline__ float largest_of(uint32_t a, const float*) { return __uint_as_float(a); }
+// -inf in every element
+template <class T>
+constexpr uint32_t kNothing = sizeof(T) == 4 ? 0xFF800000u : 0u;
+template <>
+constexpr uint32_t kNothing<__nv_bfloat16> = 0xFF80FF80u;
+template <>
+constexpr uint32_t kNothing<__half> = 0xFC00FC00u;
 
 // What the calls of a row have in common.
 struct Row {
@@ -529,7 +765,7 @@ template <class T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
-  uint32_t* const room = reinterpret_cast<uint32_t*>(smem + (sizeof(Shared) + 15) / 16 * 16);
+  uint4* const room = reinterpret_cast<uint4*>(smem + (sizeof(Shared) + 15) / 16 * 16);
   Cluster cl{cg::this_cluster(), sh, 0, 0, 0, 0};
   cl.rank = (int)cl.group.block_rank();
   cl.size = (int)cl.group.num_blocks();
@@ -542,79 +778,62 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
   r.min_p = p.min_p ? p.min_p[row] : 0.f;
   r.random = p.random[row];
 
-  // ---- the slice's keys to shared memory
+  // ---- the slice to shared memory, and its largest logit
   Slice<T> sl;
-  sl.x = static_cast<const T*>(p.logits) + row * p.stride;
   sl.begin = min(p.vocab, cl.rank * p.slice);
   sl.n = min(p.vocab, sl.begin + p.slice) - sl.begin;
+  sl.x = static_cast<const T*>(p.logits) + row * p.stride + sl.begin;
   constexpr int kVec = 16 / sizeof(T);
-  // (keys stand as the logits do within 16 bytes, so that aligned loads become aligned stores)
-  const T* const x0 = sl.x + sl.begin;
-  const int skew = (int)((reinterpret_cast<uintptr_t>(x0) & 15) / sizeof(T));
-  uint32_t* const keys = room + skew;
-  sl.keys = keys;
-  sl.held = min(sl.n, p.room);
-  uint32_t top = 0, valid = 0;
+  sl.skew = (int)((reinterpret_cast<uintptr_t>(sl.x) & 15) / sizeof(T));
+  sl.room = reinterpret_cast<const typename Slice<T>::Bits*>(room);
+  const int vecs = (sl.skew + sl.n + kVec - 1) / kVec;
+  sl.pairs = (sl.skew + sl.n + 1) / 2;
+  sl.held = min(sl.pairs, p.room * (kVec / 2));
+  sl.infinite = false;
+  uint32_t most = kNothing<T>;
   {
-    const uint4* const base = reinterpret_cast<const uint4*>(x0 - skew);
-    const int vecs = (skew + sl.n + kVec - 1) / kVec;
+    const uint4* const base = reinterpret_cast<const uint4*>(sl.x - sl.skew);
     constexpr int kAtOnce = 8;
     for (int v0 = tid; v0 < vecs; v0 += kThreads * kAtOnce) {
       uint4 v[kAtOnce];
 #pragma unroll
       for (int q = 0; q < kAtOnce; ++q) {
-        const int j = v0 + q * kThreads, e = j * kVec - skew;  // first element
-        v[q] = make_uint4(0u, 0u, 0u, 0u);
-        if (e >= 0 && e + kVec <= sl.n) v[q] = __ldg(base + j);
+        const int j = v0 + q * kThreads, e = j * kVec - sl.skew;  // first element
+        v[q] = make_uint4(kNothing<T>, kNothing<T>, kNothing<T>, kNothing<T>);
+        if (e >= 0 && e + kVec <= sl.n) {
+          v[q] = __ldg(base + j);
+        } else if (j < vecs) {  // the slice's ends
+          for (int i = 0; i < kVec; ++i)
+            if (e + i >= 0 && e + i < sl.n) {
+              uint32_t& to = (&v[q].x)[i * sizeof(T) / 4];
+              if constexpr (sizeof(T) == 4) to = __float_as_uint(sl.x[e + i]);
+              else to = __byte_perm(to, reinterpret_cast<const uint16_t*>(sl.x)[e + i], i & 1 ? 0x5410 : 0x3254);
+            }
+        }
       }
 #pragma unroll
       for (int q = 0; q < kAtOnce; ++q) {
-        const int j = v0 + q * kThreads, e = j * kVec - skew;
-        if (j >= vecs) break;
-        uint32_t k[kVec];
-        if (e >= 0 && e + kVec <= sl.n) {
-          float f[kVec];
-          values_of(v[q], f, x0);
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) k[i] = key_of(f[i]);
-        } else {  // the slice's ends
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) k[i] = e + i >= 0 && e + i < sl.n ? key_of((float)x0[e + i]) : 0u;
-        }
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          top = max(top, k[i]);
-          valid += k[i] != 0u;
-        }
-        if (e >= 0 && e + kVec <= sl.held) {
-#pragma unroll
-          for (int i = 0; i < kVec; i += 4)
-            *reinterpret_cast<uint4*>(keys + e + i) = make_uint4(k[i], k[i + 1], k[i + 2], k[i + 3]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < kVec; ++i)
-            if (e + i >= 0 && e + i < sl.held) keys[e + i] = k[i];
-        }
+        const int j = v0 + q * kThreads;
+        if (j < vecs && j < p.room) room[j] = v[q];
+        most = larger(larger(larger(most, v[q].x, sl.x), v[q].y, sl.x), larger(v[q].z, v[q].w, sl.x), sl.x);
       }
     }
   }
-  for (int i = tid; i < 1024; i += kThreads) sh.table[i] = __umul64hi(c_coarse[i >> 5], c_fine[i & 31]);
-  top = __reduce_max_sync(0xffffffffu, top);
-  valid = __reduce_add_sync(0xffffffffu, valid);
-  if (lane == 0) {
-    sh.warp_top[wid] = top;
-    sh.warp_n[wid] = valid;
-  }
-  __syncthreads();
-  top = valid = 0;
+  float top = largest_of(most, sl.x);
+  top = drawable(top) ? top + 0.f : -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    top = max(top, sh.warp_top[i]);
-    valid += sh.warp_n[i];
-  }
+  for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) sh.warp_top[wid] = top;
+  const uint64_t fine = c_fine[lane];
+  for (int i = tid; i < 1024; i += kThreads)
+    sh.table[i] = (uint32_t)min((__umul64hi(c_coarse[i >> 5], fine) + 0x80000000ull) >> 32, 0x7FFFFFFFull);
+  clear_bins(sh);
+  top = lane < kWarps ? sh.warp_top[lane] : -INFINITY;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   Share before;
-  const Share all = cl.exchange(Share{0, valid, top}, before);
-  if (all.count == 0 || !r.fine()) {
+  top = cl.exchange(Share{0, 0, top}, before).top;
+  if (!drawable(top) || !r.fine()) {
     if (cl.rank == 0 && tid == 0) {
       p.tokens[row] = -1;
       if (p.probs) p.probs[row] = 0.f;
@@ -624,16 +843,40 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     return;
   }
 
+  if (top == INFINITY) {  // the infinite ones share it all
+    T* const x = reinterpret_cast<T*>(room);
+    for (int i = tid; i < 2 * sl.held; i += kThreads) x[i] = (T)((float)x[i] == INFINITY ? 0.f : -INFINITY);
+    sl.infinite = true;
+    top = 0.f;
+    __syncthreads();
+  }
+
   // ---- the order's border: the last token that top-k and top-p keep
   const bool greedy = r.temperature == 0.f;
-  const Scale sc = scale_of(all.top, greedy ? 1.f : r.temperature);
+  const Scale sc = scale_of(top, greedy ? 1.f : r.temperature);
+  const uint64_t least = (uint64_t)__double2ull_ru((double)r.min_p * (double)kOne);  // min-p's weight
+  auto target_of = [&](uint64_t sum) { return min(sum - 1, (uint64_t)((double)r.random * (double)sum)); };
+  auto write = [&](int token, uint32_t n, float x, uint64_t sum) {
+    p.tokens[row] = token;
+    if (p.kept) p.kept[row] = (int32_t)n;
+    if (p.probs) {
+      // (the weight as a number: its multiple of 2^-42 may have few bits)
+      const float d = sc.max - x, b = d - sc.max, e = (sc.max - (d - b)) - (x + b);
+      const float h = d * sc.hi, l = fmaf(d, sc.hi, -h) + fmaf(d, sc.lo, e * sc.hi);
+      p.probs[row] = (float)((double)(exp2f(-h) * (1.f - 0.6931471805599453f * l)) * (double)kOne / (double)sum);
+    }
+  };
   uint64_t border = 0;
   if (greedy) {
-    border = order_of(all.top, tie(sl, sh, cl, all.top, 1));
-  } else {
-    const bool by_count = r.top_k > 0 && (uint32_t)r.top_k < all.count, by_weight = r.top_p < 1.f;
+    const uint32_t index = tie(sl, sh, cl, top, 1);
+    if (cl.rank == 0 && tid == 0) write((int)index, 1u, top, kOne);
+    cl.group.sync();  // a block's shared memory stays until the others have read it
+    return;
+  }
+  {
+    const bool by_count = r.top_k > 0 && r.top_k < p.vocab, by_weight = r.top_p < 1.f;
     if (by_count || by_weight) {
-      histogram(sl, sc, sh, 1u, 0xFFFFFFFFu, -1, by_weight);
+      first_histogram(sl, sc, sh, by_weight);
       cl.group.sync();
       Search se{};  // (of use in the first block)
       // the weight that top-p of a sum of w asks for
@@ -641,98 +884,112 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         return max((uint64_t)1, min(w, (uint64_t)__double2ull_ru((double)r.top_p * (double)w)));
       };
       auto restart = [&](uint64_t whole) {  // top-p of what top-k keeps, from the first histogram on
-        se.by_weight = true;
+        se.by_weight = se.first = true;
         se.goal = part_of(whole);
-        se.shift = -1;
         se.n_before = 0;
         se.w_before = 0;
       };
       if (cl.rank == 0) {
-        merge(cl, sh, sh.first_n, sh.first_w);
-        se.shift = -1;
-        if (by_count) {
+        merge(cl, sh, true);
+        if (tid == 0) sh.n_list = 0;
+        if (by_count && (uint32_t)r.top_k < sh.first_n[kBins - 1]) {
+          se.first = true;
           se.goal = (uint64_t)r.top_k;
-        } else {
+        } else if (by_weight) {
           restart(sh.first_w[kBins - 1]);
         }
-        sh.n_list = 0;
-        next_step(se, sc, sh, cl.message());
+        if (se.first) next_step(se, sc, sh, cl.message());
+        else if (tid == 0) *cl.message() = Message{kDone, 0, 0, 0, 0};  // all of them
       }
       for (;;) {
         const Message m = cl.receive();
+        if (m.op == kDrawn) {
+          cl.group.sync();  // a block's shared memory stays until the others have read it
+          return;
+        }
         if (m.op == kDone) {
           border = m.border;
           break;
         }
         if (m.op == kGather) {
           Shared* const to = cl.group.map_shared_rank(&sh, 0);
-          const int steps = (sl.n + kThreads - 1) / kThreads;
-          for (int s = 0; s < steps; ++s) {
-            const int i = s * kThreads + tid;
-            const uint32_t k = i < sl.n ? sl.key(i) : 0u;
-            if (k >= m.lo && k <= m.hi) {
-              const uint32_t at = atomicAdd(&to->n_list, 1u);
-              if (at < kList) to->list[at] = order_of(k, (uint32_t)(sl.begin + i));
-            }
-          }
+          constexpr int kAtOnce = 4;
+          each_pair<kAtOnce>(sl, [&](int i, const float2 (&x)[kAtOnce]) {
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float v = e ? x[q].y : x[q].x;
+                const uint32_t c = m.by_bin ? (uint32_t)bin_of(sc, v) : key_of(v);
+                if (c - m.lo <= m.hi - m.lo && drawable(v)) {
+                  const uint32_t at = atomicAdd(&to->n_list, 1u);
+                  if (at < kList) to->list[at] = order_of(key_of(v), (uint32_t)(sl.index(i + q * kThreads) + e));
+                }
+              }
+          });
           cl.group.sync();
           if (cl.rank == 0) {
             const int n = (int)min(sh.n_list, (uint32_t)kList);
-            int size = 32;
-            while (size < n) size <<= 1;
-            for (int i = n + tid; i < size; i += kThreads) sh.list[i] = 0;
-            __syncthreads();
-            sort_list(sh.list, size);
-            // running sums of the weights
-            uint64_t w[kBinsPerThread], sum = 0;
-            uint32_t none = 0;
-#pragma unroll
-            for (int q = 0; q < kBinsPerThread; ++q) {
-              const int i = tid * kBinsPerThread + q;
-              w[q] = by_weight && i < n ? weight_of(sc, sh.table, (uint32_t)(sh.list[i] >> 32)) : 0;
-              sum += w[q];
-            }
-            block_scan(none, sum, sh);
-#pragma unroll
-            for (int q = kBinsPerThread - 1; q >= 0; --q) {
-              sh.last_w[tid * kBinsPerThread + q] = sum;
-              sum -= w[q];
-            }
-            __syncthreads();
-            int at = se.by_weight ? reaches(sh.last_w, n, se.goal - se.w_before, sh) : (int)(se.goal - se.n_before) - 1;
+            sort_list(sc, sh, n);
+            auto sums = [&](int i) { return sh.sums[i]; };
+            int at = se.by_weight ? reaches(n, se.goal - se.w_before, sh, sums) : (int)(se.goal - se.n_before) - 1;
             bool done = true;
+            const bool from_top = se.n_before == 0;
             if (!se.by_weight && by_weight) {
               const uint64_t w_front = se.w_before;
-              restart(w_front + sh.last_w[at]);
+              restart(w_front + sh.sums[at]);
               done = se.goal > w_front;  // (else in front of these)
-              if (done) at = reaches(sh.last_w, n, se.goal - w_front, sh);
+              if (done) at = reaches(n, se.goal - w_front, sh, sums);
             }
-            if (done) {
-              if (tid == 0) *cl.message() = Message{kDone, 0, 0, sh.list[at]};
+            if (done && from_top) {
+              // the list begins with the order: the draw is among its first ones
+              const uint64_t mine = tid <= at ? sh.list[tid] : 0;
+              uint64_t w = tid <= at ? sh.sums[tid] - (tid ? sh.sums[tid - 1] : 0) : 0;
+              const int n_kept = __syncthreads_count(tid <= at && w >= least);
+              const uint64_t sum = sh.sums[n_kept - 1], target = target_of(sum);
+              if (tid < n_kept) {  // by index (the order's lower half falls with it)
+                int place = 0;
+                for (int j = 0; j < n_kept; ++j) place += (uint32_t)sh.list[j] > (uint32_t)mine;
+                sh.other[place] = (uint64_t)tid << 48 | w;
+              }
+              __syncthreads();
+              w = tid < n_kept ? sh.other[tid] : 0;
+              const int from = (int)(w >> 48);
+              uint64_t upto = w &= 0xFFFFFFFFFFFFull;
+              uint32_t unused = 0;
+              block_scan(unused, upto, sh);
+              if (tid < n_kept && upto > target && upto - w <= target) {
+                const uint64_t it = sh.list[from];
+                write((int)(0xFFFFFFFFu - (uint32_t)it), (uint32_t)n_kept, value_of((uint32_t)(it >> 32)), sum);
+              }
+              if (tid == 0) *cl.message() = Message{kDrawn, 0, 0, 0, 0};
+            } else if (done) {
+              if (tid == 0) *cl.message() = Message{kDone, 0, 0, 0, sh.list[at]};
             } else {
               if (tid == 0) sh.n_list = 0;
               next_step(se, sc, sh, cl.message());
             }
           }
         } else if (m.op == kRefine) {
-          const int shift = max(0, 22 - __clz(m.hi - m.lo));
-          histogram(sl, sc, sh, m.lo, m.hi, shift, by_weight);
+          clear_bins(sh);
+          histogram(sl, sc, sh, m.lo, m.hi, max(0, 22 - __clz(m.hi - m.lo)), by_weight);
           cl.group.sync();
           if (cl.rank == 0) {
-            merge(cl, sh, sh.last_n, sh.last_w);
+            merge(cl, sh, false);
             next_step(se, sc, sh, cl.message());
           }
         } else {
-          const uint32_t index = tie(sl, sh, cl, m.lo, m.border);
+          const float v = value_of(m.lo);
+          const uint32_t index = tie(sl, sh, cl, v, m.border);
           if (cl.rank == 0) {
             bool done = true;
             if (!se.by_weight && by_weight) {
-              const uint64_t w = weight_of(sc, sh.table, m.lo), w_front = se.w_before;
+              const uint64_t w = weight_of(sc, sh.table, v), w_front = se.w_before;
               restart(w_front + m.border * w);
               done = se.goal > w_front;
-              if (done && tid == 0) *cl.message() = Message{kTies, m.lo, m.lo, (se.goal - w_front + w - 1) / w};
+              if (done && tid == 0) *cl.message() = Message{kTies, m.lo, m.lo, 0, (se.goal - w_front + w - 1) / w};
             } else if (tid == 0) {
-              *cl.message() = Message{kDone, 0, 0, order_of(m.lo, index)};
+              *cl.message() = Message{kDone, 0, 0, 0, order_of(m.lo, index)};
             }
             if (!done) next_step(se, sc, sh, cl.message());
           }
@@ -742,27 +999,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
   }
 
   // ---- the draw among the tokens up to the border, and with min-p's weight
-  const uint64_t least = greedy ? 0 : (uint64_t)__double2ull_ru((double)r.min_p * (double)(1ull << kOneBits));
-  auto kept = [&](uint32_t key, int index, uint64_t& w) {
-    if (key == 0u || order_of(key, (uint32_t)index) < border) return false;
-    w = weight_of(sc, sh.table, key);
-    if (w >= least) return true;
-    w = 0;
-    return false;
+  const float last = border ? value_of((uint32_t)(border >> 32)) : -INFINITY;  // the border's logit and index
+  const int last_index = border ? (int)(0xFFFFFFFFu - (uint32_t)border) : INT_MIN;
+  auto in_order = [&](float x, int index) { return x > last || (x == last && index <= last_index); };
+  auto weigh = [&](float2 x, uint64_t& a, uint64_t& b) {
+    int i0, i1;
+    weights_of(sc, sh.table, x.x, x.y, a, b, i0, i1);
+    const bool in0 = drawable(x.x) && a >= least, in1 = drawable(x.y) && b >= least;
+    a = in0 ? a : 0;
+    b = in1 ? b : 0;
+    return (uint32_t)in0 + (uint32_t)in1;
   };
-  const Share sum = segments(sl, sh, cl, before, kept);
-  const uint64_t target = min(sum.sum - 1, (uint64_t)((double)r.random * (double)sum.sum));
-  const int i = find(sl, sh, before, target, kept);
+  const Share sum = segments(sl, sh, cl, before, in_order, weigh);
+  const int i = find(sl, sh, before, target_of(sum.sum), in_order, weigh);
   if (i >= 0 && lane == 0) {
-    p.tokens[row] = sl.begin + i;
-    if (p.kept) p.kept[row] = (int32_t)sum.count;
-    if (p.probs) {
-      // (the weight as a number: its multiple of 2^-42 may have few bits)
-      const uint32_t k = sl.key(i);
-      float h = 0.f, l = 0.f;
-      if (k != sc.top) log2_below(sc, k, h, l);
-      p.probs[row] = (float)((double)(exp2f(-h) * (1.f - 0.6931471805599453f * l)) * (double)(1ull << kOneBits) / (double)sum.sum);
-    }
+    const float2 x = sl((i + sl.skew) >> 1);
+    write(sl.begin + i, sum.count, (i + sl.skew) & 1 ? x.y : x.x, sum.sum);
   }
   cl.group.sync();  // a block's shared memory stays until the others have read it
 }
@@ -780,18 +1032,19 @@ cudaError_t launch(SampleArgs p, int sms, int most_smem, cudaStream_t s) {
   }
   // Blocks per row: more of them while the rows alone leave SMs idle or a slice is so large that only one
   // block fits an SM; a slice has at least 2,048 logits (a cluster's barriers cost what its blocks save).
-  constexpr int kTwoPerSm = 16384, kLeast = 2048;
+  const int fixed = (int)(sizeof(Shared) + 15) / 16 * 16;
+  constexpr int kLeast = 2048, kTwoPerSm = 110 * 1024;
   int blocks = 1;
   while (blocks < kMaxCluster && p.vocab / blocks >= 2 * kLeast &&
-         ((int64_t)p.n_rows * blocks < sms || (p.vocab - 1) / blocks + 1 > kTwoPerSm))
+         ((int64_t)p.n_rows * blocks < sms || fixed + ((p.vocab - 1) / blocks + 1) * (int)sizeof(T) > kTwoPerSm))
     blocks *= 2;
   p.slice = (p.vocab - 1) / blocks + 1;
-  const int fixed = (int)(sizeof(Shared) + 15) / 16 * 16 + 64;
-  p.room = std::min(p.slice, (most_smem - fixed) / 4);
+  constexpr int kVec = 16 / sizeof(T);
+  p.room = std::min((p.slice + 2 * kVec - 2) / kVec, (most_smem - fixed) / 16);
   cudaLaunchConfig_t lc{};
   lc.gridDim = dim3((unsigned)p.n_rows * blocks);
   lc.blockDim = dim3(kThreads);
-  lc.dynamicSmemBytes = fixed + 4 * (size_t)p.room;
+  lc.dynamicSmemBytes = fixed + 16 * (size_t)p.room;
   lc.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

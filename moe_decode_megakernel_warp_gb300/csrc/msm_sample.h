@@ -15,7 +15,7 @@ struct SampleArgs {
   int32_t *tokens, *kept;
   float* probs;
   int n_rows, vocab;
-  int slice, room;  // set by the launch: logits of a block, and of them in shared memory
+  int slice, room;  // set by the launch: logits of a block, and 16-byte pieces of them in shared memory
 };
 constexpr int kSampleVocab = 1 << 20;  // most logits of a row (their weights' sum has 62 bits)
 cudaError_t launch_sample(const SampleArgs& p, int dtype, int sms, cudaStream_t s);

@@ -150,7 +150,7 @@ def draw(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     none = (-1, 0, 0.0, np.inf, np.inf)
     if not (0 <= temperature < np.inf and 0 <= top_p <= 1 and 0 <= min_p <= 1 and 0 <= u <= 1):
         return none
-    valid = np.flatnonzero(x > -np.inf)
+    valid = np.flatnonzero(x == np.inf if (x == np.inf).any() else x > -np.inf)
     if not len(valid):
         return none
     order = valid[np.lexsort((valid, -x[valid]))]

@@ -134,4 +134,4 @@ def test_seen_and_draw_of_the_reference():
     assert draw(x, 0.5, top_k=1)[:2] == (1, 1) and draw(x, 0.6, top_k=3)[:2] == (2, 3)
     assert draw(x, 0.9, top_p=0.5)[:2] == (2, 2) and draw(x, 0.0, min_p=0.5)[:2] == (1, 2)
     assert draw(x, 0.3, temperature=0)[:3] == (1, 1, 1.0) and draw([-np.inf, np.nan], 0.3)[0] == -1
-    assert draw([0.0, np.inf, np.inf], 0.7)[:3] == (2, 3, 0.5) and draw(x, 1.5)[0] == -1
+    assert draw([0.0, np.inf, np.inf], 0.7)[:3] == (2, 2, 0.5) and draw(x, 1.5)[0] == -1
