@@ -72,7 +72,7 @@ struct __align__(16) Share {  // what a block tells the others
   uint32_t count;
   float top;
 };
-enum Op { kGather, kRefine, kTies, kDone, kDrawn };
+enum Op { kGather, kWeigh, kRefine, kTies, kDone, kDrawn };
 struct Message {  // what the first block tells the others
   int op;
   uint32_t lo, hi;   // classes of the first histogram, or keys, of the candidates
@@ -209,6 +209,23 @@ __device__ __forceinline__ int log2_below(const Scale& s, float x) {
 // class of the first histogram; rises as the logit falls
 __device__ __forceinline__ int bin_of(int i) { return min(i >> 4, kBins - 1); }
 __device__ __forceinline__ int bin_of(const Scale& s, float x) { return bin_of(log2_below(s, x)); }
+
+// x sum, rounded down or up: x is 0 .. 1, the sum below 2^63 (the product has 24 + 63 bits)
+__device__ __forceinline__ uint64_t part_of(float x, uint64_t sum, bool up) {
+  const uint32_t b = __float_as_uint(x), e = b >> 23;
+  const uint64_t m = e ? (b & 0x7FFFFFu) | 0x800000u : b & 0x7FFFFFu;
+  const int shift = 150 - (int)(e ? e : 1);  // x = m 2^-shift, shift >= 23
+  const uint64_t lo = m * sum, hi = __umul64hi(m, sum);
+  uint64_t q, rest;
+  if (shift < 64) {
+    q = hi << (64 - shift) | lo >> shift;
+    rest = lo << (64 - shift);
+  } else {
+    q = shift < 128 ? hi >> (shift - 64) : 0;
+    rest = lo | (hi ^ (shift < 128 ? q << (shift - 64) : 0));
+  }
+  return q + (up && rest ? 1 : 0);
+}
 
 // ---- sums
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
@@ -369,10 +386,10 @@ __device__ void first_histogram(const Slice<T>& sl, const Scale& sc, Shared& sh,
   constexpr int kAtOnce = 2;
   uint64_t tail_w = 0;
   uint32_t tail_n = 0;
+  bool look = true, queue = false;  // a row of logits that lie close (or a high temperature): whole warps in one class
   each_pair<kAtOnce>(sl, [&](int, const float2 (&x)[kAtOnce]) {
     uint64_t w[kAtOnce][2];
     int b[kAtOnce][2];
-    bool all_in = true, one = true;  // a row of logits that lie close: whole warps in one class
 #pragma unroll
     for (int q = 0; q < kAtOnce; ++q) {
       int i0, i1;
@@ -385,10 +402,11 @@ __device__ void first_histogram(const Slice<T>& sl, const Scale& sc, Shared& sh,
       }
       b[q][0] = bin_of(i0);
       b[q][1] = bin_of(i1);
-      one = one && b[q][0] == b[q][1] && b[q][0] == b[0][0];
-      all_in = all_in && b[q][0] < kBins - 1;
     }
-    const bool queue = __all_sync(0xffffffffu, one && all_in);
+    if (look) {  // at the warp's first ones
+      queue = __all_sync(0xffffffffu, b[0][0] == __shfl_sync(0xffffffffu, b[0][0], 0));
+      look = false;
+    }
 #pragma unroll
     for (int q = 0; q < kAtOnce; ++q)
 #pragma unroll
@@ -429,6 +447,7 @@ __device__ void histogram(const Slice<T>& sl, const Scale& sc, Shared& sh, uint3
 // What the first block knows of the search for a border.
 struct Search {
   bool by_weight;     // the goal is a sum of weights (else a count)
+  bool weighed;       // the first histogram has weights
   bool first;         // the last histogram is the first one
   uint64_t goal;      // the border is the first token in the order with which the sum reaches it
   uint32_t lo, hi;    // keys of the classes of the last histogram
@@ -463,30 +482,39 @@ __device__ uint32_t key_at(const Scale& sc, int bin, bool largest) {
 }
 
 // The first block: sums the cluster's histograms, two classes a thread, as running sums.
-__device__ void merge(Cluster& cl, Shared& sh, bool first) {
+__device__ void merge(Cluster& cl, Shared& sh, bool first, bool weights) {
   static_assert(kBinsPerThread == 2, "");
   uint32_t n[2] = {0, 0};
   uint64_t w[2] = {0, 0};
-  constexpr int kRanks = 8;  // whose loads travel together
-  for (int r0 = 0; r0 < cl.size; r0 += kRanks) {
-    uint2 v[kRanks][3];
+  auto gather = [&](int which, uint2 (&v)[kMaxCluster]) {  // all blocks' loads travel together
 #pragma unroll
-    for (int r = 0; r < kRanks; ++r) {
-#pragma unroll
-      for (int q = 0; q < 3; ++q) v[r][q] = make_uint2(0u, 0u);
-      if (r0 + r < cl.size) {
-        const Shared* const o = cl.group.map_shared_rank(&sh, r0 + r);
-        v[r][0] = reinterpret_cast<const uint2*>(o->bins.n)[threadIdx.x];
-        v[r][1] = reinterpret_cast<const uint2*>(o->bins.lo)[threadIdx.x];
-        v[r][2] = reinterpret_cast<const uint2*>(o->bins.hi)[threadIdx.x];
+    for (int r = 0; r < kMaxCluster; ++r) {
+      v[r] = make_uint2(0u, 0u);
+      if (r < cl.size) {
+        const Shared* const o = cl.group.map_shared_rank(&sh, r);
+        v[r] = reinterpret_cast<const uint2*>(which == 0 ? o->bins.n : which == 1 ? o->bins.lo : o->bins.hi)[threadIdx.x];
       }
     }
+  };
+  uint2 v[kMaxCluster];
+  gather(0, v);
 #pragma unroll
-    for (int r = 0; r < kRanks; ++r) {
-      n[0] += v[r][0].x;
-      n[1] += v[r][0].y;
-      w[0] += (uint64_t)v[r][2].x << 32 | v[r][1].x;
-      w[1] += (uint64_t)v[r][2].y << 32 | v[r][1].y;
+  for (int r = 0; r < kMaxCluster; ++r) {
+    n[0] += v[r].x;
+    n[1] += v[r].y;
+  }
+  if (weights) {
+    gather(1, v);
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      w[0] += v[r].x;
+      w[1] += v[r].y;
+    }
+    gather(2, v);
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      w[0] += (uint64_t)v[r].x << 32;
+      w[1] += (uint64_t)v[r].y << 32;
     }
   }
   uint32_t tn = n[0] + n[1];
@@ -532,6 +560,8 @@ __device__ void next_step(Search& s, const Scale& sc, Shared& sh, Message* out) 
     m.op = kGather;
     m.by_bin = 1;
     m.hi = (uint32_t)b;
+  } else if (!s.weighed) {
+    m.op = kWeigh;  // a long list of top-k's: what top-p keeps of it takes the first histogram's weights
   } else {
     const bool first = s.first;
     s.n_before += in_front;
@@ -794,7 +824,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
   {
     const uint4* const base = reinterpret_cast<const uint4*>(sl.x - sl.skew);
     constexpr int kAtOnce = 8;
-    for (int v0 = tid; v0 < vecs; v0 += kThreads * kAtOnce) {
+    const uint64_t fine = c_fine[lane];
+    for (int v0 = tid; v0 < vecs || v0 == tid; v0 += kThreads * kAtOnce) {
       uint4 v[kAtOnce];
 #pragma unroll
       for (int q = 0; q < kAtOnce; ++q) {
@@ -811,6 +842,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
             }
         }
       }
+      if (v0 == tid) {  // while the first ones travel
+        for (int i = tid; i < 1024; i += kThreads)
+          sh.table[i] = (uint32_t)min((__umul64hi(c_coarse[i >> 5], fine) + 0x80000000ull) >> 32, 0x7FFFFFFFull);
+        clear_bins(sh);
+      }
 #pragma unroll
       for (int q = 0; q < kAtOnce; ++q) {
         const int j = v0 + q * kThreads;
@@ -824,10 +860,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (lane == 0) sh.warp_top[wid] = top;
-  const uint64_t fine = c_fine[lane];
-  for (int i = tid; i < 1024; i += kThreads)
-    sh.table[i] = (uint32_t)min((__umul64hi(c_coarse[i >> 5], fine) + 0x80000000ull) >> 32, 0x7FFFFFFFull);
-  clear_bins(sh);
+  __syncthreads();
   top = lane < kWarps ? sh.warp_top[lane] : -INFINITY;
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -854,8 +887,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
   // ---- the order's border: the last token that top-k and top-p keep
   const bool greedy = r.temperature == 0.f;
   const Scale sc = scale_of(top, greedy ? 1.f : r.temperature);
-  const uint64_t least = (uint64_t)__double2ull_ru((double)r.min_p * (double)kOne);  // min-p's weight
-  auto target_of = [&](uint64_t sum) { return min(sum - 1, (uint64_t)((double)r.random * (double)sum)); };
+  const uint64_t least = part_of(r.min_p, kOne, true);  // min-p's weight
+  auto target_of = [&](uint64_t sum) { return min(sum - 1, part_of(r.random, sum, false)); };
   auto write = [&](int token, uint32_t n, float x, uint64_t sum) {
     p.tokens[row] = token;
     if (p.kept) p.kept[row] = (int32_t)n;
@@ -876,30 +909,29 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
   {
     const bool by_count = r.top_k > 0 && r.top_k < p.vocab, by_weight = r.top_p < 1.f;
     if (by_count || by_weight) {
-      first_histogram(sl, sc, sh, by_weight);
+      // (weights with the counts only where there is no top-k: its candidates are few, as a rule, and are weighed
+      // in their list)
+      first_histogram(sl, sc, sh, !by_count);
       cl.group.sync();
       Search se{};  // (of use in the first block)
-      // the weight that top-p of a sum of w asks for
-      auto part_of = [&](uint64_t w) {
-        return max((uint64_t)1, min(w, (uint64_t)__double2ull_ru((double)r.top_p * (double)w)));
-      };
       auto restart = [&](uint64_t whole) {  // top-p of what top-k keeps, from the first histogram on
         se.by_weight = se.first = true;
-        se.goal = part_of(whole);
+        se.goal = max((uint64_t)1, part_of(r.top_p, whole, true));
         se.n_before = 0;
         se.w_before = 0;
       };
       if (cl.rank == 0) {
-        merge(cl, sh, true);
+        merge(cl, sh, true, !by_count);
+        se.weighed = !by_count || !by_weight;
         if (tid == 0) sh.n_list = 0;
         if (by_count && (uint32_t)r.top_k < sh.first_n[kBins - 1]) {
           se.first = true;
           se.goal = (uint64_t)r.top_k;
-        } else if (by_weight) {
+        } else if (by_weight && !by_count) {
           restart(sh.first_w[kBins - 1]);
         }
         if (se.first) next_step(se, sc, sh, cl.message());
-        else if (tid == 0) *cl.message() = Message{kDone, 0, 0, 0, 0};  // all of them
+        else if (tid == 0) *cl.message() = Message{by_weight ? kWeigh : kDone, 0, 0, 0, 0};  // top-k keeps all
       }
       for (;;) {
         const Message m = cl.receive();
@@ -970,12 +1002,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
               next_step(se, sc, sh, cl.message());
             }
           }
+        } else if (m.op == kWeigh) {
+          clear_bins(sh);
+          first_histogram(sl, sc, sh, true);
+          cl.group.sync();
+          if (cl.rank == 0) {
+            merge(cl, sh, true, true);
+            se.weighed = true;
+            if (!se.first) restart(sh.first_w[kBins - 1]);
+            next_step(se, sc, sh, cl.message());
+          }
         } else if (m.op == kRefine) {
           clear_bins(sh);
           histogram(sl, sc, sh, m.lo, m.hi, max(0, 22 - __clz(m.hi - m.lo)), by_weight);
           cl.group.sync();
           if (cl.rank == 0) {
-            merge(cl, sh, false);
+            merge(cl, sh, false, by_weight);
             next_step(se, sc, sh, cl.message());
           }
         } else {
