@@ -75,24 +75,44 @@ struct QPagesWrite {
 };
 cudaError_t launch_qpages_write(const QPagesWrite& p, int dtype, int head_dim, cudaStream_t s);
 
+// Division of 0 .. 2^31 - 1 by a number that a launch knows: with 2^l the least power of two that is not below d,
+// m = ceil(2^(31 + l) / d) is below 2^32 and exceeds the quotient by less than 2^l / 2^(31 + l) of it, so the
+// product's upper part is the quotient's integer.
+struct Divisor {
+  uint32_t d, mul, shift;
+  explicit Divisor(int by = 1) : d((uint32_t)by), mul(0), shift(0) {
+    if (by <= 1) return;
+    int l = 0;
+    while ((int64_t(1) << l) < by) ++l;
+    mul = (uint32_t)(((uint64_t(1) << (31 + l)) + d - 1) / d);
+    shift = (uint32_t)(l - 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t of(uint32_t n) const { return mul ? __umulhi(n, mul) >> shift : n; }
+#endif
+};
+
 // attention of one new token per sequence (msm_paged_attn.cu)
 struct PagedAttn {
   const int32_t *table, *lens;
   int32_t* status;
   int n_seqs, max_pages, n_pages, page_rows, n_kv_heads, group, window;
-  int sinks;  // rows at the front that stay visible (0 without a window)
+  int sinks;   // rows at the front that stay visible (0 without a window)
+  int finish;  // what an item costs beside its tiles, in tiles
   const uint16_t* q;
   const void *k, *v;  // the layer's pools
   // a cache in 8 bits (else null): fp32 [n_pages][n_kv_heads][page_blocks], a scale for block_rows rows each
   const float *k_scales, *v_scales;
   int block_rows, page_blocks;
+  Divisor by_page, by_block;  // page_rows, block_rows
   uint16_t* out;
   int64_t q_seq, q_head, out_seq, out_head;  // strides in elements
   float scale_log2;                          // softmax scale x log2(e)
   uint32_t* counters;                        // workspace: three per block, zero between calls,
   float* part;                               // and partial results, two per block
 };
-constexpr int kPagedAttnPerSm = 2;  // blocks per SM
+constexpr int kPagedFinish = 1, kQPagedFinish = 4;
+constexpr int kPagedAttnPerSm = 2, kQPagedAttnPerSm = 2;  // blocks per SM (of 16 and of 8 bits)
 size_t paged_attn_workspace(int blocks, int group, int head_dim);
 cudaError_t launch_paged_attn(const PagedAttn& p, int dtype, int head_dim, int blocks, cudaStream_t s);
 

@@ -123,6 +123,9 @@ const msm_pages* base(const msm_qpages* c) { return &c->pages; }
 const msm_qpages* held8(const msm_pages*) { return nullptr; }
 const msm_qpages* held8(const msm_qpages* c) { return c; }
 
+int per_sm(const msm_pages*) { return kPagedAttnPerSm; }
+int per_sm(const msm_qpages*) { return kQPagedAttnPerSm; }
+
 int page_blocks(const msm_qpages* c) { return (c->pages.page_rows - 1) / c->block_rows + 1; }
 
 PagesMeta meta(const msm_pages* c, const int32_t* arg) {
@@ -235,7 +238,7 @@ size_t attention_workspace(const Cache* c, int n_q_heads) {
   if (check_pages(c) != MSM_OK || check_group(n_q_heads, base(c)->n_kv_heads) != MSM_OK) return 0;
   int sms = 0;
   if (device_sms(base(c)->device, &sms) != MSM_OK) return 0;
-  return paged_attn_workspace(sms * kPagedAttnPerSm, n_q_heads / base(c)->n_kv_heads, base(c)->head_dim);
+  return paged_attn_workspace(sms * per_sm(c), n_q_heads / base(c)->n_kv_heads, base(c)->head_dim);
 }
 
 template <class Cache>
@@ -260,7 +263,7 @@ msm_status attention(const Cache* cache, int layer, int dtype, const void* q, in
   REQUIRE(workspace && !misaligned(workspace, 16), MSM_ERR_INVALID_ARG, "workspace is NULL or misaligned");
   int sms = 0;
   if ((st = device_sms(c->device, &sms)) != MSM_OK) return st;
-  const int blocks = sms * kPagedAttnPerSm, group = n_q_heads / c->n_kv_heads;
+  const int blocks = sms * per_sm(cache), group = n_q_heads / c->n_kv_heads;
   REQUIRE(workspace_bytes >= paged_attn_workspace(blocks, group, c->head_dim), MSM_ERR_INVALID_ARG,
           "workspace is smaller than msm_paged_attention_workspace");
   DeviceGuard dev;
@@ -277,16 +280,19 @@ msm_status attention(const Cache* cache, int layer, int dtype, const void* q, in
   p.group = group;
   p.window = window;
   p.sinks = window > 0 ? sinks : 0;
+  p.finish = held8(cache) ? kQPagedFinish : kPagedFinish;
   p.q = static_cast<const uint16_t*>(q);
   p.k = c->k_pages[layer];
   p.v = c->v_pages[layer];
   p.k_scales = p.v_scales = nullptr;
   p.block_rows = p.page_blocks = 0;
+  p.by_page = Divisor(c->page_rows);
   if (const msm_qpages* const h = held8(cache)) {
     p.k_scales = h->k_scales[layer];
     p.v_scales = h->v_scales[layer];
     p.block_rows = h->block_rows;
     p.page_blocks = page_blocks(h);
+    p.by_block = Divisor(h->block_rows);
   }
   p.out = static_cast<uint16_t*>(out);
   p.q_seq = q_seq_stride;

@@ -91,8 +91,8 @@ __host__ __device__ constexpr int part_floats(int group, int hd) { return 2 * kH
 // tiles.  Places count them through: without sinks a place is its row, from base (lo rounded down to a
 // chunk) to hi.  With sinks in front of the window the tiles that hold them come first, from place 0,
 // and the places from `pad` on are the rows `skip` further on, from base.  (Where those tiles reach the
-// window there is nothing to skip.)  An item costs its block one unit more than its tiles: finishing it
-// takes about as long as a tile (64 sequences of 1 to 8,192 rows: 80 us without that unit, 60 us with it).
+// window there is nothing to skip.)  An item costs its block `finish` units more than its tiles, what
+// finishing it takes (64 sequences of 1 to 8,192 rows: 80 us without, 60 us with one unit).
 struct Rows {
   int lo, hi, base, tiles, units;  // hi, base: places
   int first, pad, skip;
@@ -112,7 +112,7 @@ __device__ __forceinline__ Rows seq_rows(const PagedAttn& p, int s) {
     r.base = 0;
   }
   r.tiles = (r.hi - r.base + kTile - 1) / kTile;
-  r.units = r.tiles > 0 ? r.tiles + 1 : 0;
+  r.units = r.tiles > 0 ? r.tiles + p.finish : 0;
   return r;
 }
 
@@ -128,8 +128,8 @@ struct Segment {
   __device__ __forceinline__ bool sees(int row) const { return row >= lo || row < sinks; }
 };
 
-// Walks the segments of a block's run of units [u, u1) (a whole warp together).  Unit 0 of an item
-// has no tile.
+// Walks the segments of a block's run of units [u, u1) (a whole warp together).  The first units of an
+// item, `finish` of them, have no tile.
 struct Walk {
   int64_t u, u1, before;  // before: units of the sequences in front of s
   int s;
@@ -160,7 +160,7 @@ struct Walk {
       }
       g.s = s;
       g.h = (int)((u - before) / rw.units);
-      g.unit0 = before + (int64_t)g.h * rw.units + 1;
+      g.unit0 = before + (int64_t)g.h * rw.units + p.finish;
       g.ta = max(0, (int)(u - g.unit0));
       g.tb = (int)min((int64_t)rw.tiles, u1 - g.unit0);
       g.tiles = rw.tiles;
@@ -189,7 +189,8 @@ struct Cfg {
   static constexpr int kStages = HD == 64 && kHeld8 ? 3 : 2;
   static constexpr int kOutStride = HD + 4;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-  static constexpr int kSmem = kRingBytes + kWarps * kHeads * kOutStride * 4;
+  static constexpr int kOutHeads = kHeld8 ? 4 : kHeads;  // heads whose results the warps put together at a time
+  static constexpr int kSmem = kRingBytes + kWarps * kOutHeads * kOutStride * 4;
 };
 
 // Where 16-byte piece c of row r of a chunk stands: the permutation keeps the lanes of a phase on
@@ -325,7 +326,7 @@ __device__ bool arrive_last(uint32_t* counter, int n, int* s_flag) {
 }
 
 template <class El, int HD, bool kHeld8>
-__global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(const PagedAttn p) {
+__global__ void __launch_bounds__(kThreadsA, kHeld8 ? kQPagedAttnPerSm : kPagedAttnPerSm) paged_attn_kernel(const PagedAttn p) {
   using C = Cfg<HD, kHeld8>;
   // 8-bit rows become fp16 on their way into the products (exactly), and so do q and the weights
   using Mul = typename std::conditional<kHeld8, Fp16, El>::type;
@@ -339,8 +340,8 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
   __shared__ int64_t s_find[2];  // first sequence of the block's run, units before it
   __shared__ float s_m[kWarps][kHeads], s_l[kWarps][kHeads];
   __shared__ int s_flag;
-  float (*const s_o)[kHeads][C::kOutStride] =
-      reinterpret_cast<float (*)[kHeads][C::kOutStride]>(smem + C::kRingBytes);
+  float (*const s_o)[C::kOutHeads][C::kOutStride] =
+      reinterpret_cast<float (*)[C::kOutHeads][C::kOutStride]>(smem + C::kRingBytes);
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int G = gridDim.x, b = blockIdx.x;
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
   // the page of row lane % kChunk of the next chunk
   auto look = [&]() {
     const int r = fc + lane % C::kChunk;
-    page = fc >= 0 && r < fs.end ? p.table[(size_t)fs.s * p.max_pages + fs.row(r) / p.page_rows] : -1;
+    page = fc >= 0 && r < fs.end ? p.table[(size_t)fs.s * p.max_pages + p.by_page.of(fs.row(r))] : -1;
   };
   // the next chunk of this warp, in this or a later segment
   auto find_chunk = [&]() {
@@ -445,24 +446,42 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
       }
       rows = __ballot_sync(0xffffffffu, ok);
       // pool row of row lane % kChunk
-      const uint32_t head = (uint32_t)page * p.n_kv_heads + fs.h, in_page = r % p.page_rows;
+      const uint32_t head = (uint32_t)page * p.n_kv_heads + fs.h, in_page = r - p.by_page.of(r) * p.page_rows;
       const uint32_t at = head * p.page_rows + in_page;
       if constexpr (kHeld8) {
-        const uint32_t i = head * p.page_blocks + in_page / (uint32_t)p.block_rows;
+        const uint32_t i = head * p.page_blocks + p.by_block.of(in_page);
         rs = row_scale(ok ? __ldg(p.k_scales + i) : 0.f, ok ? __ldg(p.v_scales + i) : 0.f);
       }
       const uint32_t dst = ring + f_stage * C::kStageBytes;
       constexpr int kPieces = C::kRowBytes / 16, kRowsAtOnce = 32 / kPieces;  // 16-byte pieces of a row
       const int c = lane % kPieces, sub = lane / kPieces;
+      bool run = false;  // 8 bits: are all rows there, one behind the other (in one page)?
+      if constexpr (kHeld8) {
+        const uint32_t at0 = __shfl_sync(0xffffffffu, at, 0);
+        run = __all_sync(0xffffffffu, ok && at == at0 + (uint32_t)lane);
+      }
+      if (run) {  // addresses that differ by constants (a third of the fetch's instructions)
+        const size_t off = (size_t)(at - lane) * C::kRowBytes + lane * 16;
+        const char *const k0 = static_cast<const char*>(p.k) + off, *const v0 = static_cast<const char*>(p.v) + off;
+        // (the permutation depends on the parity of i at most)
+        const uint32_t d[2] = {dst + at_piece<C::kRowBytes>(sub, c),
+                               dst + at_piece<C::kRowBytes>(kRowsAtOnce + sub, c) - 512};
 #pragma unroll
-      for (int i = 0; i < C::kChunk / kRowsAtOnce; ++i) {
-        const int row = i * kRowsAtOnce + sub;
-        const uint32_t pr = __shfl_sync(0xffffffffu, at, row);
-        const bool in = rows >> row & 1;
-        const size_t off = in ? (size_t)pr * C::kRowBytes + c * 16 : 0;
-        const uint32_t d = dst + at_piece<C::kRowBytes>(row, c);
-        cp_async16(d, static_cast<const char*>(p.k) + off, in ? 16 : 0);
-        cp_async16(d + C::kChunk * C::kRowBytes, static_cast<const char*>(p.v) + off, in ? 16 : 0);
+        for (int i = 0; i < C::kChunk / kRowsAtOnce; ++i) {
+          cp_async16(d[i & 1] + i * 512, k0 + i * 512, 16);
+          cp_async16(d[i & 1] + i * 512 + C::kChunk * C::kRowBytes, v0 + i * 512, 16);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < C::kChunk / kRowsAtOnce; ++i) {
+          const int row = i * kRowsAtOnce + sub;
+          const uint32_t pr = __shfl_sync(0xffffffffu, at, row);
+          const bool in = rows >> row & 1;
+          const size_t off = in ? (size_t)pr * C::kRowBytes + c * 16 : 0;
+          const uint32_t d = dst + at_piece<C::kRowBytes>(row, c);
+          cp_async16(d, static_cast<const char*>(p.k) + off, in ? 16 : 0);
+          cp_async16(d + C::kChunk * C::kRowBytes, static_cast<const char*>(p.v) + off, in ? 16 : 0);
+        }
       }
       f_stage = f_stage + 1 == C::kStages ? 0 : f_stage + 1;
       fc += C::kStep;
@@ -726,12 +745,16 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
       s_l[wid][2 * t] = seen ? l0 : kNoKeys;
       s_l[wid][2 * t + 1] = seen ? l1 : kNoKeys;
     }
+    auto put = [&](int h0) {  // of heads h0 .. h0 + kOutHeads - 1
+      if (C::kOutHeads < kHeads && (2 * t < h0 || 2 * t >= h0 + C::kOutHeads)) return;
 #pragma unroll
-    for (int i = 0; i < HD / 16; ++i) {
-      const int d = kHeld8 ? HD / 8 * g + 2 * i : i / 4 * 64 + 8 * g + 2 * (i % 4);
-      *reinterpret_cast<float2*>(&s_o[wid][2 * t][d]) = make_float2(o[i][0], o[i][2]);
-      *reinterpret_cast<float2*>(&s_o[wid][2 * t + 1][d]) = make_float2(o[i][1], o[i][3]);
-    }
+      for (int i = 0; i < HD / 16; ++i) {
+        const int d = kHeld8 ? HD / 8 * g + 2 * i : i / 4 * 64 + 8 * g + 2 * (i % 4);
+        *reinterpret_cast<float2*>(&s_o[wid][2 * t - h0][d]) = make_float2(o[i][0], o[i][2]);
+        *reinterpret_cast<float2*>(&s_o[wid][2 * t - h0 + 1][d]) = make_float2(o[i][1], o[i][3]);
+      }
+    };
+    put(0);
     const Segment done = sg;
     more = walk.next(p, sg);
     if (more) load_q();
@@ -740,31 +763,38 @@ __global__ void __launch_bounds__(kThreadsA, kPagedAttnPerSm) paged_attn_kernel(
     // a run's first item that began before it goes to the block's slot 0, the last one that
     // goes on behind it to slot 1
     float* const part = p.part + (size_t)(2 * b + (done.ta > 0 ? 0 : 1)) * part_len;
-    for (int i = tid; i < p.group * HD / 2; i += kThreadsA) {
-      const int hd = i / (HD / 2), d = (i - hd * (HD / 2)) * 2;
-      float m = -INFINITY;
-#pragma unroll
-      for (int q = 0; q < kWarps; ++q) m = fmaxf(m, s_m[q][hd]);
-      const float ref = m == -INFINITY ? 0.f : m;
-      float l = kNoKeys, x = 0.f, y = 0.f;
-#pragma unroll
-      for (int q = 0; q < kWarps; ++q) {
-        // (a NaN sum passes on; a warp without rows has m = -inf and zeros)
-        const float f = exp2_fast(s_m[q][hd] - ref);
-        const float2 v = *reinterpret_cast<const float2*>(&s_o[q][hd][d]);
-        l += f * s_l[q][hd];
-        x += f * v.x;
-        y += f * v.y;
+    for (int h0 = 0; h0 < p.group; h0 += C::kOutHeads) {
+      if (h0 > 0) {
+        __syncthreads();
+        put(h0);
+        __syncthreads();
       }
-      if (whole) {
-        const float inv = inverse_sum(l);
-        *reinterpret_cast<uint32_t*>(p.out + done.s * p.out_seq + (done.h * p.group + hd) * p.out_head + d) =
-            El::pack(x * inv, y * inv);
-      } else {
-        *reinterpret_cast<float2*>(part + 2 * kHeads + hd * HD + d) = make_float2(x, y);
-        if (d == 0) {
-          part[hd] = m;
-          part[kHeads + hd] = l;
+      for (int i = tid; i < min(p.group - h0, C::kOutHeads) * HD / 2; i += kThreadsA) {
+        const int hd = h0 + i / (HD / 2), d = i % (HD / 2) * 2;
+        float m = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q) m = fmaxf(m, s_m[q][hd]);
+        const float ref = m == -INFINITY ? 0.f : m;
+        float l = kNoKeys, x = 0.f, y = 0.f;
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q) {
+          // (a NaN sum passes on; a warp without rows has m = -inf and zeros)
+          const float f = exp2_fast(s_m[q][hd] - ref);
+          const float2 v = *reinterpret_cast<const float2*>(&s_o[q][hd - h0][d]);
+          l += f * s_l[q][hd];
+          x += f * v.x;
+          y += f * v.y;
+        }
+        if (whole) {
+          const float inv = inverse_sum(l);
+          *reinterpret_cast<uint32_t*>(p.out + done.s * p.out_seq + (done.h * p.group + hd) * p.out_head + d) =
+              El::pack(x * inv, y * inv);
+        } else {
+          *reinterpret_cast<float2*>(part + 2 * kHeads + hd * HD + d) = make_float2(x, y);
+          if (d == 0) {
+            part[hd] = m;
+            part[kHeads + hd] = l;
+          }
         }
       }
     }
