@@ -62,19 +62,6 @@ struct PagesWrite {
   const int32_t* starts;
 };
 
-// new rows of a cache in 8 bits (msm_qpages.cu)
-struct QPagesWrite {
-  PagesMeta m;
-  int n_kv_heads, n_tokens, block_rows, page_blocks;
-  int group;  // tokens that one unit of threads looks at
-  uint8_t *pool_k, *pool_v;
-  float *k_scales, *v_scales;
-  const uint16_t *k, *v;
-  int64_t k_token, k_head, v_token, v_head;  // strides in elements
-  const int32_t* starts;
-};
-cudaError_t launch_qpages_write(const QPagesWrite& p, int dtype, int head_dim, cudaStream_t s);
-
 // Division of 0 .. 2^31 - 1 by a number that a launch knows: with 2^l the least power of two that is not below d,
 // m = ceil(2^(31 + l) / d) is below 2^32 and exceeds the quotient by less than 2^l / 2^(31 + l) of it, so the
 // product's upper part is the quotient's integer.
@@ -91,6 +78,20 @@ struct Divisor {
   __device__ __forceinline__ uint32_t of(uint32_t n) const { return mul ? __umulhi(n, mul) >> shift : n; }
 #endif
 };
+
+// new rows of a cache in 8 bits (msm_qpages.cu)
+struct QPagesWrite {
+  PagesMeta m;
+  int n_kv_heads, n_tokens, block_rows, page_blocks;
+  int group;  // tokens that one unit of threads looks at
+  Divisor by_page, by_block;  // page_rows, block_rows
+  uint8_t *pool_k, *pool_v;
+  float *k_scales, *v_scales;
+  const uint16_t *k, *v;
+  int64_t k_token, k_head, v_token, v_head;  // strides in elements
+  const int32_t* starts;
+};
+cudaError_t launch_qpages_write(const QPagesWrite& p, int dtype, int head_dim, cudaStream_t s);
 
 // attention of one new token per sequence (msm_paged_attn.cu)
 struct PagedAttn {

@@ -411,6 +411,8 @@ msm_status msm_qpages_write(const msm_qpages* c, int layer, int dtype, const voi
   p.page_blocks = page_blocks(c);
   // a sequence's tokens in groups of a block's; a step's few tokens one by one
   p.group = std::max(1, std::min(c->block_rows, n_tokens / c->pages.n_seqs));
+  p.by_page = Divisor(c->pages.page_rows);
+  p.by_block = Divisor(c->block_rows);
   p.pool_k = static_cast<uint8_t*>(c->pages.k_pages[layer]);
   p.pool_v = static_cast<uint8_t*>(c->pages.v_pages[layer]);
   p.k_scales = c->k_scales[layer];

@@ -21,8 +21,6 @@ namespace msm {
 namespace {
 
 constexpr int kHeld = 8;      // 16-byte vectors in registers per lane
-constexpr int kManyWarps = 8;
-constexpr int kFewThreads = 128;
 
 // two fp32 values as e4m3, to nearest even, infinities to the largest value
 __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
@@ -41,6 +39,20 @@ __device__ __forceinline__ void unpack_e4m3(uint32_t x, float (&f)[4]) {
   f[1] = Fp16::value((uint16_t)(lo >> 16));
   f[2] = Fp16::value((uint16_t)hi);
   f[3] = Fp16::value((uint16_t)(hi >> 16));
+}
+
+// four 16-bit elements times s
+template <class El>
+__device__ __forceinline__ uint32_t scaled_e4m3(uint32_t x, uint32_t y, float s) {
+  float a, b, c, d;
+  if constexpr (El::kBf16) {
+    a = __uint_as_float(x << 16), b = __uint_as_float(x & 0xFFFF0000u);
+    c = __uint_as_float(y << 16), d = __uint_as_float(y & 0xFFFF0000u);
+  } else {
+    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&x)), q = __half22float2(*reinterpret_cast<const __half2*>(&y));
+    a = p.x, b = p.y, c = q.x, d = q.y;
+  }
+  return pack_e4m3(a * s, b * s, c * s, d * s);
 }
 
 // the least power of two that amax / 448 does not exceed, at least 2^-126; 0 for 0
@@ -67,21 +79,28 @@ __device__ __forceinline__ uint32_t finite2(uint32_t x) {
   return x;
 }
 
-// kWarps warps work on a unit together; a block holds one such unit, or four of a warp
-template <class El, int HD, int kWarps>
-__global__ void __launch_bounds__(kWarps == 1 ? kFewThreads : kWarps * 32) qwrite_kernel(const QPagesWrite p) {
-  constexpr int kVecs = HD / 8;             // 16-byte vectors of a new row
+// blockIdx.x: the group of tokens; blockIdx.y: the head, which kWarps = 4 or 8 warps take together, or four heads of
+// a warp each.  kLong: a block of rows may have more new rows than registers hold (the code for them costs the others
+// registers: 50,000 tokens into blocks of 16 rows 56 us without it, 79 with it).
+constexpr int threads(int warps) { return warps == 1 ? 128 : 32 * warps; }
+template <class El, int HD, int kWarps, bool kLong>
+__global__ void __launch_bounds__(threads(kWarps), 512 / threads(kWarps))
+    qwrite_kernel(const QPagesWrite p) {
+  constexpr int kVecs = HD / 8;               // 16-byte vectors of a new row
   constexpr int kRows = 32 / kVecs * kWarps;  // new rows of one step
-  constexpr int kUnits = kWarps == 1 ? kFewThreads / 32 : 1;
+  constexpr int kIn = kHeld * kRows;          // and of those that registers hold (more are read twice, kMore steps
+  constexpr int kMore = 2;                    // at a time)
   __shared__ uint32_t s_max[2][kWarps];
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int w = kWarps == 1 ? 0 : wid;
   const int c = lane % kVecs, sub = w * (32 / kVecs) + lane / kVecs;
-  const int limit = min(p.n_tokens, max(p.starts[p.m.n_seqs], 0));
-  const int groups = (limit - 1) / p.group + 1;
-  if (limit == 0) return;
-  const bool stop = stopped(p.m.status);
-  if (stop) return;
+  // (up to 31 sequences: all of their starts and lengths at once, one wait instead of four in a row)
+  const bool few = p.m.n_seqs < 32;
+  const int my_start = few ? p.starts[min(lane, p.m.n_seqs)] : 0, my_len = few ? p.m.lens[min(lane, p.m.n_seqs - 1)] : 0;
+  const int limit = min(p.n_tokens, max(few ? __shfl_sync(0xffffffffu, my_start, p.m.n_seqs) : p.starts[p.m.n_seqs], 0));
+  const int64_t t_first = (int64_t)blockIdx.x * p.group;
+  const int head = kWarps == 1 ? (int)blockIdx.y * 4 + wid : (int)blockIdx.y;
+  if (t_first >= limit || head >= p.n_kv_heads || stopped(p.m.status)) return;
   const int64_t cap = (int64_t)p.m.max_pages * p.m.page_rows;
   int flip = 0;
   // the largest of all the unit's lanes' elements (two in each)
@@ -97,80 +116,79 @@ __global__ void __launch_bounds__(kWarps == 1 ? kFewThreads : kWarps * 32) qwrit
     }
     return m;
   };
-  for (int64_t unit = (int64_t)blockIdx.x * kUnits + (kWarps == 1 ? wid : 0); unit < (int64_t)groups * 2 * p.n_kv_heads;
-       unit += (int64_t)gridDim.x * kUnits) {
-    const int head = (int)(unit % p.n_kv_heads), is_v = (int)(unit / p.n_kv_heads & 1);
-    const int64_t t_first = unit / p.n_kv_heads / 2 * p.group;
-    const int t_end = (int)min((int64_t)limit, t_first + p.group);
-    const uint16_t* const src = (is_v ? p.v : p.k) + head * (is_v ? p.v_head : p.k_head);
-    const int64_t token = is_v ? p.v_token : p.k_token;
-    uint8_t* const pool = is_v ? p.pool_v : p.pool_k;
-    float* const scales = is_v ? p.v_scales : p.k_scales;
-    auto load = [&](int t) { return __ldcs(reinterpret_cast<const uint4*>(src + t * token) + c); };
-    for (int t = (int)t_first; t < t_end;) {
-      // most units: the rows of one block, from the group's first token on (their loads do not wait for the search)
-      uint4 x[kHeld];
-      const int t_loaded = t;
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        const int r = i * kRows + sub;
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < p.group && r < limit - t) x[i] = load(t + r);
-      }
-      // the last sequence that starts at or before the token, 32 probes at a time
-      int lo = 0, hi = p.m.n_seqs;
-      while (hi - lo > 1) {
+  const int t_end = (int)min((int64_t)limit, t_first + p.group);
+  for (int t = (int)t_first; t < t_end;) {
+    // the last sequence that starts at or before the token, 32 probes at a time
+    int lo = 0, first, end, len;
+    if (few) {
+      const uint32_t le = __ballot_sync(0xffffffffu, lane < p.m.n_seqs && my_start <= t);
+      lo = le ? 31 - __clz(le) : 0;
+      first = __shfl_sync(0xffffffffu, my_start, lo);
+      end = __shfl_sync(0xffffffffu, my_start, lo + 1);
+      len = __shfl_sync(0xffffffffu, my_len, lo);
+    } else {
+      for (int hi = p.m.n_seqs; hi - lo > 1;) {
         const int step = (hi - lo + 31) / 32, i = lo + lane * step;
         const uint32_t le = __ballot_sync(0xffffffffu, i < hi && p.starts[i] <= t);
         lo += le ? (31 - __clz(le)) * step : 0;
         hi = min(hi, lo + step);
       }
-      const int first = p.starts[lo], end = p.starts[lo + 1];
-      bool bad = t < first || t >= end;
-      const int64_t pos = (int64_t)p.m.lens[lo] - end + t;
-      int next = bad ? t + 1 : min(end, limit);
-      if (!bad && pos < 0) {  // tokens in front of the sequence's first row
-        bad = true;
-        next = (int)min((int64_t)next, t - pos);
-      }
-      bad |= pos >= cap;
-      if (bad) {
-        if (lane == 0 && w == 0) latch(p.m.status, MSM_ERR_INVALID_ARG, kCallWrite);
-        t = next;
-        continue;
-      }
-      // the block of rows that holds the token's, and how many of the tokens go there
-      const int in_page = (int)pos % p.m.page_rows, block = in_page / p.block_rows, row0 = block * p.block_rows;
-      const int older = in_page - row0, left = min(p.block_rows - older, p.m.page_rows - in_page);
-      const int n = min(left, next - t);
-      if (older > 0 && t != first) {  // another unit's, which has the block's first new row
-        t += n;
-        continue;
-      }
-      const int pg = p.m.table[(size_t)lo * p.m.max_pages + (int)pos / p.m.page_rows];
-      if (pg < 0 || pg >= p.m.n_pages || p.m.refs[pg] != 1) {
-        if (lane == 0 && w == 0) latch(p.m.status, MSM_ERR_INVALID_ARG, kCallWrite);
-        t += n;
-        continue;
-      }
-      const int64_t at = (int64_t)pg * p.n_kv_heads + head;
-      float* const scale = scales + at * p.page_blocks + block;
-      uint8_t* const rows = pool + (at * p.m.page_rows + row0) * HD;
-      const float old = older > 0 ? *scale : 0.f;
-
-      // what is held in registers begins at t_loaded = t (a group begins, or the loop came around)
-      auto step_of = [&](int i0, uint4 (&y)[kHeld]) {
+      first = p.starts[lo];
+      end = p.starts[lo + 1];
+      len = p.m.lens[lo];
+    }
+    bool bad = t < first || t >= end;
+    const int64_t pos = (int64_t)len - end + t;
+    int next = bad ? t + 1 : min(end, limit);
+    if (!bad && pos < 0) {  // tokens in front of the sequence's first row
+      bad = true;
+      next = (int)min((int64_t)next, t - pos);
+    }
+    bad |= pos >= cap;
+    if (bad) {
+      if (lane == 0 && w == 0) latch(p.m.status, MSM_ERR_INVALID_ARG, kCallWrite);
+      t = next;
+      continue;
+    }
+    // the block of rows that holds the token's, and how many of the tokens go there
+    const int page = (int)p.by_page.of((uint32_t)pos), in_page = (int)pos - page * p.m.page_rows;
+    const int block = (int)p.by_block.of((uint32_t)in_page), row0 = block * p.block_rows;
+    const int older = in_page - row0, left = min(p.block_rows - older, p.m.page_rows - in_page);
+    const int n = min(left, next - t);
+    if (older > 0 && t != first) {  // another unit's, which has the block's first new row
+      t += n;
+      continue;
+    }
+    // rows i0 + i kRows + sub of K or V (what is behind the n-th stays as it was)
+    auto load = [&](bool is_v, int i0, auto& y) {
+      const int64_t token = is_v ? p.v_token : p.k_token;
+      const uint16_t* const from = (is_v ? p.v + head * p.v_head : p.k + head * p.k_head) + (t + i0 + sub) * token + c * 8;
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-          const int r = i0 + i * kRows + sub;
-          y[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < n) y[i] = load(t_loaded + r);
-        }
-      };
+      for (int i = 0; i < (int)(sizeof(y) / sizeof(y[0])); ++i)
+        if (i0 + i * kRows + sub < n) y[i] = __ldcs(reinterpret_cast<const uint4*>(from + i * kRows * token));
+    };
+    uint4 x[2][kHeld];  // K, V (these travel while the page is looked up)
+#pragma unroll
+    for (int side = 0; side < 2; ++side) load(side != 0, 0, x[side]);
+    const int pg = p.m.table[(size_t)lo * p.m.max_pages + page];
+    if (pg < 0 || pg >= p.m.n_pages || p.m.refs[pg] != 1) {
+      if (lane == 0 && w == 0) latch(p.m.status, MSM_ERR_INVALID_ARG, kCallWrite);
+      t += n;
+      continue;
+    }
+    const int64_t at = (int64_t)pg * p.n_kv_heads + head;
+    float old[2];
+#pragma unroll
+    for (int side = 0; side < 2; ++side)
+      old[side] = older > 0 ? (side ? p.v_scales : p.k_scales)[at * p.page_blocks + block] : 0.f;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      const bool is_v = side != 0;
+      uint8_t* const rows = (is_v ? p.pool_v : p.pool_k) + (at * p.m.page_rows + row0) * HD;
       uint32_t most = 0;
-      auto add = [&](const uint4 (&y)[kHeld], int i0, bool finite) {
+      auto add = [&](const auto& y, int i0, bool finite) {
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i)
+        for (int i = 0; i < (int)(sizeof(y) / sizeof(y[0])); ++i)
           if (i0 + i * kRows + sub < n) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -179,30 +197,28 @@ __global__ void __launch_bounds__(kWarps == 1 ? kFewThreads : kWarps * 32) qwrit
             }
           }
       };
-      // (rows behind the group's end belong to it as well)
-      constexpr int kIn = kHeld * kRows;
-      if (n > p.group) step_of(0, x);
-      add(x, 0, false);
-      for (int i0 = kIn; i0 < n; i0 += kIn) {
-        uint4 y[kHeld];
-        step_of(i0, y);
-        add(y, i0, false);
-      }
+      auto add_all = [&](bool finite) {
+        add(x[side], 0, finite);
+        if constexpr (kLong) {
+#pragma unroll 1
+          for (int i0 = kIn; i0 < n; i0 += kMore * kRows) {
+            uint4 y[kMore];
+            load(is_v, i0, y);
+            add(y, i0, finite);
+          }
+        }
+      };
+      add_all(false);
       uint32_t top = largest(most);
       if (top >= El::kExponent) {  // an infinite element: the largest finite one decides
         most = 0;
-        add(x, 0, true);
-        for (int i0 = kIn; i0 < n; i0 += kIn) {
-          uint4 y[kHeld];
-          step_of(i0, y);
-          add(y, i0, true);
-        }
+        add_all(true);
         top = largest(most);
       }
-      const float now = fmaxf(old, scale_for(El::value((uint16_t)top)));
-      if (now != old) {
+      const float now = fmaxf(old[side], scale_for(El::value((uint16_t)top)));
+      if (now != old[side]) {
         // the older rows on the new scale
-        const float ratio = old / now;
+        const float ratio = old[side] / now;
         constexpr int kOld = HD / 16, kOldRows = 32 / kOld * kWarps;  // 16-byte vectors of a row, rows of one step
         for (int r0 = 0; r0 < older; r0 += 4 * kOldRows) {
           uint4 y[4];
@@ -227,46 +243,48 @@ __global__ void __launch_bounds__(kWarps == 1 ? kFewThreads : kWarps * 32) qwrit
         }
       }
       const float inverse = now > 0.f ? 1.f / now : 0.f;
-      auto store = [&](const uint4 (&y)[kHeld], int i0) {
+      auto store = [&](const auto& y, int i0) {
+        uint8_t* const to = rows + (int64_t)(older + i0 + sub) * HD + c * 8;
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-          const int r = i0 + i * kRows + sub;
-          if (r < n) {
-            float f[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) f[q] = El::value((uint16_t)((&y[i].x)[q >> 1] >> (16 * (q & 1)))) * inverse;
+        for (int i = 0; i < (int)(sizeof(y) / sizeof(y[0])); ++i)
+          if (i0 + i * kRows + sub < n) {
             uint2 o;
-            o.x = pack_e4m3(f[0], f[1], f[2], f[3]);
-            o.y = pack_e4m3(f[4], f[5], f[6], f[7]);
-            reinterpret_cast<uint2*>(rows + (int64_t)(older + r) * HD)[c] = o;
+            o.x = scaled_e4m3<El>(y[i].x, y[i].y, inverse);
+            o.y = scaled_e4m3<El>(y[i].z, y[i].w, inverse);
+            *reinterpret_cast<uint2*>(to + i * kRows * HD) = o;
           }
-        }
       };
-      store(x, 0);
-      for (int i0 = kIn; i0 < n; i0 += kIn) {
-        uint4 y[kHeld];
-        step_of(i0, y);
-        store(y, i0);
+      store(x[side], 0);
+      if constexpr (kLong) {
+#pragma unroll 1
+        for (int i0 = kIn; i0 < n; i0 += kMore * kRows) {
+          uint4 y[kMore];
+          load(is_v, i0, y);
+          store(y, i0);
+        }
       }
       // (every thread has read the old one: there was a barrier since)
-      if (lane == 0 && w == 0) *scale = now;
-      t += n;
+      if (lane == 0 && w == 0) (is_v ? p.v_scales : p.k_scales)[at * p.page_blocks + block] = now;
     }
+    t += n;
   }
 }
 
+template <class El, int HD, int kWarps>
+cudaError_t launch_of(const QPagesWrite& p, cudaStream_t s) {
+  const dim3 grid((unsigned)((p.n_tokens - 1) / p.group + 1), kWarps == 1 ? (p.n_kv_heads - 1) / 4 + 1 : p.n_kv_heads);
+  if (p.block_rows > kHeld * (32 / (HD / 8)) * kWarps)
+    qwrite_kernel<El, HD, kWarps, true><<<grid, threads(kWarps), 0, s>>>(p);
+  else
+    qwrite_kernel<El, HD, kWarps, false><<<grid, threads(kWarps), 0, s>>>(p);
+  return cudaGetLastError();
+}
 template <class El, int HD>
 cudaError_t launch(const QPagesWrite& p, cudaStream_t s) {
-  const int64_t units = ((int64_t)(p.n_tokens - 1) / p.group + 1) * 2 * p.n_kv_heads;
-  const int64_t most = 1 << 30;
-  // Eight warps where a block of rows is more than a warp holds in registers: also a step's few tokens may have
-  // to multiply all of its older rows.
-  if (p.block_rows > kHeld * (32 / (HD / 8)))
-    qwrite_kernel<El, HD, kManyWarps><<<(unsigned)(units < most ? units : most), kManyWarps * 32, 0, s>>>(p);
-  else
-    qwrite_kernel<El, HD, 1><<<(unsigned)((units - 1) / (kFewThreads / 32) + 1 < most ? (units - 1) / (kFewThreads / 32) + 1 : most),
-                               kFewThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  // as many warps as the tokens that come together to a block of rows keep busy
+  constexpr int kWarpRows = kHeld * (32 / (HD / 8));
+  if (p.group <= kWarpRows) return launch_of<El, HD, 1>(p, s);
+  return p.group <= 4 * kWarpRows ? launch_of<El, HD, 4>(p, s) : launch_of<El, HD, 8>(p, s);
 }
 }  // namespace
 
