@@ -206,6 +206,13 @@ __device__ __forceinline__ uint64_t weight_of(const Scale& s, const uint32_t* ta
 __device__ __forceinline__ int log2_below(const Scale& s, float x) {
   return __float_as_int(__fadd_rn(__fmul_rn(s.max - x, s.hi), kRound)) - kRoundBits;
 }
+__device__ __forceinline__ void log2_below(const Scale& s, float2 x, int& i0, int& i1) {
+  const uint64_t d = fma2(pair(x.x, x.y), pair(-1.f, -1.f), pair(s.max, s.max));
+  float y0, y1;
+  unpair(add2(mul2(d, pair(s.hi, s.hi)), pair(kRound, kRound)), y0, y1);
+  i0 = __float_as_int(y0) - kRoundBits;
+  i1 = __float_as_int(y1) - kRoundBits;
+}
 // class of the first histogram; rises as the logit falls
 __device__ __forceinline__ int bin_of(int i) { return min(i >> 4, kBins - 1); }
 __device__ __forceinline__ int bin_of(const Scale& s, float x) { return bin_of(log2_below(s, x)); }
@@ -277,7 +284,8 @@ struct Pair<float> {
   using Bits = uint2;
 };
 
-template <class T>
+// kAll: all of the slice is in shared memory.
+template <class T, bool kAll>
 struct Slice {
   using Bits = typename Pair<T>::Bits;
   const T* x;        // the slice in the row
@@ -287,7 +295,7 @@ struct Slice {
   int held;          // so many of the pairs are in shared memory
   bool infinite;     // the row has an infinite logit: such read as 0, all others as -inf
   __device__ __forceinline__ float2 operator()(int i) const {
-    if (i < held) return floats(room[i], x);
+    if (kAll || i < held) return floats(room[i], x);
     return make_float2(far(2 * i - skew), far(2 * i + 1 - skew));
   }
   __device__ float far(int e) const {
@@ -336,8 +344,8 @@ struct Cluster {
 };
 
 // Calls f(i, pair) for this thread's pairs of the slice, kAtOnce of them at a time; whole warps together.
-template <int kAtOnce, class T, class F>
-__device__ __forceinline__ void each_pair(const Slice<T>& sl, F f) {
+template <int kAtOnce, class T, bool kAll, class F>
+__device__ __forceinline__ void each_pair(const Slice<T, kAll>& sl, F f) {
   for (int i0 = threadIdx.x & ~31; i0 < sl.pairs; i0 += kThreads * kAtOnce) {
     float2 x[kAtOnce];
 #pragma unroll
@@ -349,30 +357,31 @@ __device__ __forceinline__ void each_pair(const Slice<T>& sl, F f) {
   }
 }
 
-// Adds to a class (all lanes; lanes without `in` add nothing).
-__device__ __forceinline__ void add_to_bin(Shared& sh, bool in, int b, uint64_t w, bool weights) {
-  if (in) {
-    atomicAdd(&sh.bins.n[b], 1u);
-    if (weights) {
-      const uint32_t was = atomicAdd(&sh.bins.lo[b], (uint32_t)w), up = (uint32_t)(w >> 32) + (was + (uint32_t)w < was);
-      if (up) atomicAdd(&sh.bins.hi[b], up);
-    }
+// Adds to a class (lanes without `in` add nothing).
+template <bool kWeights>
+__device__ __forceinline__ void add_to_bin(Shared& sh, bool in, int b, uint64_t w) {
+  if (!in) return;
+  atomicAdd(&sh.bins.n[b], 1u);
+  if (kWeights) {
+    const uint32_t was = atomicAdd(&sh.bins.lo[b], (uint32_t)w), up = (uint32_t)(w >> 32) + (was + (uint32_t)w < was);
+    if (up) atomicAdd(&sh.bins.hi[b], up);
   }
 }
-// The same where a whole warp's elements may be in one class and would queue up.
-__device__ __forceinline__ void add_to_one_bin(Shared& sh, bool in, int b, uint64_t w, bool weights) {
+// The same (all lanes) where a whole warp's elements may be in one class and would queue up.
+template <bool kWeights>
+__device__ __forceinline__ void add_to_one_bin(Shared& sh, bool in, int b, uint64_t w) {
   const uint32_t lanes = __ballot_sync(0xffffffffu, in);
   if (!lanes) return;
   const int b0 = __shfl_sync(0xffffffffu, b, __ffs(lanes) - 1);
   if (__all_sync(0xffffffffu, !in || b == b0)) {
-    const uint64_t sum = weights ? warp_sum_few(in ? w : 0ull) : 0ull;
+    const uint64_t sum = kWeights ? warp_sum_few(in ? w : 0ull) : 0ull;
     if ((threadIdx.x & 31) == 0) {
       atomicAdd(&sh.bins.n[b0], __popc(lanes));
       const uint32_t was = atomicAdd(&sh.bins.lo[b0], (uint32_t)sum);
       atomicAdd(&sh.bins.hi[b0], (uint32_t)(sum >> 32) + (was + (uint32_t)sum < was));
     }
   } else {
-    add_to_bin(sh, in, b, w, weights);
+    add_to_bin<kWeights>(sh, in, b, w);
   }
 }
 __device__ __forceinline__ void clear_bins(Shared& sh) {
@@ -381,44 +390,45 @@ __device__ __forceinline__ void clear_bins(Shared& sh) {
 }
 
 // The first histogram of the slice.  Its last class, most of the logits, is summed up in registers.
-template <class T>
-__device__ void first_histogram(const Slice<T>& sl, const Scale& sc, Shared& sh, bool weights) {
+template <bool kWeights, class T, bool kAll>
+__device__ void first_histogram(const Slice<T, kAll>& sl, const Scale& sc, Shared& sh) {
   constexpr int kAtOnce = 2;
   uint64_t tail_w = 0;
   uint32_t tail_n = 0;
   bool look = true, queue = false;  // a row of logits that lie close (or a high temperature): whole warps in one class
   each_pair<kAtOnce>(sl, [&](int, const float2 (&x)[kAtOnce]) {
-    uint64_t w[kAtOnce][2];
-    int b[kAtOnce][2];
+    uint64_t w[2 * kAtOnce];
+    int b[2 * kAtOnce];
 #pragma unroll
     for (int q = 0; q < kAtOnce; ++q) {
       int i0, i1;
-      if (weights) {
-        weights_of(sc, sh.table, x[q].x, x[q].y, w[q][0], w[q][1], i0, i1);
+      if (kWeights) {
+        weights_of(sc, sh.table, x[q].x, x[q].y, w[2 * q], w[2 * q + 1], i0, i1);
       } else {
-        w[q][0] = w[q][1] = 0;
-        i0 = log2_below(sc, x[q].x);
-        i1 = log2_below(sc, x[q].y);
+        w[2 * q] = w[2 * q + 1] = 0;
+        log2_below(sc, x[q], i0, i1);
       }
-      b[q][0] = bin_of(i0);
-      b[q][1] = bin_of(i1);
+      b[2 * q] = bin_of(i0);
+      b[2 * q + 1] = bin_of(i1);
     }
     if (look) {  // at the warp's first ones
-      queue = __all_sync(0xffffffffu, b[0][0] == __shfl_sync(0xffffffffu, b[0][0], 0));
+      const int b0 = __shfl_sync(0xffffffffu, b[0], 0);
+      queue = __all_sync(0xffffffffu, b[0] == b0);
       look = false;
     }
 #pragma unroll
-    for (int q = 0; q < kAtOnce; ++q)
+    for (int e = 0; e < 2 * kAtOnce; ++e) {
+      const bool tail = b[e] == kBins - 1;
+      tail_n += tail && drawable(e & 1 ? x[e / 2].y : x[e / 2].x);
+      if (kWeights) tail_w += tail ? w[e] : 0;
+    }
+    if (queue) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const bool in = b[q][e] < kBins - 1;
-        if (!in && drawable(e ? x[q].y : x[q].x)) {
-          ++tail_n;
-          tail_w += w[q][e];
-        }
-        if (queue) add_to_one_bin(sh, in, b[q][e], w[q][e], weights);
-        else add_to_bin(sh, in, b[q][e], w[q][e], weights);
-      }
+      for (int e = 0; e < 2 * kAtOnce; ++e) add_to_one_bin<kWeights>(sh, b[e] < kBins - 1, b[e], w[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2 * kAtOnce; ++e) add_to_bin<kWeights>(sh, b[e] < kBins - 1, b[e], w[e]);
+    }
   });
   block_scan(tail_n, tail_w, sh);
   if (threadIdx.x == kThreads - 1) {
@@ -429,8 +439,8 @@ __device__ void first_histogram(const Slice<T>& sl, const Scale& sc, Shared& sh,
 }
 
 // A later one, over the keys lo .. hi, in classes of 2^shift keys from hi down.
-template <class T>
-__device__ void histogram(const Slice<T>& sl, const Scale& sc, Shared& sh, uint32_t lo, uint32_t hi, int shift, bool weights) {
+template <class T, bool kAll>
+__device__ void histogram(const Slice<T, kAll>& sl, const Scale& sc, Shared& sh, uint32_t lo, uint32_t hi, int shift, bool weights) {
   each_pair<1>(sl, [&](int, const float2 (&x)[1]) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -439,7 +449,7 @@ __device__ void histogram(const Slice<T>& sl, const Scale& sc, Shared& sh, uint3
       const bool in = drawable(v) && k >= lo && k <= hi;
       if (!__any_sync(0xffffffffu, in)) continue;
       const uint64_t w = weights ? weight_of(sc, sh.table, v) : 0;
-      add_to_one_bin(sh, in, in ? (int)((hi - k) >> shift) : 0, w, weights);
+      add_to_one_bin<true>(sh, in, in ? (int)((hi - k) >> shift) : 0, w);
     }
   });
 }
@@ -621,17 +631,23 @@ __device__ void sort_list(const Scale& sc, Shared& sh, int n) {
   __syncthreads();
 }
 
-// Sums of a slice by segment in the order of the index: in(x, index) says whether a logit counts, weigh(x, w) gives
-// two logits' weights and how many of them count after all.  Few of a row's logits do, as a rule: each lane first
-// marks those of its pairs, then weighs them two at a time.  Afterwards `find` gives the index with which the sum over
-// the row exceeds `target`.
-constexpr int kStep = 4;  // pairs of a lane at a time
-template <class T>
-__device__ __forceinline__ int segment_pairs(const Slice<T>& sl) {
+// Sums of a slice by segment in the order of the index.  Of the logits from `last` up (of those that equal it the ones up
+// to an index) weigh(x, w) gives two logits' weights and how many of them count after all.  Few of a row's logits do,
+// as a rule: each lane first marks those of its pairs, then weighs them two at a time.  Afterwards `find` gives the
+// index with which the sum over the row exceeds `target`.
+struct Border {
+  float last;
+  int last_index;
+  __device__ __forceinline__ bool in(float x, int index) const { return x > last || (x == last && index <= last_index); }
+};
+constexpr int kStep = 16;  // pairs of a lane at a time, a bit for each logit
+template <class T, bool kAll>
+__device__ __forceinline__ int segment_pairs(const Slice<T, kAll>& sl) {
   return ((sl.pairs + kSegs - 1) / kSegs + 32 * kStep - 1) / (32 * kStep) * (32 * kStep);
 }
-template <class T, class In, class Weigh>
-__device__ Share segments(const Slice<T>& sl, Shared& sh, Cluster& cl, Share& before, In in, Weigh weigh) {
+template <class T, bool kAll, class Weigh>
+__device__ Share segments(const Slice<T, kAll>& sl, Shared& sh, Cluster& cl, Share& before, const Border& border,
+                          Weigh weigh) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int len = segment_pairs(sl);
   for (int s = wid; s < kSegs; s += kWarps) {
@@ -640,11 +656,24 @@ __device__ Share segments(const Slice<T>& sl, Shared& sh, Cluster& cl, Share& be
     const int end = min(sl.pairs, (s + 1) * len);
     for (int i0 = s * len; i0 < end; i0 += 32 * kStep) {
       uint32_t marks = 0;
+      // (the equals are all in or all out but in one step of a row)
+      const int i_first = sl.index(i0), i_last = sl.index(i0 + 32 * kStep);
+      if (i_last <= border.last_index || i_first > border.last_index) {
+        const bool equals = i_last <= border.last_index;
 #pragma unroll
-      for (int q = 0; q < kStep; ++q) {
-        const int i = i0 + 32 * q + lane;
-        const float2 x = i < end ? sl(i) : make_float2(-INFINITY, -INFINITY);
-        marks |= (uint32_t)in(x.x, sl.index(i)) << (2 * q) | (uint32_t)in(x.y, sl.index(i) + 1) << (2 * q + 1);
+        for (int q = 0; q < kStep; ++q) {
+          const int i = i0 + 32 * q + lane;
+          const float2 x = i < end ? sl(i) : make_float2(-INFINITY, -INFINITY);
+          const bool a = x.x > border.last || (equals && x.x == border.last), c = x.y > border.last || (equals && x.y == border.last);
+          marks |= (a ? 1u << (2 * q) : 0u) | (c ? 2u << (2 * q) : 0u);
+        }
+      } else {
+#pragma unroll 1
+        for (int q = 0; q < kStep; ++q) {
+          const int i = i0 + 32 * q + lane;
+          const float2 x = i < end ? sl(i) : make_float2(-INFINITY, -INFINITY);
+          marks |= ((uint32_t)border.in(x.x, sl.index(i)) | (uint32_t)border.in(x.y, sl.index(i) + 1) << 1) << (2 * q);
+        }
       }
       while (__any_sync(0xffffffffu, marks != 0)) {
         float2 x = make_float2(-INFINITY, -INFINITY);
@@ -700,8 +729,9 @@ __device__ Share segments(const Slice<T>& sl, Shared& sh, Cluster& cl, Share& be
   return cl.exchange(Share{sh.warp_w[0], sh.warp_n[0], 0.f}, before);
 }
 // (the first warp of the block that holds it; else -1)
-template <class T, class In, class Weigh>
-__device__ int find(const Slice<T>& sl, Shared& sh, const Share& before, uint64_t target, In in, Weigh weigh) {
+template <class T, bool kAll, class Weigh>
+__device__ int find(const Slice<T, kAll>& sl, Shared& sh, const Share& before, uint64_t target, const Border& border,
+                    Weigh weigh) {
   const int lane = threadIdx.x & 31;
   if (threadIdx.x >= 32 || target < before.sum || target - before.sum >= sh.seg_sum[kSegs - 1]) return -1;
   const uint64_t rest = target - before.sum;
@@ -713,8 +743,8 @@ __device__ int find(const Slice<T>& sl, Shared& sh, const Share& before, uint64_
   const int end = min(sl.pairs, (s + 1) * len);
   for (int i = s * len; i < end; i += 32) {
     float2 x = i + lane < end ? sl(i + lane) : make_float2(-INFINITY, -INFINITY);
-    if (!in(x.x, sl.index(i + lane))) x.x = -INFINITY;
-    if (!in(x.y, sl.index(i + lane) + 1)) x.y = -INFINITY;
+    if (!border.in(x.x, sl.index(i + lane))) x.x = -INFINITY;
+    if (!border.in(x.y, sl.index(i + lane) + 1)) x.y = -INFINITY;
     if (!__any_sync(0xffffffffu, drawable(x.x) || drawable(x.y))) continue;
     uint64_t a, b;
     weigh(x, a, b);
@@ -737,17 +767,17 @@ __device__ int find(const Slice<T>& sl, Shared& sh, const Share& before, uint64_
 }
 
 // The index of the m-th logit (from 1) that equals v.
-template <class T>
-__device__ uint32_t tie(const Slice<T>& sl, Shared& sh, Cluster& cl, float v, uint64_t m) {
-  auto equal = [&](float x, int) { return x == v; };
+template <class T, bool kAll>
+__device__ uint32_t tie(const Slice<T, kAll>& sl, Shared& sh, Cluster& cl, float v, uint64_t m) {
+  const Border up{v, INT_MAX};  // (larger ones are marked, too, and weigh nothing)
   auto one = [&](float2 x, uint64_t& a, uint64_t& b) {
     a = x.x == v;
     b = x.y == v;
     return (uint32_t)(a + b);
   };
   Share before, unused;
-  segments(sl, sh, cl, before, equal, one);
-  const int i = find(sl, sh, before, m - 1, equal, one);
+  segments(sl, sh, cl, before, up, one);
+  const int i = find(sl, sh, before, m - 1, up, one);
   if (threadIdx.x == 0) sh.found = i >= 0 ? (uint32_t)(sl.begin + i) + 1u : 0u;
   __syncthreads();
   return cl.exchange(Share{0, sh.found, 0.f}, unused).count - 1u;
@@ -791,7 +821,7 @@ struct Row {
   }
 };
 
-template <class T>
+template <class T, bool kAll>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
@@ -809,13 +839,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
   r.random = p.random[row];
 
   // ---- the slice to shared memory, and its largest logit
-  Slice<T> sl;
+  Slice<T, kAll> sl;
   sl.begin = min(p.vocab, cl.rank * p.slice);
   sl.n = min(p.vocab, sl.begin + p.slice) - sl.begin;
   sl.x = static_cast<const T*>(p.logits) + row * p.stride + sl.begin;
   constexpr int kVec = 16 / sizeof(T);
   sl.skew = (int)((reinterpret_cast<uintptr_t>(sl.x) & 15) / sizeof(T));
-  sl.room = reinterpret_cast<const typename Slice<T>::Bits*>(room);
+  sl.room = reinterpret_cast<const typename Slice<T, kAll>::Bits*>(room);
   const int vecs = (sl.skew + sl.n + kVec - 1) / kVec;
   sl.pairs = (sl.skew + sl.n + 1) / 2;
   sl.held = min(sl.pairs, p.room * (kVec / 2));
@@ -911,7 +941,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     if (by_count || by_weight) {
       // (weights with the counts only where there is no top-k: its candidates are few, as a rule, and are weighed
       // in their list)
-      first_histogram(sl, sc, sh, !by_count);
+      if (by_count) first_histogram<false>(sl, sc, sh);
+      else first_histogram<true>(sl, sc, sh);
       cl.group.sync();
       Search se{};  // (of use in the first block)
       auto restart = [&](uint64_t whole) {  // top-p of what top-k keeps, from the first histogram on
@@ -946,18 +977,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
         if (m.op == kGather) {
           Shared* const to = cl.group.map_shared_rank(&sh, 0);
           constexpr int kAtOnce = 4;
+          // (a class is a range of t in units of 2^-10, the last one without an end)
+          const uint32_t lo = m.by_bin ? m.lo * 16u : m.lo;
+          const uint32_t range = (m.by_bin ? m.hi == kBins - 1 ? 0x7FFFFFFFu : m.hi * 16u + 15u : m.hi) - lo;
           each_pair<kAtOnce>(sl, [&](int i, const float2 (&x)[kAtOnce]) {
 #pragma unroll
-            for (int q = 0; q < kAtOnce; ++q)
+            for (int q = 0; q < kAtOnce; ++q) {
+              int c[2];
+              log2_below(sc, x[q], c[0], c[1]);
+              if (!m.by_bin) {
+                c[0] = (int)key_of(x[q].x);
+                c[1] = (int)key_of(x[q].y);
+              }
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const float v = e ? x[q].y : x[q].x;
-                const uint32_t c = m.by_bin ? (uint32_t)bin_of(sc, v) : key_of(v);
-                if (c - m.lo <= m.hi - m.lo && drawable(v)) {
+                if ((uint32_t)c[e] - lo <= range && drawable(v)) {
                   const uint32_t at = atomicAdd(&to->n_list, 1u);
                   if (at < kList) to->list[at] = order_of(key_of(v), (uint32_t)(sl.index(i + q * kThreads) + e));
                 }
               }
+            }
           });
           cl.group.sync();
           if (cl.rank == 0) {
@@ -1004,7 +1044,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
           }
         } else if (m.op == kWeigh) {
           clear_bins(sh);
-          first_histogram(sl, sc, sh, true);
+          first_histogram<true>(sl, sc, sh);
           cl.group.sync();
           if (cl.rank == 0) {
             merge(cl, sh, true, true);
@@ -1041,9 +1081,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
   }
 
   // ---- the draw among the tokens up to the border, and with min-p's weight
-  const float last = border ? value_of((uint32_t)(border >> 32)) : -INFINITY;  // the border's logit and index
-  const int last_index = border ? (int)(0xFFFFFFFFu - (uint32_t)border) : INT_MIN;
-  auto in_order = [&](float x, int index) { return x > last || (x == last && index <= last_index); };
+  const Border kept{border ? value_of((uint32_t)(border >> 32)) : -INFINITY,  // the border's logit and index
+                    border ? (int)(0xFFFFFFFFu - (uint32_t)border) : INT_MIN};
   auto weigh = [&](float2 x, uint64_t& a, uint64_t& b) {
     int i0, i1;
     weights_of(sc, sh.table, x.x, x.y, a, b, i0, i1);
@@ -1052,8 +1091,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
     b = in1 ? b : 0;
     return (uint32_t)in0 + (uint32_t)in1;
   };
-  const Share sum = segments(sl, sh, cl, before, in_order, weigh);
-  const int i = find(sl, sh, before, target_of(sum.sum), in_order, weigh);
+  const Share sum = segments(sl, sh, cl, before, kept, weigh);
+  const int i = find(sl, sh, before, target_of(sum.sum), kept, weigh);
   if (i >= 0 && lane == 0) {
     const float2 x = sl((i + sl.skew) >> 1);
     write(sl.begin + i, sum.count, (i + sl.skew) & 1 ? x.y : x.x, sum.sum);
@@ -1061,17 +1100,33 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p)
   cl.group.sync();  // a block's shared memory stays until the others have read it
 }
 
-template <class T>
-cudaError_t launch(SampleArgs p, int sms, int most_smem, cudaStream_t s) {
+template <class T, bool kAll>
+cudaError_t launch_as(const SampleArgs& p, int blocks, size_t smem, int most_smem, cudaStream_t s) {
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit for this kernel is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
+    e = cudaFuncSetAttribute(sample_kernel<T, kAll>, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3((unsigned)p.n_rows * blocks);
+  lc.blockDim = dim3(kThreads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = blocks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, sample_kernel<T, kAll>, p);
+}
+
+template <class T>
+cudaError_t launch(SampleArgs p, int sms, int most_smem, cudaStream_t s) {
   // Blocks per row: more of them while the rows alone leave SMs idle or a slice is so large that only one
   // block fits an SM; a slice has at least 2,048 logits (a cluster's barriers cost what its blocks save).
   const int fixed = (int)(sizeof(Shared) + 15) / 16 * 16;
@@ -1082,19 +1137,11 @@ cudaError_t launch(SampleArgs p, int sms, int most_smem, cudaStream_t s) {
     blocks *= 2;
   p.slice = (p.vocab - 1) / blocks + 1;
   constexpr int kVec = 16 / sizeof(T);
-  p.room = std::min((p.slice + 2 * kVec - 2) / kVec, (most_smem - fixed) / 16);
-  cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3((unsigned)p.n_rows * blocks);
-  lc.blockDim = dim3(kThreads);
-  lc.dynamicSmemBytes = fixed + 16 * (size_t)p.room;
-  lc.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = blocks;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, sample_kernel<T>, p);
+  const int need = (p.slice + 2 * kVec - 2) / kVec;
+  p.room = std::min(need, (most_smem - fixed) / 16);
+  const size_t smem = fixed + 16 * (size_t)p.room;
+  return p.room == need ? launch_as<T, true>(p, blocks, smem, most_smem, s)
+                        : launch_as<T, false>(p, blocks, smem, most_smem, s);
 }
 }  // namespace
 
