@@ -73,6 +73,7 @@ struct Cfg {
 
 struct Maps {
   CUtensorMap q, k, v;
+  CUtensorMap k_piece, v_piece;  // (with sinks) kPieceRows keys at a time
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -226,24 +227,30 @@ __device__ bool find_tile(const PromptAttn& p, volatile Place* place, int t, int
   return false;
 }
 
-// 256 rows of one kv head.  With sinks (kSinks) the tiles that hold them follow those of the window,
-// where they are not among these.
+// 256 rows of one kv head.  With sinks (kSinks) the window's tiles begin at its first key, and the oldest one
+// begins with `pad` rows of sinks in front of it; more than kMostPad sinks have tiles of their own, behind the
+// window's.  (32,768 tokens on a window of 2,048 with 4 sinks: 17 tiles of keys for 64 tokens, 18 or 19 with tiles
+// that begin at multiples of 128 and one for the sinks: 916 us, 876 so.)
+constexpr int kPieceRows = 16, kMostPad = kKeys - kPieceRows;
 template <bool kSinks>
 struct Work {
   int h, q0, nq, k0, shift, window;
   int row0, tok0, tok1;  // first row, its token, one past the last token
   int t_lo, n;           // first key tile, number of tiles (0: no row sees a key)
-  int n_win, sinks;      // (kSinks) tiles of the window, keys at the front that stay visible
+  int lo, n_win, pad, sinks;  // (kSinks) first key less pad, tiles of the window, keys at the front that stay visible
   bool two;              // the second tile has rows
-  __device__ int tile(int j) const {
-    if (kSinks) return j < n_win ? t_lo + n_win - 1 - j : n - 1 - j;
-    return t_lo + n - 1 - j;
+  // is tile j the one that begins with sinks?
+  __device__ bool mixed(int j) const { return kSinks && pad > 0 && j == n_win - 1; }
+  // the key of tile j's first row (mixed: of the row that it would have without sinks)
+  __device__ int start(int j) const {
+    if (kSinks) return j < n_win ? lo + (n_win - 1 - j) * kKeys : (n - 1 - j) * kKeys;
+    return (t_lo + n - 1 - j) * kKeys;
   }
   // does some row see only a part of tile j?
   __device__ bool partial(int j) const {
-    const int a = tile(j) * kKeys;
+    const int a = start(j);
     return a + kKeys - 1 > tok0 + shift ||
-           (window > 0 && a < tok1 + shift - window && (!kSinks || a + kKeys > sinks));
+           (window > 0 && a < tok1 + shift - window && (!kSinks || a + kKeys > sinks)) || mixed(j);
   }
 };
 template <bool kSinks>
@@ -260,13 +267,24 @@ __device__ bool find_work(const PromptAttn& p, volatile Place* place, int idx, W
   w.row0 = tile * kBlockRows;
   w.tok0 = w.row0 / p.group;
   w.tok1 = min(sq.nq, w.tok0 + kBlockRows / p.group);
-  const int hi = max(0, w.tok1 + w.shift), lo = p.window > 0 ? max(0, w.tok0 + w.shift - p.window + 1) : 0;
-  w.t_lo = lo / kKeys;
-  w.n = hi > 0 ? (hi + kKeys - 1) / kKeys - w.t_lo : 0;
+  const int hi = max(0, w.tok1 + w.shift);
+  int lo = p.window > 0 ? max(0, w.tok0 + w.shift - p.window + 1) : 0;
   if (kSinks) {
-    w.n_win = w.n;
     w.sinks = p.sinks;
-    if (w.n > 0) w.n += min(w.t_lo, (p.sinks + kKeys - 1) / kKeys);
+    w.pad = 0;
+    int more = 0;
+    if (lo > 0) {
+      const int rows = (p.sinks + kPieceRows - 1) / kPieceRows * kPieceRows, tiles = (p.sinks + kKeys - 1) / kKeys;
+      if (lo <= (rows <= kMostPad ? rows : tiles * kKeys)) lo = 0;  // the sinks reach the window
+      else if (rows <= kMostPad) w.pad = rows;
+      else more = tiles;
+    }
+    w.lo = lo - w.pad;
+    w.n_win = hi > 0 ? (hi - w.lo + kKeys - 1) / kKeys : 0;
+    w.n = hi > 0 ? w.n_win + more : 0;
+  } else {
+    w.t_lo = lo / kKeys;
+    w.n = hi > 0 ? (hi + kKeys - 1) / kKeys - w.t_lo : 0;
   }
   w.two = w.row0 + kRows < sq.nq * p.group;
   return true;
@@ -384,9 +402,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (before >= 0 && !(ok = wait_bar(&b_empty[sig % C::kStages], (sig / kTurn) & 1, dead))) break;
             mbar_expect_tx(&b_full[st], C::kTileBytes);
             const CUtensorMap* const map = e & 1 ? &maps.v : &maps.k;
-            for (int x = 0; x < C::kBoxes; ++x)
-              tma_load_3d(s_kv + st * C::kTileBytes + x * kBoxBytes, map, x * 64, w.h, w.k0 + w.tile(e >> 1) * kKeys,
-                          &b_full[st]);
+            const int first = w.k0 + w.start(e >> 1);
+            if (w.mixed(e >> 1)) {
+              const CUtensorMap* const pieces = e & 1 ? &maps.v_piece : &maps.k_piece;
+              for (int x = 0; x < C::kBoxes; ++x)
+                for (int r = 0; r < kKeys; r += kPieceRows)
+                  tma_load_3d(s_kv + st * C::kTileBytes + x * kBoxBytes + r * 128, pieces, x * 64, w.h,
+                              r < w.pad ? w.k0 + r : first + r, &b_full[st]);
+            } else {
+              for (int x = 0; x < C::kBoxes; ++x)
+                tma_load_3d(s_kv + st * C::kTileBytes + x * kBoxBytes, map, x * 64, w.h, first, &b_full[st]);
+            }
             ++i;
             if (e == 0) ok = load_q(0) && (!w.two || load_q(1));
           }
@@ -586,12 +612,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         for (int c = 0; c < 4; ++c) tmem_ld32(ts + c * 32, s[c]);
         tmem_ld_wait();
         if (w.partial(j)) {
-          const int a = first - w.tile(j) * kKeys, b = last - w.tile(j) * kKeys;
+          const int a = first - w.start(j), b = last - w.start(j);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t see = ~bits_upto(a - 1 - c * 32);
-            if (kSinks) see |= bits_upto(w.sinks - 1 - w.tile(j) * kKeys - c * 32);
-            see &= bits_upto(b - c * 32);
+            uint32_t see = bits_upto(b - c * 32);
+            if (kSinks) {
+              // (the sinks in front of a window are behind no row)
+              const bool mixed = w.mixed(j);
+              see &= ~bits_upto((mixed ? max(a, w.pad) : a) - 1 - c * 32) |
+                     (mixed ? 0u : bits_upto(w.sinks - 1 - w.start(j) - c * 32));
+              if (mixed) see |= bits_upto(w.sinks - 1 - c * 32);
+            } else {
+              see &= ~bits_upto(a - 1 - c * 32);
+            }
 #pragma unroll
             for (int i = 0; i < 32; ++i) s[c][i] = see >> i & 1 ? s[c][i] : 0xFF800000u;
           }
@@ -679,8 +712,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         if (taken && tok < w.nq) {
           for (int j = 0; j < w.n; ++j) {
             if (!w.partial(j)) continue;
-            const int a0 = w.tile(j) * kKeys, a = kSinks ? a0 : max(first, a0), b = min(last, a0 + kKeys - 1);
-            for (int key = a; key <= b; ++key) {
+            const int a0 = w.start(j), a = kSinks ? a0 : max(first, a0), b = min(last, a0 + kKeys - 1);
+            for (int at = a; at <= b; ++at) {
+              const int key = w.mixed(j) && at - a0 < w.pad ? at - a0 : at;
               if (kSinks && key < first && key >= w.sinks) continue;
               const uint16_t* const v = p.v + (int64_t)(w.k0 + key) * p.v_token + w.h * p.v_head + c * 32;
 #pragma unroll
@@ -761,6 +795,10 @@ cudaError_t launch(const PromptAttn& p, int sms, cudaStream_t s) {
   const cuuint64_t vs[2] = {(cuuint64_t)p.v_head * 2, (cuuint64_t)p.v_token * 2};
   const cuuint32_t kb[3] = {64, 1, kKeys};
   ok = ok && make(&maps.k, 3, p.n_k > 0 ? p.k : p.q, kd, ks, kb) && make(&maps.v, 3, p.n_k > 0 ? p.v : p.q, kd, vs, kb);
+  if (kSinks) {
+    const cuuint32_t pb[3] = {64, 1, kPieceRows};
+    ok = ok && make(&maps.k_piece, 3, p.n_k > 0 ? p.k : p.q, kd, ks, pb) && make(&maps.v_piece, 3, p.n_k > 0 ? p.v : p.q, kd, vs, pb);
+  }
   if (!ok) return cudaErrorInvalidValue;
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit for this kernel is set
   int dev = 0;
