@@ -238,6 +238,7 @@ struct Work {
   int row0, tok0, tok1;  // first row, its token, one past the last token
   int t_lo, n;           // first key tile, number of tiles (0: no row sees a key)
   int lo, n_win, pad, sinks;  // (kSinks) first key less pad, tiles of the window, keys at the front that stay visible
+  int top, low, full;  // (kSinks) tiles in front of `top` and from `low` to `full` are seen in part by some row
   bool two;              // the second tile has rows
   // is tile j the one that begins with sinks?
   __device__ bool mixed(int j) const { return kSinks && pad > 0 && j == n_win - 1; }
@@ -248,9 +249,9 @@ struct Work {
   }
   // does some row see only a part of tile j?
   __device__ bool partial(int j) const {
+    if (kSinks) return j < top || (j >= low && j < full);
     const int a = start(j);
-    return a + kKeys - 1 > tok0 + shift ||
-           (window > 0 && a < tok1 + shift - window && (!kSinks || a + kKeys > sinks)) || mixed(j);
+    return a + kKeys - 1 > tok0 + shift || (window > 0 && a < tok1 + shift - window);
   }
 };
 template <bool kSinks>
@@ -282,6 +283,12 @@ __device__ bool find_work(const PromptAttn& p, volatile Place* place, int idx, W
     w.lo = lo - w.pad;
     w.n_win = hi > 0 ? (hi - w.lo + kKeys - 1) / kKeys : 0;
     w.n = hi > 0 ? w.n_win + more : 0;
+    // (tile t of the window, from its oldest one, ends behind a row where 128 t > tok0 + shift - 127 - lo, and begins
+    // in front of one's window where 128 t < tok1 + shift - window - lo)
+    w.top = min(w.n_win, w.n_win - 1 - ((w.tok0 + w.shift - (kKeys - 1) - w.lo) >> 7));
+    w.low = max(0, w.n_win - max((w.tok1 + w.shift - p.window - w.lo + kKeys - 1) >> 7, w.pad > 0 ? 1 : 0));
+    w.low = min(w.low, w.n_win);
+    w.full = w.n_win + (more > 0 && p.sinks % kKeys > 0 ? 1 : 0);
   } else {
     w.t_lo = lo / kKeys;
     w.n = hi > 0 ? (hi + kKeys - 1) / kKeys - w.t_lo : 0;
