@@ -743,7 +743,8 @@ msm_status msm_prompt_attention_sinks(const msm_prompt* prompt, int sinks, void*
  *   - the token is the lowest index whose weight, added to those of the kept lower indices, exceeds
  *     random x the sum over all that are kept (random = 1: the last one that has a weight).
  * T = 0 takes the largest logit (the lowest index among equals).  In a row with logits of +inf these alone
- * can be drawn, with equal weights.  Weights are held as multiples of 2^-42, so sums are exact and do not depend on timing.
+ * can be drawn, with equal weights.  Weights are held as multiples of 2^-42 (of the largest; min_p is at least that),
+ * so sums are exact and do not depend on timing.
  *   logits     device MSM_FP32, MSM_BF16 or MSM_FP16 [n_rows][vocab], row_stride elements between rows (0:
  *              every row is the same one), aligned to their type
  *   temperature, top_k, top_p, min_p  device [n_rows], fp32 and int32, or NULL for 1, 0 (no limit), 1 and 0

@@ -112,6 +112,8 @@ struct PagedAttn {
   uint32_t* counters;                        // workspace: three per block, zero between calls,
   float* part;                               // and partial results, two per block
 };
+// what an item costs beside its tiles (PagedAttn::finish).  8 bits: its tiles are cheaper, its end is not (64 sequences of 1
+// to 8,192 rows: 47 us with 1, 37 with 2, 34 with 4, 35 with 6, 37 with 9)
 constexpr int kPagedFinish = 1, kQPagedFinish = 4;
 constexpr int kPagedAttnPerSm = 2, kQPagedAttnPerSm = 2;  // blocks per SM (of 16 and of 8 bits)
 size_t paged_attn_workspace(int blocks, int group, int head_dim);

@@ -10,10 +10,15 @@
 // rows that come together do, up to those.
 //
 // Bound by memory for prompts (2 bytes read, 1 written per element) and by latency for a step's few
-// tokens.  A unit of threads, one warp or a block of eight warps, takes the blocks of rows that begin
-// among `group` tokens, for one head of K or V: a unit's loads are on their way before it knows the
-// largest element, and stay in registers until they are stored (a second read where a block has more
-// rows than that).  No two units meet in a block of rows, so no atomics.
+// tokens.  A unit, one to eight warps, takes the blocks of rows that begin among `group` tokens, K and V of
+// one head.  The rows' loads are on their way while the page is looked up, and stay in registers from the search for the
+// largest element until they are stored (a second read where a block has more rows than that).  No two units meet in
+// a block of rows, so no atomics.
+//
+// On one GB300 50,000 tokens of 8 heads of 128 in blocks of 16 rows take 51 us on the GPU (6,000 GB/s; the resize in front
+// of them 8), in blocks of 64 rows 55, of 256 rows 120.  K and V apart, a warp each: 60 us (the way from a token to its
+// page is a chain of loads, which the two then share); rows loaded before it is known which of
+// the group's tokens begins a block: 72.
 #include "msm_attn.cuh"
 #include "msm_paged.h"
 

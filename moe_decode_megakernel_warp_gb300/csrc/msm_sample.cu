@@ -21,6 +21,14 @@
 // border goes on: gathered and sorted by the cluster's first block when it is small (top-k: with all classes
 // in front of it), else divided into 1,024 finer classes, down to single values, whose equals are told apart
 // by index.  Between the steps the blocks exchange sums through distributed shared memory.
+//
+// Bound by instructions and by the chain of steps, not by memory (the logits of 500 rows are 7 us of DRAM): a weight is
+// some 35 instructions, and top-p without top-k needs every logit's, those of the kept ones a second time for the draw.
+// Measured on one GB300: one row of 32,003 fp32 logits, top-k 50 and top-p 14.3 us (10 us of steps, each 0.5 to 1.5 us:
+// cluster barriers, reads of other blocks' memory, the sort of the list); 64 rows of 131,072 with settings of their
+// own 64 us; 500 rows of 50,021 bf16 logits, top-p alone 171 us (ALU 46 %; the histogram takes 38 % of a block's time,
+// the sums for the draw 19 %, gathering the border's class 12 %).  256 threads a block, four blocks per SM: 190 us; counts
+// and weights together where top-k is given 78 instead of 64 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -38,9 +46,10 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBlocksPerSm = 1024 / kThreads;
 constexpr int kBins = 1024;
 constexpr int kBinsPerThread = kBins / kThreads;
-constexpr int kList = 512;            // candidates that are sorted
+constexpr int kList = kThreads;           // candidates that are sorted
 constexpr int kSegs = 128;            // segments of a slice, in the order of the index
 constexpr int kMaxCluster = 8;
 constexpr int kBits = 42;             // weights are multiples of 2^-42 ...
@@ -491,58 +500,60 @@ __device__ uint32_t key_at(const Scale& sc, int bin, bool largest) {
   return lo;
 }
 
-// The first block: sums the cluster's histograms, two classes a thread, as running sums.
+// The first block: sums the cluster's histograms, some neighbouring classes a thread, as running sums.
 __device__ void merge(Cluster& cl, Shared& sh, bool first, bool weights) {
-  static_assert(kBinsPerThread == 2, "");
-  uint32_t n[2] = {0, 0};
-  uint64_t w[2] = {0, 0};
-  auto gather = [&](int which, uint2 (&v)[kMaxCluster]) {  // all blocks' loads travel together
+  constexpr int kPairs = kBinsPerThread / 2;
+  uint32_t n[kBinsPerThread];
+  uint64_t w[kBinsPerThread];
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) {
-      v[r] = make_uint2(0u, 0u);
-      if (r < cl.size) {
-        const Shared* const o = cl.group.map_shared_rank(&sh, r);
-        v[r] = reinterpret_cast<const uint2*>(which == 0 ? o->bins.n : which == 1 ? o->bins.lo : o->bins.hi)[threadIdx.x];
+  for (int q = 0; q < kBinsPerThread; ++q) n[q] = 0, w[q] = 0;
+#pragma unroll
+  for (int which = 0; which < 3; ++which) {
+    if (which > 0 && !weights) break;
+#pragma unroll
+    for (int h = 0; h < kPairs; ++h) {
+      uint2 v[kMaxCluster];  // all blocks' loads travel together
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        v[r] = make_uint2(0u, 0u);
+        if (r < cl.size) {
+          const Shared* const o = cl.group.map_shared_rank(&sh, r);
+          v[r] = reinterpret_cast<const uint2*>(which == 0 ? o->bins.n : which == 1 ? o->bins.lo : o->bins.hi)[threadIdx.x * kPairs + h];
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        if (which == 0) {
+          n[2 * h] += v[r].x;
+          n[2 * h + 1] += v[r].y;
+        } else {
+          w[2 * h] += (uint64_t)v[r].x << (which == 2 ? 32 : 0);
+          w[2 * h + 1] += (uint64_t)v[r].y << (which == 2 ? 32 : 0);
+        }
       }
     }
-  };
-  uint2 v[kMaxCluster];
-  gather(0, v);
-#pragma unroll
-  for (int r = 0; r < kMaxCluster; ++r) {
-    n[0] += v[r].x;
-    n[1] += v[r].y;
   }
-  if (weights) {
-    gather(1, v);
+  uint32_t tn = 0;
+  uint64_t tw = 0;
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) {
-      w[0] += v[r].x;
-      w[1] += v[r].y;
-    }
-    gather(2, v);
-#pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) {
-      w[0] += (uint64_t)v[r].x << 32;
-      w[1] += (uint64_t)v[r].y << 32;
-    }
+  for (int q = 0; q < kBinsPerThread; ++q) {
+    tn += n[q];
+    tw += w[q];
   }
-  uint32_t tn = n[0] + n[1];
-  uint64_t tw = w[0] + w[1];
   block_scan(tn, tw, sh);  // (its barriers: everybody has read this block's own counts)
-  const int b = threadIdx.x * 2;
-  if (first) {
-    sh.first_n[b] = tn - n[1];
-    sh.first_n[b + 1] = tn;
-    sh.first_w[b] = tw - w[1];
-    sh.first_w[b + 1] = tw;
-  } else {
-    sh.bins.n[b] = tn - n[1];
-    sh.bins.n[b + 1] = tn;
-    sh.bins.lo[b] = (uint32_t)(tw - w[1]);
-    sh.bins.hi[b] = (uint32_t)((tw - w[1]) >> 32);
-    sh.bins.lo[b + 1] = (uint32_t)tw;
-    sh.bins.hi[b + 1] = (uint32_t)(tw >> 32);
+#pragma unroll
+  for (int q = kBinsPerThread - 1; q >= 0; --q) {
+    const int b = threadIdx.x * kBinsPerThread + q;
+    if (first) {
+      sh.first_n[b] = tn;
+      sh.first_w[b] = tw;
+    } else {
+      sh.bins.n[b] = tn;
+      sh.bins.lo[b] = (uint32_t)tw;
+      sh.bins.hi[b] = (uint32_t)(tw >> 32);
+    }
+    tn -= n[q];
+    tw -= w[q];
   }
   __syncthreads();
 }
@@ -822,7 +833,7 @@ struct Row {
 };
 
 template <class T, bool kAll>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs p) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const SampleArgs p) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
   uint4* const room = reinterpret_cast<uint4*>(smem + (sizeof(Shared) + 15) / 16 * 16);
@@ -1130,10 +1141,10 @@ cudaError_t launch(SampleArgs p, int sms, int most_smem, cudaStream_t s) {
   // Blocks per row: more of them while the rows alone leave SMs idle or a slice is so large that only one
   // block fits an SM; a slice has at least 2,048 logits (a cluster's barriers cost what its blocks save).
   const int fixed = (int)(sizeof(Shared) + 15) / 16 * 16;
-  constexpr int kLeast = 2048, kTwoPerSm = 110 * 1024;
+  constexpr int kLeast = 2048, kShare = 224 * 1024 / kBlocksPerSm;
   int blocks = 1;
   while (blocks < kMaxCluster && p.vocab / blocks >= 2 * kLeast &&
-         ((int64_t)p.n_rows * blocks < sms || fixed + ((p.vocab - 1) / blocks + 1) * (int)sizeof(T) > kTwoPerSm))
+         ((int64_t)p.n_rows * blocks < sms || fixed + ((p.vocab - 1) / blocks + 1) * (int)sizeof(T) > kShare))
     blocks *= 2;
   p.slice = (p.vocab - 1) / blocks + 1;
   constexpr int kVec = 16 / sizeof(T);
