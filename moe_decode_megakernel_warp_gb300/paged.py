@@ -187,19 +187,24 @@ class PagedCache:
         if n > 0x7FFFFFFF:
             raise ValueError("more than 2^31 - 1 tokens")
         shape = (n, self._kv_heads, self._head_dim)
-        dtype = self._dtype or _sixteen(k)
+        dtype = _sixteen(k) if self._held8 else self._dtype
         kt, kh = _rows(k, "k", shape, dtype, i)
         vt, vh = _rows(v, "v", shape, dtype, i)
-        code = (_CODES[dtype],) if self._held8 else ()
-        _check(self._write(self._ref, _c_int(layer), *code, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh,
-                           _int32(starts, "starts", self._n_seqs + 1, i), n, _raw_stream(i)))
+        at = _int32(starts, "starts", self._n_seqs + 1, i)
+        if self._held8:
+            st = self._write(self._ref, _c_int(layer), _CODES[dtype], k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, at, n,
+                             _raw_stream(i))
+        else:
+            st = self._write(self._ref, _c_int(layer), k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, at, n, _raw_stream(i))
+        if st:
+            _check(st)
 
     def attention(self, layer, q, window=0, scale=None, out=None, sinks=0):
         """msm_paged_attention_sinks (8 bits: msm_qpages_attention): q [n_seqs, n_q_heads, head_dim]; scale
         defaults to 1 / sqrt(head_dim); with a window the first ``sinks`` rows stay visible.  Returns out."""
         if q.dim() != 3:
             raise ValueError("q must be [n_seqs, n_q_heads, head_dim]")
-        dtype = self._dtype or _sixteen(q)
+        dtype = _sixteen(q) if self._held8 else self._dtype
         heads, i, hd, layer = q.shape[1], self._index, self._head_dim, _c_int(layer)
         shape = (self._n_seqs, heads, hd)
         qs, qh = _rows(q, "q", shape, dtype, i)
@@ -213,8 +218,11 @@ class PagedCache:
         if n is None:
             of = self._lib.msm_qpages_attention_workspace if self._held8 else self._lib.msm_paged_attention_workspace
             n = of(self._ref, heads)
-            if n == 0:  # the call says what is wrong
-                self._attend(layer, dtype, None, qs, qh, heads, 1.0, 0, 0, None, os_, oh, None, 0, None)
+            if n == 0:  # (the message says what is wrong)
+                _check(self._lib.msm_paged_attention(self._ref, layer, None, qs, qh, heads, 1.0, 0, None, os_, oh, None,
+                                                     0, None) if not self._held8 else
+                       self._lib.msm_qpages_attention(self._ref, layer, _CODES[dtype], None, qs, qh, heads, 1.0, 0, 0, None,
+                                                      os_, oh, None, 0, None))
             self._bytes[heads] = n
         # one workspace per stream, and one per call that a graph records (graphs recorded on
         # one stream may be replayed on two)
@@ -224,17 +232,20 @@ class PagedCache:
             ws = self._workspace.get((stream, heads))
             if ws is None:
                 ws = self._workspace[stream, heads] = _torch.zeros(n, dtype=_torch.uint8, device=self.device)
-        self._attend(layer, dtype, q.data_ptr(), qs, qh, heads, (hd or 1) ** -0.5 if scale is None else scale,
-                     _c_int(window), _c_int(sinks), out.data_ptr(), os_, oh, ws.data_ptr(), n, stream)
-        return out
-
-    def _attend(self, layer, dtype, *args):
+        scale = (hd or 1) ** -0.5 if scale is None else scale
         if self._held8:
-            st = self._lib.msm_qpages_attention(self._ref, layer, _CODES[dtype], *args)
+            st = self._lib.msm_qpages_attention(self._ref, layer, _CODES[dtype], q.data_ptr(), qs, qh, heads, scale,
+                                                _c_int(window), _c_int(sinks), out.data_ptr(), os_, oh, ws.data_ptr(), n,
+                                                stream)
+        elif sinks:
+            st = self._lib.msm_paged_attention_sinks(self._ref, layer, q.data_ptr(), qs, qh, heads, scale, _c_int(window),
+                                                     _c_int(sinks), out.data_ptr(), os_, oh, ws.data_ptr(), n, stream)
         else:
-            st = self._lib.msm_paged_attention_sinks(self._ref, layer, *args)
+            st = self._lib.msm_paged_attention(self._ref, layer, q.data_ptr(), qs, qh, heads, scale, _c_int(window),
+                                               out.data_ptr(), os_, oh, ws.data_ptr(), n, stream)
         if st:
             _check(st)
+        return out
 
     def sync(self):
         """msm_pages_sync: waits for the current stream; raises MsmError for an error that a
@@ -283,7 +294,10 @@ def prompt_attention(q, k, v, q_starts, k_starts=None, window=0, scale=None, out
                      (hd or 1) ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                      out.data_ptr(), qt, qh, kt, kh, vt, vh, ot, oh, qs, ks,
                      0 if status is None else _int32(status, "status", 1, i), 0)
-    st = _LIBRARY.msm_prompt_attention_sinks(a, _c_int(sinks), _raw_stream(i))
+    if sinks:
+        st = _LIBRARY.msm_prompt_attention_sinks(a, _c_int(sinks), _raw_stream(i))
+    else:
+        st = _LIBRARY.msm_prompt_attention(a, _raw_stream(i))
     if st:
         _check(st)
     return out

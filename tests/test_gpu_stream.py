@@ -106,6 +106,22 @@ def test_random_calls_equal_the_reference(rows, block, heads, hd, kind):
     c.ref.check()
 
 
+@pytest.mark.parametrize("rows,block,hd,n_seqs", [(300, 300, 128, 3), (200, 190, 64, 3), (130, 128, 128, 2), (16, 5, 64, 70),
+                                                  (8, 8, 128, 31), (8, 3, 128, 32), (40, 40, 64, 33)])
+def test_long_blocks_and_many_sequences(rows, block, hd, n_seqs):
+    """Blocks of more rows than registers hold; searches of one step and of more."""
+    rng = np.random.default_rng(rows + n_seqs)
+    c = Both(rng, 1, 4 * n_seqs, rows, block, 2, hd, n_seqs, 3)
+    for step in range(5):
+        old = c.ref.lens.copy()
+        grow = rng.integers(0, [3 * rows, 3, rows, 2, 40][step] + 1, n_seqs)
+        assert c.call("resize", [int(min(n + g, 3 * rows)) for n, g in zip(old, grow)]) is None
+        c.write(c.ref.lens - old, step, sizes=float(2.0 ** rng.uniform(-3, 4)))
+        if step == 1:
+            c.call("resize", [int(n) // 2 if s % 2 else -1 for s, n in enumerate(c.ref.lens)])
+    c.ref.check()
+
+
 @pytest.mark.parametrize("block", [5, 64, 200])
 def test_one_token_at_a_time_through_growing_sizes(block):
     c = Both(np.random.default_rng(7), 1, 6, 200, block, 2, 64, 2, 3)
@@ -296,6 +312,17 @@ def test_decode_over_8_bits(kind, hq, hkv, hd, rows, block, window, sinks):
     check_decode(cache, q, table, lens, rows, kind, window, sinks, got)
 
 
+@pytest.mark.parametrize("block", [None, 4])
+def test_many_short_sequences(block):
+    """More sequences than a block has threads, most of them of a tile or none."""
+    rng = np.random.default_rng(12)
+    lens = [int(n) for n in rng.integers(0, 60, 300)] + [900]
+    cache, q, table = decode_case("fp16", 4, 2, 64, 8, lens, block=block, seed=12)
+    got = cache.attention(0, q, window=40, sinks=2)
+    cache.sync()
+    check_decode(cache, q, table, lens, 8, "fp16", 40, 2, got)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
 def test_long_and_ragged_batches_over_8_bits(kind):
     """More parts of an item than are joined at once, and scales far apart within a sequence."""
@@ -410,6 +437,44 @@ def test_prompts_with_sinks(kind, hq, hkv, hd, window, sinks):
         assert np.array_equal(bits(got), bits(msm.prompt_attention(q, k, v, ints(qs), ints(ks), window=window)))
 
 
+@pytest.mark.parametrize("sinks", [5, 40, 130])
+def test_prompts_with_sinks_out_of_a_cache(sinks):
+    """K and V in the layout of the contiguous caches, with rows to spare behind each sequence."""
+    torch, msm = _mods()
+    q_lens, k_lens, spare, window = [200, 33], [600, 450], 30, 100
+    ks = [0, 600, 630, 1080, 1110]           # a sequence without queries stands for the spare rows
+    qs = [0, 200, 200, 233, 233]
+    q = randn("bf16", 233, 8, 128, seed=1).cuda()
+    k, v = (randn("bf16", 2, 1110, 128, seed=i).cuda().transpose(0, 1) for i in (2, 3))
+    k[600:630], v[600:630], k[1080:], v[1080:] = NAN, NAN, NAN, NAN
+    out = torch.full((240, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    msm.prompt_attention(q, k, v, ints(qs), ints(ks), window=window, sinks=sinks, out=out[:233])
+    assert (out[233:] == 7).all()
+    for a, b, c, d in ((0, 200, 0, 600), (200, 233, 630, 1080)):
+        want, tol = attend_seen(f64(q[a:b]), f64(k[c:d]), f64(v[c:d]), seen(b - a, d - c, window, sinks), 128 ** -0.5, "bf16")
+        assert_close(out[a:b], want, tol)
+
+
+def test_waits_of_the_prompt_kernel_with_sinks_end():
+    """No key is loaded (the test hook): every wait runs out, the rows are NaN and the status says so."""
+    import ctypes
+    torch, msm = _mods()
+    q, k, v, qs, ks = prompt_case("bf16", 4, 2, 64, [300], [300])
+    out, status, st = torch.zeros_like(q), ints([0]), ints(qs)
+    p = msm.MsmPrompt(device=0, dtype=msm.MSM_BF16, n_seqs=1, n_q=300, n_k=300, n_q_heads=4, n_kv_heads=2, head_dim=64,
+                      window=50, scale=0.1, q=q.data_ptr(), k=k.data_ptr(), v=v.data_ptr(), out=out.data_ptr(),
+                      q_token_stride=256, q_head_stride=64, k_token_stride=128, k_head_stride=64, v_token_stride=128,
+                      v_head_stride=64, out_token_stride=256, out_head_stride=64, q_starts=st.data_ptr(),
+                      k_starts=st.data_ptr(), status=status.data_ptr(), flags=msm.MSM_FLAG_TEST_DROP_HANDOFF)
+    assert msm.msm_prompt_attention_sinks(p, 3, torch.cuda.current_stream().cuda_stream) == msm.MSM_OK
+    torch.cuda.synchronize()
+    assert int(status) == msm.MSM_ERR_DEVICE_TIMEOUT and out.isnan().all()
+    p.flags = 0
+    assert msm.msm_prompt_attention_sinks(p, 3, torch.cuda.current_stream().cuda_stream) == msm.MSM_OK
+    want, tol = attend_seen(f64(q), f64(k), f64(v), seen(300, 300, 50, 3), 0.1, "bf16")
+    assert_close(out, want, tol)
+
+
 def test_a_window_of_all_keys_makes_sinks_meaningless():
     _, msm = _mods()
     q, k, v, qs, ks = prompt_case("bf16", 8, 2, 64, [300], [300])
@@ -520,6 +585,29 @@ def test_large_vocabularies():
         x, u = logits(2, vocab, dtype, vocab)
         for par in ({}, dict(top_k=[7, 4000]), dict(top_p=[0.9, 0.3])):
             assert run_draw(x, u, **par) <= 1
+
+
+def test_borders_far_below_the_largest_logit():
+    """One logit far above a broad body: the border lies where the first histogram has its last class."""
+    for vocab, dtype, spike in ((3000, "fp32", 22.0), (60000, "fp32", 26.0), (131072, "bf16", 24.0), (40000, "fp32", 60.0)):
+        x, u = logits(4, vocab, dtype, 5, std=1.0)
+        x[:, 77] = spike
+        u = 1 - u * 2.0 ** -24
+        for par in (dict(top_p=[0.9999, 0.99999, 0.999999, 0.5]), dict(top_k=[2500, 700, 2, 1]),
+                    dict(top_k=[2900, 1300, 600, 9], top_p=[0.99999] * 4), dict(min_p=[1e-11, 1e-9, 1e-8, 0.1]), {}):
+            run_draw(x, u, **par)
+
+
+def test_logits_past_two_to_the_31_elements():
+    torch, msm = _mods()
+    stride, vocab = (1 << 30) + 3, 40000
+    room = torch.empty(2 * stride + vocab, dtype=torch.bfloat16, device="cuda")
+    x = room.as_strided((3, vocab), (stride, 1))
+    y, u = logits(3, vocab, "bf16", 9)
+    x.copy_(y)
+    ud = torch.from_numpy(u).float().cuda()
+    for par in ({}, dict(top_p=torch.full((3,), 0.8, device="cuda")), dict(top_k=ints([50, 5, 5000]))):
+        assert torch.equal(msm.sample(x, ud, **par), msm.sample(y, ud, **par))
 
 
 def test_a_batch_with_settings_of_its_own():
