@@ -66,7 +66,8 @@ __constant__ uint64_t c_coarse[32] = {
     0x52ff6b54d8a89c75ull, 0x513821818624b40cull, 0x4f7a993048d088d7ull, 0x4dc69cdceaa72a9cull,
     0x4c1bf828c6dc54b8ull, 0x4a7a77d47f7b84b1ull, 0x48e1e9b9d588e19bull, 0x47521cc5a2e6a9e0ull,
     0x45cae0f1f545eb73ull, 0x444c0740496d4294ull, 0x42d561b3e6243d8aull, 0x4166c34c5615d0ecull};
-__constant__ uint64_t c_fine[32] = {
+// (in global memory: a warp reads all 32 of them at once)
+__device__ const uint64_t c_fine[32] = {
     0xffffffffffffffffull, 0xffd3a751c0f7e10cull, 0xffa756521c8daed2ull, 0xff7b0cffbe159675ull,
     0xff4ecb59511ec8a5ull, 0xff22915d81736f63ull, 0xfef65f0afb18a3caull, 0xfeca34606a4e63dcull,
     0xfe9e115c7b8f884cull, 0xfe71f5fddb91ba4bull, 0xfe45e2433745695dull, 0xfe19d62b3bd5c123ull,
@@ -81,12 +82,13 @@ struct __align__(16) Share {  // what a block tells the others
   uint32_t count;
   float top;
 };
-enum Op { kGather, kWeigh, kRefine, kTies, kDone, kDrawn };
+enum Op { kGather, kWeigh, kRefine, kTies, kDone };
 struct Message {  // what the first block tells the others
   int op;
   uint32_t lo, hi;   // classes of the first histogram, or keys, of the candidates
   int by_bin;
-  uint64_t border;   // kTies: how many of the equals are kept; kDone: the last kept token's order (kDrawn: all is done)
+  int last;          // kGather: the list begins with the order, so the first block draws from it alone
+  uint64_t border;   // kTies: how many of the equals are kept; kDone: the last kept token's order
 };
 
 struct Shared {
@@ -106,7 +108,6 @@ struct Shared {
   uint32_t seg_n[kSegs];
   uint64_t warp_w[kWarps];
   uint32_t warp_n[kWarps];
-  float warp_top[kWarps];
   Share share[2];
   Message message[2];
   uint32_t n_list;
@@ -255,13 +256,14 @@ __device__ __forceinline__ uint64_t warp_sum_few(uint64_t w) {
                  high = __reduce_add_sync(0xffffffffu, (uint32_t)(w >> 22));
   return ((uint64_t)high << 22) + low;
 }
-// sums over the block's threads up to and including this one's
+// sums over the block's threads up to and including this one's, of counts and (kWeights) weights
+template <bool kWeights>
 __device__ void block_scan(uint32_t& n, uint64_t& w, Shared& sh) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t a = __shfl_up_sync(0xffffffffu, n, o);
-    const uint64_t b = __shfl_up_sync(0xffffffffu, w, o);
+    const uint64_t b = kWeights ? __shfl_up_sync(0xffffffffu, w, o) : 0ull;
     if (lane >= o) {
       n += a;
       w += b;
@@ -269,11 +271,11 @@ __device__ void block_scan(uint32_t& n, uint64_t& w, Shared& sh) {
   }
   if (lane == 31) {
     sh.warp_n[wid] = n;
-    sh.warp_w[wid] = w;
+    if (kWeights) sh.warp_w[wid] = w;
   }
   __syncthreads();
   n += __reduce_add_sync(0xffffffffu, lane < wid ? sh.warp_n[lane] : 0u);
-  w += warp_sum(lane < wid ? sh.warp_w[lane] : 0ull);
+  if (kWeights) w += warp_sum(lane < wid ? sh.warp_w[lane] : 0ull);
   __syncthreads();
 }
 
@@ -439,11 +441,14 @@ __device__ void first_histogram(const Slice<T, kAll>& sl, const Scale& sc, Share
       for (int e = 0; e < 2 * kAtOnce; ++e) add_to_bin<kWeights>(sh, b[e] < kBins - 1, b[e], w[e]);
     }
   });
-  block_scan(tail_n, tail_w, sh);
-  if (threadIdx.x == kThreads - 1) {
-    sh.bins.n[kBins - 1] = tail_n;
-    sh.bins.lo[kBins - 1] = (uint32_t)tail_w;
-    sh.bins.hi[kBins - 1] = (uint32_t)(tail_w >> 32);
+  tail_n = __reduce_add_sync(0xffffffffu, tail_n);
+  if (kWeights) tail_w = warp_sum(tail_w);
+  if ((threadIdx.x & 31) == 0) {
+    atomicAdd(&sh.bins.n[kBins - 1], tail_n);
+    if (kWeights) {
+      const uint32_t was = atomicAdd(&sh.bins.lo[kBins - 1], (uint32_t)tail_w);
+      atomicAdd(&sh.bins.hi[kBins - 1], (uint32_t)(tail_w >> 32) + (was + (uint32_t)tail_w < was));
+    }
   }
 }
 
@@ -540,7 +545,8 @@ __device__ void merge(Cluster& cl, Shared& sh, bool first, bool weights) {
     tn += n[q];
     tw += w[q];
   }
-  block_scan(tn, tw, sh);  // (its barriers: everybody has read this block's own counts)
+  if (weights) block_scan<true>(tn, tw, sh);
+  else block_scan<false>(tn, tw, sh);  // (its barriers: everybody has read this block's own counts)
 #pragma unroll
   for (int q = kBinsPerThread - 1; q >= 0; --q) {
     const int b = threadIdx.x * kBinsPerThread + q;
@@ -614,6 +620,7 @@ __device__ void next_step(Search& s, const Scale& sc, Shared& sh, Message* out) 
       }
     }
   }
+  m.last = m.op == kGather && s.n_before == 0;
   __syncthreads();  // (the running sums may give way to a list)
   if (threadIdx.x == 0) *out = m;
 }
@@ -637,7 +644,7 @@ __device__ void sort_list(const Scale& sc, Shared& sh, int n) {
     w = weight_of(sc, sh.table, value_of((uint32_t)(mine >> 32)));
     sh.list[i] = mine;
   }
-  block_scan(unused, w, sh);
+  block_scan<true>(unused, w, sh);
   if (i < n) sh.sums[i] = w;
   __syncthreads();
 }
@@ -865,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const Sa
   {
     const uint4* const base = reinterpret_cast<const uint4*>(sl.x - sl.skew);
     constexpr int kAtOnce = 8;
-    const uint64_t fine = c_fine[lane];
+    const uint64_t fine = __ldg(c_fine + lane);
     for (int v0 = tid; v0 < vecs || v0 == tid; v0 += kThreads * kAtOnce) {
       uint4 v[kAtOnce];
 #pragma unroll
@@ -897,14 +904,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const Sa
     }
   }
   float top = largest_of(most, sl.x);
-  top = drawable(top) ? top + 0.f : -INFINITY;
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) sh.warp_top[wid] = top;
+  uint32_t top_key = drawable(top) ? key_of(top) : 0u;
+  top_key = __reduce_max_sync(0xffffffffu, top_key);
+  if (lane == 0) sh.warp_n[wid] = top_key;
   __syncthreads();
-  top = lane < kWarps ? sh.warp_top[lane] : -INFINITY;
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  top_key = __reduce_max_sync(0xffffffffu, lane < kWarps ? sh.warp_n[lane] : 0u);
+  top = top_key ? value_of(top_key) : -INFINITY;
   Share before;
   top = cl.exchange(Share{0, 0, top}, before).top;
   if (!drawable(top) || !r.fine()) {
@@ -937,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const Sa
       // (the weight as a number: its multiple of 2^-42 may have few bits)
       const float d = sc.max - x, b = d - sc.max, e = (sc.max - (d - b)) - (x + b);
       const float h = d * sc.hi, l = fmaf(d, sc.hi, -h) + fmaf(d, sc.lo, e * sc.hi);
-      p.probs[row] = (float)((double)(exp2f(-h) * (1.f - 0.6931471805599453f * l)) * (double)kOne / (double)sum);
+      p.probs[row] = exp2f(-h) * (1.f - 0.6931471805599453f * l) * ((float)kOne / (float)sum);
     }
   };
   uint64_t border = 0;
@@ -973,14 +978,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const Sa
           restart(sh.first_w[kBins - 1]);
         }
         if (se.first) next_step(se, sc, sh, cl.message());
-        else if (tid == 0) *cl.message() = Message{by_weight ? kWeigh : kDone, 0, 0, 0, 0};  // top-k keeps all
+        else if (tid == 0) *cl.message() = Message{by_weight ? kWeigh : kDone, 0, 0, 0, 0, 0};  // top-k keeps all
       }
       for (;;) {
         const Message m = cl.receive();
-        if (m.op == kDrawn) {
-          cl.group.sync();  // a block's shared memory stays until the others have read it
-          return;
-        }
         if (m.op == kDone) {
           border = m.border;
           break;
@@ -1011,20 +1012,20 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const Sa
             }
           });
           cl.group.sync();
+          if (m.last && cl.rank != 0) return;  // (the first block reads nothing of the others' any more)
           if (cl.rank == 0) {
             const int n = (int)min(sh.n_list, (uint32_t)kList);
             sort_list(sc, sh, n);
             auto sums = [&](int i) { return sh.sums[i]; };
             int at = se.by_weight ? reaches(n, se.goal - se.w_before, sh, sums) : (int)(se.goal - se.n_before) - 1;
             bool done = true;
-            const bool from_top = se.n_before == 0;
             if (!se.by_weight && by_weight) {
               const uint64_t w_front = se.w_before;
               restart(w_front + sh.sums[at]);
               done = se.goal > w_front;  // (else in front of these)
               if (done) at = reaches(n, se.goal - w_front, sh, sums);
             }
-            if (done && from_top) {
+            if (m.last) {
               // the list begins with the order: the draw is among its first ones
               const uint64_t mine = tid <= at ? sh.list[tid] : 0;
               uint64_t w = tid <= at ? sh.sums[tid] - (tid ? sh.sums[tid - 1] : 0) : 0;
@@ -1040,14 +1041,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const Sa
               const int from = (int)(w >> 48);
               uint64_t upto = w &= 0xFFFFFFFFFFFFull;
               uint32_t unused = 0;
-              block_scan(unused, upto, sh);
+              block_scan<true>(unused, upto, sh);
               if (tid < n_kept && upto > target && upto - w <= target) {
                 const uint64_t it = sh.list[from];
                 write((int)(0xFFFFFFFFu - (uint32_t)it), (uint32_t)n_kept, value_of((uint32_t)(it >> 32)), sum);
               }
-              if (tid == 0) *cl.message() = Message{kDrawn, 0, 0, 0, 0};
-            } else if (done) {
-              if (tid == 0) *cl.message() = Message{kDone, 0, 0, 0, sh.list[at]};
+              return;
+            }
+            if (done) {
+              if (tid == 0) *cl.message() = Message{kDone, 0, 0, 0, 0, sh.list[at]};
             } else {
               if (tid == 0) sh.n_list = 0;
               next_step(se, sc, sh, cl.message());
@@ -1080,9 +1082,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const Sa
               const uint64_t w = weight_of(sc, sh.table, v), w_front = se.w_before;
               restart(w_front + m.border * w);
               done = se.goal > w_front;
-              if (done && tid == 0) *cl.message() = Message{kTies, m.lo, m.lo, 0, (se.goal - w_front + w - 1) / w};
+              if (done && tid == 0) *cl.message() = Message{kTies, m.lo, m.lo, 0, 0, (se.goal - w_front + w - 1) / w};
             } else if (tid == 0) {
-              *cl.message() = Message{kDone, 0, 0, 0, order_of(m.lo, index)};
+              *cl.message() = Message{kDone, 0, 0, 0, 0, order_of(m.lo, index)};
             }
             if (!done) next_step(se, sc, sh, cl.message());
           }
