@@ -108,7 +108,7 @@ struct Shared {
   uint32_t seg_n[kSegs];
   uint64_t warp_w[kWarps];
   uint32_t warp_n[kWarps];
-  Share share[2];
+  Share share[2][kMaxCluster];  // of every block, written by it
   Message message[2];
   uint32_t n_list;
   int bin;
@@ -323,15 +323,12 @@ struct Cluster {
   int shares, messages;  // exchanges so far: two buffers each, so that one barrier is enough
   // every block's share; returns the sums over all of them, and over those in front of this one
   __device__ Share exchange(const Share& mine, Share& before) {
-    Share* const buf = &sh.share[shares++ & 1];
-    if (threadIdx.x == 0) *buf = mine;
+    Share* const buf = sh.share[shares++ & 1];
+    if ((int)threadIdx.x < size) *group.map_shared_rank(buf + rank, threadIdx.x) = mine;
     group.sync();
     const int lane = threadIdx.x & 31;
     Share s{0, 0, -INFINITY};
-    if (lane < size) {
-      const Share* const from = group.map_shared_rank(buf, lane);
-      s = *from;
-    }
+    if (lane < size) s = buf[lane];
     Share front{lane < rank ? s.sum : 0, lane < rank ? s.count : 0, 0.f};
 #pragma unroll
     for (int o = kMaxCluster / 2; o >= 1; o >>= 1) {
@@ -344,13 +341,14 @@ struct Cluster {
     before = Share{__shfl_sync(0xffffffffu, front.sum, 0), __shfl_sync(0xffffffffu, front.count, 0), 0.f};
     return Share{__shfl_sync(0xffffffffu, s.sum, 0), __shfl_sync(0xffffffffu, s.count, 0), __shfl_sync(0xffffffffu, s.top, 0)};
   }
-  // what the first block wrote to the message buffer
-  __device__ Message* message() { return &sh.message[messages & 1]; }
+  // the first block's message to every block (all threads of it call with the same one); receive() is behind a barrier
+  __device__ void send(const Message& m) {
+    if ((int)threadIdx.x < size) *group.map_shared_rank(&sh.message[messages & 1], threadIdx.x) = m;
+  }
   __device__ Message receive() {
-    Message* const buf = message();
-    ++messages;
+    const Message* const buf = &sh.message[messages++ & 1];
     group.sync();
-    return *group.map_shared_rank(buf, 0);
+    return *buf;
   }
 };
 
@@ -576,7 +574,7 @@ __device__ int reaches(int n, uint64_t goal, Shared& sh, F cum) {
 }
 
 // The first block: what to do about the class that holds the border.
-__device__ void next_step(Search& s, const Scale& sc, Shared& sh, Message* out) {
+__device__ Message next_step(Search& s, const Scale& sc, Shared& sh) {
   auto cum_n = [&](int i) { return s.first ? sh.first_n[i] : sh.bins.n[i]; };
   auto cum_w = [&](int i) { return s.first ? sh.first_w[i] : (uint64_t)sh.bins.hi[i] << 32 | sh.bins.lo[i]; };
   const int b = s.by_weight ? reaches(kBins, s.goal - s.w_before, sh, cum_w) : reaches(kBins, s.goal - s.n_before, sh, cum_n);
@@ -622,7 +620,7 @@ __device__ void next_step(Search& s, const Scale& sc, Shared& sh, Message* out) 
   }
   m.last = m.op == kGather && s.n_before == 0;
   __syncthreads();  // (the running sums may give way to a list)
-  if (threadIdx.x == 0) *out = m;
+  return m;
 }
 
 // The first block: its list of n candidates in falling order, with the running sums of their weights.
@@ -847,6 +845,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const Sa
   Cluster cl{cg::this_cluster(), sh, 0, 0, 0, 0};
   cl.rank = (int)cl.group.block_rank();
   cl.size = (int)cl.group.num_blocks();
+  // (no block writes to another's shared memory before that one has begun: the wait is in front of the first exchange)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int row = (int)(blockIdx.x / (unsigned)cl.size);
   Row r;
@@ -911,6 +911,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const Sa
   top_key = __reduce_max_sync(0xffffffffu, lane < kWarps ? sh.warp_n[lane] : 0u);
   top = top_key ? value_of(top_key) : -INFINITY;
   Share before;
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   top = cl.exchange(Share{0, 0, top}, before).top;
   if (!drawable(top) || !r.fine()) {
     if (cl.rank == 0 && tid == 0) {
@@ -977,8 +978,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const Sa
         } else if (by_weight && !by_count) {
           restart(sh.first_w[kBins - 1]);
         }
-        if (se.first) next_step(se, sc, sh, cl.message());
-        else if (tid == 0) *cl.message() = Message{by_weight ? kWeigh : kDone, 0, 0, 0, 0, 0};  // top-k keeps all
+        if (se.first) cl.send(next_step(se, sc, sh));
+        else cl.send(Message{by_weight ? kWeigh : kDone, 0, 0, 0, 0, 0});  // top-k keeps all
       }
       for (;;) {
         const Message m = cl.receive();
@@ -1049,10 +1050,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const Sa
               return;
             }
             if (done) {
-              if (tid == 0) *cl.message() = Message{kDone, 0, 0, 0, 0, sh.list[at]};
+              cl.send(Message{kDone, 0, 0, 0, 0, sh.list[at]});
             } else {
               if (tid == 0) sh.n_list = 0;
-              next_step(se, sc, sh, cl.message());
+              cl.send(next_step(se, sc, sh));
             }
           }
         } else if (m.op == kWeigh) {
@@ -1063,7 +1064,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const Sa
             merge(cl, sh, true, true);
             se.weighed = true;
             if (!se.first) restart(sh.first_w[kBins - 1]);
-            next_step(se, sc, sh, cl.message());
+            cl.send(next_step(se, sc, sh));
           }
         } else if (m.op == kRefine) {
           clear_bins(sh);
@@ -1071,7 +1072,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const Sa
           cl.group.sync();
           if (cl.rank == 0) {
             merge(cl, sh, false, by_weight);
-            next_step(se, sc, sh, cl.message());
+            cl.send(next_step(se, sc, sh));
           }
         } else {
           const float v = value_of(m.lo);
@@ -1082,11 +1083,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const Sa
               const uint64_t w = weight_of(sc, sh.table, v), w_front = se.w_before;
               restart(w_front + m.border * w);
               done = se.goal > w_front;
-              if (done && tid == 0) *cl.message() = Message{kTies, m.lo, m.lo, 0, 0, (se.goal - w_front + w - 1) / w};
-            } else if (tid == 0) {
-              *cl.message() = Message{kDone, 0, 0, 0, 0, order_of(m.lo, index)};
+              if (done) cl.send(Message{kTies, m.lo, m.lo, 0, 0, (se.goal - w_front + w - 1) / w});
+            } else {
+              cl.send(Message{kDone, 0, 0, 0, 0, order_of(m.lo, index)});
             }
-            if (!done) next_step(se, sc, sh, cl.message());
+            if (!done) cl.send(next_step(se, sc, sh));
           }
         }
       }
