@@ -744,12 +744,12 @@ __device__ Share segments(const Slice<T, kAll>& sl, Shared& sh, Cluster& cl, Sha
   __syncthreads();
   return cl.exchange(Share{sh.warp_w[0], sh.warp_n[0], 0.f}, before);
 }
-// (the first warp of the block that holds it; else -1)
+// (in the slice, for all threads of the block that holds it; else -1)
 template <class T, bool kAll, class Weigh>
 __device__ int find(const Slice<T, kAll>& sl, Shared& sh, const Share& before, uint64_t target, const Border& border,
                     Weigh weigh) {
-  const int lane = threadIdx.x & 31;
-  if (threadIdx.x >= 32 || target < before.sum || target - before.sum >= sh.seg_sum[kSegs - 1]) return -1;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  if (target < before.sum || target - before.sum >= sh.seg_sum[kSegs - 1]) return -1;
   const uint64_t rest = target - before.sum;
   int s = 0;
 #pragma unroll
@@ -757,27 +757,31 @@ __device__ int find(const Slice<T, kAll>& sl, Shared& sh, const Share& before, u
   const int len = segment_pairs(sl);
   uint64_t sum = s ? sh.seg_sum[s - 1] : 0;
   const int end = min(sl.pairs, (s + 1) * len);
-  for (int i = s * len; i < end; i += 32) {
-    float2 x = i + lane < end ? sl(i + lane) : make_float2(-INFINITY, -INFINITY);
-    if (!border.in(x.x, sl.index(i + lane))) x.x = -INFINITY;
-    if (!border.in(x.y, sl.index(i + lane) + 1)) x.y = -INFINITY;
-    if (!__any_sync(0xffffffffu, drawable(x.x) || drawable(x.y))) continue;
+  for (int c = s * len; c < end; c += kThreads) {  // a pair of the segment to a thread
+    const int i = c + (int)threadIdx.x;
+    float2 x = i < end ? sl(i) : make_float2(-INFINITY, -INFINITY);
+    if (!border.in(x.x, sl.index(i))) x.x = -INFINITY;
+    if (!border.in(x.y, sl.index(i) + 1)) x.y = -INFINITY;
     uint64_t a, b;
     weigh(x, a, b);
-    uint64_t w = a + b;
+    const uint64_t mine = warp_sum_few(a + b);
+    if (lane == 0) sh.warp_w[wid] = mine;
+    __syncthreads();
+    const uint64_t w = lane < kWarps ? sh.warp_w[lane] : 0, front = sum + warp_sum(lane < wid ? w : 0), all = warp_sum(w);
+    if (front <= rest && rest < front + mine) {
+      uint64_t upto = a + b;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      // the first lane that exceeds, and of its pair the second logit if the sum without it does not
+      const uint32_t over = __ballot_sync(0xffffffffu, front + upto > rest);
+      if (lane == __ffs(over) - 1) sh.found = (uint32_t)(2 * i - sl.skew + (front + upto - b <= rest));
     }
-    const uint32_t over = __ballot_sync(0xffffffffu, sum + w > rest);
-    if (over) {
-      const int l = __ffs(over) - 1;
-      // the pair's second logit, if the sum without it does not exceed
-      const bool second = sum + w - b <= rest;
-      return 2 * (i + l) - sl.skew + __shfl_sync(0xffffffffu, (int)second, l);
-    }
-    sum += __shfl_sync(0xffffffffu, w, 31);
+    __syncthreads();
+    if (rest < sum + all) return (int)sh.found;
+    sum += all;
   }
   return -1;
 }
@@ -794,9 +798,7 @@ __device__ uint32_t tie(const Slice<T, kAll>& sl, Shared& sh, Cluster& cl, float
   Share before, unused;
   segments(sl, sh, cl, before, up, one);
   const int i = find(sl, sh, before, m - 1, up, one);
-  if (threadIdx.x == 0) sh.found = i >= 0 ? (uint32_t)(sl.begin + i) + 1u : 0u;
-  __syncthreads();
-  return cl.exchange(Share{0, sh.found, 0.f}, unused).count - 1u;
+  return cl.exchange(Share{0, i >= 0 ? (uint32_t)(sl.begin + i) + 1u : 0u, 0.f}, unused).count - 1u;
 }
 
 // the larger of each half's elements; NaN counts for nothing
@@ -1107,7 +1109,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) sample_kernel(const Sa
   };
   const Share sum = segments(sl, sh, cl, before, kept, weigh);
   const int i = find(sl, sh, before, target_of(sum.sum), kept, weigh);
-  if (i >= 0 && lane == 0) {
+  if (i >= 0 && tid == 0) {
     const float2 x = sl((i + sl.skew) >> 1);
     write(sl.begin + i, sum.count, (i + sl.skew) & 1 ? x.y : x.x, sum.sum);
   }
