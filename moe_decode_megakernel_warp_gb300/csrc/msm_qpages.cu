@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(threads(kWarps), 512 / threads(kWarps))
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int w = kWarps == 1 ? 0 : wid;
   const int c = lane % kVecs, sub = w * (32 / kVecs) + lane / kVecs;
+  pdl_wait();
   // (up to 31 sequences: all of their starts and lengths at once, one wait instead of four in a row)
   const bool few = p.m.n_seqs < 32;
   const int my_start = few ? p.starts[min(lane, p.m.n_seqs)] : 0, my_len = few ? p.m.lens[min(lane, p.m.n_seqs - 1)] : 0;
@@ -278,11 +279,17 @@ __global__ void __launch_bounds__(threads(kWarps), 512 / threads(kWarps))
 template <class El, int HD, int kWarps>
 cudaError_t launch_of(const QPagesWrite& p, cudaStream_t s) {
   const dim3 grid((unsigned)((p.n_tokens - 1) / p.group + 1), kWarps == 1 ? (p.n_kv_heads - 1) / 4 + 1 : p.n_kv_heads);
-  if (p.block_rows > kHeld * (32 / (HD / 8)) * kWarps)
-    qwrite_kernel<El, HD, kWarps, true><<<grid, threads(kWarps), 0, s>>>(p);
-  else
-    qwrite_kernel<El, HD, kWarps, false><<<grid, threads(kWarps), 0, s>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = grid;
+  lc.blockDim = dim3(threads(kWarps));
+  lc.stream = s;
+  cudaLaunchAttribute attr[1];  // started while the launch in front of it (the copies of a resize) ends
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return p.block_rows > kHeld * (32 / (HD / 8)) * kWarps ? cudaLaunchKernelEx(&lc, qwrite_kernel<El, HD, kWarps, true>, p)
+                                                         : cudaLaunchKernelEx(&lc, qwrite_kernel<El, HD, kWarps, false>, p);
 }
 template <class El, int HD>
 cudaError_t launch(const QPagesWrite& p, cudaStream_t s) {
