@@ -99,7 +99,7 @@ struct PagedAttn {
   int32_t* status;
   int n_seqs, max_pages, n_pages, page_rows, n_kv_heads, group, window;
   int sinks;   // rows at the front that stay visible (0 without a window)
-  int finish;  // what an item costs beside its tiles, in tiles
+  int finish, solo_tiles;  // what an item costs beside its tiles, in tiles (1: one of at most solo_tiles tiles)
   const uint16_t* q;
   const void *k, *v;  // the layer's pools
   // a cache in 8 bits (else null): fp32 [n_pages][n_kv_heads][page_blocks], a scale for block_rows rows each
@@ -115,6 +115,11 @@ struct PagedAttn {
 // what an item costs beside its tiles (PagedAttn::finish).  8 bits: its tiles are cheaper, its end is not (64 sequences of 1
 // to 8,192 rows: 47 us with 1, 37 with 2, 34 with 4, 35 with 6, 37 with 9)
 constexpr int kPagedFinish = 1, kQPagedFinish = 4;
+// 8 bits: most tiles of an item that one warp does alone, which spares the block its barriers (512 sequences of 30 rows 50 -> 26
+// us).  Up to three where there are many items, so that the warps' shares even out (512 of 1 to 200 rows: 66 us without, 63
+// with one, 50 with three, 49 with five), one where there are few (64 of 1 to 8,192: 34 us without, 33 with one, 35 with
+// three, 39 with five).
+constexpr int kQPagedSolo = 1, kQPagedSoloMany = 3, kQPagedMany = 8;  // (many: items per block)
 constexpr int kPagedAttnPerSm = 2, kQPagedAttnPerSm = 2;  // blocks per SM (of 16 and of 8 bits)
 size_t paged_attn_workspace(int blocks, int group, int head_dim);
 cudaError_t launch_paged_attn(const PagedAttn& p, int dtype, int head_dim, int blocks, cudaStream_t s);

@@ -281,6 +281,7 @@ msm_status attention(const Cache* cache, int layer, int dtype, const void* q, in
   p.window = window;
   p.sinks = window > 0 ? sinks : 0;
   p.finish = held8(cache) ? kQPagedFinish : kPagedFinish;
+  p.solo_tiles = !held8(cache) ? 0 : (int64_t)c->n_seqs * c->n_kv_heads < (int64_t)kQPagedMany * blocks ? kQPagedSolo : kQPagedSoloMany;
   p.q = static_cast<const uint16_t*>(q);
   p.k = c->k_pages[layer];
   p.v = c->v_pages[layer];

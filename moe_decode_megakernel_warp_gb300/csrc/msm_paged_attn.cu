@@ -125,7 +125,7 @@ __device__ __forceinline__ Rows seq_rows(const PagedAttn& p, int s) {
     r.base = 0;
   }
   r.tiles = (r.hi - r.base + kTile - 1) / kTile;
-  r.units = r.tiles > 0 ? r.tiles + p.finish : 0;
+  r.units = r.tiles > p.solo_tiles ? r.tiles + p.finish : r.tiles > 0 ? r.tiles + 1 : 0;
   return r;
 }
 
@@ -136,16 +136,19 @@ struct Segment {
   int pad, skip;       // as in Rows
   int end, first;
   int ta, tb, tiles;   // its tiles of the item's
+  int solo;            // 8 bits, a short item: the warp that does all of it; else -1
   int64_t unit0;       // the batch's unit that holds the item's first tile
   __device__ __forceinline__ int row(int place) const { return place < pad ? place : place + skip; }
   __device__ __forceinline__ bool sees(int row) const { return row >= lo || row < sinks; }
 };
 
 // Walks the segments of a block's run of units [u, u1) (a whole warp together).  The first units of an
-// item, `finish` of them, have no tile.
+// item, `finish` of them, have no tile.  With kSolo short items go to one warp each, in turn.
+template <bool kSolo>
 struct Walk {
   int64_t u, u1, before;  // before: units of the sequences in front of s
   int s;
+  int solos;              // items of a warp so far
   __device__ bool next(const PagedAttn& p, Segment& g) {
     while (u < u1) {
       Rows rw = seq_rows(p, s);
@@ -173,7 +176,7 @@ struct Walk {
       }
       g.s = s;
       g.h = (int)((u - before) / rw.units);
-      g.unit0 = before + (int64_t)g.h * rw.units + p.finish;
+      g.unit0 = before + (int64_t)g.h * rw.units + (rw.units - rw.tiles);
       g.ta = max(0, (int)(u - g.unit0));
       g.tb = (int)min((int64_t)rw.tiles, u1 - g.unit0);
       g.tiles = rw.tiles;
@@ -184,6 +187,7 @@ struct Walk {
       g.first = rw.base + g.ta * kTile;
       g.end = min(rw.hi, rw.base + g.tb * kTile);
       u = g.unit0 + g.tb;
+      g.solo = kSolo && g.tiles <= p.solo_tiles && g.ta == 0 && g.tb == g.tiles ? solos++ % kWarps : -1;
       if (g.tb > g.ta) return true;
     }
     return false;
@@ -426,7 +430,7 @@ __global__ void __launch_bounds__(kThreadsA, kHeld8 ? kQPagedAttnPerSm : kPagedA
   __syncthreads();
 
   // ---- loads: every warp keeps kAhead chunks of its own on the way, across the ends of items
-  Walk ahead{u0, u1, s_find[1], (int)s_find[0]};
+  Walk<kHeld8> ahead{u0, u1, s_find[1], (int)s_find[0], 0};
   Segment fs{};
   int fc = 0;  // the next chunk to fetch: place of its first row; -1: none left
   int page = 0;
@@ -443,12 +447,13 @@ __global__ void __launch_bounds__(kThreadsA, kHeld8 ? kQPagedAttnPerSm : kPagedA
         return;
       }
       fc = fs.first + wid * C::kChunk;
+      if (kHeld8 && fs.solo >= 0) fc = fs.solo == wid ? fs.first : fs.end;
     }
   };
   int f_stage = 0;
   bool lost = false;  // a table entry outside the pool
   // fetches a chunk and returns which of its rows take part (0 when none is left)
-  auto fetch = [&](RowScale& rs) -> uint32_t {
+  auto fetch = [&](float2& rs) -> uint32_t {
     uint32_t rows = 0;
     if (fc >= 0) {
       const int place = fc + lane % C::kChunk, r = fs.row(place);
@@ -463,7 +468,9 @@ __global__ void __launch_bounds__(kThreadsA, kHeld8 ? kQPagedAttnPerSm : kPagedA
       const uint32_t at = head * p.page_rows + in_page;
       if constexpr (kHeld8) {
         const uint32_t i = head * p.page_blocks + p.by_block.of(in_page);
-        rs = row_scale(ok ? __ldg(p.k_scales + i) : 0.f, ok ? __ldg(p.v_scales + i) : 0.f);
+        // (as they are loaded: what is made of them waits for the step that uses them)
+        rs = make_float2(0.f, 0.f);
+        if (ok) rs = make_float2(__ldg(p.k_scales + i), __ldg(p.v_scales + i));
       }
       const uint32_t dst = ring + f_stage * C::kStageBytes;
       constexpr int kPieces = C::kRowBytes / 16, kRowsAtOnce = 32 / kPieces;  // 16-byte pieces of a row
@@ -497,7 +504,7 @@ __global__ void __launch_bounds__(kThreadsA, kHeld8 ? kQPagedAttnPerSm : kPagedA
         }
       }
       f_stage = f_stage + 1 == C::kStages ? 0 : f_stage + 1;
-      fc += C::kStep;
+      fc += kHeld8 && fs.solo >= 0 ? C::kChunk : C::kStep;
       find_chunk();
       look();
     }
@@ -508,11 +515,11 @@ __global__ void __launch_bounds__(kThreadsA, kHeld8 ? kQPagedAttnPerSm : kPagedA
   find_chunk();
   look();
   uint32_t queue[kAhead];
-  RowScale scales[kAhead] = {};  // of row `lane`
+  float2 scales[kAhead] = {};  // of row `lane`: K's, V's
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) queue[i] = fetch(scales[i]);
 
-  Walk walk{u0, u1, s_find[1], (int)s_find[0]};
+  Walk<kHeld8> walk{u0, u1, s_find[1], (int)s_find[0], 0};
   Segment sg;
   int stage = 0;
   // q of the group as the B operand: column g = query head, the contraction index in the
@@ -554,8 +561,15 @@ __global__ void __launch_bounds__(kThreadsA, kHeld8 ? kQPagedAttnPerSm : kPagedA
       q1 = __shfl_sync(0xffffffffu, back, 8 * t + 4);
     }
   };
-  bool more = walk.next(p, sg);
-  load_q();
+  // the next segment that this warp has a part in
+  auto next_segment = [&]() {
+    bool any;
+    do any = walk.next(p, sg);
+    while (kHeld8 && any && sg.solo >= 0 && sg.solo != wid);
+    return any;
+  };
+  bool more = next_segment();
+  if (more) load_q();
   while (more) {
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2t, 2t + 1
     // 8 bits: the largest score + log2 of V's scale.  What V is multiplied with is relative to this one.
@@ -566,11 +580,12 @@ __global__ void __launch_bounds__(kThreadsA, kHeld8 ? kQPagedAttnPerSm : kPagedA
     for (int i = 0; i < HD / 16; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) o[i][q] = 0.f;
-    for (int c0 = sg.first + wid * C::kChunk; c0 < sg.end; c0 += C::kStep) {
+    const bool solo = kHeld8 && sg.solo >= 0;
+    for (int c0 = sg.first + (solo ? 0 : wid * C::kChunk); c0 < sg.end; c0 += solo ? C::kChunk : C::kStep) {
       cp_async_wait<kAhead - 1>();
       __syncwarp();
       const uint32_t rows = queue[0];
-      const RowScale rs = scales[0];
+      const RowScale rs = row_scale(scales[0].x, scales[0].y);
       seen |= rows;
       const uint32_t kb = ring + stage * C::kStageBytes, vb = kb + C::kChunk * C::kRowBytes;
       stage = stage + 1 == C::kStages ? 0 : stage + 1;
@@ -752,6 +767,19 @@ __global__ void __launch_bounds__(kThreadsA, kHeld8 ? kQPagedAttnPerSm : kPagedA
       l0 += __shfl_xor_sync(0xffffffffu, l0, q);
       l1 += __shfl_xor_sync(0xffffffffu, l1, q);
     }
+    if (solo) {  // all of the item: no other warp to wait for
+      const float inv0 = inverse_sum(seen ? l0 : kNoKeys), inv1 = inverse_sum(seen ? l1 : kNoKeys);
+      uint16_t* const to = p.out + sg.s * p.out_seq + (sg.h * p.group + 2 * t) * p.out_head + HD / 8 * g;
+#pragma unroll
+      for (int i = 0; i < HD / 16; ++i) {
+        if (2 * t < p.group) *reinterpret_cast<uint32_t*>(to + 2 * i) = El::pack(o[i][0] * inv0, o[i][2] * inv0);
+        if (2 * t + 1 < p.group)
+          *reinterpret_cast<uint32_t*>(to + p.out_head + 2 * i) = El::pack(o[i][1] * inv1, o[i][3] * inv1);
+      }
+      more = next_segment();
+      if (more) load_q();
+      continue;
+    }
     if (g == 0) {
       s_m[wid][2 * t] = m0;
       s_m[wid][2 * t + 1] = m1;
@@ -769,7 +797,7 @@ __global__ void __launch_bounds__(kThreadsA, kHeld8 ? kQPagedAttnPerSm : kPagedA
     };
     put(0);
     const Segment done = sg;
-    more = walk.next(p, sg);
+    more = next_segment();
     if (more) load_q();
     __syncthreads();
     const bool whole = done.ta == 0 && done.tb == done.tiles;

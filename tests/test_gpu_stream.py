@@ -323,6 +323,18 @@ def test_many_short_sequences(block):
     check_decode(cache, q, table, lens, 8, "fp16", 40, 2, got)
 
 
+@pytest.mark.parametrize("kind,hd,window,sinks", [("bf16", 64, 0, 0), ("fp16", 128, 70, 30)])
+def test_a_batch_of_more_items_than_blocks(kind, hd, window, sinks):
+    """Items of one to three tiles that a warp does alone, between longer ones."""
+    rng = np.random.default_rng(13)
+    lens = [int(n) for n in rng.integers(0, 230, 640)]
+    lens[100], lens[400] = 1500, 700
+    cache, q, table = decode_case(kind, 8, 4, hd, 16, lens, block=16, seed=13)
+    got = cache.attention(0, q, window=window, sinks=sinks)
+    cache.sync()
+    check_decode(cache, q, table, lens, 16, kind, window, sinks, got)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
 def test_long_and_ragged_batches_over_8_bits(kind):
     """More parts of an item than are joined at once, and scales far apart within a sequence."""
