@@ -169,7 +169,9 @@ __device__ __forceinline__ Scale scale_of(float max, float temperature) {
   }
   return s;
 }
-// t is rounded to a multiple of 2^-10 by adding 3 x 2^12: the sum's last bits are that multiple
+// t is rounded to a multiple of 2^-10 by adding 3 x 2^12: the sum's last bits are that multiple.  The product is in
+// the same operation (one rounding), wherever a logit's class is asked for: the compiler is free to join a packed
+// product and sum, and steps that did not agree on a class would lose tokens.
 constexpr float kRound = 12288.f;
 constexpr int kRoundBits = 0x46400000;
 
@@ -185,7 +187,7 @@ __device__ __forceinline__ void weights_of(const Scale& s, const uint32_t* table
   // t = h - q
   const uint64_t h = mul2(d, c_hi);
   const uint64_t q = fma2(e, n_hi, fma2(d, n_lo, fma2(d, n_hi, h)));
-  const uint64_t y = add2(h, pair(kRound, kRound));
+  const uint64_t y = fma2(d, c_hi, pair(kRound, kRound));
   const uint64_t f = fma2(add2(y, pair(-kRound, -kRound)), minus, h);  // exact, at most 2^-11
   const uint64_t r = fma2(q, minus, f);
   // 2^-r = 1 - g, g = u - u^2 / 2 + u^3 / 6, u = r ln 2 < 2^-11.5; the next term is below 2^-50
@@ -212,14 +214,14 @@ __device__ __forceinline__ uint64_t weight_of(const Scale& s, const uint32_t* ta
   weights_of(s, table, x, -INFINITY, w, unused, i, j);
   return w;
 }
-// t in units of 2^-10, as weights_of has it (one rounding each)
+// t in units of 2^-10, as weights_of has it
 __device__ __forceinline__ int log2_below(const Scale& s, float x) {
-  return __float_as_int(__fadd_rn(__fmul_rn(s.max - x, s.hi), kRound)) - kRoundBits;
+  return __float_as_int(__fmaf_rn(__fsub_rn(s.max, x), s.hi, kRound)) - kRoundBits;
 }
 __device__ __forceinline__ void log2_below(const Scale& s, float2 x, int& i0, int& i1) {
   const uint64_t d = fma2(pair(x.x, x.y), pair(-1.f, -1.f), pair(s.max, s.max));
   float y0, y1;
-  unpair(add2(mul2(d, pair(s.hi, s.hi)), pair(kRound, kRound)), y0, y1);
+  unpair(fma2(d, pair(s.hi, s.hi), pair(kRound, kRound)), y0, y1);
   i0 = __float_as_int(y0) - kRoundBits;
   i1 = __float_as_int(y1) - kRoundBits;
 }

@@ -599,6 +599,43 @@ def test_large_vocabularies():
             assert run_draw(x, u, **par) <= 1
 
 
+def edges(t, top, grid):
+    """Logits of the grid whose class (16 of 2^-10 of log2 of the weight) depends on whether the product with
+    log2(e) / t is rounded before the sum that rounds it to 2^-10."""
+    c = np.float32(1.44269502162933349609375) / np.float32(t)
+    d = (np.float32(top) - grid).astype(np.float32)
+    apart = ((d * c).astype(np.float32) + np.float32(12288)).astype(np.float32).view(np.int32) >> 4
+    at_once = (d.astype(np.float64) * np.float64(c) + 12288).astype(np.float32).view(np.int32) >> 4
+    return grid[(apart != at_once) & (d * c < 15)]
+
+
+def test_logits_on_the_edges_of_classes():
+    """Every step of a draw has to give a logit the same class: the border lies among logits on an edge."""
+    torch, _ = _mods()
+    rng = np.random.default_rng(21)
+    grid = np.arange(-4000, 4000).astype(np.float32) / 512     # exact in fp16 and fp32
+    rows, temps, ps = [], [], []
+    while len(rows) < 150:
+        t = np.float32(rng.uniform(0.4, 3.0))
+        for x in edges(t, 8.0, grid)[:3]:
+            row = np.full(3000, -6.0, np.float32)
+            at = rng.permutation(np.arange(8, 3000))
+            n = int(rng.choice([100, 900]))                    # in front: with and without them in the list
+            row[7], row[at[:120]], row[at[120:120 + n]] = 8.0, x, min(8.0, x + 0.5)
+            w = np.exp((row.astype(np.float64) - 8) / t)
+            rows.append(row)
+            temps.append(float(t))
+            ps.append(float((w[row > x].sum() + 0.4 * w[row == x].sum()) / w.sum()))
+    x, u = torch.from_numpy(np.stack(rows)).cuda(), rng.random(len(rows))
+    # The target is the sum that ends with the 48th of the 120, up to top_p's rounding to fp32, and so within 3000 x 2^-43
+    # of a border for sum(3000 x 2^-43 / (half a step of top_p)) = 2.3 of the rows on average, by the inputs alone: the
+    # number follows Poisson's law, and exceeds 8 once in 2,000 times.
+    for dtype in (torch.float32, torch.float16):
+        assert run_draw(x.to(dtype), u, temperature=temps, top_p=ps) <= 8
+        k = [int((r > 0).sum()) + 9 for r in rows]
+        assert run_draw(x.to(dtype), u, temperature=temps, top_k=k, top_p=[0.95] * len(k)) <= 2
+
+
 def test_borders_far_below_the_largest_logit():
     """One logit far above a broad body: the border lies where the first histogram has its last class."""
     for vocab, dtype, spike in ((3000, "fp32", 22.0), (60000, "fp32", 26.0), (131072, "bf16", 24.0), (40000, "fp32", 60.0)):
