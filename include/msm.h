@@ -755,7 +755,7 @@ msm_status msm_prompt_attention_sinks(const msm_prompt* prompt, int sinks, void*
  *   kept       device int32 [n_rows] or NULL: how many tokens are kept (0 beside -1)
  * Host errors: MSM_ERR_INVALID_ARG (NULL or misaligned pointers, sizes below 1 - n_rows = 0 does nothing -,
  * a negative stride, another dtype), MSM_ERR_UNSUPPORTED (vocab above 2^20, 2^24 rows or more).
- * One launch, no workspace; the logits are read once up to 409,600 of them.
+ * One launch, no workspace; the logits are read once up to about 400,000 (MSM_FP32) or 800,000 of them.
  */
 typedef struct {
   int device;

@@ -32,11 +32,12 @@
 // products; V's codes of two rows are interleaved by a byte permutation first, so that one conversion gives the
 // pair that the product wants.  K's scale multiplies the score, V's the weight.  Weights times V's scale
 // can lie anywhere, so they are relative to a maximum of their own, that of score + log2(scale), and the
-// output is brought back to the scores' maximum at the end of a segment.  Measured: 131,071 rows 53 - 55 us (5,000
+// output is brought back to the scores' maximum at the end of a segment.  An item of few tiles is done by one
+// warp alone, without the block's barriers (PagedAttn::solo_tiles).  Measured: 131,071 rows 55 us (5,000
 // GB/s: 38 us at 7,000 GB/s between 3 us of start and 6 us of join), 64 sequences of 1 to 8,192 rows 34 us (3,300
-// GB/s; bound by the ends of 512 items and by the chain of a step's products, exchanges and exponentials with two
-// warps per scheduler: leaving out the conversions changed nothing, leaving out the loads 5 %).  Three blocks per SM:
-// 58 and 33 us, and with chunks of 16 rows 64 and 39.
+// GB/s), 512 sequences of 30 rows 27 us.  The ragged batch is bound by the ends of its 512 items and by the chain of
+// a step's products, exchanges and exponentials with two warps per scheduler: leaving out the conversions changed
+// nothing, leaving out the loads 5 %.  Three blocks per SM: 58 and 33 us, and with chunks of 16 rows 64 and 39.
 
 #include <atomic>
 #include <type_traits>

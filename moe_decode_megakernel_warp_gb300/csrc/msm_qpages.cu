@@ -16,7 +16,7 @@
 // a block of rows, so no atomics.
 //
 // On one GB300 50,000 tokens of 8 heads of 128 in blocks of 16 rows take 51 us on the GPU (6,000 GB/s; the resize in front
-// of them 8), in blocks of 64 rows 55, of 256 rows 120.  K and V apart, a warp each: 60 us (the way from a token to its
+// of them 8, of which its launch hides some), in blocks of 64 rows 55, of 256 rows 120.  K and V apart, a warp each: 60 us (the way from a token to its
 // page is a chain of loads, which the two then share); rows loaded before it is known which of
 // the group's tokens begins a block: 72.
 #include "msm_attn.cuh"

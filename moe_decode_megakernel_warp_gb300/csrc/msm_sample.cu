@@ -24,11 +24,12 @@
 //
 // Bound by instructions and by the chain of steps, not by memory (the logits of 500 rows are 7 us of DRAM): a weight is
 // some 35 instructions, and top-p without top-k needs every logit's, those of the kept ones a second time for the draw.
-// Measured on one GB300: one row of 32,003 fp32 logits, top-k 50 and top-p 14.3 us (10 us of steps, each 0.5 to 1.5 us:
+// Measured on one GB300: one row of 32,003 fp32 logits, top-k 50 and top-p 12.5 us (some 8 us of steps, each 0.5 to 1.5 us:
 // cluster barriers, reads of other blocks' memory, the sort of the list); 64 rows of 131,072 with settings of their
-// own 64 us; 500 rows of 50,021 bf16 logits, top-p alone 171 us (ALU 46 %; the histogram takes 38 % of a block's time,
-// the sums for the draw 19 %, gathering the border's class 12 %).  256 threads a block, four blocks per SM: 190 us; counts
-// and weights together where top-k is given 78 instead of 64 us.
+// own 60 us; 500 rows of 50,021 bf16 logits, top-p alone 159 us (ALU 46 %; the histogram takes two fifths of a block's time,
+// the sums for the draw a fifth, gathering the border's class an eighth).  256 threads a block, four blocks per SM: a tenth
+// slower; counts and weights together where top-k is given 78 us where counts alone took 64 (64 rows); the rows behind
+// the last full round of clusters in a launch of their own with more blocks each: 174 us where one launch takes 159.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -49,7 +50,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBlocksPerSm = 1024 / kThreads;
 constexpr int kBins = 1024;
 constexpr int kBinsPerThread = kBins / kThreads;
-constexpr int kList = kThreads;           // candidates that are sorted
+constexpr int kList = kThreads;       // candidates that are sorted
 constexpr int kSegs = 128;            // segments of a slice, in the order of the index
 constexpr int kMaxCluster = 8;
 constexpr int kBits = 42;             // weights are multiples of 2^-42 ...
