@@ -1148,6 +1148,8 @@ template <class T>
 cudaError_t launch(SampleArgs p, int sms, int most_smem, cudaStream_t s) {
   // Blocks per row: more of them while the rows alone leave SMs idle or a slice is so large that only one
   // block fits an SM; a slice has at least 2,048 logits (a cluster's barriers cost what its blocks save).
+  // With 2, 4 and 8 blocks: one row of 32,003 logits 16.7, 14.6 and 12.6 us, 64 rows of 131,072 170, 79 and 61,
+  // 500 rows of 50,021 in 16 bits 159, 210 and 336; the rule takes 8, 8 and 2.
   const int fixed = (int)(sizeof(Shared) + 15) / 16 * 16;
   constexpr int kLeast = 2048, kShare = 224 * 1024 / kBlocksPerSm;
   int blocks = 1;

@@ -138,6 +138,8 @@ def attend_seen(q, k, v, see, scale, kind, weight=None, least=0.0, big=None):
             t += least * (p * f).max(1, keepdims=True) * (see @ codes)[:, None]
         elif least:
             t += least * (see @ np.abs(vv)) / l
+        if kind == "fp16":
+            t += 2.0 ** -25  # half a step of a subnormal result
         out[rows, h], tol[rows, h] = o, t
     return out, tol * (1 + 2 * u) + 1e-30
 
