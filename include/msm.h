@@ -656,8 +656,9 @@ msm_status msm_qpages_sync(const msm_qpages* pages, void* stream);
  * with amax <= 448 s (0 for amax = 0) is what they need.  A block whose first row is new takes it as its scale.
  * In one that begins with older rows of the sequence the scale becomes the larger of it and the old one,
  * and where that is larger than the old one the older codes are multiplied by old / new in 32 bits and rounded
- * again.  New elements are divided by the scale and rounded to nearest even, infinities to +-448, NaN stays
- * NaN.  (Between powers of two the older codes lose bits below 2^-6 of the scale only.)
+ * again.  New elements are divided by the scale and rounded to nearest even, infinities to +-448 (in a block of
+ * scale 0, too, where their value is 0), NaN stays NaN.  (Between powers of two the older codes lose bits below 2^-6 of
+ * the scale only.)
  */
 msm_status msm_qpages_write(const msm_qpages* pages, int layer, int dtype, const void* k, const void* v,
                             int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,

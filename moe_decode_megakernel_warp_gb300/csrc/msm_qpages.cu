@@ -248,8 +248,9 @@ __global__ void __launch_bounds__(threads(kWarps), 512 / threads(kWarps))
           }
         }
       }
-      // (behind a scale below 2^-126 no new element but 0 is finite, and the scale's reciprocal may not be: 0 stays 0)
-      const float inverse = now >= 0x1p-126f ? 1.f / now : now > 0.f ? 1.f : 0.f;
+      // (with a scale below 2^-126, 0 among them, the only finite new element is 0, and the scale's reciprocal may not be
+      // finite: 0 stays 0, and infinities become +-448)
+      const float inverse = now >= 0x1p-126f ? 1.f / now : 1.f;
       auto store = [&](const auto& y, int i0) {
         uint8_t* const to = rows + (int64_t)(older + i0 + sub) * HD + c * 8;
 #pragma unroll
