@@ -5,20 +5,23 @@
 // With amax the largest finite magnitude of a block's new rows, the least power of two s with
 // amax <= 448 s is what they need.  A block without older rows takes it; one with older rows keeps the
 // larger of it and what it has, and where that grows the older codes are multiplied by old / new and
-// rounded again.  Between powers of two this loses nothing but bits of values below 2^-6 of the scale
-// (a floating-point code has the same 4 bits at every size), so rows that come one at a time end up as
-// rows that come together do, up to those.
+// rounded again.  New elements are divided by the scale, exactly: a power of two has an exact reciprocal, and
+// with other scales, which only a cache from elsewhere has, the remainder decides (quotient).  Between powers
+// of two this loses nothing but bits of values below 2^-6 of the scale (a floating-point code has the same 4
+// bits at every size), so rows that come one at a time end up as rows that come together do, up to those.
 //
 // Bound by memory for prompts (2 bytes read, 1 written per element) and by latency for a step's few
 // tokens.  A unit, one to eight warps, takes the blocks of rows that begin among `group` tokens, K and V of
-// one head.  The rows' loads are on their way while the page is looked up, and stay in registers from the search for the
-// largest element until they are stored (a second read where a block has more rows than that).  No two units meet in
-// a block of rows, so no atomics.
+// one head.  The rows' loads are on their way while the page is looked up, and stay in registers from the
+// search for the largest element until they are stored (a second read where a block has more rows than that).
+// No two units meet in a block of rows, so no atomics.
 //
-// On one GB300 50,000 tokens of 8 heads of 128 in blocks of 16 rows take 51 us on the GPU (6,000 GB/s; the resize in front
-// of them 8, of which its launch hides some), in blocks of 64 rows 55, of 256 rows 120.  K and V apart, a warp each: 60 us (the way from a token to its
-// page is a chain of loads, which the two then share); rows loaded before it is known which of
-// the group's tokens begins a block: 72.
+// On one GB300 50,000 tokens of 8 heads of 128 in blocks of 16 rows take 52 - 54 us on the GPU (5,700 - 5,900 GB/s;
+// the resize in front of them 8, of which its launch hides some), in blocks of 64 rows 54 - 57, of 256 rows
+// 126.  How many warps share a unit follows the tokens per slot of the table, so a prompt in a table of many
+// empty slots is slow in long blocks: 4,096 tokens among 512 slots in blocks of 256 rows 102 us.
+// K and V apart, a warp each: 60 us (the way from a token to its page is a chain of loads, which the two then
+// share); rows loaded before it is known which of the group's tokens begins a block: 72.
 #include "msm_attn.cuh"
 #include "msm_paged.h"
 
@@ -46,18 +49,35 @@ __device__ __forceinline__ void unpack_e4m3(uint32_t x, float (&f)[4]) {
   f[3] = Fp16::value((uint16_t)(hi >> 16));
 }
 
-// four 16-bit elements times s
+// x / s for the rounding to a code, with `inverse` the rounded 1 / s: a number on the same side of every border between two
+// codes as the exact quotient, or on it with that.  Such a border has at most 5 bits.  The product rounded to 12 bits is either a border
+// or has none between itself and the exact quotient (less than a step of 12 bits away), and which side of it that lies on
+// is the sign of x - t s, which one operation gives.  (s from 2^-60 on, so that it does not vanish.)
+__device__ __forceinline__ float quotient(float x, float s, float inverse) {
+  const float q = x * inverse;
+  const uint32_t t = (__float_as_uint(q) + 0x800u) & 0xFFFFF000u;
+  const float rest = fmaf(-__uint_as_float(t), s, x);
+  const uint32_t beside = (t ^ __float_as_uint(rest)) >> 31 ? t - 1 : t + 1;
+  return rest == 0.f ? __uint_as_float(t) : fabsf(rest) > 0.f ? __uint_as_float(beside) : q;  // (q: an infinity, NaN)
+}
+
+// four 16-bit elements
 template <class El>
-__device__ __forceinline__ uint32_t scaled_e4m3(uint32_t x, uint32_t y, float s) {
-  float a, b, c, d;
+__device__ __forceinline__ void four(uint32_t x, uint32_t y, float (&f)[4]) {
   if constexpr (El::kBf16) {
-    a = __uint_as_float(x << 16), b = __uint_as_float(x & 0xFFFF0000u);
-    c = __uint_as_float(y << 16), d = __uint_as_float(y & 0xFFFF0000u);
+    f[0] = __uint_as_float(x << 16), f[1] = __uint_as_float(x & 0xFFFF0000u);
+    f[2] = __uint_as_float(y << 16), f[3] = __uint_as_float(y & 0xFFFF0000u);
   } else {
     const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&x)), q = __half22float2(*reinterpret_cast<const __half2*>(&y));
-    a = p.x, b = p.y, c = q.x, d = q.y;
+    f[0] = p.x, f[1] = p.y, f[2] = q.x, f[3] = q.y;
   }
-  return pack_e4m3(a * s, b * s, c * s, d * s);
+}
+// times s
+template <class El>
+__device__ __forceinline__ uint32_t scaled_e4m3(uint32_t x, uint32_t y, float s) {
+  float f[4];
+  four<El>(x, y, f);
+  return pack_e4m3(f[0] * s, f[1] * s, f[2] * s, f[3] * s);
 }
 
 // the least power of two that amax / 448 does not exceed, at least 2^-126; 0 for 0
@@ -248,27 +268,48 @@ __global__ void __launch_bounds__(threads(kWarps), 512 / threads(kWarps))
           }
         }
       }
-      // (with a scale below 2^-126, 0 among them, the only finite new element is 0, and the scale's reciprocal may not be
-      // finite: 0 stays 0, and infinities become +-448)
-      const float inverse = now >= 0x1p-126f ? 1.f / now : 1.f;
-      auto store = [&](const auto& y, int i0) {
-        uint8_t* const to = rows + (int64_t)(older + i0 + sub) * HD + c * 8;
+      // New elements over the scale.  A power of two from 2^-126 on has an exact reciprocal, whose bits are those of 2^127 less its
+      // own.  With a scale below that, 0 among them, the only finite new element is 0: 0 stays 0, and infinities become +-448.
+      const uint32_t bits = __float_as_uint(now);
+      uint8_t* const to = rows + (int64_t)(older + sub) * HD + c * 8;
+      if (bits <= 1u << 23 || (bits << 9 == 0 && bits < 254u << 23)) {
+        const float inverse = bits >= 1u << 23 ? __uint_as_float((254u << 23) - bits) : 1.f;
+        auto store = [&](const auto& y, int i0) {
 #pragma unroll
-        for (int i = 0; i < (int)(sizeof(y) / sizeof(y[0])); ++i)
-          if (i0 + i * kRows + sub < n) {
-            uint2 o;
-            o.x = scaled_e4m3<El>(y[i].x, y[i].y, inverse);
-            o.y = scaled_e4m3<El>(y[i].z, y[i].w, inverse);
-            *reinterpret_cast<uint2*>(to + i * kRows * HD) = o;
-          }
-      };
-      store(x[side], 0);
-      if constexpr (kLong) {
+          for (int i = 0; i < (int)(sizeof(y) / sizeof(y[0])); ++i)
+            if (i0 + i * kRows + sub < n) {
+              uint2 o;
+              o.x = scaled_e4m3<El>(y[i].x, y[i].y, inverse);
+              o.y = scaled_e4m3<El>(y[i].z, y[i].w, inverse);
+              *reinterpret_cast<uint2*>(to + (int64_t)i0 * HD + i * kRows * HD) = o;
+            }
+        };
+        store(x[side], 0);
+        if constexpr (kLong) {
 #pragma unroll 1
-        for (int i0 = kIn; i0 < n; i0 += kMore * kRows) {
-          uint4 y[kMore];
+          for (int i0 = kIn; i0 < n; i0 += kMore * kRows) {
+            uint4 y[kMore];
+            load(is_v, i0, y);
+            store(y, i0);
+          }
+        }
+      } else {
+        // Any other scale is one that the block came with, and divides.  (A row at a time, read again, so that this takes few
+        // registers of the way above: 50,000 tokens in blocks of 16 rows 53.6 -> 54.3 us, of 64 56.3 -> 57.1, of 256 119 -> 126.
+        // As a function, or behind all stores, 3 to 55 us.)
+        const float up = now < 0x1p-60f ? 0x1p64f : 1.f, by = now * up, inverse = 1.f / by;
+#pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += kRows) {
+          uint4 y[1];
           load(is_v, i0, y);
-          store(y, i0);
+#pragma unroll 1
+          for (int q = 0; q < 2 && i0 + sub < n; ++q) {
+            float f[4];
+            four<El>(q ? y[0].z : y[0].x, q ? y[0].w : y[0].y, f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = quotient(f[i] * up, by, inverse);
+            *reinterpret_cast<uint32_t*>(to + (int64_t)i0 * HD + 4 * q) = pack_e4m3(f[0], f[1], f[2], f[3]);
+          }
         }
       }
       // (every thread has read the old one: there was a barrier since)

@@ -31,6 +31,64 @@ def test_zeros_behind_rows_of_the_smallest_scales(kind, scale):
     assert not c.gpu.attention(0, randn(kind, 2, 4, 64, seed=3).cuda()).isnan().any()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,hd,older,new", [(16, 64, 3, 1), (16, 128, 3, 13), (100, 128, 30, 60), (300, 128, 100, 190),
+                                               (70, 64, 1, 69)])
+def test_quotients_next_to_the_borders_of_codes(kind, rows, hd, older, new):
+    """Blocks that keep a scale which is no power of two: elements that lie on a border between two codes but for the
+    rounding of the scale, and any others.  (The reference's quotient has 53 bits.  An element has at most 11 and a scale 24, so
+    a quotient that is not on a border is at least 2^-30 of itself away from it: the reference decides all of them.)"""
+    torch, _ = _mods()
+    rng = np.random.default_rng(rows + new)
+    n, heads = 12, 3
+    c = Both(rng, 1, n, rows, rows, heads, hd, n, 1, kind)
+    c.call("resize", [older] * n)
+    c.write([older] * n, 1)
+    digits, least, most = (128, -60, 60) if kind == "bf16" else (1024, -18, -8)
+    unit = rng.integers(digits, 2 * digits, (n, 2 * heads)) * 2.0 ** rng.integers(least, most, (n, 2 * heads))
+    tie = rng.integers(8, 16, (n, 2 * heads)) * 2 + 1                              # 17 .. 31: halfway between codes 8 .. 16
+    step = rng.integers(-1, 2, (n, 2 * heads))
+    scale = (unit / (tie / 16.0)).astype(np.float32)
+    scale = (scale.view(np.int32) + step.astype(np.int32)).view(np.float32)     # the nearest one and its neighbours
+    page = c.ref.table[:, 0]
+
+    def make(i, shape):
+        s = np.ones(shape, np.float32)
+        s[page, :, 0] = scale[:, i * heads:(i + 1) * heads]
+        return s
+    set_scales(c, make)
+
+    def change(kv):
+        shape = (n, new, 2 * heads, hd)
+        x = unit[:, None, :, None] * 2.0 ** rng.integers(-9, 7, shape) * rng.choice([-1.0, 1.0], shape)
+        other = scale[:, None, :, None] * rng.uniform(-220.0, 220.0, shape) * 2.0 ** rng.integers(-10, 1, shape)
+        x = np.where(rng.random(shape) < 0.6, x, other)
+        x = torch.from_numpy(x.reshape(n * new, 2 * heads, hd)).to(kv.dtype)
+        kv[:n * new] = x
+    c.call("resize", [older + new] * n)
+    c.write([new] * n, 2, change=change)
+    assert np.array_equal(c.ref.scales[0][page, :, 0], scale[:, :heads])        # (none of the rows made them grow)
+
+
+@pytest.mark.parametrize("rows,block,older,new", [(16, 8, 3, 5), (100, 100, 40, 50), (300, 300, 250, 40)])
+def test_scales_that_are_no_powers_of_two_grow_and_stay(rows, block, older, new):
+    """Scales as a cache may have that was quantised elsewhere (the largest magnitude over 448).  (20 bits of them, so that a code,
+    4 bits, times old / new has the 24 that the product is taken in.)"""
+    rng = np.random.default_rng(rows)
+    c = Both(rng, 1, 8, rows, block, 2, 128, 4, 2)
+    c.call("resize", [older] * 4)
+    c.write([older] * 4, 1)
+
+    def make(i, shape):
+        s = (rng.uniform(0.3, 4.0, shape) / 448).astype(np.float32)
+        return (s.view(np.uint32) & np.uint32(0xFFFFFFF0)).view(np.float32)
+    set_scales(c, make)
+    for step, sizes in enumerate((0.02, 1.0, 40.0)):
+        old = c.ref.lens.copy()
+        c.call("resize", [int(n) + new for n in old] if step < 1 else [int(n) + 1 for n in old])
+        c.write(c.ref.lens - old, step + 2, sizes=sizes)
+
+
 def write_special(kind, rows, older, new, pattern, old_scale):
     """Codes and scales after rows of zeros with some special elements, behind `older` rows."""
     torch, msm = _mods()
