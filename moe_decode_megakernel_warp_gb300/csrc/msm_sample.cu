@@ -230,9 +230,9 @@ __device__ __forceinline__ void log2_below(const Scale& s, float2 x, int& i0, in
 __device__ __forceinline__ int bin_of(int i) { return min(i >> 4, kBins - 1); }
 __device__ __forceinline__ int bin_of(const Scale& s, float x) { return bin_of(log2_below(s, x)); }
 
-// x sum, rounded down or up: x is 0 .. 1, the sum below 2^63 (the product has 24 + 63 bits)
+// x sum, rounded down or up: x is 0 .. 1 or -0, the sum below 2^63 (the product has 24 + 63 bits)
 __device__ __forceinline__ uint64_t part_of(float x, uint64_t sum, bool up) {
-  const uint32_t b = __float_as_uint(x), e = b >> 23;
+  const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu, e = b >> 23;
   const uint64_t m = e ? (b & 0x7FFFFFu) | 0x800000u : b & 0x7FFFFFu;
   const int shift = 150 - (int)(e ? e : 1);  // x = m 2^-shift, shift >= 23
   const uint64_t lo = m * sum, hi = __umul64hi(m, sum);

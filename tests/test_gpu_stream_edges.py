@@ -1,9 +1,11 @@
-"""Writes into 8-bit blocks whose scales come from elsewhere, against the reference in stream_reference.py."""
+"""Writes into 8-bit blocks whose scales come from elsewhere, and sampling with the numbers at the ends of their ranges, against
+the reference in stream_reference.py."""
 import numpy as np
 import pytest
 
-from test_gpu_paged import _mods, ints, randn
-from test_gpu_stream import Both, INF, NAN, codes
+from stream_reference import draw
+from test_gpu_paged import _mods, f64, ints, randn
+from test_gpu_stream import Both, INF, NAN, codes, logits
 
 pytestmark = pytest.mark.gpu
 
@@ -132,3 +134,28 @@ def test_infinities_where_nothing_else_gives_a_scale(kind, rows, older, new):
             assert code[new - 1, 7] & 0x7F == 0x7F
             code[new - 1, 7] = 0
             assert np.array_equal(code, want) and scale == np.float32(old_scale if older else 0.0)
+
+
+# ------------------------------------------------------------------ sampling
+def test_zeros_of_either_sign():
+    """-0 is 0, as temperature, top-p, min-p and random number."""
+    torch, msm = _mods()
+    for vocab in (5, 3000, 40000):
+        x, u = logits(6, vocab, "fp32", vocab)
+        plus, minus = torch.zeros(6, device="cuda"), torch.full((6,), -0.0, device="cuda")
+        ud = torch.as_tensor(u, dtype=torch.float32).cuda()
+        for name in ("temperature", "top_p", "min_p", "random"):
+            got = []
+            for z in (plus, minus):
+                kept, probs = torch.full((6,), -7, dtype=torch.int32, device="cuda"), torch.full((6,), NAN, device="cuda")
+                par = dict(random=ud, kept=kept, probs=probs)
+                par[name] = z
+                if name == "random":
+                    par["top_p"] = torch.full((6,), 0.7, device="cuda")
+                got.append((msm.sample(x, **par), kept, probs))
+            for a, b in zip(*got):
+                assert torch.equal(a, b), name
+            host = {name: -0.0} if name != "random" else dict(top_p=float(np.float32(0.7)))
+            for i in range(6):
+                want = draw(f64(x[i]), -0.0 if name == "random" else float(ud[i]), **host)
+                assert (int(got[1][0][i]), int(got[1][1][i])) == want[:2], (name, i)
