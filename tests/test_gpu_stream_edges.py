@@ -137,6 +137,116 @@ def test_infinities_where_nothing_else_gives_a_scale(kind, rows, older, new):
 
 
 # ------------------------------------------------------------------ sampling
+def drawn(x, u, **par):
+    """Draws and compares every row; (tokens, kept, rows too near a border to be decided).  A weight w is off by at most
+    1.1 x 2^-30 w (two roundings of 1/2 .. 1 to 2^-31) + 2^-43 (the largest logit's by nothing), so sums, which are at least 1, by 1.1 x 2^-30
+    of the share of the others + 2^-43 for each of them.  Borders nearer than that are not compared.  (min_p is one that no
+    weight is near to.)"""
+    torch, msm = _mods()
+    n = len(x)
+    kept, probs = torch.full((n,), -7, dtype=torch.int32, device="cuda"), torch.full((n,), NAN, device="cuda")
+    dev = {k: torch.tensor(np.asarray(v), dtype=torch.int32 if k == "top_k" else torch.float32).cuda() for k, v in par.items()}
+    u = torch.as_tensor(np.asarray(u), dtype=torch.float32).cuda()
+    tokens = msm.sample(x, u, probs=probs, kept=kept, **dev).cpu().numpy()
+    kept, probs = kept.cpu().numpy(), probs.cpu().double().numpy()
+    host = {k: v.cpu().double().numpy() for k, v in dev.items()}
+    rows, close = f64(x), 0
+    for i, row in enumerate(rows):
+        one = {k: int(v[i]) if k == "top_k" else float(v[i]) for k, v in host.items()}
+        token, m, p, room, near = draw(row, float(u[i].double()), **one)
+        if "min_p" in one:
+            near = draw(row, 0.5, **{k: v for k, v in one.items() if k != "min_p"})[4]
+        t, top = one.get("temperature", 1.0), np.nanmax(row)
+        with np.errstate(invalid="ignore", over="ignore"):
+            w = np.exp(np.where(row == top, 0.0, (row - top) / t)) if t else (row == top) * 1.0
+        w = np.nan_to_num(w, nan=0.0)
+        limit = 1.1 * 2.0 ** -30 * (1 - (w == 1).sum() / max(1.0, w.sum())) + 2.0 ** -43 * ((w > 0) & (w < 1)).sum()
+        if min(room, near) <= limit:
+            close += 1
+            continue
+        assert (tokens[i], kept[i]) == (token, m), (i, one, room, near, tokens[i], token, kept[i], m)
+        assert abs(probs[i] - p) <= 2.0 ** -20 * p + 2.0 ** -40, (i, probs[i], p)
+    return tokens, kept, close
+
+
+def tails(n, vocab, many, levels, seed, dtype="fp32"):
+    """Rows of one logit far above `many` others, weights of 2^-17 to 2^-22 of its own at `levels` different values (0: all
+    different), and nothing else: the first histogram's last class begins at 2^-16."""
+    torch, _ = _mods()
+    rng = np.random.default_rng(seed)
+    x = np.full((n, vocab), -INF, np.float32)
+    for i in range(n):
+        at = rng.permutation(vocab)[:many + 1]
+        t = rng.uniform(17.0, 22.0, levels or many)
+        x[i, at[1:]] = 5.0 - np.log(2.0) * (rng.choice(t, many) if levels else t)
+        x[i, vocab // 2] = 5.0
+    return torch.from_numpy(x).to({"fp32": torch.float32, "bf16": torch.bfloat16}[dtype]).cuda(), rng
+
+
+@pytest.mark.parametrize("vocab,many,levels,dtype", [(3000, 2500, 0, "fp32"), (3000, 2500, 7, "fp32"), (40000, 5000, 0, "fp32"),
+                                                     (60000, 8000, 300, "fp32"), (131072, 8000, 0, "bf16"), (9000, 400, 0, "fp32")])
+def test_borders_and_draws_among_the_smallest_weights(vocab, many, levels, dtype):
+    """The border of top-k, top-p and min-p and the token lie in the first histogram's last class.  Borders of sums are some
+    2^-19.5 of the sum apart, 1,000 times what decides, and min-p's number lies between two weights: of a case's 128 rows and 250
+    borders 0.7 at most are too near one on average."""
+    n = 16
+    x, rng = tails(n, vocab, many, levels, vocab + many + levels, dtype)
+    w = np.exp(f64(x) - 5.0)
+    tail = (w.sum(1) - 1) / w.sum(1)
+    front = w[:, :vocab // 2].sum(1) / w.sum(1)
+    u = front * rng.uniform(0.001, 0.2, n)      # a token in front of the large one, where the border leaves enough of them
+    p = 1 - tail * rng.uniform(0.1, 0.9, n)
+    k = rng.integers(many // 8, many, n)
+    m = []
+    for i in range(n):                          # halfway between two weights, of the wider half of the gaps
+        v = np.unique(w[i][(w[i] > 0) & (w[i] < 1)])
+        gaps = np.diff(v)
+        g = rng.choice(np.flatnonzero(gaps >= np.median(gaps)))
+        m.append((v[g] + v[g + 1]) / 2)
+    near = others = 0
+    for par in ({}, dict(top_p=p), dict(top_k=k), dict(top_k=k, top_p=p), dict(min_p=m), dict(top_k=k, min_p=m),
+                dict(top_p=p, min_p=m), dict(top_k=k, top_p=p, min_p=m)):
+        tokens, kept, close = drawn(x, u, **par)
+        near += close
+        others += int((tokens != vocab // 2).sum())
+        if par:
+            assert (kept <= many).all() and (kept > 1).mean() > 0.7, par
+    assert near <= 4
+    assert others > 8 * n * 0.6
+
+
+@pytest.mark.parametrize("vocab", [40, 2500, 33000])
+def test_equal_logits_with_borders_between_two_of_them(vocab):
+    """All rows are decided: top-p and the random number lie halfway between borders."""
+    torch, _ = _mods()
+    rng = np.random.default_rng(vocab)
+    n = 12
+    k = rng.integers(1, vocab + 1, n)
+    m = rng.integers(0, vocab, n)
+    j = np.array([rng.integers(0, i + 1) for i in m])
+    for x in (torch.full((n, vocab), 3.25, device="cuda"), torch.full((n, vocab), -7.0, dtype=torch.float16, device="cuda")):
+        tokens, kept, close = drawn(x, (j + 0.5) / (m + 1), top_p=(m + 0.5) / vocab)
+        assert close == 0 and (tokens == j).all() and (kept == m + 1).all()
+        tokens, kept, close = drawn(x, (np.minimum(j, k - 1) + 0.5) / k, top_k=k)
+        assert close == 0 and (tokens == np.minimum(j, k - 1)).all() and (kept == k).all()
+
+
+def test_masked_rows_are_all_decided():
+    """The rows of test_rows_without_a_choice_and_masked_rows (where the border of top-p 0.5 among equal weights lies
+    on the target) with numbers between the borders."""
+    torch, _ = _mods()
+    x, u = logits(10, 5000, "fp32", 1)
+    x[0], x[1], x[2, :], x[2, 4321], x[3, ::2] = -INF, NAN, -INF, -3.0, NAN
+    x[4, 1:], x[5] = torch.finfo(torch.float32).min, torch.finfo(torch.float32).min
+    x[6, 17], x[6, 99], x[7, 5], x[8, 100:] = INF, INF, torch.finfo(torch.float32).max, -INF
+    for y in (x, x.bfloat16()):
+        for par in ({}, dict(top_k=[50] * 10), dict(top_p=[0.8003] * 10), dict(min_p=[0.1] * 10), dict(temperature=[1e-38] * 10),
+                    dict(temperature=[3e38] * 10, top_p=[0.50013] * 10), dict(top_k=[4999] * 10, top_p=[0.99903] * 10)):
+            tokens, _, close = drawn(y, u, **par)
+            none = [0, 1] if y.dtype == torch.float32 else [0, 1, 5]    # (the lowest fp32 value is -inf in bf16)
+            assert close == 0 and list(np.flatnonzero(tokens == -1)) == none, par
+
+
 def test_zeros_of_either_sign():
     """-0 is 0, as temperature, top-p, min-p and random number."""
     torch, msm = _mods()
