@@ -745,14 +745,18 @@ msm_status msm_prompt_attention_sinks(const msm_prompt* prompt, int sinks, void*
  *     random x the sum over all that are kept (random = 1: the last one that has a weight).
  * T = 0 takes the largest logit (the lowest index among equals).  In a row with logits of +inf these alone
  * can be drawn, with equal weights.  Weights are held as multiples of 2^-42 (of the largest; min_p is at least that),
- * so sums are exact and do not depend on timing.
+ * so sums are exact and do not depend on timing: each is off by at most 1.1 x 2^-30 of itself and 2^-43 of the
+ * largest, so that small ones keep few bits, and a border or a number that is nearer to a sum than these errors add up to
+ * may fall to its other side.  (With logits or temperatures beyond 2^110 they have 32-bit floating point's precision, and
+ * differences of logits beyond its largest number count as infinite; temperatures between 0 and 2^-127 count as about that.)
  *   logits     device MSM_FP32, MSM_BF16 or MSM_FP16 [n_rows][vocab], row_stride elements between rows (0:
  *              every row is the same one), aligned to their type
  *   temperature, top_k, top_p, min_p  device [n_rows], fp32 and int32, or NULL for 1, 0 (no limit), 1 and 0
  *   random     device fp32 [n_rows], 0 .. 1
  *   tokens     device int32 [n_rows]: the tokens; -1 for a row without a token that can be drawn, and for one
  *              whose temperature is negative or not finite, or whose top_p, min_p or random is outside 0 .. 1
- *   probs      device fp32 [n_rows] or NULL: the token's probability among those kept (0 beside -1)
+ *   probs      device fp32 [n_rows] or NULL: the token's probability among those kept (0 beside -1), computed in 32
+ *              bits (off by at most 2^-20 of itself)
  *   kept       device int32 [n_rows] or NULL: how many tokens are kept (0 beside -1)
  * Host errors: MSM_ERR_INVALID_ARG (NULL or misaligned pointers, sizes below 1 - n_rows = 0 does nothing -,
  * a negative stride, another dtype), MSM_ERR_UNSUPPORTED (vocab above 2^20, 2^24 rows or more).

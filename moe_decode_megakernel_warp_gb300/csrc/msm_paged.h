@@ -113,12 +113,12 @@ struct PagedAttn {
   float* part;                               // and partial results, two per block
 };
 // what an item costs beside its tiles (PagedAttn::finish).  8 bits: its tiles are cheaper, its end is not (64 sequences of 1
-// to 8,192 rows: 47 us with 1, 37 with 2, 34 with 4, 35 with 6, 37 with 9)
+// to 8,192 rows: 47 us with 1, 37 with 2, 34 with 4, 35 with 6, 37 with 9; that batch alone was looked at, 32 query heads on 8 of 128)
 constexpr int kPagedFinish = 1, kQPagedFinish = 4;
 // 8 bits: most tiles of an item that one warp does alone, which spares the block its barriers (512 sequences of 30 rows 50 -> 26
 // us).  Up to three where there are many items, so that the warps' shares even out (512 of 1 to 200 rows: 66 us without, 63
 // with one, 50 with three, 49 with five), one where there are few (64 of 1 to 8,192: 34 us without, 33 with one, 35 with
-// three, 39 with five).
+// three, 39 with five).  (These two batches were looked at, not head_dim 64, other groups or windows.)
 constexpr int kQPagedSolo = 1, kQPagedSoloMany = 3, kQPagedMany = 8;  // (many: items per block)
 constexpr int kPagedAttnPerSm = 2, kQPagedAttnPerSm = 2;  // blocks per SM (of 16 and of 8 bits)
 size_t paged_attn_workspace(int blocks, int group, int head_dim);

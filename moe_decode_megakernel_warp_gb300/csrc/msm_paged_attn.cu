@@ -35,7 +35,10 @@
 // output is brought back to the scores' maximum at the end of a segment.  An item of few tiles is done by one
 // warp alone, without the block's barriers (PagedAttn::solo_tiles).  Measured: 131,071 rows 55 us (5,000
 // GB/s: 38 us at 7,000 GB/s between 3 us of start and 6 us of join), 64 sequences of 1 to 8,192 rows 34 us (3,300
-// GB/s), 512 sequences of 30 rows 27 us.  The ragged batch is bound by the ends of its 512 items and by the chain of
+// GB/s; on a window of 2,048 with 64 sinks 27 us), 512 sequences of 30 rows 27 us.  These have pages of 64 rows and
+// more: 32 rows that lie in one page are fetched with addresses that differ by constants.  Pages of 16 rows never
+// allow that: 131,071 rows 56 us, the ragged batch 36, and 128 streams of 700 to 8,192 rows on a window of 2,048
+// with 64 sinks 95 where pages of 64 rows take 86.  The ragged batch is bound by the ends of its 512 items and by the chain of
 // a step's products, exchanges and exponentials with two warps per scheduler: leaving out the conversions changed
 // nothing, leaving out the loads 5 %.  Three blocks per SM: 58 and 33 us, and with chunks of 16 rows 64 and 39.
 

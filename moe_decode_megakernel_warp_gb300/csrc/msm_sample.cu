@@ -10,10 +10,13 @@
 //
 // Weights are whole multiples of 2^-42 (of the largest weight), so their sums are exact in 64 bits whatever
 // their order: which token is drawn depends on no thread's timing, and the sums say the same as the
-// definition in 64-bit floating point but for the weights' own rounding, 2^-31 of each.  That matters: a
-// row's 100,000 borders between tokens lie so close that weights of 32-bit floating point draw another token
-// in one of some thousand rows.  w = 2^-t, t = (M - x) log2(e) / T as two floats: t = k + j / 1024 + r, a
-// table of 1,024 entries for j, a polynomial of third degree for r, two logits per instruction.
+// definition in 64-bit floating point but for the weights' own rounding.  That is two roundings of a number of
+// 1/2 .. 1 to 2^-31, together 1.1 x 2^-30 of the weight, and one to 2^-42, which is 2^-43 of the largest weight:
+// below 2^-13 of the largest the second counts (a weight of 2^-38 keeps five bits).  A sum is off by at most
+// 1.1 x 2^-30 of itself and 2^-43 for each of its weights.  That matters: a row's 100,000 borders between tokens
+// lie so close that weights of 32-bit floating point draw another token in one of some thousand rows.
+// w = 2^-t, t = (M - x) log2(e) / T as two floats: t = k + j / 1024 + r, a table of 1,024 entries for j, a
+// polynomial of third degree for r, two logits per instruction.
 //
 // A row belongs to one cluster of up to eight blocks, each with a slice of it in shared memory, so the
 // logits are read once.  The order's border is found without sorting the row: a histogram over 1,024
@@ -23,12 +26,13 @@
 // by index.  Between the steps the blocks exchange sums through distributed shared memory.
 //
 // Bound by instructions and by the chain of steps, not by memory (the logits of 500 rows are 7 us of DRAM): a weight is
-// some 35 instructions, and top-p without top-k needs every logit's, those of the kept ones a second time for the draw.
+// some 35 instructions, and top-p without top-k needs every logit's, those of the kept ones a second time for the draw; and
+// the other blocks of a cluster wait at barriers (the largest stall) while the first one merges, searches and sorts.
 // Measured on one GB300: one row of 32,003 fp32 logits, top-k 50 and top-p 12.5 us (some 8 us of steps, each 0.5 to 1.5 us:
 // cluster barriers, reads of other blocks' memory, the sort of the list); 64 rows of 131,072 with settings of their
-// own 60 us; 500 rows of 50,021 bf16 logits, top-p alone 159 us (ALU 46 %; the histogram takes two fifths of a block's time,
-// the sums for the draw a fifth, gathering the border's class an eighth).  256 threads a block, four blocks per SM: a tenth
-// slower; counts and weights together where top-k is given 78 us where counts alone took 64 (64 rows); the rows behind
+// own 60 us; 500 rows of 50,021 bf16 logits, top-p alone 159 us (ALU 48 %, issue slots 55 %; the histogram takes two
+// fifths of a block's time, the sums for the draw a fifth, gathering the border's class an eighth).  256 threads a
+// block, four blocks per SM: a tenth slower; counts and weights together where top-k is given 78 us where counts alone took 64 (64 rows); the rows behind
 // the last full round of clusters in a launch of their own with more blocks each: 174 us where one launch takes 159.
 #include <cooperative_groups.h>
 

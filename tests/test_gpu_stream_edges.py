@@ -156,7 +156,7 @@ def drawn(x, u, **par):
         token, m, p, room, near = draw(row, float(u[i].double()), **one)
         if "min_p" in one:
             near = draw(row, 0.5, **{k: v for k, v in one.items() if k != "min_p"})[4]
-        t, top = one.get("temperature", 1.0), np.nanmax(row)
+        t, top = one.get("temperature", 1.0), np.fmax.reduce(row)
         with np.errstate(invalid="ignore", over="ignore"):
             w = np.exp(np.where(row == top, 0.0, (row - top) / t)) if t else (row == top) * 1.0
         w = np.nan_to_num(w, nan=0.0)
